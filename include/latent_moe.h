@@ -374,6 +374,127 @@ lmoe_status lmoe_workspace_guards(const lmoe_config* cfg, int host_io, long long
  * counterpart on the pages: a stand-in for a device bounds sanitiser.                   */
 lmoe_status lmoe_validate_routing(const lmoe_config* cfg, void* workspace, cudaStream_t stream);
 
+/* ---- Training the router ------------------------------------------------------------------
+ * The router's two auxiliary losses with the per-expert counts, and the gradient of its logits.
+ * Row t holds E logits l = logits[t] (+ router_bias), p = softmax(l), lse = log sum exp(l).  A row
+ * is live when its mask byte is not 0 (row_mask NULL: every row) and at least one of its logits
+ * is above -inf; the logits and ids of a row that the mask drops are not read.  n: live rows;
+ * counts[e]: slots of live rows that name expert e; an id outside [0, E) is an empty slot.
+ *   losses[0] = E sum_e f_e P_e,  f_e = counts[e] / (k n),  P_e = mean_probs[e] = mean p_e
+ *               (the balance loss: 1 when either is uniform)
+ *   losses[1] = mean lse^2  (the z loss)
+ * Without a live row all of them are 0.  The caller scales and adds the losses.  Sums are taken
+ * in a fixed order: the same inputs give the same bits.
+ * Device pointers:
+ *  logits      [T, ld_logits] logits_dtype (LMOE_F32 or LMOE_BF16), ld_logits >= E elements (the
+ *              workspace's logits of a forward call have rows of E rounded up to 32)
+ *  router_bias [E] fp32 or NULL; row_mask [T] bytes or NULL; topk_idx [T, k] int32
+ *  counts      [E + 1] int32 out: counts, then n;  mean_probs [E] fp32 out;  losses [2] fp32 out
+ *  workspace   lmoe_router_losses_workspace_size() bytes, nothing to be set or kept
+ * 0 <= T <= 1 << 20, E <= 1024, k <= min(E, 16).  Pointers are aligned to their elements.    */
+lmoe_status lmoe_router_losses_workspace_size(int T, int E, size_t* bytes);
+lmoe_status lmoe_router_losses(const void* logits, lmoe_dtype logits_dtype, long long ld_logits,
+                               const float* router_bias, const uint8_t* row_mask,
+                               const int32_t* topk_idx, int T, int E, int k, int32_t* counts,
+                               float* mean_probs, float* losses, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradient of the logits (and, summed over the rows, of router_bias) from the routing weights'
+ * gradient topk_w_grad [T, k] fp32 and the losses' gradients loss_grads [2] fp32 (device; either
+ * pointer may be NULL, not both), in one pass:
+ *   dlogits_e = p_e (gb E / n (f_e - sum_j f_j p_j) + gz (2 / n) lse)
+ *               + sum over the row's slots j of expert e of w_j (gw_j - sum_i w_i gw_i),
+ * w the softmax of the row's selected logits over its slots (the routing weights of the block).
+ * f and n come from counts (of lmoe_router_losses; needed with loss_grads).  f is constant: no
+ * gradient flows through the counts.  Rows that are not live get zeros; the gradients of empty
+ * slots are not used.  dlogits [T, ld_dlogits] has the logits' dtype and may be the logits
+ * themselves (then with the same row length).                                              */
+lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dtype, long long ld_logits,
+                             const float* router_bias, const uint8_t* row_mask,
+                             const int32_t* topk_idx, const float* topk_w_grad,
+                             const int32_t* counts, const float* loss_grads, int T, int E, int k,
+                             void* dlogits, long long ld_dlogits, cudaStream_t stream);
+
+/* ---- 8-bit floating point with a scale per block of 128 -------------------------------------
+ * Experts (or any linear layer) in E4M3 or E5M2 with one fp32 scale per block, forward and
+ * backward, on the expert-contiguous rows of lmoe_permute_noalloc (offsets, tok_of).
+ *
+ * Quantisation rule, each rounding in fp32 (M = 448 for E4M3, 57344 for E5M2):
+ *   s = max(amax(block) / M, 2^-126), with pow2_scales rounded up to a power of two
+ *   code = nearest, ties to even, of v * (1 / s), saturating;   value = code * s
+ * A block holding an infinity or NaN gets a scale that is not finite.  A K that is not a multiple
+ * of 128 ends in a short block.  K is a multiple of 16 (the tensor memory accelerator's rows).
+ * Codes are 16-byte aligned and contiguous, other pointers aligned to their elements.        */
+typedef enum { LMOE_FP8_E4M3 = 0, LMOE_FP8_E5M2 = 1 } lmoe_fp8_format;
+
+/* Rows, a block is 128 elements of a row: codes [rows, K], scales [ceil(K/128), rows] fp32.
+ *  src        [src_rows, ld_src] LMOE_F32 or LMOE_BF16, ld_src >= K elements
+ *  row_index  [rows] int32: row r is src[row_index[r]] (e.g. tok_of; outside [0, src_rows): a row
+ *             of zeros), or NULL: row r is src[r]                                          */
+lmoe_status lmoe_quantize_fp8_rows(const void* src, lmoe_dtype src_dtype, long long ld_src,
+                                   const int32_t* row_index, long long src_rows, long long rows,
+                                   int K, lmoe_fp8_format format, int pow2_scales, uint8_t* codes,
+                                   float* scales, cudaStream_t stream);
+
+/* Weights, a block is 128 x 128: src [n_experts, N, K] contiguous; codes [n_experts, N, K], scales
+ * [n_experts, ceil(N/128), ceil(K/128)].  codes_t [n_experts, K, N] and scales_t [n_experts,
+ * ceil(K/128), ceil(N/128)] (both or neither; N then a multiple of 16): the transpose, with the
+ * same values, for the input gradient.                                                      */
+lmoe_status lmoe_quantize_fp8_weight(const void* src, lmoe_dtype src_dtype, int n_experts, int N,
+                                     int K, lmoe_fp8_format format, int pow2_scales,
+                                     uint8_t* codes, float* scales, uint8_t* codes_t,
+                                     float* scales_t, cudaStream_t stream);
+
+/* Columns of the rows of each expert, transposed, for the weight gradient: a block is 128 rows of
+ * one column.  Expert e's rows offsets[e] .. offsets[e+1] of the routed rows (row_index as
+ * above; offsets [n_experts + 1] int32 device, or NULL with n_experts = 1: all rows) are padded
+ * with zeros to whole blocks of 128, expert after expert; block b is columns 128 b .. of
+ * codes_t [K, padded_rows] and row b of scales_t [padded_rows / 128, K].  padded_rows must be
+ * lmoe_fp8_padded_rows(rows, n_experts), which holds any split of the rows; columns and scales
+ * behind the last expert's blocks are left as they were.  Offsets are clamped into [0, rows]. */
+long long lmoe_fp8_padded_rows(long long rows, int n_experts);
+lmoe_status lmoe_quantize_fp8_cols(const void* src, lmoe_dtype src_dtype, long long ld_src,
+                                   const int32_t* row_index, long long src_rows, long long rows,
+                                   int K, const int32_t* offsets, int n_experts,
+                                   long long padded_rows, lmoe_fp8_format format, int pow2_scales,
+                                   uint8_t* codes_t, float* scales_t, cudaStream_t stream);
+
+/* Shape of an 8-bit product.
+ *  rows       rows of a and of the product (matmul), or padded rows (wgrad)
+ *  N, K       a weight is [N, K]        n_experts  1..1024
+ *  a_format, b_format  formats of the first and of the second operand
+ *  out_dtype  LMOE_F32 or LMOE_BF16 (one rounding, at the end)
+ *  accumulate wgrad: nonzero adds to what dw holds (matmul: must be 0)                      */
+typedef struct {
+  long long rows;
+  int N, K, n_experts;
+  lmoe_fp8_format a_format, b_format;
+  lmoe_dtype out_dtype;
+  int accumulate;
+} lmoe_fp8_matmul;
+
+/* out[r, n] = sum_k a[r, k] w[e, n, k] for the rows offsets[e] <= r < offsets[e+1] of each expert
+ * (offsets [n_experts + 1] int32 device, non-decreasing, clamped into [0, rows]; NULL with
+ * n_experts = 1: all rows); rows of no expert are left as they were.
+ *  a [rows, K], a_scales [ceil(K/128), rows]   (lmoe_quantize_fp8_rows)
+ *  w [n_experts, N, K], w_scales [n_experts, ceil(N/128), ceil(K/128)]   (.._weight; for the input
+ *  gradient the transposed pair, with N and K exchanged)
+ *  out [rows, N].  Products of a block of 128 are summed by the tensor cores and added, scaled, to
+ *  fp32 sums.  status (device, may be NULL): error word as lmoe_check_status reports it, a bit
+ *  is set if a device wait gives up; the caller zeroes it.                                  */
+lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* shape, const uint8_t* a, const float* a_scales,
+                            const uint8_t* w, const float* w_scales, const int32_t* offsets,
+                            void* out, uint32_t* status, cudaStream_t stream);
+
+/* dw[e, n, k] (+)= sum over expert e's rows r of dy[r, n] x[r, k], from the column-quantised
+ * dy_t [N, rows], dy_scales [rows/128, N] (a_format) and x_t [K, rows], x_scales [rows/128, K]
+ * (b_format) of lmoe_quantize_fp8_cols, rows = its padded rows, offsets the same as there (of
+ * the rows before padding).  An expert without rows gets zeros (accumulate: is left as it was). */
+lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* shape, const uint8_t* dy_t,
+                                  const float* dy_scales, const uint8_t* x_t,
+                                  const float* x_scales, const int32_t* offsets, void* dw,
+                                  uint32_t* status, cudaStream_t stream);
+
 /* Number of kernels this library has launched in this process (all devices, all calls). */
 unsigned long long lmoe_kernel_launches(void);
 

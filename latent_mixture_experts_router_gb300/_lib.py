@@ -67,6 +67,12 @@ _LAYOUT_FIELDS = ["xa", "logits", "topk_idx", "topk_w", "counts", "offsets", "ro
 _LAYOUT_FIELDS_NVFP4 = ["xq", "xq_scale", "xq_rowscale", "xe_rowscale", "h_scale", "c_scale", "c_rowscale"]
 
 
+class lmoe_fp8_matmul(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("N", ctypes.c_int), ("K", ctypes.c_int), ("n_experts", ctypes.c_int),
+                ("a_format", ctypes.c_int), ("b_format", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("accumulate", ctypes.c_int)]
+
+
 class lmoe_workspace_layout(ctypes.Structure):
     _fields_ = ([(f, ctypes.c_longlong) for f in _LAYOUT_FIELDS + _LAYOUT_FIELDS_NVFP4]
                 + [("xa_cols", ctypes.c_int), ("grouped_splits", ctypes.c_longlong)])
@@ -105,6 +111,21 @@ def _lib():
         L.lmoe_wait_selftest.restype = ctypes.c_int
         L.lmoe_expert_pair.argtypes = [ctypes.POINTER(lmoe_config), ctypes.POINTER(ctypes.c_int)]
         L.lmoe_expert_pair.restype = ctypes.c_int
+        I, LL = ctypes.c_int, ctypes.c_longlong
+        L.lmoe_router_losses_workspace_size.argtypes = [I, I, ctypes.POINTER(ctypes.c_size_t)]
+        L.lmoe_router_losses.argtypes = [_P, I, LL, _P, _P, _P, I, I, I, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.lmoe_router_grad.argtypes = [_P, I, LL, _P, _P, _P, _P, _P, _P, I, I, I, _P, LL, _P]
+        L.lmoe_quantize_fp8_rows.argtypes = [_P, I, LL, _P, LL, LL, I, I, I, _P, _P, _P]
+        L.lmoe_quantize_fp8_weight.argtypes = [_P, I, I, I, I, I, I, _P, _P, _P, _P, _P]
+        L.lmoe_quantize_fp8_cols.argtypes = [_P, I, LL, _P, LL, LL, I, _P, I, LL, I, I, _P, _P, _P]
+        L.lmoe_fp8_padded_rows.argtypes = [LL, I]
+        L.lmoe_fp8_padded_rows.restype = LL
+        for name in ("lmoe_matmul_fp8", "lmoe_matmul_fp8_wgrad"):
+            getattr(L, name).argtypes = [ctypes.POINTER(lmoe_fp8_matmul), _P, _P, _P, _P, _P, _P, _P, _P]
+            getattr(L, name).restype = ctypes.c_int
+        for name in ("lmoe_router_losses_workspace_size", "lmoe_router_losses", "lmoe_router_grad",
+                     "lmoe_quantize_fp8_rows", "lmoe_quantize_fp8_weight", "lmoe_quantize_fp8_cols"):
+            getattr(L, name).restype = ctypes.c_int
         L.lmoe_kernel_launches.restype = ctypes.c_ulonglong
         L.lmoe_kernel_launches.argtypes = []
         _lib_handle = L
@@ -361,3 +382,209 @@ def lmoe_nvfp4_block_scales(src, K: int, block_rows: int = 128, dst=None, stream
     _check(fn(_ptr(src), rows, int(K), int(block_rows), _ptr(dst), _stream(stream)),
            "lmoe_nvfp4_block_scales")
     return dst
+
+
+# ------------------------------------------------------------------ router training, 8-bit products
+# These take tensors whose shapes and dtypes say the sizes; what does not fit is refused with a
+# ValueError before the library is called.
+_FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}          # lmoe_fp8_format
+_DENSE = {torch.float32: LMOE_F32, torch.bfloat16: LMOE_BF16}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _want(t, name, dtypes, shape, device, strided=False):
+    """``t``: a CUDA tensor on ``device`` of one of ``dtypes`` (or the one) and of ``shape``,
+    contiguous (strided: a matrix whose rows are)."""
+    if not (t.is_cuda and t.device == device):
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtypes if isinstance(dtypes, torch.dtype) else t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} is not one of {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if strided:
+        _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{name}: rows must be contiguous")
+        _need(t.shape[0] <= 1 or t.stride(0) >= t.shape[1], f"{name}: rows overlap")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _ld(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _call(fn, where, device, stream, *args):
+    """Calls ``fn`` with ``device`` current, on ``stream`` or that device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, where, device, stream, *args)
+    status = fn(*args, _stream(stream))
+    if status != 0:
+        raise LmoeError(status, where)
+
+
+def lmoe_router_losses_workspace_size(T: int, E: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib().lmoe_router_losses_workspace_size(int(T), int(E), ctypes.byref(n)),
+           "lmoe_router_losses_workspace_size")
+    return n.value
+
+
+def _router_args(logits, topk_idx, router_bias, row_mask):
+    _need(logits.dim() == 2 and topk_idx.dim() == 2, "logits [T, E] and topk_idx [T, k]")
+    dev, (T, E), k = logits.device, logits.shape, topk_idx.shape[1]
+    _want(logits, "logits", _DENSE, (T, E), dev, strided=True)
+    _want(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+    if router_bias is not None:
+        _want(router_bias, "router_bias", torch.float32, (E,), dev)
+    if row_mask is not None:
+        _want(row_mask, "row_mask", (torch.uint8, torch.bool), (T,), dev)
+    return dev, T, E, k
+
+
+def lmoe_router_losses(logits, topk_idx, counts, mean_probs, losses, workspace, router_bias=None, row_mask=None,
+                       stream=None):
+    """Balance loss and z loss of router ``logits`` [T, E] (fp32 or bf16, rows may be strided) with
+    the selected experts ``topk_idx`` [T, k] (int32): writes ``losses`` [2] fp32, ``mean_probs``
+    [E] fp32 and ``counts`` [E + 1] int32 (slots per expert, then live rows).  ``row_mask`` [T]
+    (uint8 or bool): rows that are 0 are left out.  ``workspace``: at least
+    lmoe_router_losses_workspace_size(T, E) bytes."""
+    dev, T, E, k = _router_args(logits, topk_idx, router_bias, row_mask)
+    _want(counts, "counts", torch.int32, (E + 1,), dev)
+    _want(mean_probs, "mean_probs", torch.float32, (E,), dev)
+    _want(losses, "losses", torch.float32, (2,), dev)
+    _need(workspace.device == dev and workspace.is_contiguous(), f"workspace must be contiguous on {dev}")
+    _call(_lib().lmoe_router_losses, "lmoe_router_losses", dev, stream, logits.data_ptr(), _DENSE[logits.dtype],
+          _ld(logits), _ptr(router_bias), _ptr(row_mask), topk_idx.data_ptr(), T, E, k, counts.data_ptr(),
+          mean_probs.data_ptr(), losses.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+
+
+def lmoe_router_grad(logits, topk_idx, counts, dlogits, topk_w_grad=None, loss_grads=None, router_bias=None,
+                     row_mask=None, stream=None):
+    """Gradient ``dlogits`` (dtype and shape of ``logits``, which it may be) from the routing
+    weights' gradient ``topk_w_grad`` [T, k] fp32 and the losses' gradients ``loss_grads`` [2]
+    fp32 (on the device).  ``counts``: as lmoe_router_losses wrote them (None without
+    ``loss_grads``)."""
+    dev, T, E, k = _router_args(logits, topk_idx, router_bias, row_mask)
+    _want(dlogits, "dlogits", logits.dtype, (T, E), dev, strided=True)
+    if topk_w_grad is not None:
+        _want(topk_w_grad, "topk_w_grad", torch.float32, (T, k), dev)
+    if loss_grads is not None:
+        _want(loss_grads, "loss_grads", torch.float32, (2,), dev)
+    if counts is not None:
+        _want(counts, "counts", torch.int32, (E + 1,), dev)
+    _call(_lib().lmoe_router_grad, "lmoe_router_grad", dev, stream, logits.data_ptr(), _DENSE[logits.dtype],
+          _ld(logits), _ptr(router_bias), _ptr(row_mask), topk_idx.data_ptr(), _ptr(topk_w_grad), _ptr(counts),
+          _ptr(loss_grads), T, E, k, dlogits.data_ptr(), _ld(dlogits))
+
+
+def lmoe_fp8_padded_rows(rows: int, n_experts: int) -> int:
+    """Columns that any split of ``rows`` among ``n_experts`` fits in, each padded to blocks of 128."""
+    return int(_lib().lmoe_fp8_padded_rows(int(rows), int(n_experts)))
+
+
+def _routed_src(src, row_index):
+    _need(src.dim() == 2, "src [rows, K]")
+    dev, (n, K) = src.device, src.shape
+    _want(src, "src", _DENSE, (n, K), dev, strided=True)
+    if row_index is None:
+        return dev, n, K, n
+    _need(row_index.dim() == 1, "row_index [rows]")
+    _want(row_index, "row_index", torch.int32, row_index.shape, dev)
+    return dev, n, K, row_index.shape[0]
+
+
+def lmoe_quantize_fp8_rows(src, codes, scales, row_index=None, pow2_scales=False, stream=None):
+    """Rows of ``src`` [*, K] (fp32 or bf16), gathered by ``row_index`` [rows] (int32; outside src: a
+    row of zeros) if given, into 8-bit ``codes`` [rows, K] (its dtype is the format) with a scale
+    per 128 elements, ``scales`` [ceil(K/128), rows] fp32."""
+    dev, n, K, rows = _routed_src(src, row_index)
+    _want(codes, "codes", _FP8, (rows, K), dev)
+    _want(scales, "scales", torch.float32, (-(-K // 128), rows), dev)
+    _call(_lib().lmoe_quantize_fp8_rows, "lmoe_quantize_fp8_rows", dev, stream, src.data_ptr(), _DENSE[src.dtype],
+          _ld(src), _ptr(row_index), n, rows, K, _FP8[codes.dtype], 1 if pow2_scales else 0, codes.data_ptr(),
+          scales.data_ptr())
+
+
+def lmoe_quantize_fp8_weight(src, codes, scales, codes_t=None, scales_t=None, pow2_scales=False, stream=None):
+    """Weights ``src`` [N, K] or [E, N, K] (fp32 or bf16) into 8-bit ``codes`` of the same shape with a
+    scale per 128 x 128 block, ``scales`` [(E,) ceil(N/128), ceil(K/128)]; ``codes_t``, ``scales_t``:
+    also the transposed pair."""
+    _need(src.dim() in (2, 3), "src [N, K] or [E, N, K]")
+    dev, (N, K), lead = src.device, src.shape[-2:], src.shape[:-2]
+    nb, kb = -(-N // 128), -(-K // 128)
+    _want(src, "src", _DENSE, src.shape, dev)
+    _want(codes, "codes", _FP8, src.shape, dev)
+    _want(scales, "scales", torch.float32, (*lead, nb, kb), dev)
+    if codes_t is not None:
+        _want(codes_t, "codes_t", codes.dtype, (*lead, K, N), dev)
+    if scales_t is not None:
+        _want(scales_t, "scales_t", torch.float32, (*lead, kb, nb), dev)
+    _call(_lib().lmoe_quantize_fp8_weight, "lmoe_quantize_fp8_weight", dev, stream, src.data_ptr(),
+          _DENSE[src.dtype], lead[0] if lead else 1, N, K, _FP8[codes.dtype], 1 if pow2_scales else 0,
+          codes.data_ptr(), scales.data_ptr(), _ptr(codes_t), _ptr(scales_t))
+
+
+def lmoe_quantize_fp8_cols(src, codes_t, scales_t, offsets=None, row_index=None, pow2_scales=False, stream=None):
+    """The routed rows of ``src`` (as lmoe_quantize_fp8_rows), expert by expert (``offsets`` [E + 1]
+    int32; None: one group), each padded to blocks of 128 rows, into transposed 8-bit ``codes_t``
+    [K, P] with a scale per 128 rows of a column, ``scales_t`` [P / 128, K] fp32;
+    P = lmoe_fp8_padded_rows(rows, E)."""
+    dev, n, K, rows = _routed_src(src, row_index)
+    E = 1
+    if offsets is not None:
+        _need(offsets.dim() == 1 and offsets.shape[0] > 1, "offsets [E + 1]")
+        E = offsets.shape[0] - 1
+        _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+    P = lmoe_fp8_padded_rows(rows, E)
+    _want(codes_t, "codes_t", _FP8, (K, P), dev)
+    _want(scales_t, "scales_t", torch.float32, (P // 128, K), dev)
+    _call(_lib().lmoe_quantize_fp8_cols, "lmoe_quantize_fp8_cols", dev, stream, src.data_ptr(), _DENSE[src.dtype],
+          _ld(src), _ptr(row_index), n, rows, K, _ptr(offsets), E, P, _FP8[codes_t.dtype],
+          1 if pow2_scales else 0, codes_t.data_ptr(), scales_t.data_ptr())
+
+
+def _fp8_product(fn, where, dev, stream, rows, N, K, E, a, a_scales, b, b_scales, offsets, out, accumulate, status):
+    if offsets is not None:
+        _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+    if status is not None:
+        _want(status, "status", (torch.int32, torch.uint32), (1,), dev)
+    shape = lmoe_fp8_matmul(rows, N, K, E, _FP8[a.dtype], _FP8[b.dtype], _DENSE[out.dtype], 1 if accumulate else 0)
+    _call(fn, where, dev, stream, ctypes.byref(shape), a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
+          b_scales.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(status))
+
+
+def lmoe_matmul_fp8(a, a_scales, w, w_scales, out, offsets=None, status=None, stream=None):
+    """``out`` [rows, N] (fp32 or bf16) = ``a`` [rows, K] times ``w`` [N, K] transposed, or, with ``w`` [E, N,
+    K] and ``offsets`` [E + 1] (int32), each expert's rows times its own; scales as
+    lmoe_quantize_fp8_rows and lmoe_quantize_fp8_weight write them."""
+    _need(a.dim() == 2 and w.dim() in (2, 3), "a [rows, K] and w [N, K] or [E, N, K]")
+    dev, (rows, K), N, lead = a.device, a.shape, w.shape[-2], w.shape[:-2]
+    kb = -(-K // 128)
+    _want(a, "a", _FP8, (rows, K), dev)
+    _want(a_scales, "a_scales", torch.float32, (kb, rows), dev)
+    _want(w, "w", _FP8, (*lead, N, K), dev)
+    _want(w_scales, "w_scales", torch.float32, (*lead, -(-N // 128), kb), dev)
+    _want(out, "out", _DENSE, (rows, N), dev)
+    _fp8_product(_lib().lmoe_matmul_fp8, "lmoe_matmul_fp8", dev, stream, rows, N, K, lead[0] if lead else 1, a,
+                 a_scales, w, w_scales, offsets, out, False, status)
+
+
+def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate=False, status=None,
+                          stream=None):
+    """``dw`` [(E,) N, K] (fp32 or bf16) (+)= each expert's rows of dy transposed times its rows of x, from
+    ``dy_t`` [N, P] and ``x_t`` [K, P] as lmoe_quantize_fp8_cols writes them for ``offsets`` [E + 1]."""
+    _need(dy_t.dim() == 2 and x_t.dim() == 2 and dw.dim() in (2, 3), "dy_t [N, P], x_t [K, P], dw [(E,) N, K]")
+    dev, (N, P), K, lead = dy_t.device, dy_t.shape, x_t.shape[0], dw.shape[:-2]
+    _need(P % 128 == 0, "P must be a multiple of 128")
+    _want(dy_t, "dy_t", _FP8, (N, P), dev)
+    _want(dy_scales, "dy_scales", torch.float32, (P // 128, N), dev)
+    _want(x_t, "x_t", _FP8, (K, P), dev)
+    _want(x_scales, "x_scales", torch.float32, (P // 128, K), dev)
+    _want(dw, "dw", _DENSE, (*lead, N, K), dev)
+    _fp8_product(_lib().lmoe_matmul_fp8_wgrad, "lmoe_matmul_fp8_wgrad", dev, stream, P, N, K, lead[0] if lead else 1,
+                 dy_t, dy_scales, x_t, x_scales, offsets, dw, accumulate, status)

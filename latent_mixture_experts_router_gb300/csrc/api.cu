@@ -309,6 +309,57 @@ bool encode_u8_2d(CUtensorMap* m, const void* base, unsigned long long cols, uns
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace lmoe {
+bool encode_u8_swizzled(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                        const unsigned long long* strides, const unsigned* box) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr || rank < 2 || rank > 3) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3];
+  const cuuint32_t estr[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, st, b, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t allow_smem(const void* kernel, int bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  // what each kernel has been allowed on each device; a full table only costs the call again
+  struct Entry {
+    const void* kernel;
+    int dev, bytes;
+  };
+  static Entry table[128];
+  static int used = 0;
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  Entry* at = nullptr;
+  for (int i = 0; i < used; ++i)
+    if (table[i].kernel == kernel && table[i].dev == dev) at = &table[i];
+  if (at != nullptr && at->bytes >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  if (at == nullptr && used < 128) {
+    at = &table[used++];
+    *at = {kernel, dev, 0};
+  }
+  if (at != nullptr) at->bytes = bytes;
+  return cudaSuccess;
+}
+}  // namespace lmoe
+
+namespace {
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 #define LMOE_CUDA(call)                       \

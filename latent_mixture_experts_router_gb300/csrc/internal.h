@@ -167,6 +167,14 @@ cudaError_t launch_swiglu_reduce_nvfp4(const float* partial, const int* splits_d
                                        const Tile* tiles, const int* n_tiles, int max_tiles,
                                        uint8_t* codes, uint8_t* scales, cudaStream_t s);
 
+// Allows `kernel` `bytes` of dynamic shared memory on the current device (once per kernel and
+// device; nothing to do up to 48 KB).
+cudaError_t allow_smem(const void* kernel, int bytes);
+// Tensor map of a byte matrix (rank 2 or 3, innermost dimension first; strides in bytes of the
+// dimensions after it) with 128-byte swizzled boxes; elements outside read as 0.
+bool encode_u8_swizzled(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                        const unsigned long long* strides, const unsigned* box);
+
 // Counts every kernel launch of the library (lmoe_kernel_launches).
 void count_launch();
 
