@@ -11,7 +11,7 @@
 // several TMEM buffers, and the epilogue warps add buffer x scales to fp32 accumulators in
 // registers while the next block's MMAs run.  Adding a 128 x 256 block takes 128 x 256 fused
 // multiply-adds on the CUDA cores (128 a cycle) beside 128 x 256 x 128 on the tensor cores
-// (8192 a cycle): half the time, as packed pairs a quarter of the issue slots.
+// (8192 a cycle): half the time.
 //
 // The weights' rows are the MMA's 128 lanes and the tokens its columns ("lane" and "column"
 // operand below): the column count of an MMA is any multiple of 16, so an expert with 40 rows
@@ -48,6 +48,7 @@ struct Fp8Args {
   long long ldq;
   void* out;
   int out_f32, accumulate;
+  int out_vec;           // bf16: 16-byte stores fit the output's base and rows
   unsigned fmt_p, fmt_q;   // 0 e4m3, 1 e5m2
   unsigned* status;      // error word or nullptr
   long long budget;
@@ -68,8 +69,10 @@ struct Fp8Cfg {
   static constexpr uint32_t kTmemCols = BN * kBufs;
   static constexpr int kMaxS = BN == 16 ? kMaxSplit : 4;
   static constexpr int kRedBytes = MODE == kSplit ? (kMaxS - 1) * BN * 128 * 4 : 0;
+  static constexpr int kStageCols = 16;               // columns of one pass of the bf16 store
+  static constexpr int kOutBytes = kEpiWarps * kStageCols * 64;
   static constexpr int kTableBytes = 3 * (kMaxGroups + 4) * 4;
-  static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kTableBytes + 512 + 1024;
+  static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kOutBytes + kTableBytes + 512 + 1024;
   static constexpr int kStagesFit = (227 * 1024 - kFixed) / kStageBytes;
   static constexpr int kStages = kStagesFit > 11 ? 11 : kStagesFit;
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
@@ -99,47 +102,40 @@ LMOE_DEV void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, i
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
-// 16 consecutive columns of the warp's 32 lanes
-LMOE_DEV void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 lanes x 8 N columns: thread l gets, per 8 columns, columns 2 (l % 4), + 1 of lanes l / 4
+// (registers 0, 1) and l / 4 + 8 (registers 2, 3).
+LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// Waits for the warp's TMEM reads; r passes through, so that no use of it moves ahead of the wait.
-LMOE_DEV void tmem_ld_wait(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
+LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// d += (value read from TMEM) * s, and (value) *= s: volatile, so that the compiler keeps them
+// behind the wait for the read that the value comes from.
+LMOE_DEV void fma_acc(float& d, uint32_t v, float s) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "r"(v), "f"(s));
+}
+LMOE_DEV void scale_in_place(uint32_t& v, float s) { asm volatile("mul.rn.f32 %0, %0, %1;" : "+r"(v) : "f"(s)); }
+// Stores four 8 x 8 matrices of 16-bit values transposed: thread l names the 16-byte row l % 8
+// of matrix l / 8; matrix m's elements (row t / 4, columns 2 (t % 4), + 1) are thread t's r[m].
+LMOE_DEV void stmatrix_x4_trans(uint32_t saddr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
-// packed pairs of fp32
-LMOE_DEV uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-LMOE_DEV void unpack2(uint64_t v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-LMOE_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-LMOE_DEV uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // Registers of a warpgroup (all four of its warps).  256-column tiles: the epilogue's two
-// warpgroups hold 128 accumulators a thread; 4 x 32 x 72 + 8 x 32 x 216 = 384 x 168, what the
+// warpgroups hold 128 accumulators a thread; 4 x 32 x 56 + 8 x 32 x 224 = 384 x 168, what the
 // block was launched with.
 template <int N>
 LMOE_DEV void regs_dec() {
@@ -218,8 +214,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   float* red = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
-  float* sc = red + C::kRedBytes / 4;                       // [kSlots][BN]
-  int* start = reinterpret_cast<int*>(sc + C::kSlots * BN);   // [E + 1], then lo, hi
+  uint8_t* stage_out = reinterpret_cast<uint8_t*>(red) + C::kRedBytes;
+  float* sc = reinterpret_cast<float*>(stage_out + C::kOutBytes);   // [kSlots][BN]
+  int* start = reinterpret_cast<int*>(sc + C::kSlots * BN);         // [E + 1], then lo, hi
   int* lo = start + kMaxGroups + 4;
   int* hi = lo + kMaxGroups + 4;
   uint64_t* full = reinterpret_cast<uint64_t*>(hi + kMaxGroups + 4);
@@ -308,7 +305,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   if (MODE == kSplit) cluster_arrive();   // every CTA of the cluster has started (waited for below)
 
   if (warp < 4) {
-  if constexpr (BN == 256) regs_dec<72>();
+  if constexpr (BN == 256) regs_dec<56>();
   if (warp == 0) {
     if (lane == 0) {
       // ---- TMA producer
@@ -371,9 +368,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
       mma_commit(mma_done);
     }
   } else if (warp == 2) {
-    // ---- column scales (times the lane block's scale where there is one), four blocks' loads
-    // in flight at a time
-    constexpr int kPer = (BN + 31) / 32, kBatch = 4;
+    // ---- column scales (times the lane block's scale where there is one), the loads of
+    // several blocks in flight at a time
+    constexpr int kPer = (BN + 31) / 32, kBatch = BN == 256 ? 2 : 4;
     int it = 0;
     bool ok = true;
     for (int id = id0; ok && id < walk.total; id += step) {
@@ -412,78 +409,113 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
     }
   }
   } else {
-    // ---- epilogue
-    if constexpr (BN == 256) regs_inc<216>();
+    // ---- epilogue.  A TMEM read in the 16 x 256-bit shape gives a thread two columns of four
+    // lanes per 8 columns, so that it needs two of their scales, not eight: with a lane's whole
+    // row per thread every scale goes to every thread, and returning those from shared memory
+    // (128 bytes a cycle) takes twice the MMAs' time.
+    if constexpr (BN == 256) regs_inc<224>();
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    const int r = quad * 32 + lane, c0 = half * C::kCols;
+    const int r = quad * 32 + (lane >> 2);                 // lanes r, + 8, + 16, + 24 of the tile
+    const int c0 = half * C::kCols, cl = (lane & 3) * 2;   // columns c0 + 8 g + cl, + 1
     const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-    constexpr int kCh = 16;   // columns of one TMEM read (two are held: 32 registers beside the accumulators)
-    constexpr int kN = C::kCols / kCh;
+    constexpr int kChC = C::kCols >= 64 ? 64 : 16;         // columns of one TMEM read
+    constexpr int kG = kChC / 8, kN = C::kCols / kChC * 2;
     int it = 0;
     bool ok = true;
     for (int id = id0; ok && id < walk.total; id += step) {
-      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-      const bool lane_ok = t.p0 + r < args.lanes;
-      uint64_t acc[C::kCols / 2];
+      // (the tile is worked out again for the stores: its registers are the accumulators' here)
+      int kb, kb1;
+      const float* ps = nullptr;   // wgrad: scale of this thread's first lane in the next block
+      int left = 0;                // lanes of the operand from there on
+      {
+        const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
+        kb = t.kb0;
+        kb1 = t.kb1;
+        if (MODE == kWgrad) {
+          ps = args.ps + static_cast<long long>(kb) * args.lanes + t.p0 + r;
+          left = args.lanes - t.p0 - r;
+        }
+      }
+      // acc[g][j][u]: column u of group g's pair, lane 8 j + l / 4 of the warp's 32
+      float acc[C::kCols / 8][4][2];
 #pragma unroll
-      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
-      const float* ps = MODE == kWgrad ? args.ps + t.p0 + r : nullptr;
-      float sp_next = (MODE == kWgrad && lane_ok && t.kb0 < t.kb1) ? ps[static_cast<long long>(t.kb0) * args.lanes] : 0.f;
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        const float sp = sp_next;
-        if (MODE == kWgrad && lane_ok && kb + 1 < t.kb1) sp_next = ps[static_cast<long long>(kb + 1) * args.lanes];
-        const int buf = it % C::kBufs, s = it % C::kSlots;
-        if (!mbar_wait(&sfull[s], (it / C::kSlots) & 1, budget) ||
-            !mbar_wait(&acc_full[buf], (it / C::kBufs) & 1, budget)) {
+      for (int i = 0; i < C::kCols; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] = 0.f;
+      float sp_next[4] = {};
+      if (MODE == kWgrad && kb < kb1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (8 * j < left) sp_next[j] = ps[8 * j];
+      }
+      uint32_t v[2][kG * 4];
+      // waits for block `i` of the ring and reads its first columns
+      const auto begin = [&](int i) {
+        const int buf = i % C::kBufs, s = i % C::kSlots;
+        if (!mbar_wait(&sfull[s], (i / C::kSlots) & 1, budget) ||
+            !mbar_wait(&acc_full[buf], (i / C::kBufs) & 1, budget)) {
           if (args.status) atomicOr(args.status, kErrWaitEpilogue);
-          ok = false;
-          break;
+          return false;
         }
         tc_fence_after();
-        const float* scs = sc + s * BN + c0;
-        const uint64_t sp2 = pack2(__float_as_uint(sp), __float_as_uint(sp));
-        uint32_t v[2][kCh];
-        tmem_ld_16cols(tq + buf * BN, v[0]);
-
-        tmem_ld_wait(v[0]);
+        tmem_ld_frag(tq + buf * BN, v[0]);
+        return true;
+      };
+      for (; kb < kb1; ++kb, ++it) {
+        ok = begin(it);
+        if (!ok) break;
+        tmem_ld_wait();
+        float sp[4];
+        if (MODE == kWgrad) {
+          ps += args.lanes;
 #pragma unroll
-        for (int ch = 0; ch < kN; ++ch) {
+          for (int j = 0; j < 4; ++j) {
+            sp[j] = sp_next[j];
+            if (kb + 1 < kb1 && 8 * j < left) sp_next[j] = ps[8 * j];
+          }
+        }
+        const int s = it % C::kSlots;
+        const float* scs = sc + s * BN + c0 + cl;
+#pragma unroll
+        for (int ch = 0; ch < kN; ++ch) {   // 16 lanes x kChC columns: lane half ch % 2
+          const int h = ch & 1, g0 = (ch >> 1) * kG;
+          // the next read is under way while these columns are added: of this block, or, every
+          // column of its buffer having been read, the first of the next block's
           if (ch + 1 < kN) {
-            tmem_ld_16cols(tq + buf * BN + (ch + 1) * kCh, v[(ch + 1) & 1]);
-          } else {   // every column of the buffer has been read
+            tmem_ld_frag(tq + (it % C::kBufs) * BN + ((ch + 1) >> 1) * kChC + (((ch + 1) & 1) ? (16u << 16) : 0u),
+                         v[(ch + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            if (lane == 0) mbar_arrive(&acc_empty[it % C::kBufs]);
           }
 #pragma unroll
-          for (int i = 0; i < kCh; i += 4) {
-            const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(scs + ch * kCh + i);
-            uint64_t a = pack2(v[ch & 1][i], v[ch & 1][i + 1]), b = pack2(v[ch & 1][i + 2], v[ch & 1][i + 3]);
-            if (MODE == kWgrad) {
-              a = mul2(a, sp2);
-              b = mul2(b, sp2);
+          for (int g = 0; g < kG; ++g) {
+            const float2 s2 = *reinterpret_cast<const float2*>(scs + (g0 + g) * 8);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t *w = &v[ch & 1][4 * g + 2 * q];
+              if (MODE == kWgrad) {
+                scale_in_place(w[0], sp[2 * h + q]);
+                scale_in_place(w[1], sp[2 * h + q]);
+              }
+              float(&d)[2] = acc[g0 + g][2 * h + q];
+              fma_acc(d[0], w[0], s2.x);
+              fma_acc(d[1], w[1], s2.y);
             }
-            const int q = (ch * kCh + i) / 2;
-            acc[q] = fma2(a, s2.x, acc[q]);
-            acc[q + 1] = fma2(b, s2.y, acc[q + 1]);
           }
-          if (ch + 1 < kN) tmem_ld_wait(v[(ch + 1) & 1]);
+          if (ch + 1 < kN) tmem_ld_wait();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[s]);
       }
       if (MODE == kSplit) {
-        // one tile per cluster: the accumulators of ranks 1.. go to rank 0 (below)
+        // one tile per cluster: the accumulators of ranks 1.. go to rank 0 (element i of thread x
+        // at i * 128 + x: threads beside each other, words beside each other)
+        const int tid = threadIdx.x - 128;
         if (rank > 0) {
           cluster_wait();
-          const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * BN * 128 + c0 * 128 + r), 0);
+          const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * BN * 128 + tid), 0);
 #pragma unroll
-          for (int i = 0; i < C::kCols / 2; ++i) {
-            float x, y;
-            unpack2(acc[i], x, y);
-            cluster_store(dst + (2 * i) * 512, x);
-            cluster_store(dst + (2 * i + 1) * 512, y);
-          }
+          for (int i = 0; i < C::kCols; ++i) cluster_store(dst + i * 512, acc[i >> 3][(i >> 1) & 3][i & 1]);
           cluster_arrive();
           cluster_wait();
         } else {
@@ -491,45 +523,76 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
           cluster_arrive();
           cluster_wait();
           for (int q = 1; q < S; ++q) {
-            const float* src = red + (q - 1) * BN * 128 + c0 * 128 + r;
+            const float* src = red + (q - 1) * BN * 128 + tid;
 #pragma unroll
-            for (int i = 0; i < C::kCols / 2; ++i) {
-              float x, y;
-              unpack2(acc[i], x, y);
-              x += src[(2 * i) * 128];
-              y += src[(2 * i + 1) * 128];
-              acc[i] = pack2(__float_as_uint(x), __float_as_uint(y));
-            }
+            for (int i = 0; i < C::kCols; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] += src[i * 128];
           }
         }
       }
-      const bool adds_nothing = args.accumulate && t.kb0 == t.kb1;
-      if (ok && lane_ok && rank == 0 && !adds_nothing) {
-        const int n = min(C::kCols, t.ncols - c0);
-        const long long base = t.out + static_cast<long long>(c0) * args.lanes + r;
-        if (args.out_f32) {
-          float* o = static_cast<float*>(args.out) + base;
+      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
+      if (!ok || rank != 0 || (args.accumulate && t.kb0 == t.kb1)) continue;
+      const int n = min(C::kCols, t.ncols - c0);   // live columns (may be negative)
+      if (!args.out_f32 && !args.accumulate) {
+        // bf16: 16 columns at a time through this warp's shared memory, transposed there: a store
+        // instruction then writes 64 bytes (32 lanes' values) of each of 8 columns (rows of the
+        // output).  16-byte chunk i of column c is at place i ^ (c / 2 % 4): no bank conflicts
+        // either way.
+        uint8_t* so = stage_out + (warp - 4) * C::kStageCols * 64;
+        const int left_n = args.lanes - t.p0 - quad * 32 - (lane & 3) * 8;   // of this thread's chunk
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + t.out + quad * 32 + (lane & 3) * 8 +
+                           static_cast<long long>(c0 + (lane >> 2)) * args.lanes;
 #pragma unroll
-          for (int i = 0; i < C::kCols / 2; ++i) {
-            float x, y;
-            unpack2(acc[i], x, y);
-            if (2 * i < n) *o = args.accumulate ? *o + x : x;
-            o += args.lanes;
-            if (2 * i + 1 < n) *o = args.accumulate ? *o + y : y;
-            o += args.lanes;
-          }
-        } else {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + base;
+        for (int g = 0; g < C::kCols / 8; g += 2) {
+          if (8 * g >= n) break;
 #pragma unroll
-          for (int i = 0; i < C::kCols / 2; ++i) {
-            float x, y;
-            unpack2(acc[i], x, y);
-            if (2 * i < n) *o = __float2bfloat16_rn(args.accumulate ? __bfloat162float(*o) + x : x);
-            o += args.lanes;
-            if (2 * i + 1 < n) *o = __float2bfloat16_rn(args.accumulate ? __bfloat162float(*o) + y : y);
-            o += args.lanes;
+          for (int u = 0; u < 2; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[g + u][j][0], acc[g + u][j][1]);
+            const int c = 8 * u + (lane & 7), chunk = lane >> 3;
+            stmatrix_x4_trans(smem_u32(so + c * 64 + ((chunk ^ ((c >> 1) & 3)) << 4)), w);
           }
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int c = 8 * u + (lane >> 2), chunk = lane & 3;
+            const uint4 q = *reinterpret_cast<const uint4*>(so + c * 64 + ((chunk ^ ((c >> 1) & 3)) << 4));
+            if (8 * g + c < n && left_n > 0) {
+              if (args.out_vec) {
+                *reinterpret_cast<uint4*>(o) = q;
+              } else {
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (i < left_n) o[i] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1))));
+              }
+            }
+            o += 8LL * args.lanes;
+          }
+          __syncwarp();
         }
+      } else {
+        // fp32: a store instruction writes 8 lanes' words of 4 columns: whole 32-byte sectors
+#pragma unroll
+        for (int g = 0; g < C::kCols / 8; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int c = 8 * g + cl + u;
+            if (c >= n) continue;
+            const long long base = t.out + static_cast<long long>(c0 + c) * args.lanes + r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (t.p0 + r + 8 * j >= args.lanes) continue;
+              const float val = acc[g][j][u];
+              if (args.out_f32) {
+                float* o = static_cast<float*>(args.out) + base + 8 * j;
+                *o = args.accumulate ? *o + val : val;
+              } else {
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + base + 8 * j;
+                *o = __float2bfloat16_rn(__bfloat162float(*o) + val);
+              }
+            }
+          }
       }
     }
   }
@@ -608,6 +671,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   g.ldq = c->rows;
   g.out = out;
   g.out_f32 = c->out_dtype == LMOE_F32;
+  g.out_vec = aligned(out, 16) && c->N % 8 == 0;
   g.fmt_p = c->b_format;
   g.fmt_q = c->a_format;
   g.status = status;
@@ -673,6 +737,7 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   g.ldq = c->N;
   g.out = dw;
   g.out_f32 = c->out_dtype == LMOE_F32;
+  g.out_vec = aligned(dw, 16) && c->K % 8 == 0;
   g.accumulate = c->accumulate;
   g.fmt_p = c->b_format;
   g.fmt_q = c->a_format;
