@@ -389,6 +389,9 @@ def lmoe_nvfp4_block_scales(src, K: int, block_rows: int = 128, dst=None, stream
 # ValueError before the library is called.
 _FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}          # lmoe_fp8_format
 _DENSE = {torch.float32: LMOE_F32, torch.bfloat16: LMOE_BF16}
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _need(ok, what):
@@ -397,19 +400,18 @@ def _need(ok, what):
 
 
 def _want(t, name, dtypes, shape, device, strided=False):
-    """``t``: a CUDA tensor on ``device`` of one of ``dtypes`` (or the one) and of ``shape``,
-    contiguous (strided: a matrix whose rows are)."""
-    if not (t.is_cuda and t.device == device):
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtypes if isinstance(dtypes, torch.dtype) else t.dtype not in dtypes:
+    """``t``: a CUDA tensor on device number ``device`` of one of ``dtypes`` (or the one) and of
+    ``shape``, contiguous (strided: a matrix whose rows are)."""
+    if t.dtype is not dtypes and (isinstance(dtypes, torch.dtype) or t.dtype not in dtypes):
         raise ValueError(f"{name}: dtype {t.dtype} is not one of {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if strided:
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{device}" if device >= 0 else ""))
+    if not t.is_contiguous():
+        _need(strided, f"{name} must be contiguous")
         _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{name}: rows must be contiguous")
         _need(t.shape[0] <= 1 or t.stride(0) >= t.shape[1], f"{name}: rows overlap")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def _ld(t):
@@ -417,11 +419,11 @@ def _ld(t):
 
 
 def _call(fn, where, device, stream, *args):
-    """Calls ``fn`` with ``device`` current, on ``stream`` or that device's current stream."""
-    if device.index != torch.cuda.current_device():
+    """Calls ``fn`` with device number ``device`` current, on ``stream`` or that device's current one."""
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(fn, where, device, stream, *args)
-    status = fn(*args, _stream(stream))
+    status = fn(*args, _raw_stream(device) if stream is None else _stream(stream))
     if status != 0:
         raise LmoeError(status, where)
 
@@ -435,7 +437,7 @@ def lmoe_router_losses_workspace_size(T: int, E: int) -> int:
 
 def _router_args(logits, topk_idx, router_bias, row_mask):
     _need(logits.dim() == 2 and topk_idx.dim() == 2, "logits [T, E] and topk_idx [T, k]")
-    dev, (T, E), k = logits.device, logits.shape, topk_idx.shape[1]
+    dev, (T, E), k = logits.get_device(), logits.shape, topk_idx.shape[1]
     _want(logits, "logits", _DENSE, (T, E), dev, strided=True)
     _want(topk_idx, "topk_idx", torch.int32, (T, k), dev)
     if router_bias is not None:
@@ -456,7 +458,7 @@ def lmoe_router_losses(logits, topk_idx, counts, mean_probs, losses, workspace, 
     _want(counts, "counts", torch.int32, (E + 1,), dev)
     _want(mean_probs, "mean_probs", torch.float32, (E,), dev)
     _want(losses, "losses", torch.float32, (2,), dev)
-    _need(workspace.device == dev and workspace.is_contiguous(), f"workspace must be contiguous on {dev}")
+    _need(workspace.get_device() == dev and workspace.is_contiguous(), f"workspace must be contiguous on cuda:{dev}")
     _call(_lib().lmoe_router_losses, "lmoe_router_losses", dev, stream, logits.data_ptr(), _DENSE[logits.dtype],
           _ld(logits), _ptr(router_bias), _ptr(row_mask), topk_idx.data_ptr(), T, E, k, counts.data_ptr(),
           mean_probs.data_ptr(), losses.data_ptr(), workspace.data_ptr(),
@@ -489,7 +491,7 @@ def lmoe_fp8_padded_rows(rows: int, n_experts: int) -> int:
 
 def _routed_src(src, row_index):
     _need(src.dim() == 2, "src [rows, K]")
-    dev, (n, K) = src.device, src.shape
+    dev, (n, K) = src.get_device(), src.shape
     _want(src, "src", _DENSE, (n, K), dev, strided=True)
     if row_index is None:
         return dev, n, K, n
@@ -515,7 +517,7 @@ def lmoe_quantize_fp8_weight(src, codes, scales, codes_t=None, scales_t=None, po
     scale per 128 x 128 block, ``scales`` [(E,) ceil(N/128), ceil(K/128)]; ``codes_t``, ``scales_t``:
     also the transposed pair."""
     _need(src.dim() in (2, 3), "src [N, K] or [E, N, K]")
-    dev, (N, K), lead = src.device, src.shape[-2:], src.shape[:-2]
+    dev, (N, K), lead = src.get_device(), src.shape[-2:], src.shape[:-2]
     nb, kb = -(-N // 128), -(-K // 128)
     _want(src, "src", _DENSE, src.shape, dev)
     _want(codes, "codes", _FP8, src.shape, dev)
@@ -563,7 +565,7 @@ def lmoe_matmul_fp8(a, a_scales, w, w_scales, out, offsets=None, status=None, st
     K] and ``offsets`` [E + 1] (int32), each expert's rows times its own; scales as
     lmoe_quantize_fp8_rows and lmoe_quantize_fp8_weight write them."""
     _need(a.dim() == 2 and w.dim() in (2, 3), "a [rows, K] and w [N, K] or [E, N, K]")
-    dev, (rows, K), N, lead = a.device, a.shape, w.shape[-2], w.shape[:-2]
+    dev, (rows, K), N, lead = a.get_device(), a.shape, w.shape[-2], w.shape[:-2]
     kb = -(-K // 128)
     _want(a, "a", _FP8, (rows, K), dev)
     _want(a_scales, "a_scales", torch.float32, (kb, rows), dev)
@@ -579,7 +581,7 @@ def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accu
     """``dw`` [(E,) N, K] (fp32 or bf16) (+)= each expert's rows of dy transposed times its rows of x, from
     ``dy_t`` [N, P] and ``x_t`` [K, P] as lmoe_quantize_fp8_cols writes them for ``offsets`` [E + 1]."""
     _need(dy_t.dim() == 2 and x_t.dim() == 2 and dw.dim() in (2, 3), "dy_t [N, P], x_t [K, P], dw [(E,) N, K]")
-    dev, (N, P), K, lead = dy_t.device, dy_t.shape, x_t.shape[0], dw.shape[:-2]
+    dev, (N, P), K, lead = dy_t.get_device(), dy_t.shape, x_t.shape[0], dw.shape[:-2]
     _need(P % 128 == 0, "P must be a multiple of 128")
     _want(dy_t, "dy_t", _FP8, (N, P), dev)
     _want(dy_scales, "dy_scales", torch.float32, (P // 128, N), dev)

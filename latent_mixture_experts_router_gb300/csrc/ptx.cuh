@@ -267,6 +267,30 @@ LMOE_DEV bool grouped_tile(int id, int total_m, int nt, int group, int& m, int& 
 }
 constexpr int kRasterGroup = 16;
 
+// ------------------------------------------------------------------ clusters
+// Every thread of the cluster arrives and waits, warps converged.
+LMOE_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+LMOE_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+LMOE_DEV void cluster_sync() {
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+}
+// Address in CTA `rank`'s shared memory of what is at saddr in this CTA's.
+LMOE_DEV uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+LMOE_DEV void cluster_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+LMOE_DEV uint32_t cluster_load(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------ misc
 LMOE_DEV float bf16_round(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
 

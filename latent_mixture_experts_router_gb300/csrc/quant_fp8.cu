@@ -50,39 +50,60 @@ LMOE_DEV uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 LMOE_DEV float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 LMOE_DEV float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// N consecutive elements as fp32
-template <bool VEC, int N>
-LMOE_DEV void load_n(const float* p, float (&v)[N]) {
-  if constexpr (VEC) {
+// N consecutive elements of a row, as loaded, and their magnitudes.  Magnitudes are compared as
+// bit patterns: 32 bits for fp32, 16 for bf16 (two to a word).
+template <typename T, int N>
+struct Raw;
+template <int N>
+struct Raw<float, N> {
+  float4 q[N / 4];
+  LMOE_DEV void zero() {
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) q[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  template <bool VEC>
+  LMOE_DEV void load(const float* p) {
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
-      const float4 q = reinterpret_cast<const float4*>(p)[j];
-      v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+      if constexpr (VEC) q[j] = reinterpret_cast<const float4*>(p)[j];
+      else q[j] = make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = p[j];
   }
-}
-template <bool VEC, int N>
-LMOE_DEV void load_n(const __nv_bfloat16* p, float (&v)[N]) {
-  if constexpr (VEC && N == 8) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    v[0] = lo16(q.x), v[1] = hi16(q.x), v[2] = lo16(q.y), v[3] = hi16(q.y);
-    v[4] = lo16(q.z), v[5] = hi16(q.z), v[6] = lo16(q.w), v[7] = hi16(q.w);
-  } else if constexpr (VEC) {
-    const uint2 q = *reinterpret_cast<const uint2*>(p);
-    v[0] = lo16(q.x), v[1] = hi16(q.x), v[2] = lo16(q.y), v[3] = hi16(q.y);
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = __bfloat162float(p[j]);
+  LMOE_DEV float get(int i) const {
+    const float4& v = q[i >> 2];
+    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
   }
-}
+};
+template <int N>
+struct Raw<__nv_bfloat16, N> {
+  uint32_t w[N / 2];
+  LMOE_DEV void zero() {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) w[j] = 0u;
+  }
+  template <bool VEC>
+  LMOE_DEV void load(const __nv_bfloat16* p) {
+    if constexpr (VEC && N == 8) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else if constexpr (VEC) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x, w[1] = q.y;
+    } else {
+      const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) w[j] = u[2 * j] | (static_cast<uint32_t>(u[2 * j + 1]) << 16);
+    }
+  }
+  LMOE_DEV float get(int i) const { return i & 1 ? hi16(w[i >> 1]) : lo16(w[i >> 1]); }
+};
 
 // ------------------------------------------------------------------ rows
-// A warp takes 8 rows of one block of columns: half a warp reads a row's 128 elements (8 per
-// lane), four rows each in flight at once, and the eight scales are one 32-byte sector of
-// scales[kb].  Warps beside each other take the next blocks of the same rows.
+// Half a warp reads 128 elements of a row (8 per lane), of all its rows before it works on any; a
+// warp takes 16 (fp32: 8) rows of one block of columns, warps beside each other the next blocks
+// of the same rows.  The maxima of a half's rows are reduced together: each step of the butterfly
+// halves the rows a lane carries, so that eight rows cost five shuffles and a lane ends up with
+// one row, whose scale it alone works out; the reciprocals are then handed round.
 struct RowsArgs {
   const void* src;
   long long ld, src_rows, rows;
@@ -92,49 +113,77 @@ struct RowsArgs {
   uint8_t* codes;
   float* scales;
 };
+template <typename T>
+constexpr int kHalfRows = sizeof(T) == 2 ? 8 : 4;   // rows of half a warp
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) rows_kernel(const RowsArgs a) {
   griddep_enter();
-  const int lane = threadIdx.x & 31, half = lane >> 4, l16 = lane & 15;
+  constexpr int R = kHalfRows<T>;
+  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
   const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long r0 = unit / a.kb * 8;
+  const long long r0 = unit / a.kb * (2 * R) + half * R;   // this half's first row
   const int kb = static_cast<int>(unit % a.kb);
-  if (r0 >= a.rows) return;
-  const int c = kb * 128 + l16 * 8;
+  if (r0 - half * R >= a.rows) return;
+  const int c = kb * 128 + l * 8;
   const bool in_k = c < a.K;   // K is a multiple of 16
-  float v[4][8];
+  long long mine = -1;         // lane j < R of a half: source row of row r0 + j
+  if (l < R && r0 + l < a.rows) {
+    mine = a.index != nullptr ? a.index[r0 + l] : r0 + l;
+    if (mine < 0 || mine >= a.src_rows) mine = -1;
+  }
+  Raw<T, 8> v[R];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const long long r = r0 + 2 * j + half;
-    long long q = r;
-    bool ok = in_k && r < a.rows;
-    if (ok && a.index != nullptr) {
-      q = a.index[r];
-      ok = q >= 0 && q < a.src_rows;
-    }
-    if (ok) {
-      load_n<VEC>(static_cast<const T*>(a.src) + q * a.ld + c, v[j]);
+  for (int j = 0; j < R; ++j) {
+    const long long q = __shfl_sync(~0u, mine, half * 16 + j);
+    if (q >= 0 && in_k) v[j].template load<VEC>(static_cast<const T*>(a.src) + q * a.ld + c);
+    else v[j].zero();
+  }
+  uint32_t m[4];   // bf16: rows i (low half) and i + 4 (high half); fp32: row i
+  const auto mx = [](uint32_t x, uint32_t y) { return sizeof(T) == 2 ? __vmaxu2(x, y) : max(x, y); };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t p[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t* w = v[i + 4 * h].w;
+        p[h] = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                        __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        p[h] = max(p[h] & 0xffffu, p[h] >> 16);
+      }
+      m[i] = p[0] | (p[1] << 16);
     } else {
+      m[i] = 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+      for (int e = 0; e < 8; ++e) m[i] = max(m[i], mag(v[i].get(e)));
     }
   }
+  {   // lane l keeps row (l >> 3 & 1) * 2 + (l >> 2 & 1)
+    const bool b3 = l & 8, b2 = l & 4;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const long long r = r0 + 2 * j + half;
-    uint32_t m = 0;
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t other = __shfl_xor_sync(~0u, b3 ? m[i] : m[i + 2], 8);
+      m[i] = mx(b3 ? m[i + 2] : m[i], other);
+    }
+    const uint32_t other = __shfl_xor_sync(~0u, b2 ? m[0] : m[1], 4);
+    m[0] = mx(b2 ? m[1] : m[0], other);
+    m[0] = mx(m[0], __shfl_xor_sync(~0u, m[0], 2));
+    m[0] = mx(m[0], __shfl_xor_sync(~0u, m[0], 1));
+  }
+  // bf16: the even lanes work out the low half's row, the odd ones the high half's
+  const int row = ((l >> 3) & 1) * 2 + ((l >> 2) & 1) + (sizeof(T) == 2 ? 4 * (l & 1) : 0);
+  const uint32_t bits = sizeof(T) == 2 ? (l & 1 ? m[0] & 0xffff0000u : m[0] << 16) : m[0];
+  const float s = scale_of(bits, a.f), inv = __frcp_rn(s);
+  if ((l & 2) == 0 && (sizeof(T) == 2 || (l & 1) == 0) && r0 + row < a.rows)
+    a.scales[static_cast<long long>(kb) * a.rows + r0 + row] = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, mag(v[j][i]));
-#pragma unroll
-    for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
-    const float s = scale_of(m, a.f), inv = __frcp_rn(s);
+  for (int j = 0; j < R; ++j) {
+    const float rj = __shfl_sync(~0u, inv, half * 16 + ((j >> 1) & 1) * 8 + (j & 1) * 4 + (j >> 2));
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = cvt2(v[j][2 * i] * inv, v[j][2 * i + 1] * inv, a.f.e5m2);
-    if (r < a.rows) {
-      if (in_k) *reinterpret_cast<uint2*>(a.codes + r * a.K + c) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-      if (l16 == 0) a.scales[static_cast<long long>(kb) * a.rows + r] = s;
-    }
+    for (int i = 0; i < 4; ++i) w[i] = cvt2(v[j].get(2 * i) * rj, v[j].get(2 * i + 1) * rj, a.f.e5m2);
+    if (r0 + j < a.rows && in_k)
+      *reinterpret_cast<uint2*>(a.codes + (r0 + j) * a.K + c) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
   }
 }
 
@@ -143,34 +192,36 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
 // stores are whole lines, and a thread's 16 rows of one column are 16 bytes of the transpose.
 // Those pass through shared memory, chunk w of column c at place w ^ ((c / 4) % 8), which keeps
 // both the writes (32 columns apart by 128 bytes) and the reads free of bank conflicts.
+// Magnitudes of a thread's four columns over its rows: two words of packed 16-bit patterns for
+// bf16, four words for fp32.
 template <typename T>
-struct Raw;
+struct ColMax;
 template <>
-struct Raw<float> {
-  float4 q;
-  LMOE_DEV void zero() { q = make_float4(0.f, 0.f, 0.f, 0.f); }
-  template <bool VEC>
-  LMOE_DEV void load(const float* p) {
-    if constexpr (VEC) q = *reinterpret_cast<const float4*>(p);
-    else q = make_float4(p[0], p[1], p[2], p[3]);
+struct ColMax<float> {
+  uint4 m;
+  LMOE_DEV void add(const Raw<float, 4>& v) {
+    m = make_uint4(max(m.x, mag(v.q[0].x)), max(m.y, mag(v.q[0].y)), max(m.z, mag(v.q[0].z)), max(m.w, mag(v.q[0].w)));
   }
-  LMOE_DEV float get(int i) const { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
+  LMOE_DEV void add(const ColMax& o) {
+    m = make_uint4(max(m.x, o.m.x), max(m.y, o.m.y), max(m.z, o.m.z), max(m.w, o.m.w));
+  }
+  LMOE_DEV uint32_t bits(int j) const { return j == 0 ? m.x : j == 1 ? m.y : j == 2 ? m.z : m.w; }
 };
 template <>
-struct Raw<__nv_bfloat16> {
-  uint2 q;
-  LMOE_DEV void zero() { q = make_uint2(0u, 0u); }
-  template <bool VEC>
-  LMOE_DEV void load(const __nv_bfloat16* p) {
-    if constexpr (VEC) {
-      q = *reinterpret_cast<const uint2*>(p);
-    } else {
-      const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
-      q = make_uint2(u[0] | (static_cast<uint32_t>(u[1]) << 16), u[2] | (static_cast<uint32_t>(u[3]) << 16));
-    }
+struct ColMax<__nv_bfloat16> {
+  uint2 m;
+  LMOE_DEV void add(const Raw<__nv_bfloat16, 4>& v) {
+    m = make_uint2(__vmaxu2(m.x, v.w[0] & 0x7fff7fffu), __vmaxu2(m.y, v.w[1] & 0x7fff7fffu));
   }
-  LMOE_DEV float get(int i) const { return i == 0 ? lo16(q.x) : i == 1 ? hi16(q.x) : i == 2 ? lo16(q.y) : hi16(q.y); }
+  LMOE_DEV void add(const ColMax& o) { m = make_uint2(__vmaxu2(m.x, o.m.x), __vmaxu2(m.y, o.m.y)); }
+  LMOE_DEV uint32_t bits(int j) const {
+    const uint32_t w = j < 2 ? m.x : m.y;
+    return j & 1 ? w & 0xffff0000u : w << 16;
+  }
 };
+// CTAs an SM holds: bf16 rows take half the registers
+template <typename T>
+constexpr int kTileCtas = sizeof(T) == 2 ? 4 : 2;
 
 // writes the transposed tile from shared memory: column c's 128 bytes to dst + c * ld
 LMOE_DEV void store_transposed(const uint8_t* tile, uint8_t* dst, long long ld, int ncols, int nbytes) {
@@ -192,7 +243,7 @@ struct WeightArgs {
   float *scales, *scales_t;
 };
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) weight_kernel(const WeightArgs a) {
+__global__ void __launch_bounds__(kThreads, kTileCtas<T>) weight_kernel(const WeightArgs a) {
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ uint32_t wmax[kThreads / 32];
   griddep_enter();
@@ -203,18 +254,16 @@ __global__ void __launch_bounds__(kThreads) weight_kernel(const WeightArgs a) {
   const int nb = static_cast<int>(gn % a.nb);
   const int n0 = nb * 128 + warp * 16, k0 = kb * 128 + lane * 4;
   const T* src = static_cast<const T*>(a.src) + (g * a.N + n0) * a.K + k0;
-  Raw<T> v[16];
+  Raw<T, 4> v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     if (n0 + i < a.N && k0 < a.K) v[i].template load<VEC>(src + static_cast<long long>(i) * a.K);
     else v[i].zero();
   }
-  uint32_t m = 0;
+  ColMax<T> cm{};
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, mag(v[i].get(j)));
-  m = __reduce_max_sync(~0u, m);
+  for (int i = 0; i < 16; ++i) cm.add(v[i]);
+  uint32_t m = __reduce_max_sync(~0u, max(max(cm.bits(0), cm.bits(1)), max(cm.bits(2), cm.bits(3))));
   if (lane == 0) wmax[warp] = m;
   __syncthreads();
 #pragma unroll
@@ -255,9 +304,9 @@ struct ColsArgs {
   float* scales;
 };
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) cols_kernel(const ColsArgs a) {
+__global__ void __launch_bounds__(kThreads, kTileCtas<T>) cols_kernel(const ColsArgs a) {
   __shared__ __align__(16) uint8_t tile[128 * 128];
-  __shared__ __align__(16) uint32_t cmax[kThreads / 32][128];
+  __shared__ ColMax<T> cmax[kThreads / 32][32];
   __shared__ int start[kMaxGroups + 1], lo[kMaxGroups], hi[kMaxGroups];
   griddep_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -307,33 +356,24 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(const ColsArgs a) {
       mine = a.index != nullptr ? a.index[r0 + lane] : r0 + lane;
       if (mine < 0 || mine >= a.src_rows) mine = -1;
     }
-    Raw<T> v[16];
+    Raw<T, 4> v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const long long q = __shfl_sync(~0u, mine, i);
       if (q >= 0 && k0 < a.K) v[i].template load<VEC>(static_cast<const T*>(a.src) + q * a.ld + k0);
       else v[i].zero();
     }
-    uint4 m = make_uint4(0u, 0u, 0u, 0u);
+    ColMax<T> m{};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      m.x = max(m.x, mag(v[i].get(0)));
-      m.y = max(m.y, mag(v[i].get(1)));
-      m.z = max(m.z, mag(v[i].get(2)));
-      m.w = max(m.w, mag(v[i].get(3)));
-    }
-    *reinterpret_cast<uint4*>(&cmax[warp][lane * 4]) = m;
+    for (int i = 0; i < 16; ++i) m.add(v[i]);
+    cmax[warp][lane] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const uint4 o = *reinterpret_cast<const uint4*>(&cmax[w][lane * 4]);
-      m = make_uint4(max(m.x, o.x), max(m.y, o.y), max(m.z, o.z), max(m.w, o.w));
-    }
-    const uint32_t mm[4] = {m.x, m.y, m.z, m.w};
+    for (int w = 0; w < kThreads / 32; ++w) m.add(cmax[w][lane]);
     float inv[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float s = scale_of(mm[j], a.f);
+      const float s = scale_of(m.bits(j), a.f);
       inv[j] = __frcp_rn(s);
       if (warp == 0 && k0 + j < a.K) a.scales[static_cast<long long>(blk) * a.K + k0 + j] = s;
     }
@@ -390,7 +430,8 @@ extern "C" lmoe_status lmoe_quantize_fp8_rows(const void* src, lmoe_dtype src_dt
   if (!on(src, es) || !on(codes, 16) || !on(scales, 4) || !on(row_index, 4)) return LMOE_ERR_ALIGN;
   const int kb = cdiv(K, 128);
   const RowsArgs a = {src, ld_src, src_rows, rows, row_index, K, kb, fmt_of(format, pow2_scales), codes, scales};
-  const long long ctas = ((rows + 7) / 8 * kb + kThreads / 32 - 1) / (kThreads / 32);
+  const int unit_rows = 2 * (es == 2 ? kHalfRows<__nv_bfloat16> : kHalfRows<float>);
+  const long long ctas = ((rows + unit_rows - 1) / unit_rows * kb + kThreads / 32 - 1) / (kThreads / 32);
   if (ctas > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
   const cudaError_t e = by_source(src_dtype, on(src, 16) && ld_src * es % 16 == 0, [&](auto t, auto v) {
     return launch_pdl(rows_kernel<decltype(t), decltype(v)::value>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, stream, a);
@@ -439,7 +480,7 @@ extern "C" lmoe_status lmoe_quantize_fp8_cols(const void* src, lmoe_dtype src_dt
   const ColsArgs a = {src,     ld_src,    src_rows, rows, padded_rows, row_index, offsets,
                       n_experts, K, cdiv(K, 128), fmt_of(format, pow2_scales), codes_t, scales_t};
   const long long units = padded_rows / 128 * a.kb;
-  const int grid = static_cast<int>(std::min<long long>(units, 2LL * sm_count()));
+  const int grid = static_cast<int>(std::min<long long>(units, (es == 2 ? kTileCtas<__nv_bfloat16> : kTileCtas<float>) * sm_count()));
   const cudaError_t e = by_source(src_dtype, on(src, 4 * es) && ld_src % 4 == 0, [&](auto t, auto v) {
     return launch_pdl(cols_kernel<decltype(t), decltype(v)::value>, dim3(grid), dim3(kThreads), 0, stream, a);
   });

@@ -10,9 +10,12 @@
 //   w = softmax of the row's selected logits over its slots (the routing weights).
 // (f is a count: no gradient flows through it.)
 //
-// Both read each logit once; the memory traffic bounds them.  A warp takes a row at a time, V
-// values per lane in registers, and loads its next row before it works on the present one.  exp
-// is one FMA and ex2: exp2(l log2e - m log2e), exact in m's part (it cancels in p).
+// Both read each logit once; the memory traffic bounds them.  G lanes take a row, V values each in
+// registers (G V >= E), so a warp has 32 / G rows under way, and loads its next ones before it
+// works on the present ones.  exp is one FMA and ex2: exp2(l log2e - m log2e), exact in m's part
+// (it cancels in p).  The column sums of p stay in registers over a warp's rows, are added over the
+// CTA's warps and, through the cluster's shared memory, over eight CTAs, always in the same order;
+// one cluster finishes by itself, several leave a row of sums each for a second kernel.
 #include <algorithm>
 
 #include "../../include/latent_moe.h"
@@ -22,8 +25,9 @@
 namespace lmoe {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = kWarps * 32;
+constexpr int kLossWarps = 16, kGradWarps = 8;
+constexpr int kLossThreads = kLossWarps * 32, kGradThreads = kGradWarps * 32;
+constexpr int kCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
 LMOE_DEV float to_f32(float v) { return v; }
@@ -36,30 +40,33 @@ LMOE_DEV float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-LMOE_DEV float warp_max_nan(float v) {
+// over a group of G lanes
+template <int G>
+LMOE_DEV float group_max_nan(float v) {
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, d));
+  for (int d = G / 2; d; d >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, d));
   return v;
 }
-LMOE_DEV float warp_sum(float v) {
+template <int G>
+LMOE_DEV float group_sum(float v) {
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+  for (int d = G / 2; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
   return v;
 }
 
-// Value i of a lane is element col<VEC>(lane, i) of the row: four neighbours at a time where the
-// rows allow 4-element loads, else every 32nd.
-template <bool VEC>
-LMOE_DEV int col(int lane, int i) {
-  return VEC ? (i >> 2) * 128 + lane * 4 + (i & 3) : lane + 32 * i;
+// Value i of lane l of a group is element col(l, i) of the row: four neighbours at a time where
+// the rows allow 4-element loads, else every G-th.
+template <int G, bool VEC>
+LMOE_DEV int col(int l, int i) {
+  return VEC ? (i >> 2) * (4 * G) + l * 4 + (i & 3) : l + G * i;
 }
 
-template <typename T, int V, bool VEC>
-LMOE_DEV void load_row(const T* row, int E, int lane, float (&v)[V]) {
+template <typename T, int G, int V, bool VEC>
+LMOE_DEV void load_row(const T* row, int E, int l, float (&v)[V]) {
   if constexpr (VEC) {
 #pragma unroll
     for (int j = 0; j < V / 4; ++j) {
-      const int e = col<true>(lane, 4 * j);
+      const int e = col<G, true>(l, 4 * j);
       if (e < E) {
         if constexpr (sizeof(T) == 4) {
           const float4 q = *reinterpret_cast<const float4*>(row + e);
@@ -76,21 +83,21 @@ LMOE_DEV void load_row(const T* row, int E, int lane, float (&v)[V]) {
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = col<false>(lane, i);
+      const int e = col<G, false>(l, i);
       v[i] = e < E ? to_f32(row[e]) : -INFINITY;
     }
   }
 }
-template <int V, bool VEC>
-LMOE_DEV void add_bias(const float* bias, int E, int lane, float (&v)[V]) {
+template <int G, int V, bool VEC>
+LMOE_DEV void add_bias(const float* bias, int E, int l, float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = col<VEC>(lane, i);
+    const int e = col<G, VEC>(l, i);
     if (e < E) v[i] += bias[e];
   }
 }
-// v becomes exp(l - max); returns their sum over the row.  m: the row's maximum.
-template <int V>
+// v becomes exp(l - max); returns their sum over the row.  m: the row's maximum, not -inf.
+template <int G, int V>
 LMOE_DEV float exp_row(float (&v)[V], float m) {
   const float c = m * kLog2e;
   float s = 0.f;
@@ -99,14 +106,14 @@ LMOE_DEV float exp_row(float (&v)[V], float m) {
     v[i] = exp2f(fmaf(v[i], kLog2e, -c));
     s += v[i];
   }
-  return warp_sum(s);
+  return group_sum<G>(s);
 }
-template <int V>
+template <int G, int V>
 LMOE_DEV float row_max(const float (&v)[V]) {
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = max_nan(m, v[i]);
-  return warp_max_nan(m);
+  return group_max_nan<G>(m);
 }
 
 struct LossArgs {
@@ -119,185 +126,199 @@ struct LossArgs {
   int32_t* counts;      // [E + 1], the last the live rows
   float* mean;          // [E]
   float* losses;        // [2]
-  float* part_p;        // [grid][E]
-  int32_t* part_c;      // [grid][E]
-  float* part_z;        // [grid]
-  int32_t* part_n;      // [grid]
-  int grid;
+  float* part_p;        // [clusters][E]
+  int32_t* part_c;      // [clusters][E]
+  float* part_z;        // [clusters]
+  int32_t* part_n;      // [clusters]
+  int cluster, clusters;
 };
 
-// Sum over a CTA of kThreads, in warp order.
-LMOE_DEV double block_sum(double v, double* sm) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+// Sum over a CTA of kLossThreads, in warp order, in every thread.
+LMOE_DEV float block_sum(float v, float* sm) {
+  v = group_sum<32>(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = 0;
-  for (int w = 0; w < kWarps; ++w) s += sm[w];
+  float s = 0.f;
+  for (int w = 0; w < kLossWarps; ++w) s += sm[w];
   return s;
 }
 
-// The results from the column sums of p and the counts: expert e = threadIdx.x, + kThreads, ..
-// through `at(e, p, c)`.
-template <typename F>
-LMOE_DEV void finish(const LossArgs& a, int n, double zsum, F at, double* sm) {
-  const double inv = n > 0 ? 1.0 / n : 0.0;
-  double dot = 0;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    double p;
-    int c;
-    at(e, p, c);
-    a.mean[e] = static_cast<float>(p * inv);
-    a.counts[e] = c;
-    dot += p * c;
-  }
-  dot = block_sum(dot, sm);
-  if (threadIdx.x == 0) {
-    a.counts[a.E] = n;
-    a.losses[0] = static_cast<float>(dot * inv * inv * a.E / a.k);
-    a.losses[1] = static_cast<float>(zsum * inv);
-  }
-}
-
-template <typename T, int V, bool VEC>
-__global__ void __launch_bounds__(kThreads) losses_kernel(const LossArgs a) {
-  extern __shared__ float sm_p[];   // [kWarps][E], then int hist[E]
-  int* hist = reinterpret_cast<int*>(sm_p + kWarps * a.E);
-  __shared__ float sm_z[kWarps];
-  __shared__ int sm_n[kWarps];
-  __shared__ double sm_d[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+template <typename T, int G, int V, bool VEC>
+__global__ void __launch_bounds__(kLossThreads) losses_kernel(const LossArgs a) {
+  constexpr int kRows = 32 / G, kSlots = G < 16 ? 16 / G : 1;
+  extern __shared__ float sm_p[];   // [kLossWarps][E], whose first row becomes the CTA's sums; hist [E]
+  int* hist = reinterpret_cast<int*>(sm_p + kLossWarps * a.E);
+  __shared__ float sm_z[kLossWarps];
+  __shared__ int sm_n[kLossWarps];
+  __shared__ float sm_d[kLossWarps];
+  __shared__ float cta_z, cta_dot;
+  __shared__ int cta_n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / G, l = lane % G;
+  for (int e = threadIdx.x; e < a.E; e += kLossThreads) hist[e] = 0;
   griddep_enter();
   __syncthreads();
   const T* logits = static_cast<const T*>(a.logits);
-  const int step = gridDim.x * kWarps;
+  const int step = gridDim.x * kLossWarps * kRows;
   float acc[V], next[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
   float z = 0.f;
-  int n = 0;
-  int t = blockIdx.x * kWarps + warp;
-  bool live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
-  int id = -1;
-  if (live) {
-    load_row<T, V, VEC>(logits + t * a.ld, a.E, lane, next);
-    if (lane < a.k) id = a.idx[static_cast<long long>(t) * a.k + lane];
-  }
-  while (t < a.T) {
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = next[i];
-    const bool here = live;
-    const int slot = id;
-    t += step;
+  int n = 0, ids[kSlots];
+  int t = (blockIdx.x * kLossWarps + warp) * kRows + g;
+  bool live;
+  const auto fetch = [&] {   // row t, if there is one and the mask keeps it
     live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
     if (live) {
-      load_row<T, V, VEC>(logits + t * a.ld, a.E, lane, next);
-      if (lane < a.k) id = a.idx[static_cast<long long>(t) * a.k + lane];
+      load_row<T, G, V, VEC>(logits + t * a.ld, a.E, l, next);
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        ids[s] = l + G * s < a.k ? a.idx[static_cast<long long>(t) * a.k + l + G * s] : -1;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) next[i] = -INFINITY;
     }
-    if (!here) continue;
-    if (a.bias != nullptr) add_bias<V, VEC>(a.bias, a.E, lane, v);
-    const float m = row_max(v);
-    if (m == -INFINITY) continue;
-    const float s = exp_row(v, m);
-    const float r = 1.f / s;
+  };
+  fetch();
+  while (t - g < a.T) {   // (the same for the warp)
+    float v[V];
+    int slot[kSlots];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = next[i];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) slot[s] = ids[s];
+    const bool here = live;
+    t += step;
+    fetch();
+    if (a.bias != nullptr && here) add_bias<G, V, VEC>(a.bias, a.E, l, v);
+    float m = row_max<G>(v);
+    const bool on = here && m != -INFINITY;
+    m = on ? m : 0.f;   // (a row that is not live: every exp is 0)
+    const float s = exp_row<G>(v, m);
+    const float r = on ? 1.f / s : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], r, acc[i]);
-    const float lse = m + logf(s);
-    z = fmaf(lse, lse, z);
-    ++n;
-    if (lane < a.k && slot >= 0 && slot < a.E) atomicAdd(&hist[slot], 1);
-  }
+    if (on) {
+      const float lse = m + logf(s);
+      z = fmaf(lse, lse, z);
+      ++n;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = col<VEC>(lane, i);
-    if (e < a.E) sm_p[warp * a.E + e] = acc[i];
+      for (int q = 0; q < kSlots; ++q)
+        if (slot[q] >= 0 && slot[q] < a.E) atomicAdd(&hist[slot[q]], 1);
+    }
+  }
+  // the CTA's sums: groups of a warp, then warps
+#pragma unroll
+  for (int d = G; d < 32; d <<= 1) {
+    z += __shfl_xor_sync(~0u, z, d);
+    n += __shfl_xor_sync(~0u, n, d);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += __shfl_xor_sync(~0u, acc[i], d);
+  }
+  if (g == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = col<G, VEC>(l, i);
+      if (e < a.E) sm_p[warp * a.E + e] = acc[i];
+    }
   }
   if (lane == 0) {
     sm_z[warp] = z;
     sm_n[warp] = n;
   }
   __syncthreads();
-  int nb = 0;
-  float zb = 0.f;
-  for (int w = 0; w < kWarps; ++w) {
-    nb += sm_n[w];
-    zb += sm_z[w];
-  }
-  const auto column = [&](int e) {
+  for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
     float p = 0.f;
-    for (int w = 0; w < kWarps; ++w) p += sm_p[w * a.E + e];
-    return p;
-  };
-  if (a.grid == 1) {
-    finish(a, nb, zb, [&](int e, double& p, int& c) { p = column(e), c = hist[e]; }, sm_d);
-    return;
-  }
-  const long long o = static_cast<long long>(blockIdx.x) * a.E;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    a.part_p[o + e] = column(e);
-    a.part_c[o + e] = hist[e];
+    for (int w = 0; w < kLossWarps; ++w) p += sm_p[w * a.E + e];
+    sm_p[e] = p;   // (column e is this thread's alone)
   }
   if (threadIdx.x == 0) {
-    a.part_z[blockIdx.x] = zb;
-    a.part_n[blockIdx.x] = nb;
+    float zz = 0.f;
+    int nn = 0;
+    for (int w = 0; w < kLossWarps; ++w) {
+      zz += sm_z[w];
+      nn += sm_n[w];
+    }
+    cta_z = zz;
+    cta_n = nn;
   }
-}
-
-// Sums the CTAs' partials in order.  Each of kThreads / W groups of W threads takes every
-// (kThreads / W)-th CTA, W the experts rounded up to a power of two.
-__global__ void __launch_bounds__(kThreads) losses_finish_kernel(const LossArgs a) {
-  __shared__ double sm_p[kThreads];
-  __shared__ int sm_c[kThreads];
-  __shared__ double sm_d[kWarps];
-  griddep_enter();
-  int n = 0;
-  double z = 0;
-  for (int g = threadIdx.x; g < a.grid; g += kThreads) {
-    n += a.part_n[g];
-    z += a.part_z[g];
+  // the cluster's: each CTA adds its share of the columns over all of them
+  cluster_sync();
+  const int rank = blockIdx.x % a.cluster, cl = blockIdx.x / a.cluster;
+  const int share = (a.E + a.cluster - 1) / a.cluster, e0 = rank * share, e1 = min(e0 + share, a.E);
+  float zz = 0.f, dot = 0.f;
+  int nn = 0;
+  for (int q = 0; q < a.cluster; ++q) {
+    zz += __uint_as_float(cluster_load(cluster_map(smem_u32(&cta_z), q)));
+    nn += static_cast<int>(cluster_load(cluster_map(smem_u32(&cta_n), q)));
   }
-  const int nb = static_cast<int>(block_sum(n, sm_d));
-  z = block_sum(z, sm_d);
-  int W = 32;
-  while (W < a.E && W < kThreads) W *= 2;
-  const int groups = kThreads / W, grp = threadIdx.x / W, e0 = threadIdx.x % W;
-  if (groups == 1) {
-    finish(a, nb, z,
-           [&](int e, double& p, int& c) {
-             p = 0, c = 0;
-#pragma unroll 8
-             for (int g = 0; g < a.grid; ++g) {
-               p += a.part_p[static_cast<long long>(g) * a.E + e];
-               c += a.part_c[static_cast<long long>(g) * a.E + e];
-             }
-           },
-           sm_d);
-    return;
-  }
-  double p = 0;
-  int c = 0;
-  if (e0 < a.E) {
-#pragma unroll 8
-    for (int g = grp; g < a.grid; g += groups) {
-      p += a.part_p[static_cast<long long>(g) * a.E + e0];
-      c += a.part_c[static_cast<long long>(g) * a.E + e0];
+  const float inv = nn > 0 ? 1.f / nn : 0.f;
+  for (int e = e0 + threadIdx.x; e < e1; e += kLossThreads) {
+    float p = 0.f;
+    int c = 0;
+    for (int q = 0; q < a.cluster; ++q) {
+      p += __uint_as_float(cluster_load(cluster_map(smem_u32(sm_p + e), q)));
+      c += static_cast<int>(cluster_load(cluster_map(smem_u32(hist + e), q)));
+    }
+    if (a.clusters == 1) {
+      a.mean[e] = p * inv;
+      a.counts[e] = c;
+      dot = fmaf(p * inv, c * inv, dot);
+    } else {
+      a.part_p[static_cast<long long>(cl) * a.E + e] = p;
+      a.part_c[static_cast<long long>(cl) * a.E + e] = c;
     }
   }
-  sm_p[threadIdx.x] = p;
-  sm_c[threadIdx.x] = c;
-  __syncthreads();
-  finish(a, nb, z,
-         [&](int e, double& pp, int& cc) {
-           pp = 0, cc = 0;
-           for (int g = 0; g < groups; ++g) {
-             pp += sm_p[g * W + e];
-             cc += sm_c[g * W + e];
-           }
-         },
-         sm_d);
+  if (a.clusters == 1) {
+    dot = block_sum(dot, sm_d);
+    if (threadIdx.x == 0) cta_dot = dot;
+  }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    if (a.clusters == 1) {
+      float d = 0.f;
+      for (int q = 0; q < a.cluster; ++q) d += __uint_as_float(cluster_load(cluster_map(smem_u32(&cta_dot), q)));
+      a.counts[a.E] = nn;
+      a.losses[0] = d * a.E / a.k;
+      a.losses[1] = zz * inv;
+    } else {
+      a.part_z[cl] = zz;
+      a.part_n[cl] = nn;
+    }
+  }
+  cluster_sync();   // no CTA leaves while another reads its shared memory
+}
+
+// Adds the clusters' sums, in order.
+__global__ void __launch_bounds__(kLossThreads) losses_finish_kernel(const LossArgs a) {
+  __shared__ float sm_d[kLossWarps];
+  griddep_enter();
+  float z = 0.f, dot = 0.f;
+  int n = 0;
+#pragma unroll 4
+  for (int q = 0; q < a.clusters; ++q) {
+    n += a.part_n[q];
+    z += a.part_z[q];
+  }
+  const float inv = n > 0 ? 1.f / n : 0.f;
+  for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
+    float p = 0.f;
+    int c = 0;
+#pragma unroll 8
+    for (int q = 0; q < a.clusters; ++q) {
+      p += a.part_p[static_cast<long long>(q) * a.E + e];
+      c += a.part_c[static_cast<long long>(q) * a.E + e];
+    }
+    a.mean[e] = p * inv;
+    a.counts[e] = c;
+    dot = fmaf(p * inv, c * inv, dot);
+  }
+  dot = block_sum(dot, sm_d);
+  if (threadIdx.x == 0) {
+    a.counts[a.E] = n;
+    a.losses[0] = dot * a.E / a.k;
+    a.losses[1] = z * inv;
+  }
 }
 
 struct GradArgs {
@@ -314,115 +335,174 @@ struct GradArgs {
   long long ldo;
 };
 
-template <typename T, int V, bool VEC>
-__global__ void __launch_bounds__(kThreads) grad_kernel(const GradArgs a) {
-  extern __shared__ float sm_row[];   // [kWarps][E]: one row while its slots' terms are added
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* row = sm_row + warp * a.E;
+template <typename T, int G, int V, bool VEC>
+__global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradArgs a) {
+  constexpr int kRows = 32 / G, kSlots = G < 16 ? 16 / G : 1;
+  extern __shared__ float sm_row[];   // [rows of the CTA][E]: a row while its slots' terms are added
+  __shared__ int sm_id[G < 16 ? kGradWarps * kRows : 1][16];
+  __shared__ float sm_g[G < 16 ? kGradWarps * kRows : 1][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / G, l = lane % G;
+  const int local = warp * kRows + g;
+  float* row = sm_row + local * a.E;
   griddep_enter();
   const T* logits = static_cast<const T*>(a.logits);
   T* out = static_cast<T*>(a.out);
-  const int step = gridDim.x * kWarps;
-  float f[V], next[V], cb = 0.f, cz = 0.f;
+  const int step = gridDim.x * kGradWarps * kRows;
+  float next[V], gnext[kSlots];
+  int inext[kSlots];
+  int t = (blockIdx.x * kGradWarps + warp) * kRows + g;
+  bool live;
+  const auto fetch = [&] {   // row t, if there is one and the mask keeps it
+    live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      inext[s] = -1;
+      gnext[s] = 0.f;
+    }
+    if (live) {
+      load_row<T, G, V, VEC>(logits + t * a.ld, a.E, l, next);
+      if (a.gw != nullptr) {
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+          if (l + G * s < a.k) {
+            inext[s] = a.idx[static_cast<long long>(t) * a.k + l + G * s];
+            gnext[s] = a.gw[static_cast<long long>(t) * a.k + l + G * s];
+          }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) next[i] = -INFINITY;
+    }
+  };
+  fetch();
+  float f[V], cb = 0.f, cz = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = 0.f;
   if (a.gl != nullptr) {
-    const int n = max(a.counts[a.E], 1);
-    const float inv = 1.f / n;
+    const float inv = 1.f / max(a.counts[a.E], 1);
     cb = a.gl[0] * a.E * inv;
     cz = a.gl[1] * 2.f * inv;
+    const float fk = inv / a.k;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = col<VEC>(lane, i);
-      f[i] = e < a.E ? a.counts[e] * inv / a.k : 0.f;
+      const int e = col<G, VEC>(l, i);
+      if (e < a.E) f[i] = a.counts[e] * fk;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = 0.f;
   }
-  int t = blockIdx.x * kWarps + warp;
-  bool live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
-  if (live) load_row<T, V, VEC>(logits + t * a.ld, a.E, lane, next);
-  while (t < a.T) {
-    float v[V];
+  while (t - g < a.T) {   // (the same for the warp)
+    float v[V], gw[kSlots], sel[kSlots];
+    int id[kSlots];
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = next[i];
     const int here = t;
     bool on = live;
-    // the row's slots: their logits are read before the row is written (it may be written in place)
-    int id = -1;
-    float sel = -INFINITY, gw = 0.f;
-    if (on && a.gw != nullptr && lane < a.k) {
-      id = a.idx[static_cast<long long>(here) * a.k + lane];
-      if (id >= 0 && id < a.E) {
-        sel = to_f32(logits[here * a.ld + id]) + (a.bias != nullptr ? a.bias[id] : 0.f);
-        gw = a.gw[static_cast<long long>(here) * a.k + lane];
-      } else {
-        id = -1;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      id[s] = inext[s];
+      gw[s] = gnext[s];
+    }
+    // the slots' logits are read before the row is written (it may be written in place)
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      if (id[s] < 0 || id[s] >= a.E) {
+        id[s] = -1;
+        gw[s] = 0.f;
       }
+      sel[s] = id[s] < 0 ? -INFINITY
+                         : to_f32(logits[here * a.ld + id[s]]) + (a.bias != nullptr ? a.bias[id[s]] : 0.f);
     }
     t += step;
-    live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
-    if (live) load_row<T, V, VEC>(logits + t * a.ld, a.E, lane, next);
-    float m = -INFINITY;
-    if (on) {
-      if (a.bias != nullptr) add_bias<V, VEC>(a.bias, a.E, lane, v);
-      m = row_max(v);
-      on = m != -INFINITY;
+    fetch();
+    if (a.bias != nullptr && on) add_bias<G, V, VEC>(a.bias, a.E, l, v);
+    float m = row_max<G>(v);
+    on = on && m != -INFINITY;
+    m = on ? m : 0.f;
+    const float s = exp_row<G>(v, m), r = on ? 1.f / s : 0.f;
+    const float lz = on ? cz * (m + logf(s)) : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] *= r;
+      dot = fmaf(v[i], f[i], dot);
     }
-    if (on) {
-      const float s = exp_row(v, m), r = 1.f / s;
-      const float lz = cz * (m + logf(s));
-      float dot = 0.f;
+    dot = group_sum<G>(dot);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] *= fmaf(cb, f[i] - dot, lz);
+    if (a.gw != nullptr) {
+      float sm = sel[0];
+#pragma unroll
+      for (int q = 1; q < kSlots; ++q) sm = max_nan(sm, sel[q]);
+      sm = group_max_nan<G>(sm);
+      const bool none = sm == -INFINITY;   // no slot with a logit above -inf: no weights, no gradient
+      float w[kSlots], d[kSlots], ws = 0.f, wg = 0.f;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        w[q] = none ? 0.f : exp2f((sel[q] - sm) * kLog2e);
+        ws += w[q];
+      }
+      ws = group_sum<G>(ws);
+      const float wr = none ? 0.f : 1.f / ws;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        w[q] *= wr;
+        wg = fmaf(w[q], gw[q], wg);
+      }
+      wg = group_sum<G>(wg);
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) d[q] = on && id[q] >= 0 ? w[q] * (gw[q] - wg) : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[i] *= r;
-        dot = fmaf(v[i], f[i], dot);
+        const int e = col<G, VEC>(l, i);
+        if (e < a.E) row[e] = v[i];
       }
-      dot = warp_sum(dot);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= fmaf(cb, f[i] - dot, lz);
-      if (a.gw != nullptr) {
-        const float sm = warp_max_nan(sel);
-        // (no slot with a finite logit: the weights are undefined and give no gradient)
-        float w = sm == -INFINITY ? 0.f : exp2f((sel - sm) * kLog2e);
-        const float ws = warp_sum(w);
-        w = ws == 0.f ? 0.f : w / ws;
-        const float g = warp_sum(w == 0.f ? 0.f : w * gw);
-        float d = w == 0.f ? 0.f : w * (gw - g);
-        // an expert named by several slots of the row: its first slot adds them all, in order
-        const unsigned same = __match_any_sync(~0u, id);
-        const bool first = id >= 0 && lane == __ffs(same) - 1;
-        if (__any_sync(~0u, id >= 0 && __popc(same) > 1)) {
+      // an expert named by several slots of the row: its first slot adds them all, in order
+      if constexpr (G >= 16) {
+        const unsigned same = __match_any_sync(~0u, (g << 16) | (id[0] & 0xffff));
+        const bool first = id[0] >= 0 && lane == __ffs(same) - 1;
+        if (__any_sync(~0u, id[0] >= 0 && __popc(same) > 1)) {
           float tot = 0.f;
           for (int j = 0; j < a.k; ++j) {
-            const float dj = __shfl_sync(~0u, d, j);
-            if ((same >> j) & 1u) tot += dj;
+            const float dj = __shfl_sync(~0u, d[0], g * G + j);
+            if ((same >> (g * G + j)) & 1u) tot += dj;
           }
-          d = tot;
+          d[0] = tot;
         }
+        __syncwarp();
+        if (first) row[id[0]] += d[0];
+      } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = col<VEC>(lane, i);
-          if (e < a.E) row[e] = v[i];
-        }
-        __syncwarp();
-        if (first) row[id] += d;
+        for (int q = 0; q < kSlots; ++q)
+          if (l + G * q < 16) {
+            sm_id[local][l + G * q] = id[q];
+            sm_g[local][l + G * q] = d[q];
+          }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = col<VEC>(lane, i);
-          if (e < a.E) v[i] = row[e];
+        for (int q = 0; q < kSlots; ++q) {
+          bool first = id[q] >= 0;
+          float tot = 0.f;
+          for (int j = 0; j < a.k; ++j) {
+            if (sm_id[local][j] != id[q]) continue;
+            if (j < l + G * q) first = false;
+            tot += sm_g[local][j];
+          }
+          if (first) row[id[q]] += tot;
         }
-        __syncwarp();
       }
-    } else {
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = 0.f;
+      for (int i = 0; i < V; ++i) {
+        const int e = col<G, VEC>(l, i);
+        if (e < a.E) v[i] = row[e];
+      }
+      __syncwarp();
     }
+    if (here >= a.T) continue;
     T* o = out + here * a.ldo;
     if constexpr (VEC) {
 #pragma unroll
       for (int j = 0; j < V / 4; ++j) {
-        const int e = col<true>(lane, 4 * j);
+        const int e = col<G, true>(l, 4 * j);
         if (e < a.E) {
           if constexpr (sizeof(T) == 4)
             *reinterpret_cast<float4*>(o + e) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -434,32 +514,48 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int e = col<false>(lane, i);
+        const int e = col<G, false>(l, i);
         if (e < a.E) store_as(o + e, v[i]);
       }
     }
   }
 }
 
-// Calls f with (T, V, VEC) of the smallest V that holds E.
+// Calls f with (T, G, V, VEC) for E experts.
+template <int V>
+using Int = std::integral_constant<int, V>;
 template <typename F>
 cudaError_t by_shape(bool f32, int E, bool vec, F f) {
-  const auto with_v = [&](auto v) {
-    if (f32) return vec ? f(float{}, v, std::true_type{}) : f(float{}, v, std::false_type{});
-    return vec ? f(__nv_bfloat16{}, v, std::true_type{}) : f(__nv_bfloat16{}, v, std::false_type{});
+  const auto with = [&](auto g, auto v) {
+    if (f32) return vec ? f(float{}, g, v, std::true_type{}) : f(float{}, g, v, std::false_type{});
+    return vec ? f(__nv_bfloat16{}, g, v, std::true_type{}) : f(__nv_bfloat16{}, g, v, std::false_type{});
   };
-  if (E <= 128) return with_v(std::integral_constant<int, 4>{});
-  if (E <= 256) return with_v(std::integral_constant<int, 8>{});
-  if (E <= 512) return with_v(std::integral_constant<int, 16>{});
-  return with_v(std::integral_constant<int, 32>{});
+  if (E <= 16) return with(Int<4>{}, Int<4>{});
+  if (E <= 64) return with(Int<8>{}, Int<8>{});
+  if (E <= 128) return with(Int<8>{}, Int<16>{});
+  if (E <= 256) return with(Int<16>{}, Int<16>{});
+  if (E <= 512) return with(Int<32>{}, Int<16>{});
+  return with(Int<32>{}, Int<32>{});
 }
+// rows of a warp at a time
+int warp_rows(int E) { return E <= 16 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1; }
 
 // rows of 4-element loads: base, row length and the count of elements allow them
 bool rows_vec(const void* p, long long ld, int E, int es) {
   return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * es) == 0;
 }
-constexpr int kMaxGrid = 152;   // CTAs of the losses kernel: the partials a workspace holds
-int losses_grid(int T) { return std::max(1, std::min(kMaxGrid, (T + 4 * kWarps - 1) / (4 * kWarps))); }
+// CTAs of the losses kernel, in clusters of one or eight: one CTA while each warp takes up to four
+// turns of rows, then clusters of two turns, as many as the SMs hold.
+constexpr int kMaxClusters = 19;   // 152 SMs
+struct LossGrid {
+  int cluster, clusters;
+};
+LossGrid losses_grid(int T, int E) {
+  const int turn = kLossWarps * warp_rows(E);   // rows of a CTA at a time
+  if (T <= 4 * turn) return {1, 1};
+  const int want = (T + 2 * turn * kCluster - 1) / (2 * turn * kCluster);
+  return {kCluster, std::min(want, kMaxClusters)};
+}
 
 lmoe_status check_rows(const void* logits, lmoe_dtype dt, long long ld, const float* bias, const int32_t* idx, int T,
                        int E, int k) {
@@ -480,7 +576,7 @@ using namespace lmoe;
 extern "C" lmoe_status lmoe_router_losses_workspace_size(int T, int E, size_t* bytes) {
   if (bytes == nullptr || T < 0 || T > (1 << 20) || E < 1) return LMOE_ERR_ARG;
   if (E > 1024) return LMOE_ERR_UNSUPPORTED;
-  *bytes = static_cast<size_t>(losses_grid(T)) * (2 * E + 2) * 4;
+  *bytes = static_cast<size_t>(losses_grid(T, E).clusters) * (2 * E + 2) * 4;
   return LMOE_OK;
 }
 
@@ -496,21 +592,26 @@ extern "C" lmoe_status lmoe_router_losses(const void* logits, lmoe_dtype logits_
       reinterpret_cast<uintptr_t>(losses) % 4 || reinterpret_cast<uintptr_t>(workspace) % 4)
     return LMOE_ERR_ALIGN;
   LossArgs a = {logits, ld_logits, router_bias, row_mask, topk_idx, T, E, k, counts, mean_probs, losses};
-  a.grid = losses_grid(T);
-  const size_t need = static_cast<size_t>(a.grid) * (2 * E + 2) * 4;
+  const LossGrid lg = losses_grid(T, E);
+  a.cluster = lg.cluster;
+  a.clusters = lg.clusters;
+  const size_t need = static_cast<size_t>(lg.clusters) * (2 * E + 2) * 4;
   if (workspace == nullptr || workspace_bytes < need) return LMOE_ERR_WORKSPACE;
   a.part_p = static_cast<float*>(workspace);
-  a.part_c = reinterpret_cast<int32_t*>(a.part_p + static_cast<size_t>(a.grid) * E);
-  a.part_z = reinterpret_cast<float*>(a.part_c + static_cast<size_t>(a.grid) * E);
-  a.part_n = reinterpret_cast<int32_t*>(a.part_z + a.grid);
-  const size_t smem = static_cast<size_t>(kWarps + 1) * E * 4;
+  a.part_c = reinterpret_cast<int32_t*>(a.part_p + static_cast<size_t>(lg.clusters) * E);
+  a.part_z = reinterpret_cast<float*>(a.part_c + static_cast<size_t>(lg.clusters) * E);
+  a.part_n = reinterpret_cast<int32_t*>(a.part_z + lg.clusters);
+  const size_t smem = static_cast<size_t>(kLossWarps + 1) * E * 4;
   const bool f32 = logits_dtype == LMOE_F32;
-  cudaError_t e = by_shape(f32, E, rows_vec(logits, ld_logits, E, f32 ? 4 : 2), [&](auto t, auto v, auto vec) {
-    auto kern = losses_kernel<decltype(t), decltype(v)::value, decltype(vec)::value>;
+  cudaError_t e = by_shape(f32, E, rows_vec(logits, ld_logits, E, f32 ? 4 : 2), [&](auto t, auto g, auto v, auto vec) {
+    auto kern = losses_kernel<decltype(t), decltype(g)::value, decltype(v)::value, decltype(vec)::value>;
     const cudaError_t r = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
-    return r != cudaSuccess ? r : launch_pdl(kern, dim3(a.grid), dim3(kThreads), smem, stream, a);
+    return r != cudaSuccess ? r
+                            : launch_pdl_cluster(kern, dim3(lg.cluster * lg.clusters), dim3(kLossThreads), smem,
+                                                 stream, lg.cluster, a);
   });
-  if (e == cudaSuccess && a.grid > 1) e = launch_pdl(losses_finish_kernel, dim3(1), dim3(kThreads), 0, stream, a);
+  if (e == cudaSuccess && lg.clusters > 1)
+    e = launch_pdl(losses_finish_kernel, dim3(1), dim3(kLossThreads), 0, stream, a);
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
@@ -533,13 +634,14 @@ extern "C" lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dt
     return LMOE_ERR_ALIGN;
   const GradArgs a = {logits, ld_logits, router_bias, row_mask, topk_idx, topk_w_grad, counts, loss_grads,
                       T,      E,         k,           dlogits,  ld_dlogits};
-  const size_t smem = static_cast<size_t>(kWarps) * E * 4;
+  const int turn = kGradWarps * warp_rows(E);   // rows of a CTA at a time
+  const size_t smem = static_cast<size_t>(turn) * E * 4;
   const bool vec = rows_vec(logits, ld_logits, E, es) && rows_vec(dlogits, ld_dlogits, E, es);
-  const int grid = std::max(1, std::min(4 * sm_count(), (T + kWarps - 1) / kWarps));
-  const cudaError_t e = by_shape(f32, E, vec, [&](auto t, auto v, auto vc) {
-    auto kern = grad_kernel<decltype(t), decltype(v)::value, decltype(vc)::value>;
+  const int grid = std::max(1, std::min(4 * sm_count(), (T + turn - 1) / turn));
+  const cudaError_t e = by_shape(f32, E, vec, [&](auto t, auto g, auto v, auto vc) {
+    auto kern = grad_kernel<decltype(t), decltype(g)::value, decltype(v)::value, decltype(vc)::value>;
     const cudaError_t r = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
-    return r != cudaSuccess ? r : launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, a);
+    return r != cudaSuccess ? r : launch_pdl(kern, dim3(grid), dim3(kGradThreads), smem, stream, a);
   });
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
