@@ -28,13 +28,22 @@ constexpr int kMaxGroups = 1024;
 
 struct Fmt {
   float largest;
-  int e5m2, pow2;
+  int pow2;
 };
-// two codes, a's in the low byte
-LMOE_DEV uint32_t cvt2(float a, float b, int e5m2) {
-  uint16_t r;
-  if (e5m2) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-  else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+// four codes, a's in the low byte
+template <bool E5M2>
+LMOE_DEV uint32_t cvt4(float a, float b, float c, float d) {
+  uint32_t r;
+  if constexpr (E5M2)
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
 LMOE_DEV float scale_of(uint32_t amax_bits, const Fmt& f) {
@@ -46,7 +55,39 @@ LMOE_DEV float scale_of(uint32_t amax_bits, const Fmt& f) {
   }
   return s;
 }
-LMOE_DEV uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+LMOE_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// the larger magnitudes of two pairs of bf16 (of any sign: masked when the last is found), NaN if
+// either is
+LMOE_DEV uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 16 or 8 bytes, with ALL or zeros where `on` is not set (a predicated load: no branch around it)
+template <bool ALL>
+LMOE_DEV uint4 load16(const void* p, bool on) {
+  if constexpr (ALL) return *static_cast<const uint4*>(p);
+  uint4 q;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+               "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+               "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+               : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w) : "l"(p), "r"(static_cast<int>(on)));
+  return q;
+}
+template <bool ALL>
+LMOE_DEV uint2 load8(const void* p, bool on) {
+  if constexpr (ALL) return *static_cast<const uint2*>(p);
+  uint2 q;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+               "@p ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
+               : "=&r"(q.x), "=&r"(q.y) : "l"(p), "r"(static_cast<int>(on)));
+  return q;
+}
+constexpr uint32_t kMag = 0x7fffffffu;   // an fp32's magnitude
 LMOE_DEV float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 LMOE_DEV float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -56,43 +97,37 @@ template <typename T, int N>
 struct Raw;
 template <int N>
 struct Raw<float, N> {
-  float4 q[N / 4];
-  LMOE_DEV void zero() {
-#pragma unroll
-    for (int j = 0; j < N / 4; ++j) q[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  template <bool VEC>
-  LMOE_DEV void load(const float* p) {
+  uint32_t w[N];
+  template <bool VEC, bool ALL = false>
+  LMOE_DEV void load(const float* p, bool on = true) {   // zeros where `on` is not set
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
-      if constexpr (VEC) q[j] = reinterpret_cast<const float4*>(p)[j];
-      else q[j] = make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+      if constexpr (VEC) {
+        const uint4 q = load16<ALL>(p + 4 * j, on);
+        w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * j + i] = on ? __float_as_uint(p[4 * j + i]) : 0u;
+      }
     }
   }
-  LMOE_DEV float get(int i) const {
-    const float4& v = q[i >> 2];
-    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
-  }
+  LMOE_DEV float get(int i) const { return __uint_as_float(w[i]); }
 };
 template <int N>
 struct Raw<__nv_bfloat16, N> {
   uint32_t w[N / 2];
-  LMOE_DEV void zero() {
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) w[j] = 0u;
-  }
-  template <bool VEC>
-  LMOE_DEV void load(const __nv_bfloat16* p) {
+  template <bool VEC, bool ALL = false>
+  LMOE_DEV void load(const __nv_bfloat16* p, bool on = true) {
     if constexpr (VEC && N == 8) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      const uint4 q = load16<ALL>(p, on);
       w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
     } else if constexpr (VEC) {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      const uint2 q = load8<ALL>(p, on);
       w[0] = q.x, w[1] = q.y;
     } else {
       const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) w[j] = u[2 * j] | (static_cast<uint32_t>(u[2 * j + 1]) << 16);
+      for (int j = 0; j < N / 2; ++j) w[j] = on ? u[2 * j] | (static_cast<uint32_t>(u[2 * j + 1]) << 16) : 0u;
     }
   }
   LMOE_DEV float get(int i) const { return i & 1 ? hi16(w[i >> 1]) : lo16(w[i >> 1]); }
@@ -109,37 +144,43 @@ struct RowsArgs {
   long long ld, src_rows, rows;
   const int32_t* index;
   int K, kb;
+  unsigned chunks;   // ceil(kb / kb_warps)
+  int kb_warps;
   Fmt f;
   uint8_t* codes;
   float* scales;
 };
 template <typename T>
 constexpr int kHalfRows = sizeof(T) == 2 ? 8 : 4;   // rows of half a warp
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool E5M2>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) rows_kernel(const RowsArgs a) {
   griddep_enter();
   constexpr int R = kHalfRows<T>;
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long r0 = unit / a.kb * (2 * R) + half * R;   // this half's first row
-  const int kb = static_cast<int>(unit % a.kb);
-  if (r0 - half * R >= a.rows) return;
+  // the CTA's warps: kb_warps blocks of columns (a power of two) x the rest in rows
+  const int warp = threadIdx.x >> 5;
+  const int kb = (blockIdx.x % a.chunks) * a.kb_warps + (warp & (a.kb_warps - 1));
+  const long long w0 = static_cast<long long>(blockIdx.x / a.chunks) * (kThreads / 32 / a.kb_warps) + warp / a.kb_warps;
+  const long long r0 = w0 * (2 * R) + half * R;   // this half's first row
+  if (r0 - half * R >= a.rows || kb >= a.kb) return;
   const int c = kb * 128 + l * 8;
   const bool in_k = c < a.K;   // K is a multiple of 16
-  long long mine = -1;         // lane j < R of a half: source row of row r0 + j
+  int mine = -1;               // lane j < R of a half: source row of row r0 + j (at most 2^24)
   if (l < R && r0 + l < a.rows) {
-    mine = a.index != nullptr ? a.index[r0 + l] : r0 + l;
+    mine = a.index != nullptr ? a.index[r0 + l] : static_cast<int>(r0) + l;
     if (mine < 0 || mine >= a.src_rows) mine = -1;
   }
+  const T* src = static_cast<const T*>(a.src) + c;
+  const bool whole = __all_sync(~0u, in_k && (l >= R || mine >= 0));   // nothing to leave out
   Raw<T, 8> v[R];
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    const long long q = __shfl_sync(~0u, mine, half * 16 + j);
-    if (q >= 0 && in_k) v[j].template load<VEC>(static_cast<const T*>(a.src) + q * a.ld + c);
-    else v[j].zero();
+    const int q = __shfl_sync(~0u, mine, half * 16 + j);
+    if (whole) v[j].template load<VEC, true>(src + q * a.ld);
+    else v[j].template load<VEC>(src + q * a.ld, q >= 0 && in_k);
   }
   uint32_t m[4];   // bf16: rows i (low half) and i + 4 (high half); fp32: row i
-  const auto mx = [](uint32_t x, uint32_t y) { return sizeof(T) == 2 ? __vmaxu2(x, y) : max(x, y); };
+  const auto mx = [](uint32_t x, uint32_t y) { return sizeof(T) == 2 ? max_u16x2(x, y) : max(x, y); };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(T) == 2) {
@@ -147,15 +188,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) rows_kernel(
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t* w = v[i + 4 * h].w;
-        p[h] = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                        __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-        p[h] = max(p[h] & 0xffffu, p[h] >> 16);
+        p[h] = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
       }
-      m[i] = p[0] | (p[1] << 16);
+      // row i's two halves in the low halves of two words, row i + 4's in the high ones
+      m[i] = max_u16x2(__byte_perm(p[0], p[1], 0x5410) & 0x7fff7fffu, __byte_perm(p[0], p[1], 0x7632) & 0x7fff7fffu);
     } else {
       m[i] = 0u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m[i] = max(m[i], mag(v[i].get(e)));
+      for (int e = 0; e < 8; ++e) m[i] = max(m[i], v[i].w[e] & kMag);
     }
   }
   {   // lane l keeps row (l >> 3 & 1) * 2 + (l >> 2 & 1)
@@ -176,14 +216,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) rows_kernel(
   const float s = scale_of(bits, a.f), inv = __frcp_rn(s);
   if ((l & 2) == 0 && (sizeof(T) == 2 || (l & 1) == 0) && r0 + row < a.rows)
     a.scales[static_cast<long long>(kb) * a.rows + r0 + row] = s;
+  uint8_t* dst = a.codes + r0 * a.K + c;
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
+  for (int j = 0; j < R; ++j, dst += a.K) {
     const float rj = __shfl_sync(~0u, inv, half * 16 + ((j >> 1) & 1) * 8 + (j & 1) * 4 + (j >> 2));
-    uint32_t w[4];
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = cvt2(v[j].get(2 * i) * rj, v[j].get(2 * i + 1) * rj, a.f.e5m2);
-    if (r0 + j < a.rows && in_k)
-      *reinterpret_cast<uint2*>(a.codes + (r0 + j) * a.K + c) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    for (int i = 0; i < 2; ++i)
+      w[i] = cvt4<E5M2>(v[j].get(4 * i) * rj, v[j].get(4 * i + 1) * rj, v[j].get(4 * i + 2) * rj, v[j].get(4 * i + 3) * rj);
+    if (r0 + j < a.rows && in_k) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   }
 }
 
@@ -200,7 +241,7 @@ template <>
 struct ColMax<float> {
   uint4 m;
   LMOE_DEV void add(const Raw<float, 4>& v) {
-    m = make_uint4(max(m.x, mag(v.q[0].x)), max(m.y, mag(v.q[0].y)), max(m.z, mag(v.q[0].z)), max(m.w, mag(v.q[0].w)));
+    m = make_uint4(max(m.x, v.w[0] & kMag), max(m.y, v.w[1] & kMag), max(m.z, v.w[2] & kMag), max(m.w, v.w[3] & kMag));
   }
   LMOE_DEV void add(const ColMax& o) {
     m = make_uint4(max(m.x, o.m.x), max(m.y, o.m.y), max(m.z, o.m.z), max(m.w, o.m.w));
@@ -211,17 +252,20 @@ template <>
 struct ColMax<__nv_bfloat16> {
   uint2 m;
   LMOE_DEV void add(const Raw<__nv_bfloat16, 4>& v) {
-    m = make_uint2(__vmaxu2(m.x, v.w[0] & 0x7fff7fffu), __vmaxu2(m.y, v.w[1] & 0x7fff7fffu));
+    m = make_uint2(max_u16x2(m.x, v.w[0] & 0x7fff7fffu), max_u16x2(m.y, v.w[1] & 0x7fff7fffu));
   }
-  LMOE_DEV void add(const ColMax& o) { m = make_uint2(__vmaxu2(m.x, o.m.x), __vmaxu2(m.y, o.m.y)); }
+  LMOE_DEV void add(const ColMax& o) { m = make_uint2(max_u16x2(m.x, o.m.x), max_u16x2(m.y, o.m.y)); }
   LMOE_DEV uint32_t bits(int j) const {
     const uint32_t w = j < 2 ? m.x : m.y;
     return j & 1 ? w & 0xffff0000u : w << 16;
   }
 };
-// CTAs an SM holds: bf16 rows take half the registers
+// CTAs an SM holds: bf16 rows take half the registers.  (bf16, 8 x 4096 x 4096 weights: 3 CTAs 85 us,
+// 4 87; columns of 16384 x 4096: 4 CTAs 41 us, 3 44)
 template <typename T>
-constexpr int kTileCtas = sizeof(T) == 2 ? 4 : 2;
+constexpr int kWeightCtas = sizeof(T) == 2 ? 3 : 2;
+template <typename T>
+constexpr int kColsCtas = sizeof(T) == 2 ? 4 : 2;
 
 // writes the transposed tile from shared memory: column c's 128 bytes to dst + c * ld
 LMOE_DEV void store_transposed(const uint8_t* tile, uint8_t* dst, long long ld, int ncols, int nbytes) {
@@ -242,8 +286,8 @@ struct WeightArgs {
   uint8_t *codes, *codes_t;
   float *scales, *scales_t;
 };
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, kTileCtas<T>) weight_kernel(const WeightArgs a) {
+template <typename T, bool VEC, bool E5M2>
+__global__ void __launch_bounds__(kThreads, kWeightCtas<T>) weight_kernel(const WeightArgs a) {
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ uint32_t wmax[kThreads / 32];
   griddep_enter();
@@ -257,8 +301,7 @@ __global__ void __launch_bounds__(kThreads, kTileCtas<T>) weight_kernel(const We
   Raw<T, 4> v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    if (n0 + i < a.N && k0 < a.K) v[i].template load<VEC>(src + static_cast<long long>(i) * a.K);
-    else v[i].zero();
+    v[i].template load<VEC>(src + static_cast<long long>(i) * a.K, n0 + i < a.N && k0 < a.K);
   }
   ColMax<T> cm{};
 #pragma unroll
@@ -273,16 +316,23 @@ __global__ void __launch_bounds__(kThreads, kTileCtas<T>) weight_kernel(const We
     a.scales[(g * a.nb + nb) * a.kb + kb] = s;
     if (a.scales_t != nullptr) a.scales_t[(g * a.kb + kb) * a.nb + nb] = s;
   }
-  uint32_t tr[4][4];
+  uint32_t tr[4][4];   // tr[j][q]: column j, rows 4 q .. 4 q + 3
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t w01 = cvt2(v[i].get(0) * inv, v[i].get(1) * inv, a.f.e5m2);
-    const uint32_t w23 = cvt2(v[i].get(2) * inv, v[i].get(3) * inv, a.f.e5m2);
-    if (n0 + i < a.N && k0 < a.K)
-      *reinterpret_cast<uint32_t*>(a.codes + (g * a.N + n0 + i) * a.K + k0) = w01 | (w23 << 16);
-    const uint32_t b[4] = {w01 & 0xffu, w01 >> 8, w23 & 0xffu, w23 >> 8};
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];   // four rows of four columns
 #pragma unroll
-    for (int j = 0; j < 4; ++j) tr[j][i >> 2] = (i & 3) == 0 ? b[j] : tr[j][i >> 2] | (b[j] << (8 * (i & 3)));
+    for (int i = 0; i < 4; ++i) {
+      const Raw<T, 4>& x = v[4 * q + i];
+      w[i] = cvt4<E5M2>(x.get(0) * inv, x.get(1) * inv, x.get(2) * inv, x.get(3) * inv);
+      if (n0 + 4 * q + i < a.N && k0 < a.K)
+        *reinterpret_cast<uint32_t*>(a.codes + (g * a.N + n0 + 4 * q + i) * a.K + k0) = w[i];
+    }
+    const uint32_t lo = __byte_perm(w[0], w[1], 0x5140), lo2 = __byte_perm(w[2], w[3], 0x5140);   // columns 0, 1
+    const uint32_t up = __byte_perm(w[0], w[1], 0x7362), up2 = __byte_perm(w[2], w[3], 0x7362);   // columns 2, 3
+    tr[0][q] = __byte_perm(lo, lo2, 0x5410);
+    tr[1][q] = __byte_perm(lo, lo2, 0x7632);
+    tr[2][q] = __byte_perm(up, up2, 0x5410);
+    tr[3][q] = __byte_perm(up, up2, 0x7632);
   }
   if (a.codes_t == nullptr) return;
 #pragma unroll
@@ -303,8 +353,8 @@ struct ColsArgs {
   uint8_t* codes;
   float* scales;
 };
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, kTileCtas<T>) cols_kernel(const ColsArgs a) {
+template <typename T, bool VEC, bool E5M2>
+__global__ void __launch_bounds__(kThreads, kColsCtas<T>) cols_kernel(const ColsArgs a) {
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ ColMax<T> cmax[kThreads / 32][32];
   __shared__ int start[kMaxGroups + 1], lo[kMaxGroups], hi[kMaxGroups];
@@ -351,17 +401,17 @@ __global__ void __launch_bounds__(kThreads, kTileCtas<T>) cols_kernel(const Cols
     }
     const int r0 = lo[l] + (blk - start[l]) * 128 + warp * 16, k0 = kb * 128 + lane * 4;
     const int rend = hi[l];
-    long long mine = -1;   // lane i < 16: source row of row r0 + i
+    int mine = -1;   // lane i < 16: source row of row r0 + i
     if (lane < 16 && r0 + lane < rend) {
       mine = a.index != nullptr ? a.index[r0 + lane] : r0 + lane;
       if (mine < 0 || mine >= a.src_rows) mine = -1;
     }
+    const T* src = static_cast<const T*>(a.src) + k0;
     Raw<T, 4> v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const long long q = __shfl_sync(~0u, mine, i);
-      if (q >= 0 && k0 < a.K) v[i].template load<VEC>(static_cast<const T*>(a.src) + q * a.ld + k0);
-      else v[i].zero();
+      const int q = __shfl_sync(~0u, mine, i);
+      v[i].template load<VEC>(src + q * a.ld, q >= 0 && k0 < a.K);
     }
     ColMax<T> m{};
 #pragma unroll
@@ -382,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, kTileCtas<T>) cols_kernel(const Cols
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        w[q] = cvt2(v[4 * q].get(j) * inv[j], v[4 * q + 1].get(j) * inv[j], a.f.e5m2) |
-               (cvt2(v[4 * q + 2].get(j) * inv[j], v[4 * q + 3].get(j) * inv[j], a.f.e5m2) << 16);
+        w[q] = cvt4<E5M2>(v[4 * q].get(j) * inv[j], v[4 * q + 1].get(j) * inv[j], v[4 * q + 2].get(j) * inv[j],
+                          v[4 * q + 3].get(j) * inv[j]);
       *reinterpret_cast<uint4*>(tile + (lane * 4 + j) * 128 + ((warp ^ (lane & 7)) << 4)) =
           make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -397,13 +447,16 @@ __global__ void __launch_bounds__(kThreads, kTileCtas<T>) cols_kernel(const Cols
 bool on(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 bool dtype_ok(lmoe_dtype d) { return d == LMOE_F32 || d == LMOE_BF16; }
-Fmt fmt_of(lmoe_fp8_format f, int pow2) { return Fmt{f == LMOE_FP8_E5M2 ? 57344.f : 448.f, f == LMOE_FP8_E5M2, pow2 != 0}; }
+Fmt fmt_of(lmoe_fp8_format f, int pow2) { return Fmt{f == LMOE_FP8_E5M2 ? 57344.f : 448.f, pow2 != 0}; }
 
-// f(T, VEC) for the source's type and alignment
+// f(T, VEC, E5M2) for the source's type and alignment and the codes' format
 template <typename F>
-cudaError_t by_source(lmoe_dtype d, bool vec, F f) {
-  if (d == LMOE_F32) return vec ? f(float{}, std::true_type{}) : f(float{}, std::false_type{});
-  return vec ? f(__nv_bfloat16{}, std::true_type{}) : f(__nv_bfloat16{}, std::false_type{});
+cudaError_t by_source(lmoe_dtype d, bool vec, lmoe_fp8_format fmt, F f) {
+  const auto with = [&](auto t, auto v) {
+    return fmt == LMOE_FP8_E5M2 ? f(t, v, std::true_type{}) : f(t, v, std::false_type{});
+  };
+  if (d == LMOE_F32) return vec ? with(float{}, std::true_type{}) : with(float{}, std::false_type{});
+  return vec ? with(__nv_bfloat16{}, std::true_type{}) : with(__nv_bfloat16{}, std::false_type{});
 }
 
 }  // namespace
@@ -429,12 +482,15 @@ extern "C" lmoe_status lmoe_quantize_fp8_rows(const void* src, lmoe_dtype src_dt
   const int es = src_dtype == LMOE_F32 ? 4 : 2;
   if (!on(src, es) || !on(codes, 16) || !on(scales, 4) || !on(row_index, 4)) return LMOE_ERR_ALIGN;
   const int kb = cdiv(K, 128);
-  const RowsArgs a = {src, ld_src, src_rows, rows, row_index, K, kb, fmt_of(format, pow2_scales), codes, scales};
-  const int unit_rows = 2 * (es == 2 ? kHalfRows<__nv_bfloat16> : kHalfRows<float>);
-  const long long ctas = ((rows + unit_rows - 1) / unit_rows * kb + kThreads / 32 - 1) / (kThreads / 32);
+  int kb_warps = 1;
+  while (kb_warps < kb && kb_warps < kThreads / 32) kb_warps *= 2;
+  const RowsArgs a = {src,      ld_src, src_rows, rows, row_index, K, kb, static_cast<unsigned>(cdiv(kb, kb_warps)),
+                      kb_warps, fmt_of(format, pow2_scales), codes, scales};
+  const int cta_rows = 2 * (es == 2 ? kHalfRows<__nv_bfloat16> : kHalfRows<float>) * (kThreads / 32 / kb_warps);
+  const long long ctas = (rows + cta_rows - 1) / cta_rows * a.chunks;
   if (ctas > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
-  const cudaError_t e = by_source(src_dtype, on(src, 16) && ld_src * es % 16 == 0, [&](auto t, auto v) {
-    return launch_pdl(rows_kernel<decltype(t), decltype(v)::value>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, stream, a);
+  const cudaError_t e = by_source(src_dtype, on(src, 16) && ld_src * es % 16 == 0, format, [&](auto t, auto v, auto f) {
+    return launch_pdl(rows_kernel<decltype(t), decltype(v)::value, decltype(f)::value>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, stream, a);
   });
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
@@ -445,8 +501,7 @@ extern "C" lmoe_status lmoe_quantize_fp8_weight(const void* src, lmoe_dtype src_
                                                 cudaStream_t stream) {
   if (n_experts < 0 || N <= 0 || K <= 0 || (format != LMOE_FP8_E4M3 && format != LMOE_FP8_E5M2)) return LMOE_ERR_ARG;
   if ((codes_t == nullptr) != (scales_t == nullptr)) return LMOE_ERR_ARG;
-  if (!dtype_ok(src_dtype) || K % 16 || (codes_t != nullptr && N % 16) || K > (1 << 20) || N > (1 << 20) ||
-      n_experts > kMaxGroups)
+  if (!dtype_ok(src_dtype) || K % 16 || (codes_t != nullptr && N % 16) || K > (1 << 20) || N > (1 << 20))
     return LMOE_ERR_UNSUPPORTED;
   if (n_experts == 0) return LMOE_OK;
   if (src == nullptr || codes == nullptr || scales == nullptr) return LMOE_ERR_ARG;
@@ -455,8 +510,8 @@ extern "C" lmoe_status lmoe_quantize_fp8_weight(const void* src, lmoe_dtype src_
   const WeightArgs a = {src, N, K, cdiv(N, 128), cdiv(K, 128), fmt_of(format, pow2_scales), codes, codes_t, scales, scales_t};
   const long long ctas = static_cast<long long>(n_experts) * a.nb * a.kb;
   if (ctas > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
-  const cudaError_t e = by_source(src_dtype, on(src, 4 * es), [&](auto t, auto v) {
-    return launch_pdl(weight_kernel<decltype(t), decltype(v)::value>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, stream, a);
+  const cudaError_t e = by_source(src_dtype, on(src, 4 * es), format, [&](auto t, auto v, auto f) {
+    return launch_pdl(weight_kernel<decltype(t), decltype(v)::value, decltype(f)::value>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, stream, a);
   });
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
@@ -480,9 +535,9 @@ extern "C" lmoe_status lmoe_quantize_fp8_cols(const void* src, lmoe_dtype src_dt
   const ColsArgs a = {src,     ld_src,    src_rows, rows, padded_rows, row_index, offsets,
                       n_experts, K, cdiv(K, 128), fmt_of(format, pow2_scales), codes_t, scales_t};
   const long long units = padded_rows / 128 * a.kb;
-  const int grid = static_cast<int>(std::min<long long>(units, (es == 2 ? kTileCtas<__nv_bfloat16> : kTileCtas<float>) * sm_count()));
-  const cudaError_t e = by_source(src_dtype, on(src, 4 * es) && ld_src % 4 == 0, [&](auto t, auto v) {
-    return launch_pdl(cols_kernel<decltype(t), decltype(v)::value>, dim3(grid), dim3(kThreads), 0, stream, a);
+  const int grid = static_cast<int>(std::min<long long>(units, (es == 2 ? kColsCtas<__nv_bfloat16> : kColsCtas<float>) * sm_count()));
+  const cudaError_t e = by_source(src_dtype, on(src, 4 * es) && ld_src % 4 == 0, format, [&](auto t, auto v, auto f) {
+    return launch_pdl(cols_kernel<decltype(t), decltype(v)::value, decltype(f)::value>, dim3(grid), dim3(kThreads), 0, stream, a);
   });
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }

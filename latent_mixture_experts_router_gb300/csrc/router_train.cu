@@ -14,7 +14,7 @@
 // registers (G V >= E), so a warp has 32 / G rows under way, and loads its next ones before it
 // works on the present ones.  exp is one FMA and ex2: exp2(l log2e - m log2e), exact in m's part
 // (it cancels in p).  The column sums of p stay in registers over a warp's rows, are added over the
-// CTA's warps and, through the cluster's shared memory, over eight CTAs, always in the same order;
+// CTA's warps and, through the cluster's shared memory, over four CTAs, always in the same order;
 // one cluster finishes by itself, several leave a row of sums each for a second kernel.
 #include <algorithm>
 
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kLossWarps = 16, kGradWarps = 8;
 constexpr int kLossThreads = kLossWarps * 32, kGradThreads = kGradWarps * 32;
-constexpr int kCluster = 8;
+constexpr int kCluster = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 LMOE_DEV float to_f32(float v) { return v; }
@@ -544,9 +544,9 @@ int warp_rows(int E) { return E <= 16 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1; }
 bool rows_vec(const void* p, long long ld, int E, int es) {
   return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * es) == 0;
 }
-// CTAs of the losses kernel, in clusters of one or eight: one CTA while each warp takes up to four
+// CTAs of the losses kernel, in clusters of one or four: one CTA while each warp takes up to four
 // turns of rows, then clusters of two turns, as many as the SMs hold.
-constexpr int kMaxClusters = 19;   // 152 SMs
+constexpr int kMaxClusters = 36;   // 144 of 152 SMs: what fits beside the units' borders
 struct LossGrid {
   int cluster, clusters;
 };
