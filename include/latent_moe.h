@@ -378,7 +378,7 @@ lmoe_status lmoe_validate_routing(const lmoe_config* cfg, void* workspace, cudaS
  * The router's two auxiliary losses with the per-expert counts, and the gradient of its logits.
  * Row t holds E logits l = logits[t] (+ router_bias), p = softmax(l), lse = log sum exp(l).  A row
  * is live when its mask byte is not 0 (row_mask NULL: every row) and at least one of its logits
- * is above -inf; the logits and ids of a row that the mask drops are not read.  n: live rows;
+ * is above -inf; what a row that the mask drops holds (NaN, any ids) does not matter.  n: live rows;
  * counts[e]: slots of live rows that name expert e; an id outside [0, E) is an empty slot.
  *   losses[0] = E sum_e f_e P_e,  f_e = counts[e] / (k n),  P_e = mean_probs[e] = mean p_e
  *               (the balance loss: 1 when either is uniform)

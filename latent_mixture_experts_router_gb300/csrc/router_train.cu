@@ -145,7 +145,7 @@ LMOE_DEV float block_sum(float v, float* sm) {
 }
 
 template <typename T, int G, int V, bool VEC>
-__global__ void __launch_bounds__(kLossThreads) losses_kernel(const LossArgs a) {
+__global__ void __launch_bounds__(kLossThreads, V <= 16 ? 2 : 1) losses_kernel(const LossArgs a) {
   constexpr int kRows = 32 / G, kSlots = G < 16 ? 16 / G : 1;
   extern __shared__ float sm_p[];   // [kLossWarps][E], whose first row becomes the CTA's sums; hist [E]
   int* hist = reinterpret_cast<int*>(sm_p + kLossWarps * a.E);
@@ -167,16 +167,17 @@ __global__ void __launch_bounds__(kLossThreads) losses_kernel(const LossArgs a) 
   int n = 0, ids[kSlots];
   int t = (blockIdx.x * kLossWarps + warp) * kRows + g;
   bool live;
-  const auto fetch = [&] {   // row t, if there is one and the mask keeps it
-    live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
+#pragma unroll
+  for (int i = 0; i < V; ++i) next[i] = -INFINITY;
+  // row t, if there is one: loaded beside its mask, not after it
+  const auto fetch = [&] {
+    live = t < a.T;
     if (live) {
       load_row<T, G, V, VEC>(logits + t * a.ld, a.E, l, next);
 #pragma unroll
       for (int s = 0; s < kSlots; ++s)
         ids[s] = l + G * s < a.k ? a.idx[static_cast<long long>(t) * a.k + l + G * s] : -1;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) next[i] = -INFINITY;
+      if (a.mask != nullptr) live = a.mask[t] != 0;
     }
   };
   fetch();
@@ -190,15 +191,15 @@ __global__ void __launch_bounds__(kLossThreads) losses_kernel(const LossArgs a) 
     const bool here = live;
     t += step;
     fetch();
-    if (a.bias != nullptr && here) add_bias<G, V, VEC>(a.bias, a.E, l, v);
+    if (a.bias != nullptr) add_bias<G, V, VEC>(a.bias, a.E, l, v);
     float m = row_max<G>(v);
     const bool on = here && m != -INFINITY;
-    m = on ? m : 0.f;   // (a row that is not live: every exp is 0)
+    m = on ? m : 0.f;
     const float s = exp_row<G>(v, m);
-    const float r = on ? 1.f / s : 0.f;
+    const float r = 1.f / s;
+    if (on) {   // (a row that is not live may hold anything)
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], r, acc[i]);
-    if (on) {
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], r, acc[i]);
       const float lse = m + logf(s);
       z = fmaf(lse, lse, z);
       ++n;
@@ -289,35 +290,58 @@ __global__ void __launch_bounds__(kLossThreads) losses_kernel(const LossArgs a) 
   cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
-// Adds the clusters' sums, in order.
-__global__ void __launch_bounds__(kLossThreads) losses_finish_kernel(const LossArgs a) {
-  __shared__ float sm_d[kLossWarps];
+// Adds the clusters' sums, in order: groups of threads, one to an expert each, take every
+// groups-th cluster, whose loads are then under way together.
+constexpr int kFinishThreads = 1024;
+__global__ void __launch_bounds__(kFinishThreads) losses_finish_kernel(const LossArgs a) {
+  __shared__ float sm_p[kFinishThreads];
+  __shared__ int sm_c[kFinishThreads];
+  __shared__ float sm_d[kFinishThreads / 32];
   griddep_enter();
-  float z = 0.f, dot = 0.f;
-  int n = 0;
-#pragma unroll 4
-  for (int q = 0; q < a.clusters; ++q) {
-    n += a.part_n[q];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int W = 32;
+  while (W < a.E) W *= 2;   // E <= 1024
+  const int groups = kFinishThreads / W, grp = threadIdx.x / W, e = threadIdx.x % W;
+  float p = 0.f, z = 0.f, n = 0.f;   // (counts of rows are exact in fp32: at most 2^20)
+  int c = 0;
+#pragma unroll 1
+  for (int q = lane; q < a.clusters; q += 32) {
+    n += static_cast<float>(a.part_n[q]);
     z += a.part_z[q];
   }
-  const float inv = n > 0 ? 1.f / n : 0.f;
-  for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
-    float p = 0.f;
-    int c = 0;
-#pragma unroll 8
-    for (int q = 0; q < a.clusters; ++q) {
-      p += a.part_p[static_cast<long long>(q) * a.E + e];
-      c += a.part_c[static_cast<long long>(q) * a.E + e];
+  if (e < a.E) {
+#pragma unroll 10
+    for (int q = grp; q < a.clusters; q += groups) {
+      p += a.part_p[q * a.E + e];
+      c += a.part_c[q * a.E + e];
+    }
+  }
+  n = group_sum<32>(n);
+  z = group_sum<32>(z);
+  const float inv = n > 0.f ? 1.f / n : 0.f;
+  sm_p[threadIdx.x] = p;
+  sm_c[threadIdx.x] = c;
+  __syncthreads();
+  float dot = 0.f;
+  if (threadIdx.x < a.E) {
+    for (int g = 1; g < groups; ++g) {
+      p += sm_p[g * W + e];
+      c += sm_c[g * W + e];
     }
     a.mean[e] = p * inv;
     a.counts[e] = c;
-    dot = fmaf(p * inv, c * inv, dot);
+    dot = p * inv * (c * inv);
   }
-  dot = block_sum(dot, sm_d);
-  if (threadIdx.x == 0) {
-    a.counts[a.E] = n;
-    a.losses[0] = dot * a.E / a.k;
-    a.losses[1] = z * inv;
+  dot = group_sum<32>(dot);
+  if (lane == 0) sm_d[warp] = dot;
+  __syncthreads();
+  if (warp == 0) {
+    dot = group_sum<32>(sm_d[lane]);
+    if (lane == 0) {
+      a.counts[a.E] = static_cast<int>(n);
+      a.losses[0] = dot * a.E / a.k;
+      a.losses[1] = z * inv;
+    }
   }
 }
 
@@ -336,13 +360,14 @@ struct GradArgs {
 };
 
 template <typename T, int G, int V, bool VEC>
-__global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, V <= 16 ? 3 : 2) grad_kernel(const GradArgs a) {
   constexpr int kRows = 32 / G, kSlots = G < 16 ? 16 / G : 1;
   extern __shared__ float sm_row[];   // [rows of the CTA][E]: a row while its slots' terms are added
   __shared__ int sm_id[G < 16 ? kGradWarps * kRows : 1][16];
   __shared__ float sm_g[G < 16 ? kGradWarps * kRows : 1][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / G, l = lane % G;
   const int local = warp * kRows + g;
+  float* sm_f = sm_row + kGradWarps * kRows * a.E;   // [E] shares of the slots
   float* row = sm_row + local * a.E;
   griddep_enter();
   const T* logits = static_cast<const T*>(a.logits);
@@ -352,8 +377,11 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradArgs a) {
   int inext[kSlots];
   int t = (blockIdx.x * kGradWarps + warp) * kRows + g;
   bool live;
-  const auto fetch = [&] {   // row t, if there is one and the mask keeps it
-    live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
+#pragma unroll
+  for (int i = 0; i < V; ++i) next[i] = -INFINITY;
+  // row t, if there is one: loaded beside its mask, not after it
+  const auto fetch = [&] {
+    live = t < a.T;
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
       inext[s] = -1;
@@ -369,25 +397,18 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradArgs a) {
             gnext[s] = a.gw[static_cast<long long>(t) * a.k + l + G * s];
           }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) next[i] = -INFINITY;
+      if (a.mask != nullptr) live = a.mask[t] != 0;
     }
   };
   fetch();
-  float f[V], cb = 0.f, cz = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = 0.f;
+  float cb = 0.f, cz = 0.f;
   if (a.gl != nullptr) {
     const float inv = 1.f / max(a.counts[a.E], 1);
     cb = a.gl[0] * a.E * inv;
     cz = a.gl[1] * 2.f * inv;
     const float fk = inv / a.k;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = col<G, VEC>(l, i);
-      if (e < a.E) f[i] = a.counts[e] * fk;
-    }
+    for (int e = threadIdx.x; e < a.E; e += kGradThreads) sm_f[e] = a.counts[e] * fk;
+    __syncthreads();
   }
   while (t - g < a.T) {   // (the same for the warp)
     float v[V], gw[kSlots], sel[kSlots];
@@ -413,21 +434,31 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradArgs a) {
     }
     t += step;
     fetch();
-    if (a.bias != nullptr && on) add_bias<G, V, VEC>(a.bias, a.E, l, v);
+    if (a.bias != nullptr) add_bias<G, V, VEC>(a.bias, a.E, l, v);
     float m = row_max<G>(v);
     on = on && m != -INFINITY;
     m = on ? m : 0.f;
-    const float s = exp_row<G>(v, m), r = on ? 1.f / s : 0.f;
-    const float lz = on ? cz * (m + logf(s)) : 0.f;
-    float dot = 0.f;
+    const float s = exp_row<G>(v, m), r = 1.f / s;
+    if (a.gl != nullptr) {
+      const float lz = cz * (m + logf(s));
+      float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] *= r;
-      dot = fmaf(v[i], f[i], dot);
+      for (int i = 0; i < V; ++i) {
+        const int e = col<G, VEC>(l, i);
+        v[i] *= r;
+        if (e < a.E) dot = fmaf(v[i], sm_f[e], dot);
+      }
+      dot = group_sum<G>(dot);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = col<G, VEC>(l, i);
+        if (e < a.E) v[i] *= fmaf(cb, sm_f[e] - dot, lz);
+      }
     }
-    dot = group_sum<G>(dot);
+    if (!on || a.gl == nullptr) {   // (a row that is not live may hold anything)
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= fmaf(cb, f[i] - dot, lz);
+      for (int i = 0; i < V; ++i) v[i] = 0.f;
+    }
     if (a.gw != nullptr) {
       float sm = sel[0];
 #pragma unroll
@@ -546,7 +577,7 @@ bool rows_vec(const void* p, long long ld, int E, int es) {
 }
 // CTAs of the losses kernel, in clusters of one or four: one CTA while each warp takes up to four
 // turns of rows, then clusters of two turns, as many as the SMs hold.
-constexpr int kMaxClusters = 36;   // 144 of 152 SMs: what fits beside the units' borders
+constexpr int kMaxClusters = 72;   // two CTAs on 144 of 152 SMs: what fits inside the units' borders
 struct LossGrid {
   int cluster, clusters;
 };
@@ -554,7 +585,7 @@ LossGrid losses_grid(int T, int E) {
   const int turn = kLossWarps * warp_rows(E);   // rows of a CTA at a time
   if (T <= 4 * turn) return {1, 1};
   const int want = (T + 2 * turn * kCluster - 1) / (2 * turn * kCluster);
-  return {kCluster, std::min(want, kMaxClusters)};
+  return {kCluster, std::min(want, E <= 512 ? kMaxClusters : kMaxClusters / 2)};
 }
 
 lmoe_status check_rows(const void* logits, lmoe_dtype dt, long long ld, const float* bias, const int32_t* idx, int T,
@@ -611,7 +642,7 @@ extern "C" lmoe_status lmoe_router_losses(const void* logits, lmoe_dtype logits_
                                                  stream, lg.cluster, a);
   });
   if (e == cudaSuccess && lg.clusters > 1)
-    e = launch_pdl(losses_finish_kernel, dim3(1), dim3(kLossThreads), 0, stream, a);
+    e = launch_pdl(losses_finish_kernel, dim3(1), dim3(kFinishThreads), 0, stream, a);
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
@@ -635,9 +666,9 @@ extern "C" lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dt
   const GradArgs a = {logits, ld_logits, router_bias, row_mask, topk_idx, topk_w_grad, counts, loss_grads,
                       T,      E,         k,           dlogits,  ld_dlogits};
   const int turn = kGradWarps * warp_rows(E);   // rows of a CTA at a time
-  const size_t smem = static_cast<size_t>(turn) * E * 4;
+  const size_t smem = static_cast<size_t>(turn + 1) * E * 4;
   const bool vec = rows_vec(logits, ld_logits, E, es) && rows_vec(dlogits, ld_dlogits, E, es);
-  const int grid = std::max(1, std::min(4 * sm_count(), (T + turn - 1) / turn));
+  const int grid = std::max(1, std::min((E <= 512 ? 3 : 2) * sm_count(), (T + turn - 1) / turn));
   const cudaError_t e = by_shape(f32, E, vec, [&](auto t, auto g, auto v, auto vc) {
     auto kern = grad_kernel<decltype(t), decltype(g)::value, decltype(v)::value, decltype(vc)::value>;
     const cudaError_t r = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
