@@ -13,19 +13,20 @@
 // multiply-adds on the CUDA cores (128 a cycle) beside 128 x 256 x 128 on the tensor cores
 // (8192 a cycle): half the time.
 //
-// The weights' rows are the MMA's 128 lanes and the tokens its columns ("lane" and "column"
-// operand below): the column count of an MMA is any multiple of 16, so an expert with 40 rows
-// costs 48 columns, not a 128-row tile; one token costs 16.  A weight's 128 x 128 block is
-// exactly a tile's lanes, so its scale is one number per block and is folded into the columns'
-// scales; in wgrad every lane has a scale of its own.
+// Which operand is the MMA's 128 lanes ("lane operand") and which its columns:
+//   kRows   rows of a are lanes, rows of w columns (128 x 256 tiles): many rows per expert.  A thread
+//           holds one lane, so its scale as ws is one register for 128 columns.
+//   kCols   rows of w are lanes, rows of a columns: the column count is any multiple of 16, so an
+//           expert with 20 rows costs 32 columns, not a 128-row tile, and one token costs 16.
+//   kSplit  kCols where the tiles are few (a few tokens): a cluster of S CTAs computes one tile,
+//           each a range of the blocks; the others leave their sums in the first one's shared
+//           memory, which adds them in rank order.
+//   kWgrad  rows of x_t are lanes, rows of dy_t columns; both have scales of their own.
 //
 // Roles of a CTA: warp 0 lane 0 TMA producer; warp 1 lane 0 MMA issuer (warp 1 owns the TMEM);
-// warp 2 stages the column scales of each block in shared memory; warps 4.. epilogue, warp w on
-// TMEM lanes 32 (w % 4) .. (and column half (w - 4) / 4 with eight of them).
-//
-// kSplit: few tiles (a few tokens).  A cluster of S CTAs computes one tile, each a range of the
-// blocks; the others leave their accumulators in the first one's shared memory, which adds them
-// in rank order.
+// warp 2 stages the scales of each block in shared memory; warps 4.. epilogue, warp w on TMEM lanes
+// 32 (w % 4) .. (and column half (w - 4) / 4 with eight of them).  The epilogue leaves a finished
+// tile in shared memory, from where bulk copies store it while the next tile is computed.
 #include "../../include/latent_moe.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -33,22 +34,22 @@
 namespace lmoe {
 namespace {
 
-enum Fp8Mode : int { kMatmul = 0, kWgrad = 1, kSplit = 2 };
+enum Fp8Mode : int { kCols = 0, kWgrad = 1, kSplit = 2, kRows = 3 };
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSplit = 8;
 
 struct Fp8Args {
-  long long rows;        // matmul: rows of a and y; wgrad: columns of dy and x (a multiple of 128)
-  int lanes, cols;       // extents of the lane operand and (wgrad) of the column operand
+  long long rows;        // matmul: rows of a and y; wgrad: columns of dy_t and x_t (a multiple of 128)
+  int n, k;              // matmul: rows of w; wgrad: rows of dy_t and of x_t
   int num_kb;            // matmul: blocks of the reduction
   int E;
   const int32_t* offsets;   // [E + 1], or nullptr: one group of all rows
   const float* ps;       // scales of the lane operand
-  const float* qs;       // scales of the column operand, [block][ldq]
-  long long ldq;
+  const float* qs;       // scales of the column operand
   void* out;
+  int ldo;               // elements of an output row
   int out_f32, accumulate;
-  int out_vec;           // bf16: 16-byte stores fit the output's base and rows
+  int out_vec;           // output rows start on 16 bytes: bulk copies
   unsigned fmt_p, fmt_q;   // 0 e4m3, 1 e5m2
   unsigned* status;      // error word or nullptr
   long long budget;
@@ -58,27 +59,29 @@ struct Fp8Args {
 template <int BN, int MODE>
 struct Fp8Cfg {
   static constexpr int kEpiWarps = BN == 256 ? 8 : 4;
-  static constexpr int kCols = BN * 4 / kEpiWarps;   // accumulator columns of one thread
+  static constexpr int kAcc = BN * 4 / kEpiWarps;   // accumulator columns of one thread's warpgroup
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kPBytes = 128 * 128;
   static constexpr int kQBytes = BN * 128;
   static constexpr int kStageBytes = kPBytes + kQBytes;
-  static constexpr int kBox = BN < 64 ? BN : 64;      // rows of one column-operand box
+  static constexpr int kBox = MODE == kRows ? 256 : BN < 64 ? BN : 64;   // rows of a column-operand box
   static constexpr int kSlots = 8;                    // staged scale blocks
   static constexpr int kBufs = BN == 256 ? 2 : 8;     // TMEM buffers
   static constexpr uint32_t kTmemCols = BN * kBufs;
   static constexpr int kMaxS = BN == 16 ? kMaxSplit : 4;
   static constexpr int kRedBytes = MODE == kSplit ? (kMaxS - 1) * BN * 128 * 4 : 0;
-  static constexpr int kStageCols = 16;               // columns of one pass of the bf16 store
-  static constexpr int kOutBytes = kEpiWarps * kStageCols * 64;
-  static constexpr int kTableBytes = 3 * (kMaxGroups + 4) * 4;
-  static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kOutBytes + kTableBytes + 512 + 1024;
+  // output staging of a warpgroup: kAcc columns of 128 bf16, or kOutCols of 128 fp32 at a time (kRows:
+  // 128 rows of 128 bf16 or of 64 fp32), each with 16 bytes of padding against bank conflicts
+  static constexpr int kOutCols = kAcc >= 64 ? kAcc / 2 : kAcc;
+  static constexpr int kOutBytes = MODE == kRows ? 128 * 272 : kAcc * 272 > kOutCols * 528 ? kAcc * 272 : kOutCols * 528;
+  static constexpr int kTableBytes = (kMaxGroups + 4) * 4;
+  static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kOutBytes * (kEpiWarps / 4) + kTableBytes + 512 + 1024;
   static constexpr int kStagesFit = (227 * 1024 - kFixed) / kStageBytes;
   static constexpr int kStages = kStagesFit > 11 ? 11 : kStagesFit;
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
   static_assert(kStages >= 3, "pipeline depth");
   static_assert((2 * kStages + 2 * kBufs + 2 * kSlots + 1) * 8 + 8 <= 512, "barriers");
-  static_assert(MODE == kMatmul || BN != 256 || MODE == kWgrad, "split tiles are narrow");
+  static_assert((BN == 256) == (MODE == kRows || MODE == kWgrad), "tile widths");
 };
 
 // Instruction descriptor of kind::f8f6f4: D fp32 ([4,6) = 1), formats at [7,10) and [10,13),
@@ -146,53 +149,393 @@ LMOE_DEV void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The tiles of a launch, the same walk for every role.  Tables in shared memory, per group e:
-// start[e] its first column tile (matmul) or first block (wgrad), lo/hi its rows (matmul).
+LMOE_DEV void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// ---- bulk copies shared -> global (16-byte aligned addresses and sizes), in groups per thread
+LMOE_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+LMOE_DEV void bulk_store(void* dst, uint32_t saddr, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(saddr), "r"(bytes)
+               : "memory");
+}
+// *dst += (fp32)
+LMOE_DEV void bulk_add(void* dst, uint32_t saddr, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(saddr),
+               "r"(bytes)
+               : "memory");
+}
+LMOE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// this thread's copies have read their shared memory / are complete
+LMOE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+LMOE_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Rows of group e, clamped into the rows there are, so that no offsets send a load or a store out
+// of range.
+LMOE_DEV void group_rows(const Fp8Args& a, int e, int& lo, int& hi) {
+  const int cap = static_cast<int>(a.rows);
+  lo = 0;
+  hi = cap;
+  if (a.offsets != nullptr) {
+    lo = min(max(a.offsets[e], 0), cap);
+    hi = min(max(a.offsets[e + 1], lo), cap);
+  }
+}
+
+// The tiles of a launch, the same walk for every role.  start[e] (shared memory): the first row
+// tile of group e (matmul) or its first block (wgrad).
 struct Fp8Walk {
-  const int *start, *lo, *hi;
-  int E, lane_tiles, col_tiles, total;
+  const int* start;
+  int E, others, total;   // others: tiles across, per row tile; wgrad: lane tiles
+  int cols;               // wgrad: column tiles
 };
 struct Fp8Tile {
-  int e, p0, q0, ncols, kb0, kb1;
-  long long out;   // element offset of (first column, first lane)
+  int e, p0, q0, ncols, lanes, kb0, kb1;   // lanes, ncols: live ones
+  long long out;   // kRows: element offset of (first lane, first column), else of (column, lane)
 };
 
 template <int BN, int MODE>
 LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
   Fp8Tile t;
-  int lt, ct;
+  int ot, rt;
   if (MODE == kWgrad) {
-    const int per = w.lane_tiles * w.col_tiles;
+    const int per = w.others * w.cols;
     t.e = id / per;
-    grouped_tile(id - t.e * per, w.col_tiles, w.lane_tiles, kRasterGroup, ct, lt);
-    t.p0 = lt * 128;
-    t.q0 = ct * BN;
-    t.ncols = min(BN, a.cols - t.q0);
+    grouped_tile(id - t.e * per, w.cols, w.others, kRasterGroup, rt, ot);
+    t.p0 = ot * 128;
+    t.q0 = rt * BN;
+    t.ncols = min(BN, a.n - t.q0);
+    t.lanes = a.k - t.p0;
     t.kb0 = w.start[t.e];
     t.kb1 = w.start[t.e + 1];
-    t.out = (static_cast<long long>(t.e) * a.cols + t.q0) * a.lanes + t.p0;
+    t.out = (static_cast<long long>(t.e) * a.n + t.q0) * a.ldo + t.p0;
+    return t;
+  }
+  int l = 0, h = w.E, lo, hi;   // the last e with start[e] * others <= id
+  const int s = id / w.others;
+  while (h - l > 1) {
+    const int m = (l + h) >> 1;
+    if (w.start[m] <= s) l = m;
+    else h = m;
+  }
+  t.e = l;
+  grouped_tile(id - w.start[l] * w.others, w.start[l + 1] - w.start[l], w.others, kRasterGroup, rt, ot);
+  group_rows(a, l, lo, hi);
+  t.kb0 = 0;
+  t.kb1 = a.num_kb;
+  if (MODE == kRows) {
+    t.p0 = lo + rt * 128;
+    t.q0 = ot * BN;
+    t.lanes = hi - t.p0;
+    t.ncols = min(BN, a.n - t.q0);
+    t.out = static_cast<long long>(t.p0) * a.ldo + t.q0;
   } else {
-    int l = 0, h = w.E;   // the last e with start[e] * lane_tiles <= id
-    const int s = id / w.lane_tiles;
-    while (h - l > 1) {
-      const int m = (l + h) >> 1;
-      if (w.start[m] <= s) l = m;
-      else h = m;
-    }
-    t.e = l;
-    grouped_tile(id - w.start[l] * w.lane_tiles, w.start[l + 1] - w.start[l], w.lane_tiles, kRasterGroup, ct, lt);
-    t.p0 = lt * 128;
-    t.q0 = w.lo[l] + ct * BN;
-    t.ncols = min(BN, w.hi[l] - t.q0);
-    t.kb0 = 0;
-    t.kb1 = a.num_kb;
+    t.p0 = ot * 128;
+    t.q0 = lo + rt * BN;
+    t.lanes = a.n - t.p0;
+    t.ncols = min(BN, hi - t.q0);
+    t.out = static_cast<long long>(t.q0) * a.ldo + t.p0;
     if (MODE == kSplit) {
       t.kb0 = static_cast<int>(static_cast<long long>(a.num_kb) * rank / a.splits);
       t.kb1 = static_cast<int>(static_cast<long long>(a.num_kb) * (rank + 1) / a.splits);
     }
-    t.out = static_cast<long long>(t.q0) * a.lanes + t.p0;
   }
   return t;
+}
+
+// What an epilogue thread needs to wait for the blocks of its tile.
+template <int BN, int MODE>
+struct Fp8Ring {
+  uint64_t *acc_full, *acc_empty, *sfull, *sempty;
+  unsigned* status;
+  long long budget;
+  LMOE_DEV bool wait(int it) const {
+    using C = Fp8Cfg<BN, MODE>;
+    if (mbar_wait(&sfull[it % C::kSlots], (it / C::kSlots) & 1, budget) &&
+        mbar_wait(&acc_full[it % C::kBufs], (it / C::kBufs) & 1, budget)) {
+      tc_fence_after();
+      return true;
+    }
+    if (status) atomicOr(status, kErrWaitEpilogue);
+    return false;
+  }
+  // the warp has read the TMEM buffer / the scales
+  LMOE_DEV void buffer_read(int it, int lane) const {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&acc_empty[it % Fp8Cfg<BN, MODE>::kBufs]);
+  }
+  LMOE_DEV void scales_read(int it, int lane) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sempty[it % Fp8Cfg<BN, MODE>::kSlots]);
+  }
+};
+
+// ---- epilogue of kRows: a thread owns lane (row) r and 128 columns
+template <int BN>
+LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8Ring<BN, kRows>& ring, const float* sc,
+                            uint8_t* stage_out, uint32_t tmem, int id0, int step) {
+  using C = Fp8Cfg<BN, kRows>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
+  const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+  uint8_t* row = stage_out + half * C::kOutBytes + r * 272;
+  int it = 0;
+  bool ok = true;
+  for (int id = id0; ok && id < walk.total; id += step) {
+    // (the tile is worked out again for the stores: its registers are the accumulators' here)
+    int kb, kb1;
+    {
+      const Fp8Tile t = tile_at<BN, kRows>(walk, args, id, 0);
+      kb = t.kb0;
+      kb1 = t.kb1;
+    }
+    float acc[128];
+#pragma unroll
+    for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+    for (; kb < kb1; ++kb, ++it) {
+      ok = ring.wait(it);
+      if (!ok) break;
+      const uint32_t tb = tq + (it % C::kBufs) * BN;
+      uint32_t v[2][32];
+      tmem_ld_32cols(tb, v[0]);
+      const float s = sc[(it % C::kSlots) * BN + half * 128 + r];
+      tmem_ld_wait();
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        if (ch < 3) tmem_ld_32cols(tb + (ch + 1) * 32, v[(ch + 1) & 1]);
+        else ring.buffer_read(it, lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) fma_acc(acc[ch * 32 + i], v[ch & 1][i], s);
+        if (ch < 3) tmem_ld_wait();
+      }
+      ring.scales_read(it, lane);
+    }
+    const Fp8Tile t = tile_at<BN, kRows>(walk, args, id, 0);
+    const int n = min(128, t.ncols - half * 128);   // live columns (may be negative)
+    if (ok && r < t.lanes && n > 0) {
+      const long long base = t.out + static_cast<long long>(r) * args.ldo + half * 128;
+      // this thread's row through its own shared memory, 256 bytes at a time
+      const int rounds = args.out_f32 ? 2 : 1;
+#pragma unroll
+      for (int round = 0; round < 2; ++round) {
+        if (round >= rounds) break;
+        bulk_wait_read();
+        if (args.out_f32) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float* a = acc + round * 64 + 4 * i;
+            *reinterpret_cast<float4*>(row + 16 * i) = make_float4(a[0], a[1], a[2], a[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float* a = acc + 8 * i;
+            *reinterpret_cast<uint4*>(row + 16 * i) = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                                 pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+          }
+        }
+        const int cols = args.out_f32 ? min(64, n - round * 64) : n;
+        if (cols <= 0) break;
+        if (args.out_vec) {
+          fence_async_smem();
+          if (args.out_f32)
+            bulk_store(static_cast<float*>(args.out) + base + round * 64, smem_u32(row), cols * 4);
+          else
+            bulk_store(static_cast<__nv_bfloat16*>(args.out) + base, smem_u32(row), cols * 2);
+          bulk_commit();
+        } else if (args.out_f32) {
+          for (int i = 0; i < cols; ++i)
+            static_cast<float*>(args.out)[base + round * 64 + i] = reinterpret_cast<const float*>(row)[i];
+        } else {
+          for (int i = 0; i < cols; ++i)
+            static_cast<__nv_bfloat16*>(args.out)[base + i] = reinterpret_cast<const __nv_bfloat16*>(row)[i];
+        }
+      }
+    }
+    __syncwarp();
+  }
+  bulk_wait();
+}
+
+// ---- epilogue of the other modes.  A TMEM read in the 16 x 256-bit shape gives a thread two
+// columns of four lanes per 8 columns, so that it needs two of their scales, not eight.
+template <int BN, int MODE>
+LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8Ring<BN, MODE>& ring, const float* sc,
+                            float* red, uint8_t* stage_out, uint32_t tmem, int id0, int step, int rank) {
+  using C = Fp8Cfg<BN, MODE>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = (warp - 4) >> 2;
+  const int tid = threadIdx.x & 127;                    // within the warpgroup
+  const int r = quad * 32 + (lane >> 2);                // lanes r, + 8, + 16, + 24 of the tile
+  const int c0 = half * C::kAcc, cl = (lane & 3) * 2;   // columns c0 + 8 g + cl, + 1
+  const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
+  constexpr int kChC = C::kAcc >= 64 ? 64 : 16;         // columns of one TMEM read
+  constexpr int kG = kChC / 8, kN = C::kAcc / kChC * 2;
+  uint8_t* so = stage_out + half * C::kOutBytes;
+  int it = 0;
+  bool ok = true;
+  for (int id = id0; ok && id < walk.total; id += step) {
+    // (the tile is worked out again for the stores: its registers are the accumulators' here)
+    int kb, kb1;
+    const float* ps = nullptr;   // wgrad: scale of this thread's first lane in the next block
+    int left = 0;                // lanes of the operand from there on
+    {
+      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
+      kb = t.kb0;
+      kb1 = t.kb1;
+      if (MODE == kWgrad) {
+        ps = args.ps + static_cast<long long>(kb) * args.k + t.p0 + r;
+        left = t.lanes - r;
+      }
+    }
+    // acc[g][j][u]: column u of group g's pair, lane 8 j + l / 4 of the warp's 32
+    float acc[C::kAcc / 8][4][2];
+#pragma unroll
+    for (int i = 0; i < C::kAcc; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] = 0.f;
+    float sp_next[4] = {};
+    if (MODE == kWgrad && kb < kb1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (8 * j < left) sp_next[j] = ps[8 * j];
+    }
+    for (; kb < kb1; ++kb, ++it) {
+      ok = ring.wait(it);
+      if (!ok) break;
+      const uint32_t tb = tq + (it % C::kBufs) * BN;
+      uint32_t v[2][kG * 4];
+      tmem_ld_frag(tb, v[0]);
+      float sp[4];
+      if (MODE == kWgrad) {
+        ps += args.k;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sp[j] = sp_next[j];
+          if (kb + 1 < kb1 && 8 * j < left) sp_next[j] = ps[8 * j];
+        }
+      }
+      const float* scs = sc + (it % C::kSlots) * BN + c0 + cl;
+      tmem_ld_wait();
+#pragma unroll
+      for (int ch = 0; ch < kN; ++ch) {   // 16 lanes x kChC columns: lane half ch % 2
+        const int h = ch & 1, g0 = (ch >> 1) * kG;
+        if (ch + 1 < kN)
+          tmem_ld_frag(tb + ((ch + 1) >> 1) * kChC + (((ch + 1) & 1) ? (16u << 16) : 0u), v[(ch + 1) & 1]);
+        else
+          ring.buffer_read(it, lane);
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          const float2 s2 = *reinterpret_cast<const float2*>(scs + (g0 + g) * 8);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t* w = &v[ch & 1][4 * g + 2 * q];
+            if (MODE == kWgrad) {
+              scale_in_place(w[0], sp[2 * h + q]);
+              scale_in_place(w[1], sp[2 * h + q]);
+            }
+            float(&d)[2] = acc[g0 + g][2 * h + q];
+            fma_acc(d[0], w[0], s2.x);
+            fma_acc(d[1], w[1], s2.y);
+          }
+        }
+        if (ch + 1 < kN) tmem_ld_wait();
+      }
+      ring.scales_read(it, lane);
+    }
+    if (MODE == kSplit) {
+      // one tile per cluster: the sums of ranks 1.. go to rank 0 (element i of thread x at
+      // i * 128 + x: threads beside each other, words beside each other)
+      if (rank > 0) {
+        cluster_wait();
+        const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * BN * 128 + tid), 0);
+#pragma unroll
+        for (int i = 0; i < C::kAcc; ++i) cluster_store(dst + i * 512, acc[i >> 3][(i >> 1) & 3][i & 1]);
+        cluster_arrive();
+        cluster_wait();
+      } else {
+        cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+        for (int q = 1; q < args.splits; ++q) {
+          const float* src = red + (q - 1) * BN * 128 + tid;
+#pragma unroll
+          for (int i = 0; i < C::kAcc; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] += src[i * 128];
+        }
+      }
+    }
+    const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
+    const int n = min(C::kAcc, t.ncols - c0);   // live columns (may be negative)
+    // (ok, rank and n are the same for the warpgroup)
+    if (!ok || rank != 0 || n <= 0 || (args.accumulate && t.kb0 == t.kb1)) continue;
+    const int lanes = min(128, t.lanes);
+    const long long base = t.out + static_cast<long long>(c0) * args.ldo;
+    const bool f32 = args.out_f32 || args.accumulate;   // (a bf16 sum is rounded once, after the addition)
+    if (!f32) {
+      // all columns, transposed on the way: column c is 256 bytes at so + 272 c
+      bulk_wait_read();
+      named_barrier(1 + half, 128);
+#pragma unroll
+      for (int g = 0; g < C::kAcc / 8; ++g) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[g][j][0], acc[g][j][1]);
+        stmatrix_x4_trans(smem_u32(so + (8 * g + (lane & 7)) * 272 + (quad * 4 + (lane >> 3)) * 16), w);
+      }
+      fence_async_smem();
+      named_barrier(1 + half, 128);
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + base;
+      if (args.out_vec) {
+        if (tid < n) {
+          bulk_store(o + static_cast<long long>(tid) * args.ldo, smem_u32(so + tid * 272), lanes * 2);
+          bulk_commit();
+        }
+      } else if (tid < lanes) {
+        for (int c = 0; c < n; ++c)
+          o[static_cast<long long>(c) * args.ldo + tid] = *reinterpret_cast<const __nv_bfloat16*>(so + c * 272 + tid * 2);
+      }
+    } else {
+      // kOutCols columns at a time: column c is 512 bytes at so + 528 c
+#pragma unroll
+      for (int round = 0; round < C::kAcc / C::kOutCols; ++round) {
+        const int here = min(C::kOutCols, n - round * C::kOutCols);
+        if (here <= 0) break;   // (the same for the warpgroup)
+        bulk_wait_read();
+        named_barrier(1 + half, 128);
+#pragma unroll
+        for (int g = 0; g < C::kOutCols / 8; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              *reinterpret_cast<float*>(so + (8 * g + cl + u) * 528 + (r + 8 * j) * 4) =
+                  acc[round * (C::kOutCols / 8) + g][j][u];
+        fence_async_smem();
+        named_barrier(1 + half, 128);
+        const long long o = base + static_cast<long long>(round * C::kOutCols) * args.ldo;
+        if (args.out_vec && args.out_f32) {
+          if (tid < here) {
+            float* d = static_cast<float*>(args.out) + o + static_cast<long long>(tid) * args.ldo;
+            if (args.accumulate) bulk_add(d, smem_u32(so + tid * 528), lanes * 4);
+            else bulk_store(d, smem_u32(so + tid * 528), lanes * 4);
+            bulk_commit();
+          }
+        } else if (tid < lanes) {
+          for (int c = 0; c < here; ++c) {
+            float v = *reinterpret_cast<const float*>(so + c * 528 + tid * 4);
+            const long long at = o + static_cast<long long>(c) * args.ldo + tid;
+            if (args.out_f32) {
+              float* d = static_cast<float*>(args.out) + at;
+              *d = args.accumulate ? *d + v : v;
+            } else {
+              __nv_bfloat16* d = static_cast<__nv_bfloat16*>(args.out) + at;
+              *d = __float2bfloat16_rn(__bfloat162float(*d) + v);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+  bulk_wait();
 }
 
 template <int BN, int MODE>
@@ -205,11 +548,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   float* red = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
   uint8_t* stage_out = reinterpret_cast<uint8_t*>(red) + C::kRedBytes;
-  float* sc = reinterpret_cast<float*>(stage_out + C::kOutBytes);   // [kSlots][BN]
-  int* start = reinterpret_cast<int*>(sc + C::kSlots * BN);         // [E + 1], then lo, hi
-  int* lo = start + kMaxGroups + 4;
-  int* hi = lo + kMaxGroups + 4;
-  uint64_t* full = reinterpret_cast<uint64_t*>(hi + kMaxGroups + 4);
+  float* sc = reinterpret_cast<float*>(stage_out + C::kOutBytes * (C::kEpiWarps / 4));   // [kSlots][BN]
+  int* start = reinterpret_cast<int*>(sc + C::kSlots * BN);                              // [E + 1]
+  uint64_t* full = reinterpret_cast<uint64_t*>(start + kMaxGroups + 4);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + C::kBufs;
@@ -243,32 +584,19 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   }
   griddep_enter();
 
-  // the groups: offsets are clamped into the rows there are, so that no table sends a load or a
-  // store out of range
-  Fp8Walk walk;
-  walk.start = start;
-  walk.lo = lo;
-  walk.hi = hi;
-  walk.E = args.E;
-  walk.lane_tiles = (args.lanes + 127) / 128;
-  walk.col_tiles = MODE == kWgrad ? (args.cols + BN - 1) / BN : 0;
-  constexpr int kUnit = MODE == kWgrad ? 128 : BN;   // rows of one unit of start[]
+  // start[]: exclusive prefix sum of the groups' units (row tiles, or blocks)
+  constexpr int kUnit = MODE == kWgrad || MODE == kRows ? 128 : BN;
   for (int e = threadIdx.x; e < args.E; e += C::kThreads) {
-    int l = 0, h = static_cast<int>(args.rows);
-    if (args.offsets != nullptr) {
-      const int cap = static_cast<int>(args.rows);
-      l = min(max(args.offsets[e], 0), cap);
-      h = min(max(args.offsets[e + 1], l), cap);
-    }
-    lo[e] = l;
-    hi[e] = h;
+    int lo, hi;
+    group_rows(args, e, lo, hi);
+    start[e] = (hi - lo + kUnit - 1) / kUnit;
   }
   __syncthreads();
-  if (warp == 0) {   // exclusive prefix sum of the groups' units, a run of groups per lane
+  if (warp == 0) {   // a run of groups per lane
     const int per = (args.E + 31) / 32, e0 = min(lane * per, args.E), e1 = min(e0 + per, args.E);
     const int cap = MODE == kWgrad ? static_cast<int>(args.rows / 128) : 0x7fffffff;
     int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += (hi[e] - lo[e] + kUnit - 1) / kUnit;
+    for (int e = e0; e < e1; ++e) sum += start[e];
     int run = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -278,8 +606,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
     const int tot = __shfl_sync(~0u, run, 31);
     run -= sum;
     for (int e = e0; e < e1; ++e) {
+      const int c = start[e];
       start[e] = min(run, cap);
-      run += (hi[e] - lo[e] + kUnit - 1) / kUnit;
+      run += c;
     }
     if (lane == 0) start[args.E] = min(tot, cap);
   }
@@ -287,7 +616,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  walk.total = (MODE == kWgrad ? args.E * walk.col_tiles : start[args.E]) * walk.lane_tiles;
+  Fp8Walk walk;
+  walk.start = start;
+  walk.E = args.E;
+  walk.others = MODE == kWgrad ? (args.k + 127) / 128 : MODE == kRows ? (args.n + BN - 1) / BN : (args.n + 127) / 128;
+  walk.cols = (args.n + BN - 1) / BN;
+  walk.total = (MODE == kWgrad ? args.E * walk.cols : start[args.E]) * walk.others;
   const int S = MODE == kSplit ? args.splits : 1;
   const int rank = MODE == kSplit ? static_cast<int>(blockIdx.x % S) : 0;
   const int id0 = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
@@ -295,11 +629,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   if (MODE == kSplit) cluster_arrive();   // every CTA of the cluster has started (waited for below)
 
   if (warp < 4) {
-  if constexpr (BN == 256) regs_dec<56>();
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---- TMA producer
-      // (narrow tiles: few rows, each weight is read about once)
+    if constexpr (BN == 256) regs_dec<56>();
+    if (warp == 0 && lane == 0) {
+      // ---- TMA producer (narrow tiles: few rows, each weight is read about once)
       const uint64_t pol_p = BN == 256 ? policy_evict_normal() : policy_evict_first();
       const uint64_t pol_q = policy_evict_normal();
       int it = 0;
@@ -317,20 +649,23 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
           }
           uint8_t* sp = smem + s * C::kStageBytes;
           mbar_arrive_expect_tx(&full[s], tx);
-          if (MODE == kWgrad) tma_load_2d_hint(sp, &tmP, &full[s], kb * 128, t.p0, pol_p);
-          else tma_load_3d_hint(sp, &tmP, &full[s], kb * 128, t.p0, t.e, pol_p);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d_hint(sp + C::kPBytes + b * C::kBox * 128, &tmQ, &full[s], kb * 128, t.q0 + b * C::kBox,
-                             pol_q);
+          if (MODE == kRows) {
+            tma_load_2d_hint(sp, &tmP, &full[s], kb * 128, t.p0, pol_p);
+            tma_load_3d_hint(sp + C::kPBytes, &tmQ, &full[s], kb * 128, t.q0, t.e, pol_q);
+          } else {
+            if (MODE == kWgrad) tma_load_2d_hint(sp, &tmP, &full[s], kb * 128, t.p0, pol_p);
+            else tma_load_3d_hint(sp, &tmP, &full[s], kb * 128, t.p0, t.e, pol_p);
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_hint(sp + C::kPBytes + b * C::kBox * 128, &tmQ, &full[s], kb * 128, t.q0 + b * C::kBox,
+                               pol_q);
+          }
         }
       }
       // every copy of this thread lands before the CTA leaves
       for (int j = max(0, it - C::kStages); j < it; ++j)
         if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, kDrainBudget))
           if (args.status) atomicOr(args.status, kErrDrain);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       // ---- MMA issuer: one block of 128 into one TMEM buffer
       int it = 0;
       bool ok = true;
@@ -339,8 +674,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
         const uint32_t idesc = idesc_f8(args.fmt_p, args.fmt_q, (t.ncols + 15) / 16 * 16);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % C::kStages, buf = it % C::kBufs;
-          if (!mbar_wait(&acc_empty[buf], ((it / C::kBufs) & 1) ^ 1, budget) ||
-              !mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
+          if (!mbar_wait(&full[s], (it / C::kStages) & 1, budget) ||
+              !mbar_wait(&acc_empty[buf], ((it / C::kBufs) & 1) ^ 1, budget)) {
             if (args.status) atomicOr(args.status, kErrWaitMma);
             ok = false;
             break;
@@ -351,240 +686,64 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             mma_f8(tmem + buf * BN, sw128_kmajor_desc(p0 + kk * 32), sw128_kmajor_desc(p0 + C::kPBytes + kk * 32),
                    idesc, kk > 0);
-          mma_commit(&empty[s]);
           mma_commit(&acc_full[buf]);
+          mma_commit(&empty[s]);
         }
       }
       mma_commit(mma_done);
-    }
-  } else if (warp == 2) {
-    // ---- column scales (times the lane block's scale where there is one), the loads of
-    // several blocks in flight at a time
-    constexpr int kPer = (BN + 31) / 32, kBatch = BN == 256 ? 2 : 4;
-    int it = 0;
-    bool ok = true;
-    for (int id = id0; ok && id < walk.total; id += step) {
-      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-      const float* q = args.qs + t.q0 + lane;
-      const float* p = MODE == kWgrad ? nullptr
-                                      : args.ps + (static_cast<long long>(t.e) * walk.lane_tiles + t.p0 / 128) *
-                                                      args.num_kb;
-      for (int kb = t.kb0; ok && kb < t.kb1; kb += kBatch) {
-        float v[kBatch][kPer], u[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const bool in = kb + j < t.kb1;
-          u[j] = MODE == kWgrad ? 1.f : (in ? p[kb + j] : 0.f);
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            v[j][i] = in && lane + 32 * i < t.ncols ? q[(kb + j) * args.ldq + 32 * i] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (!ok || kb + j >= t.kb1) break;
-          const int s = it % C::kSlots;
-          if (!mbar_wait(&sempty[s], ((it / C::kSlots) & 1) ^ 1, budget)) {
-            if (args.status) atomicOr(args.status, kErrWaitProducer);
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < BN) sc[s * BN + lane + 32 * i] = v[j][i] * u[j];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfull[s]);
-          ++it;
-        }
-      }
-    }
-  }
-  } else {
-    // ---- epilogue.  A TMEM read in the 16 x 256-bit shape gives a thread two columns of four
-    // lanes per 8 columns, so that it needs two of their scales, not eight: with a lane's whole
-    // row per thread every scale goes to every thread, and returning those from shared memory
-    // (128 bytes a cycle) takes twice the MMAs' time.
-    if constexpr (BN == 256) regs_inc<224>();
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    const int r = quad * 32 + (lane >> 2);                 // lanes r, + 8, + 16, + 24 of the tile
-    const int c0 = half * C::kCols, cl = (lane & 3) * 2;   // columns c0 + 8 g + cl, + 1
-    const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-    constexpr int kChC = C::kCols >= 64 ? 64 : 16;         // columns of one TMEM read
-    constexpr int kG = kChC / 8, kN = C::kCols / kChC * 2;
-    int it = 0;
-    bool ok = true;
-    for (int id = id0; ok && id < walk.total; id += step) {
-      // (the tile is worked out again for the stores: its registers are the accumulators' here)
-      int kb, kb1;
-      const float* ps = nullptr;   // wgrad: scale of this thread's first lane in the next block
-      int left = 0;                // lanes of the operand from there on
-      {
+    } else if (warp == 2) {
+      // ---- scales, the loads of several blocks in flight at a time.  kRows: as[row] ws[half] for
+      // the 128 lanes of each column half; kCols, kSplit: as ws of each column; wgrad: of each column
+      constexpr int kPer = (BN + 31) / 32, kBatch = BN == 256 ? 2 : 4;
+      int it = 0;
+      bool ok = true;
+      for (int id = id0; ok && id < walk.total; id += step) {
         const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-        kb = t.kb0;
-        kb1 = t.kb1;
-        if (MODE == kWgrad) {
-          ps = args.ps + static_cast<long long>(kb) * args.lanes + t.p0 + r;
-          left = args.lanes - t.p0 - r;
-        }
-      }
-      // acc[g][j][u]: column u of group g's pair, lane 8 j + l / 4 of the warp's 32
-      float acc[C::kCols / 8][4][2];
+        const float* q = MODE == kRows ? args.ps + t.p0 + lane : args.qs + t.q0 + lane;
+        const long long ldq = MODE == kWgrad ? args.n : args.rows;
+        const int live = MODE == kRows ? t.lanes : t.ncols;
+        const int nb = (args.n + 127) / 128;   // the weight's 128 x 128 blocks
+        const int b0 = MODE == kRows ? t.q0 / 128 : t.p0 / 128;
+        const float* w = (MODE == kRows ? args.qs : args.ps) + (static_cast<long long>(t.e) * nb + b0) * args.num_kb;
+        const bool two = MODE == kRows && b0 + 1 < nb;
+        for (int kb = t.kb0; ok && kb < t.kb1; kb += kBatch) {
+          float v[kBatch][kPer], u[kBatch][2];
 #pragma unroll
-      for (int i = 0; i < C::kCols; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] = 0.f;
-      float sp_next[4] = {};
-      if (MODE == kWgrad && kb < kb1) {
+          for (int j = 0; j < kBatch; ++j) {
+            const bool in = kb + j < t.kb1;
+            u[j][0] = MODE == kWgrad ? 1.f : (in ? w[kb + j] : 0.f);
+            u[j][1] = two && in ? w[args.num_kb + kb + j] : u[j][0];
+            constexpr int kOwn = MODE == kRows ? 4 : kPer;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (8 * j < left) sp_next[j] = ps[8 * j];
-      }
-      uint32_t v[2][kG * 4];
-      // waits for block `i` of the ring and reads its first columns
-      const auto begin = [&](int i) {
-        const int buf = i % C::kBufs, s = i % C::kSlots;
-        if (!mbar_wait(&sfull[s], (i / C::kSlots) & 1, budget) ||
-            !mbar_wait(&acc_full[buf], (i / C::kBufs) & 1, budget)) {
-          if (args.status) atomicOr(args.status, kErrWaitEpilogue);
-          return false;
-        }
-        tc_fence_after();
-        tmem_ld_frag(tq + buf * BN, v[0]);
-        return true;
-      };
-      for (; kb < kb1; ++kb, ++it) {
-        ok = begin(it);
-        if (!ok) break;
-        tmem_ld_wait();
-        float sp[4];
-        if (MODE == kWgrad) {
-          ps += args.lanes;
+            for (int i = 0; i < kOwn; ++i)
+              v[j][i] = in && lane + 32 * i < live ? q[(kb + j) * ldq + 32 * i] : 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sp[j] = sp_next[j];
-            if (kb + 1 < kb1 && 8 * j < left) sp_next[j] = ps[8 * j];
+            for (int i = kOwn; i < kPer; ++i) v[j][i] = v[j][i - kOwn];
           }
-        }
-        const int s = it % C::kSlots;
-        const float* scs = sc + s * BN + c0 + cl;
 #pragma unroll
-        for (int ch = 0; ch < kN; ++ch) {   // 16 lanes x kChC columns: lane half ch % 2
-          const int h = ch & 1, g0 = (ch >> 1) * kG;
-          // the next read is under way while these columns are added: of this block, or, every
-          // column of its buffer having been read, the first of the next block's
-          if (ch + 1 < kN) {
-            tmem_ld_frag(tq + (it % C::kBufs) * BN + ((ch + 1) >> 1) * kChC + (((ch + 1) & 1) ? (16u << 16) : 0u),
-                         v[(ch + 1) & 1]);
-          } else {
-            tc_fence_before();
+          for (int j = 0; j < kBatch; ++j) {
+            if (!ok || kb + j >= t.kb1) break;
+            const int s = it % C::kSlots;
+            if (!mbar_wait(&sempty[s], ((it / C::kSlots) & 1) ^ 1, budget)) {
+              if (args.status) atomicOr(args.status, kErrWaitProducer);
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (lane + 32 * i < BN) sc[s * BN + lane + 32 * i] = v[j][i] * u[j][i / 4 & 1];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[it % C::kBufs]);
-          }
-#pragma unroll
-          for (int g = 0; g < kG; ++g) {
-            const float2 s2 = *reinterpret_cast<const float2*>(scs + (g0 + g) * 8);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t *w = &v[ch & 1][4 * g + 2 * q];
-              if (MODE == kWgrad) {
-                scale_in_place(w[0], sp[2 * h + q]);
-                scale_in_place(w[1], sp[2 * h + q]);
-              }
-              float(&d)[2] = acc[g0 + g][2 * h + q];
-              fma_acc(d[0], w[0], s2.x);
-              fma_acc(d[1], w[1], s2.y);
-            }
-          }
-          if (ch + 1 < kN) tmem_ld_wait();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[s]);
-      }
-      if (MODE == kSplit) {
-        // one tile per cluster: the accumulators of ranks 1.. go to rank 0 (element i of thread x
-        // at i * 128 + x: threads beside each other, words beside each other)
-        const int tid = threadIdx.x - 128;
-        if (rank > 0) {
-          cluster_wait();
-          const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * BN * 128 + tid), 0);
-#pragma unroll
-          for (int i = 0; i < C::kCols; ++i) cluster_store(dst + i * 512, acc[i >> 3][(i >> 1) & 3][i & 1]);
-          cluster_arrive();
-          cluster_wait();
-        } else {
-          cluster_wait();
-          cluster_arrive();
-          cluster_wait();
-          for (int q = 1; q < S; ++q) {
-            const float* src = red + (q - 1) * BN * 128 + tid;
-#pragma unroll
-            for (int i = 0; i < C::kCols; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] += src[i * 128];
+            if (lane == 0) mbar_arrive(&sfull[s]);
+            ++it;
           }
         }
-      }
-      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-      if (!ok || rank != 0 || (args.accumulate && t.kb0 == t.kb1)) continue;
-      const int n = min(C::kCols, t.ncols - c0);   // live columns (may be negative)
-      if (!args.out_f32 && !args.accumulate) {
-        // bf16: 16 columns at a time through this warp's shared memory, transposed there: a store
-        // instruction then writes 64 bytes (32 lanes' values) of each of 8 columns (rows of the
-        // output).  16-byte chunk i of column c is at place i ^ (c / 2 % 4): no bank conflicts
-        // either way.
-        uint8_t* so = stage_out + (warp - 4) * C::kStageCols * 64;
-        const int left_n = args.lanes - t.p0 - quad * 32 - (lane & 3) * 8;   // of this thread's chunk
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + t.out + quad * 32 + (lane & 3) * 8 +
-                           static_cast<long long>(c0 + (lane >> 2)) * args.lanes;
-#pragma unroll
-        for (int g = 0; g < C::kCols / 8; g += 2) {
-          if (8 * g >= n) break;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[g + u][j][0], acc[g + u][j][1]);
-            const int c = 8 * u + (lane & 7), chunk = lane >> 3;
-            stmatrix_x4_trans(smem_u32(so + c * 64 + ((chunk ^ ((c >> 1) & 3)) << 4)), w);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int c = 8 * u + (lane >> 2), chunk = lane & 3;
-            const uint4 q = *reinterpret_cast<const uint4*>(so + c * 64 + ((chunk ^ ((c >> 1) & 3)) << 4));
-            if (8 * g + c < n && left_n > 0) {
-              if (args.out_vec) {
-                *reinterpret_cast<uint4*>(o) = q;
-              } else {
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (i < left_n) o[i] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1))));
-              }
-            }
-            o += 8LL * args.lanes;
-          }
-          __syncwarp();
-        }
-      } else {
-        // fp32: a store instruction writes 8 lanes' words of 4 columns: whole 32-byte sectors
-#pragma unroll
-        for (int g = 0; g < C::kCols / 8; ++g)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int c = 8 * g + cl + u;
-            if (c >= n) continue;
-            const long long base = t.out + static_cast<long long>(c0 + c) * args.lanes + r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (t.p0 + r + 8 * j >= args.lanes) continue;
-              const float val = acc[g][j][u];
-              if (args.out_f32) {
-                float* o = static_cast<float*>(args.out) + base + 8 * j;
-                *o = args.accumulate ? *o + val : val;
-              } else {
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + base + 8 * j;
-                *o = __float2bfloat16_rn(__bfloat162float(*o) + val);
-              }
-            }
-          }
       }
     }
+  } else {
+    if constexpr (BN == 256) regs_inc<224>();
+    const Fp8Ring<BN, MODE> ring = {acc_full, acc_empty, sfull, sempty, args.status, budget};
+    if constexpr (MODE == kRows) epilogue_rows<BN>(args, walk, ring, sc, stage_out, tmem, id0, step);
+    else epilogue_cols<BN, MODE>(args, walk, ring, sc, red, stage_out, tmem, id0, step, rank);
   }
   if (MODE == kSplit) {
     // the cluster barriers count every thread; warps (and CTAs) without a tile pass them here
@@ -625,6 +784,7 @@ cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, const Fp8Args
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int kSms = 152;
+constexpr int kRowsMin = 65;
 
 }  // namespace
 }  // namespace lmoe
@@ -652,43 +812,50 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
 
   Fp8Args g = {};
   g.rows = c->rows;
-  g.lanes = c->N;
+  g.n = c->N;
+  g.k = c->K;
   g.num_kb = (c->K + 127) / 128;
   g.E = c->n_experts;
   g.offsets = offsets;
-  g.ps = w_scales;
-  g.qs = a_scales;
-  g.ldq = c->rows;
   g.out = out;
+  g.ldo = c->N;
   g.out_f32 = c->out_dtype == LMOE_F32;
-  g.out_vec = aligned(out, 16) && c->N % 8 == 0;
-  g.fmt_p = c->b_format;
-  g.fmt_q = c->a_format;
+  g.out_vec = aligned(out, 16) && c->N % (g.out_f32 ? 4 : 8) == 0;
   g.status = status;
   g.budget = kDefaultWaitBudget;
-  // Column tile: the widest that the rows of an expert fill.  Up to 16 rows in all: 16.  Then by
-  // the mean rows of an expert.
+  g.splits = 1;
+  // Up to 16 rows in all: 16-column tiles; then, while an expert has fewer than kRowsMin rows on
+  // average, 64; else rows as lanes.
   const long long live = c->n_experts < c->rows ? c->n_experts : c->rows;
-  const int bn = c->rows <= 16 ? 16 : (c->rows <= 64 || c->rows / c->n_experts < 48) ? 64 : 256;
-  const long long tiles = ((c->rows + bn - 1) / bn + (live - 1)) * wt;   // at most
+  const bool by_rows = c->rows / live >= kRowsMin;
+  const int bn = by_rows ? 256 : c->rows <= 16 ? 16 : 64;
   const unsigned long long K = c->K, N = c->N;
-  CUtensorMap tp, tq;
-  const unsigned long long pd[3] = {K, N, static_cast<unsigned long long>(c->n_experts)}, pst[2] = {K, K * N};
-  const unsigned pbox[3] = {128, 128, 1};
-  const unsigned long long qd[2] = {K, static_cast<unsigned long long>(c->rows)}, qst[1] = {K};
-  const unsigned qbox[2] = {128, static_cast<unsigned>(bn < 64 ? bn : 64)};
-  if (!encode_u8_swizzled(&tp, w, 3, pd, pst, pbox) || !encode_u8_swizzled(&tq, a, 2, qd, qst, qbox))
+  const unsigned long long wd[3] = {K, N, static_cast<unsigned long long>(c->n_experts)}, wst[2] = {K, K * N};
+  const unsigned long long ad[2] = {K, static_cast<unsigned long long>(c->rows)}, ast[1] = {K};
+  const unsigned wbox[3] = {128, by_rows ? 256u : 128u, 1};
+  const unsigned abox[2] = {128, by_rows ? 128u : static_cast<unsigned>(bn)};
+  CUtensorMap tw, ta;
+  if (!encode_u8_swizzled(&tw, w, 3, wd, wst, wbox) || !encode_u8_swizzled(&ta, a, 2, ad, ast, abox))
     return LMOE_ERR_CUDA;
-  // Few tiles: split the reduction among the CTAs of a cluster, at least four blocks each.
-  int split = 1;
-  if (bn < 256)
-    while (split < (bn == 16 ? 8 : 4) && tiles * split * 2 <= kSms && g.num_kb / (split * 2) >= 4) split *= 2;
-  g.splits = split;
   cudaError_t e;
-  if (split > 1) e = bn == 16 ? launch_one<16, kSplit>(tp, tq, g, tiles, stream) : launch_one<64, kSplit>(tp, tq, g, tiles, stream);
-  else if (bn == 16) e = launch_one<16, kMatmul>(tp, tq, g, tiles, stream);
-  else if (bn == 64) e = launch_one<64, kMatmul>(tp, tq, g, tiles, stream);
-  else e = launch_one<256, kMatmul>(tp, tq, g, tiles, stream);
+  if (by_rows) {
+    g.ps = a_scales;
+    g.qs = w_scales;
+    g.fmt_p = c->a_format;
+    g.fmt_q = c->b_format;
+    const long long tiles = ((c->rows + 127) / 128 + live - 1) * ((c->N + 255) / 256);   // at most
+    e = launch_one<256, kRows>(ta, tw, g, tiles, stream);
+  } else {
+    g.ps = w_scales;
+    g.qs = a_scales;
+    g.fmt_p = c->b_format;
+    g.fmt_q = c->a_format;
+    const long long tiles = ((c->rows + bn - 1) / bn + live - 1) * wt;   // at most
+    // Few tiles: split the reduction among the CTAs of a cluster, at least four blocks each.
+    while (g.splits < (bn == 16 ? 8 : 4) && tiles * g.splits * 2 <= kSms && g.num_kb / (g.splits * 2) >= 4) g.splits *= 2;
+    if (g.splits > 1) e = bn == 16 ? launch_one<16, kSplit>(tw, ta, g, tiles, stream) : launch_one<64, kSplit>(tw, ta, g, tiles, stream);
+    else e = bn == 16 ? launch_one<16, kCols>(tw, ta, g, tiles, stream) : launch_one<64, kCols>(tw, ta, g, tiles, stream);
+  }
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
@@ -718,16 +885,16 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
 
   Fp8Args g = {};
   g.rows = c->rows;
-  g.lanes = c->K;
-  g.cols = c->N;
+  g.n = c->N;
+  g.k = c->K;
   g.E = c->n_experts;
   g.offsets = offsets;
   g.ps = x_scales;
   g.qs = dy_scales;
-  g.ldq = c->N;
   g.out = dw;
+  g.ldo = c->K;
   g.out_f32 = c->out_dtype == LMOE_F32;
-  g.out_vec = aligned(dw, 16) && c->K % 8 == 0;
+  g.out_vec = aligned(dw, 16) && c->K % (g.out_f32 ? 4 : 8) == 0;
   g.accumulate = c->accumulate;
   g.fmt_p = c->b_format;
   g.fmt_q = c->a_format;
