@@ -23,7 +23,7 @@
 //           memory, which adds them in rank order.
 //   kWgrad  rows of x_t are lanes, rows of dy_t columns; both have scales of their own.
 //
-// Roles of a CTA: warp 0 lane 0 TMA producer; warp 1 lane 0 MMA issuer (warp 1 owns the TMEM);
+// Roles of a CTA: warp 0 lane 0 TMA producer; lane 0 of warps 1 and 3 MMA issuers (warp 1 owns the TMEM);
 // warp 2 stages the scales of each block in shared memory; warps 4.. epilogue, warp w on TMEM lanes
 // 32 (w % 4) .. (and column half (w - 4) / 4 with eight of them).  The epilogue leaves a finished
 // tile in shared memory, from where bulk copies store it while the next tile is computed.
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
       mbar_init(&sfull[s], 1);
       mbar_init(&sempty[s], C::kEpiWarps);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     fence_mbar_init();
     prefetch_tmap(&tmP);
     prefetch_tmap(&tmQ);
@@ -665,14 +665,19 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
       for (int j = max(0, it - C::kStages); j < it; ++j)
         if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, kDrainBudget))
           if (args.status) atomicOr(args.status, kErrDrain);
-    } else if (warp == 1 && lane == 0) {
-      // ---- MMA issuer: one block of 128 into one TMEM buffer
+    } else if ((warp == 1 || warp == 3) && lane == 0) {
+      // ---- MMA issuers: one block of 128 into one TMEM buffer, warp 1 the even blocks of the ring,
+      // warp 3 the odd ones.  Issuing a block's MMAs and commits holds a thread for most of the
+      // time they take, and its waits and arithmetic for the next one take 400 cycles more, in
+      // which the tensor cores would run dry; so the other thread does its own meanwhile.
+      const int mine = warp >> 1;
       int it = 0;
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
         const uint32_t idesc = idesc_f8(args.fmt_p, args.fmt_q, (t.ncols + 15) / 16 * 16);
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const int end = it + (t.kb1 - t.kb0);
+        for (it += (it ^ mine) & 1; it < end; it += 2) {
           const int s = it % C::kStages, buf = it % C::kBufs;
           if (!mbar_wait(&full[s], (it / C::kStages) & 1, budget) ||
               !mbar_wait(&acc_empty[buf], ((it / C::kBufs) & 1) ^ 1, budget)) {
@@ -682,13 +687,14 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
           }
           tc_fence_after();
           const uint32_t p0 = smem_u32(smem + s * C::kStageBytes);
+          const uint64_t pd = sw128_kmajor_desc(p0), qd = sw128_kmajor_desc(p0 + C::kPBytes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8(tmem + buf * BN, sw128_kmajor_desc(p0 + kk * 32), sw128_kmajor_desc(p0 + C::kPBytes + kk * 32),
-                   idesc, kk > 0);
+          for (int kk = 0; kk < 4; ++kk)   // 32 bytes on: 2 in the descriptors' 16-byte addresses
+            mma_f8(tmem + buf * BN, pd + 2 * kk, qd + 2 * kk, idesc, kk > 0);
           mma_commit(&acc_full[buf]);
           mma_commit(&empty[s]);
         }
+        it = end;
       }
       mma_commit(mma_done);
     } else if (warp == 2) {
