@@ -16,6 +16,10 @@
 // Which operand is the MMA's 128 lanes ("lane operand") and which its columns:
 //   kRows   rows of a are lanes, rows of w columns (128 x 256 tiles): many rows per expert.  A thread
 //           holds one lane, so its scale as ws is one register for 128 columns.
+//   kPair   kRows by two SMs: a cluster of two CTAs computes 256 x 256, each its 128 rows, and each
+//           loads half of the columns, which the tensor cores of both read (cta_group::2).  An SM takes
+//           in about 57 bytes a cycle: 860 cycles for a block's 48 KB, 575 for the pair's 32 KB each,
+//           beside 512 cycles of MMAs.
 //   kCols   rows of w are lanes, rows of a columns: the column count is any multiple of 16, so an
 //           expert with 20 rows costs 32 columns, not a 128-row tile, and one token costs 16.
 //   kSplit  kCols where the tiles are few (a few tokens): a cluster of S CTAs computes one tile,
@@ -34,7 +38,8 @@
 namespace lmoe {
 namespace {
 
-enum Fp8Mode : int { kCols = 0, kWgrad = 1, kSplit = 2, kRows = 3 };
+enum Fp8Mode : int { kCols = 0, kWgrad = 1, kSplit = 2, kRows = 3, kPair = 4 };
+constexpr bool by_rows(int mode) { return mode == kRows || mode == kPair; }
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSplit = 8;
 
@@ -62,7 +67,8 @@ struct Fp8Cfg {
   static constexpr int kAcc = BN * 4 / kEpiWarps;   // accumulator columns of one thread's warpgroup
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kPBytes = 128 * 128;
-  static constexpr int kQBytes = BN * 128;
+  static constexpr int kHalves = MODE == kPair ? 2 : 1;   // column halves with barriers of their own
+  static constexpr int kQBytes = BN * 128 / kHalves;      // (a CTA of a pair holds half of each)
   static constexpr int kStageBytes = kPBytes + kQBytes;
   static constexpr int kBox = MODE == kRows ? 256 : BN < 64 ? BN : 64;   // rows of a column-operand box
   static constexpr int kSlots = 8;                    // staged scale blocks
@@ -73,21 +79,25 @@ struct Fp8Cfg {
   // output staging of a warpgroup: kAcc columns of 128 bf16, or kOutCols of 128 fp32 at a time (kRows:
   // 128 rows of 128 bf16 or of 64 fp32), each with 16 bytes of padding against bank conflicts
   static constexpr int kOutCols = kAcc >= 64 ? kAcc / 2 : kAcc;
-  static constexpr int kOutBytes = MODE == kRows ? 128 * 272 : kAcc * 272 > kOutCols * 528 ? kAcc * 272 : kOutCols * 528;
+  static constexpr int kOutBytes = by_rows(MODE) ? 128 * 272 : kAcc * 272 > kOutCols * 528 ? kAcc * 272 : kOutCols * 528;
   static constexpr int kTableBytes = (kMaxGroups + 4) * 4;
   static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kOutBytes * (kEpiWarps / 4) + kTableBytes + 512 + 1024;
   static constexpr int kStagesFit = (227 * 1024 - kFixed) / kStageBytes;
-  static constexpr int kStages = kStagesFit > 11 ? 11 : kStagesFit;
+  // an odd number of stages, no more than the TMEM buffers, would break the MMA issuers' waits
+  static constexpr int kStagesMost = kStagesFit > 11 ? 11 : kStagesFit;
+  static constexpr int kStages = kStagesMost % 2 && kStagesMost <= kBufs ? kStagesMost - 1 : kStagesMost;
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
   static_assert(kStages >= 3, "pipeline depth");
-  static_assert((2 * kStages + 2 * kBufs + 2 * kSlots + 1) * 8 + 8 <= 512, "barriers");
-  static_assert((BN == 256) == (MODE == kRows || MODE == kWgrad), "tile widths");
+  static_assert(MODE == kPair || ((kStages % 2 == 0 || kStages > kBufs) && kBufs % 2 == 0), "two MMA issuers");
+  static_assert((2 * kStages + 2 * kBufs * kHalves + 2 * kSlots + 1) * 8 + 8 <= 512, "barriers");
+  static_assert((BN == 256) == (by_rows(MODE) || MODE == kWgrad), "tile widths");
 };
 
 // Instruction descriptor of kind::f8f6f4: D fp32 ([4,6) = 1), formats at [7,10) and [10,13),
 // both operands K-major, N >> 3 at [17,23), M >> 4 at [24,29).
-LMOE_DEV uint32_t idesc_f8(uint32_t fa, uint32_t fb, int n) {
-  return (1u << 4) | (fa << 7) | (fb << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+LMOE_DEV uint32_t idesc_f8(uint32_t fa, uint32_t fb, int m, int n) {
+  return (1u << 4) | (fa << 7) | (fb << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
 }
 LMOE_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -96,6 +106,57 @@ LMOE_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// ---- the same by the pair of CTAs of a cluster of two.  Issued in CTA 0: lanes 0..127 are CTA 0's A
+// rows and accumulators, 128..255 CTA 1's; each CTA holds half of B's rows.
+LMOE_DEV void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrives on the barrier of both CTAs
+LMOE_DEV void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+LMOE_DEV void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+               : "memory");
+}
+LMOE_DEV void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+LMOE_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// loads into this CTA; bar: a shared::cluster address, of either CTA of the pair
+LMOE_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+LMOE_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+LMOE_DEV void mbar_arrive_at(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// (of the memory operations before it only the TMEM reads matter, which are complete)
+LMOE_DEV void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 LMOE_DEV void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
                                uint64_t policy) {
@@ -107,16 +168,12 @@ LMOE_DEV void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, i
 }
 // 16 lanes x 8 N columns: thread l gets, per 8 columns, columns 2 (l % 4), + 1 of lanes l / 4
 // (registers 0, 1) and l / 4 + 8 (registers 2, 3).
-LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
@@ -124,12 +181,31 @@ LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-// d += (value read from TMEM) * s, and (value) *= s: volatile, so that the compiler keeps them
-// behind the wait for the read that the value comes from.
+// d += (value read from TMEM) * s: volatile, so that the compiler keeps it behind the wait for the
+// read that the value comes from.
 LMOE_DEV void fma_acc(float& d, uint32_t v, float s) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "r"(v), "f"(s));
 }
-LMOE_DEV void scale_in_place(uint32_t& v, float s) { asm volatile("mul.rn.f32 %0, %0, %1;" : "+r"(v) : "f"(s)); }
+// the same for two neighbouring columns, and scaled by p as well: d += (v p) s
+LMOE_DEV void fma_pair(uint64_t& d, uint32_t v0, uint32_t v1, uint64_t s) {
+  asm volatile("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+               : "+l"(d)
+               : "r"(v0), "r"(v1), "l"(s));
+}
+LMOE_DEV void fma_pair(uint64_t& d, uint32_t v0, uint32_t v1, uint64_t p, uint64_t s) {
+  asm volatile(
+      "{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\t"
+      "mul.rn.f32x2 t, t, %3;\n\t"
+      "fma.rn.f32x2 %0, t, %4, %0;\n\t}"
+      : "+l"(d)
+      : "r"(v0), "r"(v1), "l"(p), "l"(s));
+}
+LMOE_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+LMOE_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
 // Stores four 8 x 8 matrices of 16-bit values transposed: thread l names the 16-byte row l % 8
 // of matrix l / 8; matrix m's elements (row t / 4, columns 2 (t % 4), + 1) are thread t's r[m].
 LMOE_DEV void stmatrix_x4_trans(uint32_t saddr, const uint32_t (&r)[4]) {
@@ -190,7 +266,7 @@ struct Fp8Walk {
 };
 struct Fp8Tile {
   int e, p0, q0, ncols, lanes, kb0, kb1;   // lanes, ncols: live ones
-  long long out;   // kRows: element offset of (first lane, first column), else of (column, lane)
+  long long out;   // kRows, kPair: element offset of (first lane, first column), else of (column, lane)
 };
 
 template <int BN, int MODE>
@@ -222,8 +298,8 @@ LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
   group_rows(a, l, lo, hi);
   t.kb0 = 0;
   t.kb1 = a.num_kb;
-  if (MODE == kRows) {
-    t.p0 = lo + rt * 128;
+  if (by_rows(MODE)) {
+    t.p0 = lo + (MODE == kPair ? rt * 256 + rank * 128 : rt * 128);
     t.q0 = ot * BN;
     t.lanes = hi - t.p0;
     t.ncols = min(BN, a.n - t.q0);
@@ -245,13 +321,15 @@ LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
 // What an epilogue thread needs to wait for the blocks of its tile.
 template <int BN, int MODE>
 struct Fp8Ring {
-  uint64_t *acc_full, *acc_empty, *sfull, *sempty;
+  using C = Fp8Cfg<BN, MODE>;
+  uint64_t *acc_full, *sfull, *sempty;   // acc_full: of this thread's column half
+  uint32_t acc_empty;                    // the same; kPair: shared::cluster address in CTA 0
   unsigned* status;
   long long budget;
   LMOE_DEV bool wait(int it) const {
-    using C = Fp8Cfg<BN, MODE>;
     if (mbar_wait(&sfull[it % C::kSlots], (it / C::kSlots) & 1, budget) &&
-        mbar_wait(&acc_full[it % C::kBufs], (it / C::kBufs) & 1, budget)) {
+        mbar_wait(&acc_full[it % C::kBufs * C::kHalves], (it / C::kBufs) & 1, budget)) {
+      __syncwarp();   // (the TMEM reads that follow are the whole warp's)
       tc_fence_after();
       return true;
     }
@@ -262,19 +340,23 @@ struct Fp8Ring {
   LMOE_DEV void buffer_read(int it, int lane) const {
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&acc_empty[it % Fp8Cfg<BN, MODE>::kBufs]);
+    if (lane == 0) {
+      const uint32_t a = acc_empty + it % C::kBufs * C::kHalves * 8;
+      if constexpr (MODE == kPair) mbar_arrive_cluster(a);
+      else mbar_arrive_at(a);
+    }
   }
   LMOE_DEV void scales_read(int it, int lane) const {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sempty[it % Fp8Cfg<BN, MODE>::kSlots]);
+    if (lane == 0) mbar_arrive(&sempty[it % C::kSlots]);
   }
 };
 
-// ---- epilogue of kRows: a thread owns lane (row) r and 128 columns
-template <int BN>
-LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8Ring<BN, kRows>& ring, const float* sc,
-                            uint8_t* stage_out, uint32_t tmem, int id0, int step) {
-  using C = Fp8Cfg<BN, kRows>;
+// ---- epilogue of kRows and kPair: a thread owns lane (row) r and 128 columns
+template <int BN, int MODE>
+LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8Ring<BN, MODE>& ring, const float* sc,
+                            uint8_t* stage_out, uint32_t tmem, int id0, int step, int rank) {
+  using C = Fp8Cfg<BN, MODE>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
   const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
@@ -285,7 +367,7 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
     // (the tile is worked out again for the stores: its registers are the accumulators' here)
     int kb, kb1;
     {
-      const Fp8Tile t = tile_at<BN, kRows>(walk, args, id, 0);
+      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
       kb = t.kb0;
       kb1 = t.kb1;
     }
@@ -310,7 +392,7 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
       }
       ring.scales_read(it, lane);
     }
-    const Fp8Tile t = tile_at<BN, kRows>(walk, args, id, 0);
+    const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
     const int n = min(128, t.ncols - half * 128);   // live columns (may be negative)
     if (ok && r < t.lanes && n > 0) {
       const long long base = t.out + static_cast<long long>(r) * args.ldo + half * 128;
@@ -369,7 +451,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
   const int r = quad * 32 + (lane >> 2);                // lanes r, + 8, + 16, + 24 of the tile
   const int c0 = half * C::kAcc, cl = (lane & 3) * 2;   // columns c0 + 8 g + cl, + 1
   const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-  constexpr int kChC = C::kAcc >= 64 ? 64 : 16;         // columns of one TMEM read
+  constexpr int kChC = C::kAcc >= 32 ? 32 : 16;         // columns of one TMEM read
   constexpr int kG = kChC / 8, kN = C::kAcc / kChC * 2;
   uint8_t* so = stage_out + half * C::kOutBytes;
   int it = 0;
@@ -388,10 +470,10 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         left = t.lanes - r;
       }
     }
-    // acc[g][j][u]: column u of group g's pair, lane 8 j + l / 4 of the warp's 32
-    float acc[C::kAcc / 8][4][2];
+    // acc[g][j]: the column pair of group g, lane 8 j + l / 4 of the warp's 32
+    uint64_t acc[C::kAcc / 8][4];
 #pragma unroll
-    for (int i = 0; i < C::kAcc; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] = 0.f;
+    for (int i = 0; i < C::kAcc / 2; ++i) acc[i >> 2][i & 3] = 0;
     float sp_next[4] = {};
     if (MODE == kWgrad && kb < kb1) {
 #pragma unroll
@@ -404,12 +486,12 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
       const uint32_t tb = tq + (it % C::kBufs) * BN;
       uint32_t v[2][kG * 4];
       tmem_ld_frag(tb, v[0]);
-      float sp[4];
+      uint64_t sp[4], s2[kG];
       if (MODE == kWgrad) {
         ps += args.k;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sp[j] = sp_next[j];
+          sp[j] = pack2(sp_next[j], sp_next[j]);
           if (kb + 1 < kb1 && 8 * j < left) sp_next[j] = ps[8 * j];
         }
       }
@@ -422,21 +504,18 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
           tmem_ld_frag(tb + ((ch + 1) >> 1) * kChC + (((ch + 1) & 1) ? (16u << 16) : 0u), v[(ch + 1) & 1]);
         else
           ring.buffer_read(it, lane);
+        if (h == 0) {
 #pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          const float2 s2 = *reinterpret_cast<const float2*>(scs + (g0 + g) * 8);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t* w = &v[ch & 1][4 * g + 2 * q];
-            if (MODE == kWgrad) {
-              scale_in_place(w[0], sp[2 * h + q]);
-              scale_in_place(w[1], sp[2 * h + q]);
-            }
-            float(&d)[2] = acc[g0 + g][2 * h + q];
-            fma_acc(d[0], w[0], s2.x);
-            fma_acc(d[1], w[1], s2.y);
-          }
+          for (int g = 0; g < kG; ++g) s2[g] = *reinterpret_cast<const uint64_t*>(scs + (g0 + g) * 8);
         }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            const uint32_t* w = &v[ch & 1][4 * g + 2 * q];
+            if (MODE == kWgrad) fma_pair(acc[g0 + g][2 * h + q], w[0], w[1], sp[2 * h + q], s2[g]);
+            else fma_pair(acc[g0 + g][2 * h + q], w[0], w[1], s2[g]);
+          }
         if (ch + 1 < kN) tmem_ld_wait();
       }
       ring.scales_read(it, lane);
@@ -448,7 +527,12 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         cluster_wait();
         const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * BN * 128 + tid), 0);
 #pragma unroll
-        for (int i = 0; i < C::kAcc; ++i) cluster_store(dst + i * 512, acc[i >> 3][(i >> 1) & 3][i & 1]);
+        for (int i = 0; i < C::kAcc / 2; ++i) {
+          float x, y;
+          unpack2(acc[i >> 2][i & 3], x, y);
+          cluster_store(dst + 2 * i * 512, x);
+          cluster_store(dst + (2 * i + 1) * 512, y);
+        }
         cluster_arrive();
         cluster_wait();
       } else {
@@ -458,7 +542,11 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         for (int q = 1; q < args.splits; ++q) {
           const float* src = red + (q - 1) * BN * 128 + tid;
 #pragma unroll
-          for (int i = 0; i < C::kAcc; ++i) acc[i >> 3][(i >> 1) & 3][i & 1] += src[i * 128];
+          for (int i = 0; i < C::kAcc / 2; ++i) {
+            float x, y;
+            unpack2(acc[i >> 2][i & 3], x, y);
+            acc[i >> 2][i & 3] = pack2(x + src[2 * i * 128], y + src[(2 * i + 1) * 128]);
+          }
         }
       }
     }
@@ -477,7 +565,11 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
       for (int g = 0; g < C::kAcc / 8; ++g) {
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[g][j][0], acc[g][j][1]);
+        for (int j = 0; j < 4; ++j) {
+          float x, y;
+          unpack2(acc[g][j], x, y);
+          w[j] = pack_bf16x2(x, y);
+        }
         stmatrix_x4_trans(smem_u32(so + (8 * g + (lane & 7)) * 272 + (quad * 4 + (lane >> 3)) * 16), w);
       }
       fence_async_smem();
@@ -503,11 +595,13 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
 #pragma unroll
         for (int g = 0; g < C::kOutCols / 8; ++g)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              *reinterpret_cast<float*>(so + (8 * g + cl + u) * 528 + (r + 8 * j) * 4) =
-                  acc[round * (C::kOutCols / 8) + g][j][u];
+          for (int j = 0; j < 4; ++j) {
+            float x, y;
+            unpack2(acc[round * (C::kOutCols / 8) + g][j], x, y);
+            float* o = reinterpret_cast<float*>(so + (8 * g + cl) * 528 + (r + 8 * j) * 4);
+            o[0] = x;
+            o[132] = y;
+          }
         fence_async_smem();
         named_barrier(1 + half, 128);
         const long long o = base + static_cast<long long>(round * C::kOutCols) * args.ldo;
@@ -553,8 +647,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(start + kMaxGroups + 4);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
-  uint64_t* acc_empty = acc_full + C::kBufs;
-  uint64_t* sfull = acc_empty + C::kBufs;
+  uint64_t* acc_empty = acc_full + C::kBufs * C::kHalves;
+  uint64_t* sfull = acc_empty + C::kBufs * C::kHalves;
   uint64_t* sempty = sfull + C::kSlots;
   uint64_t* mma_done = sempty + C::kSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -563,11 +657,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], C::kHalves);
     }
-    for (int b = 0; b < C::kBufs; ++b) {
+    for (int b = 0; b < C::kBufs * C::kHalves; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], C::kEpiWarps);
+      mbar_init(&acc_empty[b], C::kEpiWarps);   // (kPair: one half's four warps of both CTAs)
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&sfull[s], 1);
@@ -579,13 +673,18 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
     prefetch_tmap(&tmQ);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
-    tmem_relinquish();
+    if constexpr (MODE == kPair) {
+      tmem_alloc_pair(tmem_slot, C::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::kTmemCols);
+      tmem_relinquish();
+    }
   }
   griddep_enter();
 
   // start[]: exclusive prefix sum of the groups' units (row tiles, or blocks)
-  constexpr int kUnit = MODE == kWgrad || MODE == kRows ? 128 : BN;
+  constexpr int kUnit = MODE == kPair ? 256 : MODE == kWgrad || MODE == kRows ? 128 : BN;
   for (int e = threadIdx.x; e < args.E; e += C::kThreads) {
     int lo, hi;
     group_rows(args, e, lo, hi);
@@ -614,16 +713,17 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (MODE == kPair) cluster_sync();   // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Fp8Walk walk;
   walk.start = start;
   walk.E = args.E;
-  walk.others = MODE == kWgrad ? (args.k + 127) / 128 : MODE == kRows ? (args.n + BN - 1) / BN : (args.n + 127) / 128;
+  walk.others = MODE == kWgrad ? (args.k + 127) / 128 : by_rows(MODE) ? (args.n + BN - 1) / BN : (args.n + 127) / 128;
   walk.cols = (args.n + BN - 1) / BN;
   walk.total = (MODE == kWgrad ? args.E * walk.cols : start[args.E]) * walk.others;
-  const int S = MODE == kSplit ? args.splits : 1;
-  const int rank = MODE == kSplit ? static_cast<int>(blockIdx.x % S) : 0;
+  const int S = MODE == kSplit ? args.splits : MODE == kPair ? 2 : 1;   // CTAs of a cluster
+  const int rank = static_cast<int>(blockIdx.x % S);
   const int id0 = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
   const long long budget = args.budget;
   if (MODE == kSplit) cluster_arrive();   // every CTA of the cluster has started (waited for below)
@@ -648,6 +748,17 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
             break;
           }
           uint8_t* sp = smem + s * C::kStageBytes;
+          if constexpr (MODE == kPair) {
+            // both CTAs' bytes arrive at CTA 0's barrier; rows that there are none of are not loaded
+            const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
+            const bool second = t.lanes > 128 || rank == 1 && t.lanes > 0;   // CTA 1 has rows
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kQBytes + C::kPBytes * (second ? 2 : 1));
+            if (rank == 0 || second) tma_load_2d_pair(sp, &tmP, bar, kb * 128, t.p0, pol_p);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d_pair(sp + C::kPBytes + h * 8192, &tmQ, bar, kb * 128, t.q0 + h * 128 + rank * 64, t.e, pol_q);
+            continue;
+          }
           mbar_arrive_expect_tx(&full[s], tx);
           if (MODE == kRows) {
             tma_load_2d_hint(sp, &tmP, &full[s], kb * 128, t.p0, pol_p);
@@ -661,42 +772,58 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
           }
         }
       }
-      // every copy of this thread lands before the CTA leaves
-      for (int j = max(0, it - C::kStages); j < it; ++j)
+      // every copy of this thread lands before the CTA leaves (kPair: CTA 0 sees to both CTAs')
+      for (int j = max(0, it - C::kStages); j < (MODE == kPair && rank ? 0 : it); ++j)
         if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, kDrainBudget))
           if (args.status) atomicOr(args.status, kErrDrain);
-    } else if ((warp == 1 || warp == 3) && lane == 0) {
-      // ---- MMA issuers: one block of 128 into one TMEM buffer, warp 1 the even blocks of the ring,
-      // warp 3 the odd ones.  Issuing a block's MMAs and commits holds a thread for most of the
-      // time they take, and its waits and arithmetic for the next one take 400 cycles more, in
-      // which the tensor cores would run dry; so the other thread does its own meanwhile.
+    } else if ((warp == 1 || warp == 3) && lane == 0 && (MODE != kPair || rank == 0)) {
+      // ---- MMA issuers: one block of 128 into one TMEM buffer.  Warp 1 issues the even blocks of
+      // the ring and warp 3 the odd ones; of a pair, warp 1 the first column half of every block and
+      // warp 3 the second (CTA 0's, for both).  Issuing a block's MMAs and commits holds a thread
+      // for most of the time they take, and its waits and arithmetic for the next one take 400
+      // cycles more, in which the tensor cores would run dry; so the other thread does its own
+      // meanwhile.
       const int mine = warp >> 1;
       int it = 0;
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-        const uint32_t idesc = idesc_f8(args.fmt_p, args.fmt_q, (t.ncols + 15) / 16 * 16);
+        const uint32_t idesc = MODE == kPair ? idesc_f8(args.fmt_p, args.fmt_q, 256, 128)
+                                             : idesc_f8(args.fmt_p, args.fmt_q, 128, (t.ncols + 15) / 16 * 16);
         const int end = it + (t.kb1 - t.kb0);
-        for (it += (it ^ mine) & 1; it < end; it += 2) {
-          const int s = it % C::kStages, buf = it % C::kBufs;
-          if (!mbar_wait(&full[s], (it / C::kStages) & 1, budget) ||
-              !mbar_wait(&acc_empty[buf], ((it / C::kBufs) & 1) ^ 1, budget)) {
+        for (it += MODE == kPair ? 0 : (it ^ mine) & 1; it < end; it += MODE == kPair ? 1 : 2) {
+          const int s = it % C::kStages, buf = it % C::kBufs, b = MODE == kPair ? 2 * buf + mine : buf;
+          const uint32_t free = ((it / C::kBufs) & 1) ^ 1;
+          // In this order: a stage's barrier may be waited for only once its previous use is over (a
+          // wait for the phase after next returns at once).  With three stages that use was the other
+          // warp's; but this buffer's release means that every block up to it - kBufs has been read.
+          if (!mbar_wait(&acc_empty[b], free, budget) || !mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
             if (args.status) atomicOr(args.status, kErrWaitMma);
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t p0 = smem_u32(smem + s * C::kStageBytes);
-          const uint64_t pd = sw128_kmajor_desc(p0), qd = sw128_kmajor_desc(p0 + C::kPBytes);
+          const uint64_t pd = sw128_kmajor_desc(p0);
+          const uint64_t qd = sw128_kmajor_desc(p0 + C::kPBytes + (MODE == kPair ? mine * 8192 : 0));
+          const uint32_t d = tmem + buf * BN + (MODE == kPair ? mine * 128 : 0);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)   // 32 bytes on: 2 in the descriptors' 16-byte addresses
-            mma_f8(tmem + buf * BN, pd + 2 * kk, qd + 2 * kk, idesc, kk > 0);
-          mma_commit(&acc_full[buf]);
-          mma_commit(&empty[s]);
+          for (int kk = 0; kk < 4; ++kk) {   // 32 bytes on: 2 in the descriptors' 16-byte addresses
+            if constexpr (MODE == kPair) mma_f8_pair(d, pd + 2 * kk, qd + 2 * kk, idesc, kk > 0);
+            else mma_f8(d, pd + 2 * kk, qd + 2 * kk, idesc, kk > 0);
+          }
+          if constexpr (MODE == kPair) {
+            mma_commit_pair(&acc_full[b]);
+            mma_commit_pair(&empty[s]);
+          } else {
+            mma_commit(&acc_full[b]);
+            mma_commit(&empty[s]);
+          }
         }
         it = end;
       }
-      mma_commit(mma_done);
+      if constexpr (MODE == kPair) mma_commit_pair(mma_done);
+      else mma_commit(mma_done);
     } else if (warp == 2) {
       // ---- scales, the loads of several blocks in flight at a time.  kRows: as[row] ws[half] for
       // the 128 lanes of each column half; kCols, kSplit: as ws of each column; wgrad: of each column
@@ -705,13 +832,13 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-        const float* q = MODE == kRows ? args.ps + t.p0 + lane : args.qs + t.q0 + lane;
+        const float* q = by_rows(MODE) ? args.ps + t.p0 + lane : args.qs + t.q0 + lane;
         const long long ldq = MODE == kWgrad ? args.n : args.rows;
-        const int live = MODE == kRows ? t.lanes : t.ncols;
+        const int live = by_rows(MODE) ? t.lanes : t.ncols;
         const int nb = (args.n + 127) / 128;   // the weight's 128 x 128 blocks
-        const int b0 = MODE == kRows ? t.q0 / 128 : t.p0 / 128;
-        const float* w = (MODE == kRows ? args.qs : args.ps) + (static_cast<long long>(t.e) * nb + b0) * args.num_kb;
-        const bool two = MODE == kRows && b0 + 1 < nb;
+        const int b0 = by_rows(MODE) ? t.q0 / 128 : t.p0 / 128;
+        const float* w = (by_rows(MODE) ? args.qs : args.ps) + (static_cast<long long>(t.e) * nb + b0) * args.num_kb;
+        const bool two = by_rows(MODE) && b0 + 1 < nb;
         for (int kb = t.kb0; ok && kb < t.kb1; kb += kBatch) {
           float v[kBatch][kPer], u[kBatch][2];
 #pragma unroll
@@ -719,7 +846,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
             const bool in = kb + j < t.kb1;
             u[j][0] = MODE == kWgrad ? 1.f : (in ? w[kb + j] : 0.f);
             u[j][1] = two && in ? w[args.num_kb + kb + j] : u[j][0];
-            constexpr int kOwn = MODE == kRows ? 4 : kPer;
+            constexpr int kOwn = by_rows(MODE) ? 4 : kPer;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
               v[j][i] = in && lane + 32 * i < live ? q[(kb + j) * ldq + 32 * i] : 0.f;
@@ -747,8 +874,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
     }
   } else {
     if constexpr (BN == 256) regs_inc<224>();
-    const Fp8Ring<BN, MODE> ring = {acc_full, acc_empty, sfull, sempty, args.status, budget};
-    if constexpr (MODE == kRows) epilogue_rows<BN>(args, walk, ring, sc, stage_out, tmem, id0, step);
+    const int half = MODE == kPair ? (warp - 4) >> 2 : 0;
+    const uint32_t ae = smem_u32(acc_empty + half);
+    const Fp8Ring<BN, MODE> ring = {acc_full + half, sfull, sempty, MODE == kPair ? cluster_map(ae, 0) : ae, args.status,
+                                    budget};
+    if constexpr (by_rows(MODE)) epilogue_rows<BN, MODE>(args, walk, ring, sc, stage_out, tmem, id0, step, rank);
     else epilogue_cols<BN, MODE>(args, walk, ring, sc, red, stage_out, tmem, id0, step, rank);
   }
   if (MODE == kSplit) {
@@ -761,15 +891,17 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
       cluster_wait();
     }
   }
-  // ---- teardown: all MMAs of this CTA have completed before the columns are released
+  // ---- teardown: all MMAs of this CTA (or pair) have completed before the columns are released
   if (warp == 1 && lane == 0)
     if (!mbar_wait(mma_done, 0, kDrainBudget))
       if (args.status) atomicOr(args.status, kErrDrain);
   tc_fence_before();
   __syncthreads();
+  if constexpr (MODE == kPair) cluster_sync();   // neither CTA's copies, commits or arrivals are under way
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    if constexpr (MODE == kPair) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
@@ -784,13 +916,16 @@ cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, const Fp8Args
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * a.splits)), dim3(C::kThreads), C::kSmemBytes,
                               s, a.splits, p, q, a);
   const long long sms = sm_count();
+  if (MODE == kPair)
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(2 * (tiles < sms / 2 ? tiles : sms / 2))),
+                              dim3(C::kThreads), C::kSmemBytes, s, 2, p, q, a);
   return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(C::kThreads), C::kSmemBytes,
                     s, p, q, a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int kSms = 152;
-constexpr int kRowsMin = 65;
+constexpr int kRowsMin = 65, kPairMin = 256;
 
 }  // namespace
 }  // namespace lmoe
@@ -833,24 +968,25 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   // Up to 16 rows in all: 16-column tiles; then, while an expert has fewer than kRowsMin rows on
   // average, 64; else rows as lanes.
   const long long live = c->n_experts < c->rows ? c->n_experts : c->rows;
-  const bool by_rows = c->rows / live >= kRowsMin;
-  const int bn = by_rows ? 256 : c->rows <= 16 ? 16 : 64;
+  const bool rows = c->rows / live >= kRowsMin, pair = c->rows / live >= kPairMin;
+  const int bn = rows ? 256 : c->rows <= 16 ? 16 : 64;
   const unsigned long long K = c->K, N = c->N;
   const unsigned long long wd[3] = {K, N, static_cast<unsigned long long>(c->n_experts)}, wst[2] = {K, K * N};
   const unsigned long long ad[2] = {K, static_cast<unsigned long long>(c->rows)}, ast[1] = {K};
-  const unsigned wbox[3] = {128, by_rows ? 256u : 128u, 1};
-  const unsigned abox[2] = {128, by_rows ? 128u : static_cast<unsigned>(bn)};
+  const unsigned wbox[3] = {128, pair ? 64u : rows ? 256u : 128u, 1};
+  const unsigned abox[2] = {128, rows ? 128u : static_cast<unsigned>(bn)};
   CUtensorMap tw, ta;
   if (!encode_u8_swizzled(&tw, w, 3, wd, wst, wbox) || !encode_u8_swizzled(&ta, a, 2, ad, ast, abox))
     return LMOE_ERR_CUDA;
   cudaError_t e;
-  if (by_rows) {
+  if (rows) {
     g.ps = a_scales;
     g.qs = w_scales;
     g.fmt_p = c->a_format;
     g.fmt_q = c->b_format;
-    const long long tiles = ((c->rows + 127) / 128 + live - 1) * ((c->N + 255) / 256);   // at most
-    e = launch_one<256, kRows>(ta, tw, g, tiles, stream);
+    const int unit = pair ? 256 : 128;
+    const long long tiles = ((c->rows + unit - 1) / unit + live - 1) * ((c->N + 255) / 256);   // at most
+    e = pair ? launch_one<256, kPair>(ta, tw, g, tiles, stream) : launch_one<256, kRows>(ta, tw, g, tiles, stream);
   } else {
     g.ps = w_scales;
     g.qs = a_scales;
