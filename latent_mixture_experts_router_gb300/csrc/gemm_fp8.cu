@@ -16,10 +16,6 @@
 // Which operand is the MMA's 128 lanes ("lane operand") and which its columns:
 //   kRows   rows of a are lanes, rows of w columns (128 x 256 tiles): many rows per expert.  A thread
 //           holds one lane, so its scale as ws is one register for 128 columns.
-//   kPair   kRows by two SMs: a cluster of two CTAs computes 256 x 256, each its 128 rows, and each
-//           loads half of the columns, which the tensor cores of both read (cta_group::2).  An SM takes
-//           in about 57 bytes a cycle: 860 cycles for a block's 48 KB, 575 for the pair's 32 KB each,
-//           beside 512 cycles of MMAs.
 //   kCols   rows of w are lanes, rows of a columns: the column count is any multiple of 16, so an
 //           expert with 20 rows costs 32 columns, not a 128-row tile, and one token costs 16.
 //   kSplit  kCols where the tiles are few (a few tokens): a cluster of S CTAs computes one tile,
@@ -38,8 +34,7 @@
 namespace lmoe {
 namespace {
 
-enum Fp8Mode : int { kCols = 0, kWgrad = 1, kSplit = 2, kRows = 3, kPair = 4 };
-constexpr bool by_rows(int mode) { return mode == kRows || mode == kPair; }
+enum Fp8Mode : int { kCols = 0, kWgrad = 1, kSplit = 2, kRows = 3 };
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSplit = 8;
 
@@ -66,38 +61,40 @@ struct Fp8Cfg {
   static constexpr int kEpiWarps = BN == 256 ? 8 : 4;
   static constexpr int kAcc = BN * 4 / kEpiWarps;   // accumulator columns of one thread's warpgroup
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  // CTAs of an SM, and the registers of the producers' and the epilogue's warpgroups (0: as launched)
+  static constexpr int kCtas = MODE == kWgrad ? 2 : 1;
+  static constexpr int kDec = BN == 256 ? 56 : MODE == kWgrad ? 40 : 0;
+  static constexpr int kInc = BN == 256 ? 224 : MODE == kWgrad ? 216 : 0;
   static constexpr int kPBytes = 128 * 128;
-  static constexpr int kHalves = MODE == kPair ? 2 : 1;   // column halves with barriers of their own
-  static constexpr int kQBytes = BN * 128 / kHalves;      // (a CTA of a pair holds half of each)
+  static constexpr int kQBytes = BN * 128;
   static constexpr int kStageBytes = kPBytes + kQBytes;
-  static constexpr int kBox = MODE == kRows ? 256 : BN < 64 ? BN : 64;   // rows of a column-operand box
+  static constexpr int kBox = MODE == kRows ? 256 : MODE == kWgrad ? 128 : BN;   // rows of a column-operand box
   static constexpr int kSlots = 8;                    // staged scale blocks
-  static constexpr int kBufs = BN == 256 ? 2 : 8;     // TMEM buffers
+  static constexpr int kBufs = BN >= 128 ? 2 : 8;     // TMEM buffers
   static constexpr uint32_t kTmemCols = BN * kBufs;
   static constexpr int kMaxS = BN == 16 ? kMaxSplit : 4;
   static constexpr int kRedBytes = MODE == kSplit ? (kMaxS - 1) * BN * 128 * 4 : 0;
   // output staging of a warpgroup: kAcc columns of 128 bf16, or kOutCols of 128 fp32 at a time (kRows:
   // 128 rows of 128 bf16 or of 64 fp32), each with 16 bytes of padding against bank conflicts
   static constexpr int kOutCols = kAcc >= 64 ? kAcc / 2 : kAcc;
-  static constexpr int kOutBytes = by_rows(MODE) ? 128 * 272 : kAcc * 272 > kOutCols * 528 ? kAcc * 272 : kOutCols * 528;
-  static constexpr int kTableBytes = (kMaxGroups + 4) * 4;
+  static constexpr int kOutBytes = MODE == kRows ? 128 * 272 : kAcc * 272 > kOutCols * 528 ? kAcc * 272 : kOutCols * 528;
+  static constexpr int kTableBytes = (kMaxGroups + 4) * 4 + (MODE == kRows ? 16 * 16 : 0);
   static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kOutBytes * (kEpiWarps / 4) + kTableBytes + 512 + 1024;
-  static constexpr int kStagesFit = (227 * 1024 - kFixed) / kStageBytes;
+  static constexpr int kStagesFit = ((kCtas == 2 ? 113 : 227) * 1024 - kFixed) / kStageBytes;
   // an odd number of stages, no more than the TMEM buffers, would break the MMA issuers' waits
   static constexpr int kStagesMost = kStagesFit > 11 ? 11 : kStagesFit;
   static constexpr int kStages = kStagesMost % 2 && kStagesMost <= kBufs ? kStagesMost - 1 : kStagesMost;
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
-  static_assert(kStages >= 3, "pipeline depth");
-  static_assert(MODE == kPair || ((kStages % 2 == 0 || kStages > kBufs) && kBufs % 2 == 0), "two MMA issuers");
-  static_assert((2 * kStages + 2 * kBufs * kHalves + 2 * kSlots + 1) * 8 + 8 <= 512, "barriers");
-  static_assert((BN == 256) == (by_rows(MODE) || MODE == kWgrad), "tile widths");
+  static_assert(kStages >= 2, "pipeline depth");
+  static_assert((kStages % 2 == 0 || kStages > kBufs) && kBufs % 2 == 0, "two MMA issuers");
+  static_assert((2 * kStages + 2 * kBufs + 2 * kSlots + 1) * 8 + 8 <= 512, "barriers");
+  static_assert((BN == 256) == (MODE == kRows) && (BN == 128) == (MODE == kWgrad), "tile widths");
 };
 
 // Instruction descriptor of kind::f8f6f4: D fp32 ([4,6) = 1), formats at [7,10) and [10,13),
 // both operands K-major, N >> 3 at [17,23), M >> 4 at [24,29).
-LMOE_DEV uint32_t idesc_f8(uint32_t fa, uint32_t fb, int m, int n) {
-  return (1u << 4) | (fa << 7) | (fb << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(m >> 4) << 24);
+LMOE_DEV uint32_t idesc_f8(uint32_t fa, uint32_t fb, int n) {
+  return (1u << 4) | (fa << 7) | (fb << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 LMOE_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -106,57 +103,6 @@ LMOE_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// ---- the same by the pair of CTAs of a cluster of two.  Issued in CTA 0: lanes 0..127 are CTA 0's A
-// rows and accumulators, 128..255 CTA 1's; each CTA holds half of B's rows.
-LMOE_DEV void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// arrives on the barrier of both CTAs
-LMOE_DEV void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-LMOE_DEV void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
-               : "memory");
-}
-LMOE_DEV void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-LMOE_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// loads into this CTA; bar: a shared::cluster address, of either CTA of the pair
-LMOE_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
-      : "memory");
-}
-LMOE_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
-                               uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
-      : "memory");
-}
-LMOE_DEV void mbar_arrive_at(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// (of the memory operations before it only the TMEM reads matter, which are complete)
-LMOE_DEV void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 LMOE_DEV void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
                                uint64_t policy) {
@@ -213,9 +159,9 @@ LMOE_DEV void stmatrix_x4_trans(uint32_t saddr, const uint32_t (&r)[4]) {
                "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
-// Registers of a warpgroup (all four of its warps).  256-column tiles: the epilogue's two
-// warpgroups hold 128 accumulators a thread; 4 x 32 x 56 + 8 x 32 x 224 = 384 x 168, what the
-// block was launched with.
+// Registers of a warpgroup (all four of its warps).  The epilogue's warpgroups hold 128
+// accumulators a thread; 4 x 32 x 56 + 8 x 32 x 224 = 384 x 168, or 4 x 32 x 40 + 4 x 32 x 216 = 256 x
+// 128, is what the block was launched with.
 template <int N>
 LMOE_DEV void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -266,8 +212,16 @@ struct Fp8Walk {
 };
 struct Fp8Tile {
   int e, p0, q0, ncols, lanes, kb0, kb1;   // lanes, ncols: live ones
-  long long out;   // kRows, kPair: element offset of (first lane, first column), else of (column, lane)
+  long long out;   // kRows: element offset of (first lane, first column), else of (column, lane)
 };
+
+// kRows: what the epilogue needs of a tile for its stores, left in shared memory by the scale warp,
+// which is at most kSlots blocks (and so tiles) ahead
+struct Fp8Info {
+  long long out;
+  int lanes, ncols;
+};
+constexpr int kInfos = 16;
 
 template <int BN, int MODE>
 LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
@@ -298,8 +252,8 @@ LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
   group_rows(a, l, lo, hi);
   t.kb0 = 0;
   t.kb1 = a.num_kb;
-  if (by_rows(MODE)) {
-    t.p0 = lo + (MODE == kPair ? rt * 256 + rank * 128 : rt * 128);
+  if (MODE == kRows) {
+    t.p0 = lo + rt * 128;
     t.q0 = ot * BN;
     t.lanes = hi - t.p0;
     t.ncols = min(BN, a.n - t.q0);
@@ -322,59 +276,50 @@ LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
 template <int BN, int MODE>
 struct Fp8Ring {
   using C = Fp8Cfg<BN, MODE>;
-  uint64_t *acc_full, *sfull, *sempty;   // acc_full: of this thread's column half
-  uint32_t acc_empty;                    // the same; kPair: shared::cluster address in CTA 0
+  uint64_t *acc_full, *acc_empty, *sempty;
   unsigned* status;
   long long budget;
+  // the block's products are in their buffer, and its scales staged (the MMA issuer waits for them)
   LMOE_DEV bool wait(int it) const {
-    if (mbar_wait(&sfull[it % C::kSlots], (it / C::kSlots) & 1, budget) &&
-        mbar_wait(&acc_full[it % C::kBufs * C::kHalves], (it / C::kBufs) & 1, budget)) {
-      __syncwarp();   // (the TMEM reads that follow are the whole warp's)
-      tc_fence_after();
-      return true;
-    }
-    if (status) atomicOr(status, kErrWaitEpilogue);
-    return false;
+    const bool ok = mbar_wait(&acc_full[it % C::kBufs], (it / C::kBufs) & 1, budget);
+    if (!ok && status) atomicOr(status, kErrWaitEpilogue);
+    __syncwarp();   // (the TMEM reads that follow are the whole warp's)
+    tc_fence_after();
+    return ok;
   }
-  // the warp has read the TMEM buffer / the scales
+  // the warp has read the TMEM buffer / the scales / both
   LMOE_DEV void buffer_read(int it, int lane) const {
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
-      const uint32_t a = acc_empty + it % C::kBufs * C::kHalves * 8;
-      if constexpr (MODE == kPair) mbar_arrive_cluster(a);
-      else mbar_arrive_at(a);
-    }
+    if (lane == 0) mbar_arrive(&acc_empty[it % C::kBufs]);
   }
   LMOE_DEV void scales_read(int it, int lane) const {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sempty[it % C::kSlots]);
   }
+  LMOE_DEV void both_read(int it, int lane) const {
+    buffer_read(it, lane);
+    if (lane == 0) mbar_arrive(&sempty[it % C::kSlots]);
+  }
 };
 
-// ---- epilogue of kRows and kPair: a thread owns lane (row) r and 128 columns
-template <int BN, int MODE>
-LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8Ring<BN, MODE>& ring, const float* sc,
-                            uint8_t* stage_out, uint32_t tmem, int id0, int step, int rank) {
-  using C = Fp8Cfg<BN, MODE>;
+// ---- epilogue of kRows: a thread owns lane (row) r and 128 columns
+template <int BN>
+LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8Ring<BN, kRows>& ring, const float* sc,
+                            const Fp8Info* infos, uint8_t* stage_out, uint32_t tmem, int id0, int step) {
+  using C = Fp8Cfg<BN, kRows>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
   const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
   uint8_t* row = stage_out + half * C::kOutBytes + r * 272;
   int it = 0;
   bool ok = true;
-  for (int id = id0; ok && id < walk.total; id += step) {
-    // (the tile is worked out again for the stores: its registers are the accumulators' here)
-    int kb, kb1;
-    {
-      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-      kb = t.kb0;
-      kb1 = t.kb1;
-    }
+  int tile = 0;
+  for (int id = id0; ok && id < walk.total; id += step, ++tile) {
     float acc[128];
 #pragma unroll
     for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-    for (; kb < kb1; ++kb, ++it) {
+    for (int kb = 0; kb < args.num_kb; ++kb, ++it) {
       ok = ring.wait(it);
       if (!ok) break;
       const uint32_t tb = tq + (it % C::kBufs) * BN;
@@ -385,14 +330,13 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
         if (ch < 3) tmem_ld_32cols(tb + (ch + 1) * 32, v[(ch + 1) & 1]);
-        else ring.buffer_read(it, lane);
+        else ring.both_read(it, lane);
 #pragma unroll
         for (int i = 0; i < 32; ++i) fma_acc(acc[ch * 32 + i], v[ch & 1][i], s);
         if (ch < 3) tmem_ld_wait();
       }
-      ring.scales_read(it, lane);
     }
-    const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
+    const Fp8Info t = infos[tile % kInfos];   // written before the tile's first scales
     const int n = min(128, t.ncols - half * 128);   // live columns (may be negative)
     if (ok && r < t.lanes && n > 0) {
       const long long base = t.out + static_cast<long long>(r) * args.ldo + half * 128;
@@ -633,7 +577,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
 }
 
 template <int BN, int MODE>
-__global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
+__global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::kCtas)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const Fp8Args args) {
   using C = Fp8Cfg<BN, MODE>;
@@ -644,11 +588,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   uint8_t* stage_out = reinterpret_cast<uint8_t*>(red) + C::kRedBytes;
   float* sc = reinterpret_cast<float*>(stage_out + C::kOutBytes * (C::kEpiWarps / 4));   // [kSlots][BN]
   int* start = reinterpret_cast<int*>(sc + C::kSlots * BN);                              // [E + 1]
-  uint64_t* full = reinterpret_cast<uint64_t*>(start + kMaxGroups + 4);
+  Fp8Info* infos = reinterpret_cast<Fp8Info*>(start + kMaxGroups + 4);                   // [kInfos] (kRows)
+  uint64_t* full = reinterpret_cast<uint64_t*>(infos + (MODE == kRows ? kInfos : 0));
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
-  uint64_t* acc_empty = acc_full + C::kBufs * C::kHalves;
-  uint64_t* sfull = acc_empty + C::kBufs * C::kHalves;
+  uint64_t* acc_empty = acc_full + C::kBufs;
+  uint64_t* sfull = acc_empty + C::kBufs;
   uint64_t* sempty = sfull + C::kSlots;
   uint64_t* mma_done = sempty + C::kSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -657,11 +602,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], C::kHalves);
+      mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < C::kBufs * C::kHalves; ++b) {
+    for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], C::kEpiWarps);   // (kPair: one half's four warps of both CTAs)
+      mbar_init(&acc_empty[b], C::kEpiWarps);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&sfull[s], 1);
@@ -673,18 +618,13 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
     prefetch_tmap(&tmQ);
   }
   if (warp == 1) {
-    if constexpr (MODE == kPair) {
-      tmem_alloc_pair(tmem_slot, C::kTmemCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, C::kTmemCols);
-      tmem_relinquish();
-    }
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
   }
   griddep_enter();
 
   // start[]: exclusive prefix sum of the groups' units (row tiles, or blocks)
-  constexpr int kUnit = MODE == kPair ? 256 : MODE == kWgrad || MODE == kRows ? 128 : BN;
+  constexpr int kUnit = MODE == kWgrad || MODE == kRows ? 128 : BN;
   for (int e = threadIdx.x; e < args.E; e += C::kThreads) {
     int lo, hi;
     group_rows(args, e, lo, hi);
@@ -713,23 +653,22 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (MODE == kPair) cluster_sync();   // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Fp8Walk walk;
   walk.start = start;
   walk.E = args.E;
-  walk.others = MODE == kWgrad ? (args.k + 127) / 128 : by_rows(MODE) ? (args.n + BN - 1) / BN : (args.n + 127) / 128;
+  walk.others = MODE == kWgrad ? (args.k + 127) / 128 : MODE == kRows ? (args.n + BN - 1) / BN : (args.n + 127) / 128;
   walk.cols = (args.n + BN - 1) / BN;
   walk.total = (MODE == kWgrad ? args.E * walk.cols : start[args.E]) * walk.others;
-  const int S = MODE == kSplit ? args.splits : MODE == kPair ? 2 : 1;   // CTAs of a cluster
+  const int S = MODE == kSplit ? args.splits : 1;   // CTAs of a cluster
   const int rank = static_cast<int>(blockIdx.x % S);
   const int id0 = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
   const long long budget = args.budget;
   if (MODE == kSplit) cluster_arrive();   // every CTA of the cluster has started (waited for below)
 
   if (warp < 4) {
-    if constexpr (BN == 256) regs_dec<56>();
+    if constexpr (C::kDec > 0) regs_dec<C::kDec>();
     if (warp == 0 && lane == 0) {
       // ---- TMA producer (narrow tiles: few rows, each weight is read about once)
       const uint64_t pol_p = BN == 256 ? policy_evict_normal() : policy_evict_first();
@@ -748,17 +687,6 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
             break;
           }
           uint8_t* sp = smem + s * C::kStageBytes;
-          if constexpr (MODE == kPair) {
-            // both CTAs' bytes arrive at CTA 0's barrier; rows that there are none of are not loaded
-            const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
-            const bool second = t.lanes > 128 || rank == 1 && t.lanes > 0;   // CTA 1 has rows
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kQBytes + C::kPBytes * (second ? 2 : 1));
-            if (rank == 0 || second) tma_load_2d_pair(sp, &tmP, bar, kb * 128, t.p0, pol_p);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d_pair(sp + C::kPBytes + h * 8192, &tmQ, bar, kb * 128, t.q0 + h * 128 + rank * 64, t.e, pol_q);
-            continue;
-          }
           mbar_arrive_expect_tx(&full[s], tx);
           if (MODE == kRows) {
             tma_load_2d_hint(sp, &tmP, &full[s], kb * 128, t.p0, pol_p);
@@ -772,73 +700,69 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
           }
         }
       }
-      // every copy of this thread lands before the CTA leaves (kPair: CTA 0 sees to both CTAs')
-      for (int j = max(0, it - C::kStages); j < (MODE == kPair && rank ? 0 : it); ++j)
+      // every copy of this thread lands before the CTA leaves
+      for (int j = max(0, it - C::kStages); j < it; ++j)
         if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, kDrainBudget))
           if (args.status) atomicOr(args.status, kErrDrain);
-    } else if ((warp == 1 || warp == 3) && lane == 0 && (MODE != kPair || rank == 0)) {
-      // ---- MMA issuers: one block of 128 into one TMEM buffer.  Warp 1 issues the even blocks of
-      // the ring and warp 3 the odd ones; of a pair, warp 1 the first column half of every block and
-      // warp 3 the second (CTA 0's, for both).  Issuing a block's MMAs and commits holds a thread
-      // for most of the time they take, and its waits and arithmetic for the next one take 400
-      // cycles more, in which the tensor cores would run dry; so the other thread does its own
-      // meanwhile.
+    } else if ((warp == 1 || warp == 3) && lane == 0) {
+      // ---- MMA issuers: one block of 128 into one TMEM buffer, warp 1 the even blocks of the ring,
+      // warp 3 the odd ones.  Issuing a block's MMAs and commits holds a thread for most of the time
+      // they take, and its waits and arithmetic for the next one take 400 cycles more, in which the
+      // tensor cores would run dry; so the other thread does its own meanwhile.
       const int mine = warp >> 1;
       int it = 0;
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
-        const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-        const uint32_t idesc = MODE == kPair ? idesc_f8(args.fmt_p, args.fmt_q, 256, 128)
-                                             : idesc_f8(args.fmt_p, args.fmt_q, 128, (t.ncols + 15) / 16 * 16);
-        const int end = it + (t.kb1 - t.kb0);
-        for (it += MODE == kPair ? 0 : (it ^ mine) & 1; it < end; it += MODE == kPair ? 1 : 2) {
-          const int s = it % C::kStages, buf = it % C::kBufs, b = MODE == kPair ? 2 * buf + mine : buf;
-          const uint32_t free = ((it / C::kBufs) & 1) ^ 1;
-          // In this order: a stage's barrier may be waited for only once its previous use is over (a
+        // (kRows: all 256 columns, whatever the tile: those past the weight's rows are zeros, and
+        // working a tile out here would hold up its first MMAs)
+        int ncols = BN, blocks = args.num_kb;
+        if (MODE != kRows) {
+          const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
+          ncols = t.ncols;
+          blocks = t.kb1 - t.kb0;
+        }
+        const uint32_t idesc = idesc_f8(args.fmt_p, args.fmt_q, (ncols + 15) / 16 * 16);
+        const int end = it + blocks;
+        for (it += (it ^ mine) & 1; it < end; it += 2) {
+          const int s = it % C::kStages, buf = it % C::kBufs, slot = it % C::kSlots;
+          // The buffer first: a stage's barrier may be waited for only once its previous use is over (a
           // wait for the phase after next returns at once).  With three stages that use was the other
           // warp's; but this buffer's release means that every block up to it - kBufs has been read.
-          if (!mbar_wait(&acc_empty[b], free, budget) || !mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
+          if (!mbar_wait(&sfull[slot], (it / C::kSlots) & 1, budget) ||
+              !mbar_wait(&acc_empty[buf], ((it / C::kBufs) & 1) ^ 1, budget) ||
+              !mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
             if (args.status) atomicOr(args.status, kErrWaitMma);
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t p0 = smem_u32(smem + s * C::kStageBytes);
-          const uint64_t pd = sw128_kmajor_desc(p0);
-          const uint64_t qd = sw128_kmajor_desc(p0 + C::kPBytes + (MODE == kPair ? mine * 8192 : 0));
-          const uint32_t d = tmem + buf * BN + (MODE == kPair ? mine * 128 : 0);
+          const uint64_t pd = sw128_kmajor_desc(p0), qd = sw128_kmajor_desc(p0 + C::kPBytes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {   // 32 bytes on: 2 in the descriptors' 16-byte addresses
-            if constexpr (MODE == kPair) mma_f8_pair(d, pd + 2 * kk, qd + 2 * kk, idesc, kk > 0);
-            else mma_f8(d, pd + 2 * kk, qd + 2 * kk, idesc, kk > 0);
-          }
-          if constexpr (MODE == kPair) {
-            mma_commit_pair(&acc_full[b]);
-            mma_commit_pair(&empty[s]);
-          } else {
-            mma_commit(&acc_full[b]);
-            mma_commit(&empty[s]);
-          }
+          for (int kk = 0; kk < 4; ++kk)   // 32 bytes on: 2 in the descriptors' 16-byte addresses
+            mma_f8(tmem + buf * BN, pd + 2 * kk, qd + 2 * kk, idesc, kk > 0);
+          mma_commit(&acc_full[buf]);
+          mma_commit(&empty[s]);
         }
         it = end;
       }
-      if constexpr (MODE == kPair) mma_commit_pair(mma_done);
-      else mma_commit(mma_done);
+      mma_commit(mma_done);
     } else if (warp == 2) {
       // ---- scales, the loads of several blocks in flight at a time.  kRows: as[row] ws[half] for
       // the 128 lanes of each column half; kCols, kSplit: as ws of each column; wgrad: of each column
-      constexpr int kPer = (BN + 31) / 32, kBatch = BN == 256 ? 2 : 4;
-      int it = 0;
+      constexpr int kPer = (BN + 31) / 32, kBatch = BN >= 128 ? 2 : 4;
+      int it = 0, tile = 0;
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-        const float* q = by_rows(MODE) ? args.ps + t.p0 + lane : args.qs + t.q0 + lane;
+        const float* q = MODE == kRows ? args.ps + t.p0 + lane : args.qs + t.q0 + lane;
         const long long ldq = MODE == kWgrad ? args.n : args.rows;
-        const int live = by_rows(MODE) ? t.lanes : t.ncols;
+        const int live = MODE == kRows ? t.lanes : t.ncols;
         const int nb = (args.n + 127) / 128;   // the weight's 128 x 128 blocks
-        const int b0 = by_rows(MODE) ? t.q0 / 128 : t.p0 / 128;
-        const float* w = (by_rows(MODE) ? args.qs : args.ps) + (static_cast<long long>(t.e) * nb + b0) * args.num_kb;
-        const bool two = by_rows(MODE) && b0 + 1 < nb;
+        const int b0 = MODE == kRows ? t.q0 / 128 : t.p0 / 128;
+        const float* w = (MODE == kRows ? args.qs : args.ps) + (static_cast<long long>(t.e) * nb + b0) * args.num_kb;
+        const bool two = MODE == kRows && b0 + 1 < nb;
+        bool told = false;
         for (int kb = t.kb0; ok && kb < t.kb1; kb += kBatch) {
           float v[kBatch][kPer], u[kBatch][2];
 #pragma unroll
@@ -846,7 +770,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
             const bool in = kb + j < t.kb1;
             u[j][0] = MODE == kWgrad ? 1.f : (in ? w[kb + j] : 0.f);
             u[j][1] = two && in ? w[args.num_kb + kb + j] : u[j][0];
-            constexpr int kOwn = by_rows(MODE) ? 4 : kPer;
+            constexpr int kOwn = MODE == kRows ? 4 : kPer;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
               v[j][i] = in && lane + 32 * i < live ? q[(kb + j) * ldq + 32 * i] : 0.f;
@@ -862,6 +786,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
               ok = false;
               break;
             }
+            if (MODE == kRows && !told) {   // (here, and not before the slot is free: see Fp8Info)
+              if (lane == 0) infos[tile % kInfos] = {t.out, t.lanes, t.ncols};
+              told = true;
+              ++tile;
+            }
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
               if (lane + 32 * i < BN) sc[s * BN + lane + 32 * i] = v[j][i] * u[j][i / 4 & 1];
@@ -873,12 +802,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (BN == 256) regs_inc<224>();
-    const int half = MODE == kPair ? (warp - 4) >> 2 : 0;
-    const uint32_t ae = smem_u32(acc_empty + half);
-    const Fp8Ring<BN, MODE> ring = {acc_full + half, sfull, sempty, MODE == kPair ? cluster_map(ae, 0) : ae, args.status,
-                                    budget};
-    if constexpr (by_rows(MODE)) epilogue_rows<BN, MODE>(args, walk, ring, sc, stage_out, tmem, id0, step, rank);
+    if constexpr (C::kInc > 0) regs_inc<C::kInc>();
+    const Fp8Ring<BN, MODE> ring = {acc_full, acc_empty, sempty, args.status, budget};
+    if constexpr (MODE == kRows) epilogue_rows<BN>(args, walk, ring, sc, infos, stage_out, tmem, id0, step);
     else epilogue_cols<BN, MODE>(args, walk, ring, sc, red, stage_out, tmem, id0, step, rank);
   }
   if (MODE == kSplit) {
@@ -891,17 +817,15 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, 1)
       cluster_wait();
     }
   }
-  // ---- teardown: all MMAs of this CTA (or pair) have completed before the columns are released
+  // ---- teardown: all MMAs of this CTA have completed before the columns are released
   if (warp == 1 && lane == 0)
     if (!mbar_wait(mma_done, 0, kDrainBudget))
       if (args.status) atomicOr(args.status, kErrDrain);
   tc_fence_before();
   __syncthreads();
-  if constexpr (MODE == kPair) cluster_sync();   // neither CTA's copies, commits or arrivals are under way
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (MODE == kPair) tmem_dealloc_pair(tmem, C::kTmemCols);
-    else tmem_dealloc(tmem, C::kTmemCols);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
@@ -915,17 +839,14 @@ cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, const Fp8Args
   if (MODE == kSplit)
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * a.splits)), dim3(C::kThreads), C::kSmemBytes,
                               s, a.splits, p, q, a);
-  const long long sms = sm_count();
-  if (MODE == kPair)
-    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(2 * (tiles < sms / 2 ? tiles : sms / 2))),
-                              dim3(C::kThreads), C::kSmemBytes, s, 2, p, q, a);
+  const long long sms = static_cast<long long>(C::kCtas) * sm_count();
   return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(C::kThreads), C::kSmemBytes,
                     s, p, q, a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int kSms = 152;
-constexpr int kRowsMin = 65, kPairMin = 256;
+constexpr int kRowsMin = 65;
 
 }  // namespace
 }  // namespace lmoe
@@ -968,12 +889,12 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   // Up to 16 rows in all: 16-column tiles; then, while an expert has fewer than kRowsMin rows on
   // average, 64; else rows as lanes.
   const long long live = c->n_experts < c->rows ? c->n_experts : c->rows;
-  const bool rows = c->rows / live >= kRowsMin, pair = c->rows / live >= kPairMin;
+  const bool rows = c->rows / live >= kRowsMin;
   const int bn = rows ? 256 : c->rows <= 16 ? 16 : 64;
   const unsigned long long K = c->K, N = c->N;
   const unsigned long long wd[3] = {K, N, static_cast<unsigned long long>(c->n_experts)}, wst[2] = {K, K * N};
   const unsigned long long ad[2] = {K, static_cast<unsigned long long>(c->rows)}, ast[1] = {K};
-  const unsigned wbox[3] = {128, pair ? 64u : rows ? 256u : 128u, 1};
+  const unsigned wbox[3] = {128, rows ? 256u : 128u, 1};
   const unsigned abox[2] = {128, rows ? 128u : static_cast<unsigned>(bn)};
   CUtensorMap tw, ta;
   if (!encode_u8_swizzled(&tw, w, 3, wd, wst, wbox) || !encode_u8_swizzled(&ta, a, 2, ad, ast, abox))
@@ -984,9 +905,8 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
     g.qs = w_scales;
     g.fmt_p = c->a_format;
     g.fmt_q = c->b_format;
-    const int unit = pair ? 256 : 128;
-    const long long tiles = ((c->rows + unit - 1) / unit + live - 1) * ((c->N + 255) / 256);   // at most
-    e = pair ? launch_one<256, kPair>(ta, tw, g, tiles, stream) : launch_one<256, kRows>(ta, tw, g, tiles, stream);
+    const long long tiles = ((c->rows + 127) / 128 + live - 1) * ((c->N + 255) / 256);   // at most
+    e = launch_one<256, kRows>(ta, tw, g, tiles, stream);
   } else {
     g.ps = w_scales;
     g.qs = a_scales;
@@ -1010,7 +930,7 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   if (c->out_dtype != LMOE_F32 && c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
   if (c->n_experts > kMaxGroups || c->K > (1 << 20) || c->N > (1 << 20) || c->rows > (1LL << 24))
     return LMOE_ERR_UNSUPPORTED;
-  const long long lt = (c->K + 127) / 128, ct = (c->N + 255) / 256, tiles = lt * ct * c->n_experts;
+  const long long lt = (c->K + 127) / 128, ct = (c->N + 127) / 128, tiles = lt * ct * c->n_experts;
   if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
   const int ob = c->out_dtype == LMOE_F32 ? 4 : 2;
   if (dw == nullptr) return LMOE_ERR_ARG;
@@ -1047,8 +967,8 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   CUtensorMap tp, tq;
   const unsigned long long pd[2] = {R, static_cast<unsigned long long>(c->K)};
   const unsigned long long qd[2] = {R, static_cast<unsigned long long>(c->N)}, st[1] = {R};
-  const unsigned pbox[2] = {128, 128}, qbox[2] = {128, 64};
-  if (!encode_u8_swizzled(&tp, x_t, 2, pd, st, pbox) || !encode_u8_swizzled(&tq, dy_t, 2, qd, st, qbox))
+  const unsigned box[2] = {128, 128};
+  if (!encode_u8_swizzled(&tp, x_t, 2, pd, st, box) || !encode_u8_swizzled(&tq, dy_t, 2, qd, st, box))
     return LMOE_ERR_CUDA;
-  return launch_one<256, kWgrad>(tp, tq, g, tiles, stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+  return launch_one<128, kWgrad>(tp, tq, g, tiles, stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
