@@ -25,8 +25,9 @@
 //
 // Roles of a CTA: warp 0 lane 0 TMA producer; lane 0 of warps 1 and 3 MMA issuers (warp 1 owns the TMEM);
 // warp 2 stages the scales of each block in shared memory; warps 4.. epilogue, warp w on TMEM lanes
-// 32 (w % 4) .. (and column half (w - 4) / 4 with eight of them).  The epilogue leaves a finished
-// tile in shared memory, from where bulk copies store it while the next tile is computed.
+// 32 (w % 4) .. (and column half (w - 4) / 4 with eight of them).  A finished tile passes
+// through shared memory on its way out, so that a store instruction writes whole rows (bulk copies of
+// single rows, 256 or 512 bytes, take the copy engine about 60 cycles each: 9000 cycles a tile).
 #include "../../include/latent_moe.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -38,7 +39,24 @@ enum Fp8Mode : int { kCols = 0, kWgrad = 1, kSplit = 2, kRows = 3 };
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSplit = 8;
 
+// Division of n < 2^31 by a fixed d, by a multiplication (Granlund and Montgomery 1994): the walk of
+// the tiles divides several times for each, and a division takes a thread beside busy ones hundreds
+// of cycles.
+struct FastDiv {
+  unsigned d, mul, shift;
+  __host__ static FastDiv of(unsigned d) {
+    unsigned shift = 0;
+    while ((1ull << shift) < d) ++shift;
+    return {d, static_cast<unsigned>(((1ull << 32) * ((1ull << shift) - d)) / d + 1), shift};
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<unsigned>(n), mul) + static_cast<unsigned>(n)) >> shift);
+  }
+  __device__ __forceinline__ int mod(int n) const { return n - div(n) * static_cast<int>(d); }
+};
+
 struct Fp8Args {
+  FastDiv by_others, by_group, by_E;   // tiles across; kRasterGroup rows of them; experts
   long long rows;        // matmul: rows of a and y; wgrad: columns of dy_t and x_t (a multiple of 128)
   int n, k;              // matmul: rows of w; wgrad: rows of dy_t and of x_t
   int num_kb;            // matmul: blocks of the reduction
@@ -49,7 +67,7 @@ struct Fp8Args {
   void* out;
   int ldo;               // elements of an output row
   int out_f32, accumulate;
-  int out_vec;           // output rows start on 16 bytes: bulk copies
+  int out_vec;           // output rows start on 16 bytes: 16-byte stores
   unsigned fmt_p, fmt_q;   // 0 e4m3, 1 e5m2
   unsigned* status;      // error word or nullptr
   long long budget;
@@ -78,7 +96,7 @@ struct Fp8Cfg {
   // 128 rows of 128 bf16 or of 64 fp32), each with 16 bytes of padding against bank conflicts
   static constexpr int kOutCols = kAcc >= 64 ? kAcc / 2 : kAcc;
   static constexpr int kOutBytes = MODE == kRows ? 128 * 272 : kAcc * 272 > kOutCols * 528 ? kAcc * 272 : kOutCols * 528;
-  static constexpr int kTableBytes = (kMaxGroups + 4) * 4 + (MODE == kRows ? 16 * 16 : 0);
+  static constexpr int kTableBytes = (kMaxGroups + 4) * 4 + (MODE == kRows ? 16 * 16 : MODE == kWgrad ? 4 * 48 : 0);
   static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kOutBytes * (kEpiWarps / 4) + kTableBytes + 512 + 1024;
   static constexpr int kStagesFit = ((kCtas == 2 ? 113 : 227) * 1024 - kFixed) / kStageBytes;
   // an odd number of stages, no more than the TMEM buffers, would break the MMA issuers' waits
@@ -87,7 +105,7 @@ struct Fp8Cfg {
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
   static_assert(kStages >= 2, "pipeline depth");
   static_assert((kStages % 2 == 0 || kStages > kBufs) && kBufs % 2 == 0, "two MMA issuers");
-  static_assert((2 * kStages + 2 * kBufs + 2 * kSlots + 1) * 8 + 8 <= 512, "barriers");
+  static_assert((2 * kStages + 2 * kBufs + 2 * kSlots + 2 * 4 + 1) * 8 + 8 <= 512, "barriers");
   static_assert((BN == 256) == (MODE == kRows) && (BN == 128) == (MODE == kWgrad), "tile widths");
 };
 
@@ -174,23 +192,6 @@ LMOE_DEV void regs_inc() {
 LMOE_DEV void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// ---- bulk copies shared -> global (16-byte aligned addresses and sizes), in groups per thread
-LMOE_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-LMOE_DEV void bulk_store(void* dst, uint32_t saddr, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(saddr), "r"(bytes)
-               : "memory");
-}
-// *dst += (fp32)
-LMOE_DEV void bulk_add(void* dst, uint32_t saddr, uint32_t bytes) {
-  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(saddr),
-               "r"(bytes)
-               : "memory");
-}
-LMOE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// this thread's copies have read their shared memory / are complete
-LMOE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-LMOE_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // Rows of group e, clamped into the rows there are, so that no offsets send a load or a store out
 // of range.
 LMOE_DEV void group_rows(const Fp8Args& a, int e, int& lo, int& hi) {
@@ -222,15 +223,35 @@ struct Fp8Info {
   int lanes, ncols;
 };
 constexpr int kInfos = 16;
+// kWgrad: whole tiles by the same way, in a ring with barriers of its own (a tile may have no
+// block).  Working one out takes an epilogue thread 1500 cycles, six divisions beside the others'
+// arithmetic.
+constexpr int kTileRing = 4;
+
+// grouped_tile (ptx.cuh) without its divisions: tile i of `rows` x by_others.d tiles
+__constant__ unsigned g_ceil_recip[kRasterGroup] = {   // ceil(2^32 / d): exact quotients below 2^28
+    0, 0, 0x80000000u, 0x55555556u, 0x40000000u, 0x33333334u, 0x2aaaaaabu, 0x24924925u,
+    0x20000000u, 0x1c71c71du, 0x1999999au, 0x1745d175u, 0x15555556u, 0x13b13b14u, 0x12492493u, 0x11111112u};
+LMOE_DEV void raster(const Fp8Args& a, int i, int rows, int& row, int& other) {
+  const int g = a.by_group.div(i), first = g * kRasterGroup, gm = min(kRasterGroup, rows - first);
+  const int local = i - g * static_cast<int>(a.by_group.d);
+  other = gm == kRasterGroup ? local / kRasterGroup
+          : gm == 1          ? local
+                             : static_cast<int>(__umulhi(static_cast<unsigned>(local), g_ceil_recip[gm]));
+  row = first + local - other * gm;
+}
 
 template <int BN, int MODE>
 LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
   Fp8Tile t;
   int ot, rt;
   if (MODE == kWgrad) {
-    const int per = w.others * w.cols;
-    t.e = id / per;
-    grouped_tile(id - t.e * per, w.cols, w.others, kRasterGroup, rt, ot);
+    // The experts take turns, tile by tile, in an order that shifts: CTAs side by side then have tiles
+    // of more and of fewer blocks, and some store while others compute (all at once, the stores of
+    // a wave of tiles fill L2 and wait for memory).
+    const int i = a.by_E.div(id);
+    t.e = a.by_E.mod(id - i * w.E + i + a.by_E.div(i));
+    raster(a, i, w.cols, rt, ot);
     t.p0 = ot * 128;
     t.q0 = rt * BN;
     t.ncols = min(BN, a.n - t.q0);
@@ -241,14 +262,14 @@ LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
     return t;
   }
   int l = 0, h = w.E, lo, hi;   // the last e with start[e] * others <= id
-  const int s = id / w.others;
+  const int s = a.by_others.div(id);
   while (h - l > 1) {
     const int m = (l + h) >> 1;
     if (w.start[m] <= s) l = m;
     else h = m;
   }
   t.e = l;
-  grouped_tile(id - w.start[l] * w.others, w.start[l + 1] - w.start[l], w.others, kRasterGroup, rt, ot);
+  raster(a, id - w.start[l] * w.others, w.start[l + 1] - w.start[l], rt, ot);
   group_rows(a, l, lo, hi);
   t.kb0 = 0;
   t.kb1 = a.num_kb;
@@ -311,7 +332,7 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
   const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
-  uint8_t* row = stage_out + half * C::kOutBytes + r * 272;
+  uint8_t* mine = stage_out + half * C::kOutBytes + quad * 32 * 272;
   int it = 0;
   bool ok = true;
   int tile = 0;
@@ -338,56 +359,63 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
     }
     const Fp8Info t = infos[tile % kInfos];   // written before the tile's first scales
     const int n = min(128, t.ncols - half * 128);   // live columns (may be negative)
-    if (ok && r < t.lanes && n > 0) {
-      const long long base = t.out + static_cast<long long>(r) * args.ldo + half * 128;
-      // this thread's row through its own shared memory, 256 bytes at a time
-      const int rounds = args.out_f32 ? 2 : 1;
+    if (ok && n > 0) {   // (the same for the warp)
+      // the warp's 32 rows through its own shared memory, 256 bytes of each at a time: a thread
+      // writes its row, a store instruction takes two rows
+      const long long base = t.out + static_cast<long long>(quad * 32) * args.ldo + half * 128;
+      const int rows = min(32, t.lanes - quad * 32);
+      const int es = args.out_f32 ? 4 : 2, rounds = args.out_f32 ? 2 : 1;
 #pragma unroll
       for (int round = 0; round < 2; ++round) {
         if (round >= rounds) break;
-        bulk_wait_read();
         if (args.out_f32) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float* a = acc + round * 64 + 4 * i;
-            *reinterpret_cast<float4*>(row + 16 * i) = make_float4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<float4*>(mine + lane * 272 + 16 * i) = make_float4(a[0], a[1], a[2], a[3]);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float* a = acc + 8 * i;
-            *reinterpret_cast<uint4*>(row + 16 * i) = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
-                                                                 pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+            *reinterpret_cast<uint4*>(mine + lane * 272 + 16 * i) =
+                make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                           pack_bf16x2(a[6], a[7]));
           }
         }
-        const int cols = args.out_f32 ? min(64, n - round * 64) : n;
-        if (cols <= 0) break;
+        __syncwarp();
+        const int bytes = (n - round * 64) * es;   // of a row, from here on (may be negative)
+        uint8_t* o = static_cast<uint8_t*>(args.out) + (base + round * 64) * es;
         if (args.out_vec) {
-          fence_async_smem();
-          if (args.out_f32)
-            bulk_store(static_cast<float*>(args.out) + base + round * 64, smem_u32(row), cols * 4);
-          else
-            bulk_store(static_cast<__nv_bfloat16*>(args.out) + base, smem_u32(row), cols * 2);
-          bulk_commit();
-        } else if (args.out_f32) {
-          for (int i = 0; i < cols; ++i)
-            static_cast<float*>(args.out)[base + round * 64 + i] = reinterpret_cast<const float*>(row)[i];
+          o += static_cast<long long>(lane >> 4) * args.ldo * es + (lane & 15) * 16;
+          const bool in = (lane & 15) * 16 < bytes;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int row = 2 * i + (lane >> 4);
+            const uint4 q = *reinterpret_cast<const uint4*>(mine + row * 272 + (lane & 15) * 16);
+            if (in && row < rows) *reinterpret_cast<uint4*>(o) = q;
+            o += 2LL * args.ldo * es;
+          }
         } else {
-          for (int i = 0; i < cols; ++i)
-            static_cast<__nv_bfloat16*>(args.out)[base + i] = reinterpret_cast<const __nv_bfloat16*>(row)[i];
+          for (int row = 0; row < rows; ++row, o += static_cast<long long>(args.ldo) * es)
+            for (int i = lane; i < min(bytes, 256) / es; i += 32) {
+              if (args.out_f32) reinterpret_cast<float*>(o)[i] = reinterpret_cast<const float*>(mine + row * 272)[i];
+              else reinterpret_cast<__nv_bfloat16*>(o)[i] = reinterpret_cast<const __nv_bfloat16*>(mine + row * 272)[i];
+            }
         }
+        __syncwarp();
       }
     }
     __syncwarp();
   }
-  bulk_wait();
 }
 
 // ---- epilogue of the other modes.  A TMEM read in the 16 x 256-bit shape gives a thread two
 // columns of four lanes per 8 columns, so that it needs two of their scales, not eight.
 template <int BN, int MODE>
 LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8Ring<BN, MODE>& ring, const float* sc,
-                            float* red, uint8_t* stage_out, uint32_t tmem, int id0, int step, int rank) {
+                            float* red, uint8_t* stage_out, uint32_t tmem, int id0, int step, int rank,
+                            const Fp8Tile* tiles, uint64_t* tfull, uint64_t* tempty) {
   using C = Fp8Cfg<BN, MODE>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = (warp - 4) >> 2;
@@ -400,31 +428,38 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
   uint8_t* so = stage_out + half * C::kOutBytes;
   int it = 0;
   bool ok = true;
-  for (int id = id0; ok && id < walk.total; id += step) {
-    // (the tile is worked out again for the stores: its registers are the accumulators' here)
-    int kb, kb1;
-    const float* ps = nullptr;   // wgrad: scale of this thread's first lane in the next block
-    int left = 0;                // lanes of the operand from there on
-    {
-      const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
-      kb = t.kb0;
-      kb1 = t.kb1;
-      if (MODE == kWgrad) {
-        ps = args.ps + static_cast<long long>(kb) * args.k + t.p0 + r;
-        left = t.lanes - r;
+  Fp8Tile t = {};
+  int tile = 0;
+  const auto fetch = [&](int id) {   // the next tile (of the ring: this warp's turn with it ends here)
+    if constexpr (MODE == kWgrad) {
+      const int i = tile++ % kTileRing;
+      ok = mbar_wait(&tfull[i], ((tile - 1) / kTileRing) & 1, ring.budget);
+      if (!ok) {
+        if (args.status) atomicOr(args.status, kErrWaitEpilogue);
+        return;
       }
+      t = tiles[i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[i]);
+    } else {
+      t = tile_at<BN, MODE>(walk, args, id, rank);
     }
+  };
+  if (id0 < walk.total) fetch(id0);
+  float sp_next[4] = {};   // wgrad: scales of this thread's four lanes in the next block
+  const auto lane_scales = [&](const Fp8Tile& u, int kb) {
+    const float* ps = args.ps + static_cast<long long>(kb) * args.k + u.p0 + r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (r + 8 * j < u.lanes) sp_next[j] = ps[8 * j];
+  };
+  if (MODE == kWgrad && ok && id0 < walk.total && t.kb0 < t.kb1) lane_scales(t, t.kb0);
+  for (int id = id0; ok && id < walk.total; id += step) {
     // acc[g][j]: the column pair of group g, lane 8 j + l / 4 of the warp's 32
     uint64_t acc[C::kAcc / 8][4];
 #pragma unroll
     for (int i = 0; i < C::kAcc / 2; ++i) acc[i >> 2][i & 3] = 0;
-    float sp_next[4] = {};
-    if (MODE == kWgrad && kb < kb1) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (8 * j < left) sp_next[j] = ps[8 * j];
-    }
-    for (; kb < kb1; ++kb, ++it) {
+    for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
       ok = ring.wait(it);
       if (!ok) break;
       const uint32_t tb = tq + (it % C::kBufs) * BN;
@@ -432,12 +467,9 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
       tmem_ld_frag(tb, v[0]);
       uint64_t sp[4], s2[kG];
       if (MODE == kWgrad) {
-        ps += args.k;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sp[j] = pack2(sp_next[j], sp_next[j]);
-          if (kb + 1 < kb1 && 8 * j < left) sp_next[j] = ps[8 * j];
-        }
+        for (int j = 0; j < 4; ++j) sp[j] = pack2(sp_next[j], sp_next[j]);
+        if (kb + 1 < t.kb1) lane_scales(t, kb + 1);
       }
       const float* scs = sc + (it % C::kSlots) * BN + c0 + cl;
       tmem_ld_wait();
@@ -494,17 +526,19 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         }
       }
     }
-    const Fp8Tile t = tile_at<BN, MODE>(walk, args, id, rank);
     const int n = min(C::kAcc, t.ncols - c0);   // live columns (may be negative)
-    // (ok, rank and n are the same for the warpgroup)
-    if (!ok || rank != 0 || n <= 0 || (args.accumulate && t.kb0 == t.kb1)) continue;
     const int lanes = min(128, t.lanes);
     const long long base = t.out + static_cast<long long>(c0) * args.ldo;
+    const bool store = ok && rank == 0 && n > 0 && !(args.accumulate && t.kb0 == t.kb1);
+    // the next tile, and its first scales, before this one is stored
+    if (id + step < walk.total) {
+      if (ok) fetch(id + step);
+      if (MODE == kWgrad && ok && t.kb0 < t.kb1) lane_scales(t, t.kb0);
+    }
+    if (!store) continue;   // (the same for the warpgroup)
     const bool f32 = args.out_f32 || args.accumulate;   // (a bf16 sum is rounded once, after the addition)
     if (!f32) {
       // all columns, transposed on the way: column c is 256 bytes at so + 272 c
-      bulk_wait_read();
-      named_barrier(1 + half, 128);
 #pragma unroll
       for (int g = 0; g < C::kAcc / 8; ++g) {
         uint32_t w[4];
@@ -516,26 +550,35 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         }
         stmatrix_x4_trans(smem_u32(so + (8 * g + (lane & 7)) * 272 + (quad * 4 + (lane >> 3)) * 16), w);
       }
-      fence_async_smem();
       named_barrier(1 + half, 128);
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + base;
       if (args.out_vec) {
-        if (tid < n) {
-          bulk_store(o + static_cast<long long>(tid) * args.ldo, smem_u32(so + tid * 272), lanes * 2);
-          bulk_commit();
+        // two columns to a store instruction, kBatch loads under way together
+        constexpr int kBatch = C::kAcc / 8 < 8 ? C::kAcc / 8 : 8;
+        const int part = (lane & 15) * 8, c0v = quad * 2 + (lane >> 4);
+        o += static_cast<long long>(c0v) * args.ldo + part;
+#pragma unroll
+        for (int b = 0; b < C::kAcc / 8; b += kBatch) {
+          uint4 q[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            q[i] = *reinterpret_cast<const uint4*>(so + (c0v + 8 * (b + i)) * 272 + part * 2);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (part < lanes && c0v + 8 * (b + i) < n)
+              *reinterpret_cast<uint4*>(o + 8LL * (b + i) * args.ldo) = q[i];
         }
       } else if (tid < lanes) {
         for (int c = 0; c < n; ++c)
           o[static_cast<long long>(c) * args.ldo + tid] = *reinterpret_cast<const __nv_bfloat16*>(so + c * 272 + tid * 2);
       }
+      named_barrier(1 + half, 128);   // (it is written again)
     } else {
       // kOutCols columns at a time: column c is 512 bytes at so + 528 c
 #pragma unroll
       for (int round = 0; round < C::kAcc / C::kOutCols; ++round) {
         const int here = min(C::kOutCols, n - round * C::kOutCols);
         if (here <= 0) break;   // (the same for the warpgroup)
-        bulk_wait_read();
-        named_barrier(1 + half, 128);
 #pragma unroll
         for (int g = 0; g < C::kOutCols / 8; ++g)
 #pragma unroll
@@ -546,15 +589,30 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
             o[0] = x;
             o[132] = y;
           }
-        fence_async_smem();
         named_barrier(1 + half, 128);
         const long long o = base + static_cast<long long>(round * C::kOutCols) * args.ldo;
         if (args.out_vec && args.out_f32) {
-          if (tid < here) {
-            float* d = static_cast<float*>(args.out) + o + static_cast<long long>(tid) * args.ldo;
-            if (args.accumulate) bulk_add(d, smem_u32(so + tid * 528), lanes * 4);
-            else bulk_store(d, smem_u32(so + tid * 528), lanes * 4);
-            bulk_commit();
+          // a column to a store instruction, kBatch columns' loads under way together
+          constexpr int kBatch = C::kOutCols / 4 < 8 ? C::kOutCols / 4 : 8;
+          const int part = lane * 4;
+          float* d = static_cast<float*>(args.out) + o + static_cast<long long>(quad) * args.ldo + part;
+#pragma unroll
+          for (int b = 0; b < C::kOutCols / 4; b += kBatch) {
+            float4 q[kBatch], old[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              q[i] = *reinterpret_cast<const float4*>(so + (quad + 4 * (b + i)) * 528 + part * 4);
+              old[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (args.accumulate && part < lanes && quad + 4 * (b + i) < here)
+                old[i] = *reinterpret_cast<const float4*>(d + 4LL * (b + i) * args.ldo);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              if (args.accumulate)
+                q[i] = make_float4(old[i].x + q[i].x, old[i].y + q[i].y, old[i].z + q[i].z, old[i].w + q[i].w);
+              if (part < lanes && quad + 4 * (b + i) < here)
+                *reinterpret_cast<float4*>(d + 4LL * (b + i) * args.ldo) = q[i];
+            }
           }
         } else if (tid < lanes) {
           for (int c = 0; c < here; ++c) {
@@ -569,11 +627,11 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
             }
           }
         }
+        named_barrier(1 + half, 128);   // (it is written again)
       }
     }
     __syncwarp();
   }
-  bulk_wait();
 }
 
 template <int BN, int MODE>
@@ -589,13 +647,17 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
   float* sc = reinterpret_cast<float*>(stage_out + C::kOutBytes * (C::kEpiWarps / 4));   // [kSlots][BN]
   int* start = reinterpret_cast<int*>(sc + C::kSlots * BN);                              // [E + 1]
   Fp8Info* infos = reinterpret_cast<Fp8Info*>(start + kMaxGroups + 4);                   // [kInfos] (kRows)
-  uint64_t* full = reinterpret_cast<uint64_t*>(infos + (MODE == kRows ? kInfos : 0));
+  Fp8Tile* tiles = reinterpret_cast<Fp8Tile*>(start + kMaxGroups + 4);                   // [kTileRing] (kWgrad)
+  uint64_t* full = MODE == kWgrad ? reinterpret_cast<uint64_t*>(tiles + kTileRing)
+                                  : reinterpret_cast<uint64_t*>(infos + (MODE == kRows ? kInfos : 0));
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + C::kBufs;
   uint64_t* sfull = acc_empty + C::kBufs;
   uint64_t* sempty = sfull + C::kSlots;
-  uint64_t* mma_done = sempty + C::kSlots;
+  uint64_t* tfull = sempty + C::kSlots;   // [kTileRing] (kWgrad)
+  uint64_t* tempty = tfull + kTileRing;
+  uint64_t* mma_done = tempty + kTileRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -611,6 +673,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&sempty[s], C::kEpiWarps);
+    }
+    for (int i = 0; i < kTileRing; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], C::kEpiWarps);
     }
     mbar_init(mma_done, 2);
     fence_mbar_init();
@@ -763,6 +829,17 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
         const float* w = (MODE == kRows ? args.qs : args.ps) + (static_cast<long long>(t.e) * nb + b0) * args.num_kb;
         const bool two = MODE == kRows && b0 + 1 < nb;
         bool told = false;
+        if (MODE == kWgrad) {
+          if (!mbar_wait(&tempty[tile % kTileRing], ((tile / kTileRing) & 1) ^ 1, budget)) {
+            if (args.status) atomicOr(args.status, kErrWaitProducer);
+            break;
+          }
+          if (lane == 0) {
+            tiles[tile % kTileRing] = t;
+            mbar_arrive(&tfull[tile % kTileRing]);
+          }
+          ++tile;
+        }
         for (int kb = t.kb0; ok && kb < t.kb1; kb += kBatch) {
           float v[kBatch][kPer], u[kBatch][2];
 #pragma unroll
@@ -805,7 +882,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
     if constexpr (C::kInc > 0) regs_inc<C::kInc>();
     const Fp8Ring<BN, MODE> ring = {acc_full, acc_empty, sempty, args.status, budget};
     if constexpr (MODE == kRows) epilogue_rows<BN>(args, walk, ring, sc, infos, stage_out, tmem, id0, step);
-    else epilogue_cols<BN, MODE>(args, walk, ring, sc, red, stage_out, tmem, id0, step, rank);
+    else epilogue_cols<BN, MODE>(args, walk, ring, sc, red, stage_out, tmem, id0, step, rank, tiles, tfull, tempty);
   }
   if (MODE == kSplit) {
     // the cluster barriers count every thread; warps (and CTAs) without a tile pass them here
@@ -830,9 +907,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
 }
 
 template <int BN, int MODE>
-cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, const Fp8Args& a, long long tiles,
-                       cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, Fp8Args a, long long tiles, cudaStream_t s) {
   using C = Fp8Cfg<BN, MODE>;
+  const unsigned others = (MODE == kWgrad ? a.k + 127 : MODE == kRows ? a.n + 255 : a.n + 127) / (MODE == kRows ? 256 : 128);
+  a.by_others = FastDiv::of(others);
+  a.by_group = FastDiv::of(others * kRasterGroup);
+  a.by_E = FastDiv::of(a.E);
   auto kern = gemm_fp8_kernel<BN, MODE>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
