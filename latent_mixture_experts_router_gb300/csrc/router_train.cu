@@ -14,7 +14,7 @@
 // registers (G V >= E), so a warp has 32 / G rows under way, and loads its next ones before it
 // works on the present ones.  exp is one FMA and ex2: exp2(l log2e - m log2e), exact in m's part
 // (it cancels in p).  The column sums of p stay in registers over a warp's rows, are added over the
-// CTA's warps and, through the cluster's shared memory, over four CTAs, always in the same order;
+// CTA's warps and, through the cluster's shared memory, over eight CTAs, always in the same order;
 // one cluster finishes by itself, several leave a row of sums each for a second kernel.
 #include <algorithm>
 
@@ -27,7 +27,8 @@ namespace {
 
 constexpr int kLossWarps = 16, kGradWarps = 8;
 constexpr int kLossThreads = kLossWarps * 32, kGradThreads = kGradWarps * 32;
-constexpr int kCluster = 4;
+constexpr int kCluster = 8;
+constexpr int kMaxClusters = 36;   // two CTAs on 144 of 152 SMs: what fits inside the units' borders
 constexpr float kLog2e = 1.4426950408889634f;
 
 LMOE_DEV float to_f32(float v) { return v; }
@@ -302,19 +303,36 @@ __global__ void __launch_bounds__(kFinishThreads) losses_finish_kernel(const Los
   int W = 32;
   while (W < a.E) W *= 2;   // E <= 1024
   const int groups = kFinishThreads / W, grp = threadIdx.x / W, e = threadIdx.x % W;
+  constexpr int kPerLane = (kMaxClusters + 31) / 32, kBatch = 12;
   float p = 0.f, z = 0.f, n = 0.f;   // (counts of rows are exact in fp32: at most 2^20)
   int c = 0;
-#pragma unroll 1
-  for (int q = lane; q < a.clusters; q += 32) {
-    n += static_cast<float>(a.part_n[q]);
-    z += a.part_z[q];
+  // every load of a thread under way before the first sum
+  float zs[kPerLane], ps[kBatch];
+  int ns[kPerLane], cs[kBatch];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const bool in = lane + 32 * i < a.clusters;
+    ns[i] = in ? a.part_n[lane + 32 * i] : 0;
+    zs[i] = in ? a.part_z[lane + 32 * i] : 0.f;
   }
-  if (e < a.E) {
-#pragma unroll 10
-    for (int q = grp; q < a.clusters; q += groups) {
-      p += a.part_p[q * a.E + e];
-      c += a.part_c[q * a.E + e];
+  for (int q0 = grp; q0 < a.clusters; q0 += groups * kBatch) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int q = q0 + i * groups;
+      const bool in = q < a.clusters && e < a.E;
+      ps[i] = in ? a.part_p[q * a.E + e] : 0.f;
+      cs[i] = in ? a.part_c[q * a.E + e] : 0;
     }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      p += ps[i];
+      c += cs[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    n += static_cast<float>(ns[i]);
+    z += zs[i];
   }
   n = group_sum<32>(n);
   z = group_sum<32>(z);
@@ -360,7 +378,7 @@ struct GradArgs {
 };
 
 template <typename T, int G, int V, bool VEC>
-__global__ void __launch_bounds__(kGradThreads, V <= 16 ? 3 : 2) grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, V <= 16 ? 4 : 2) grad_kernel(const GradArgs a) {
   constexpr int kRows = 32 / G, kSlots = G < 16 ? 16 / G : 1;
   extern __shared__ float sm_row[];   // [rows of the CTA][E]: a row while its slots' terms are added
   __shared__ int sm_id[G < 16 ? kGradWarps * kRows : 1][16];
@@ -372,35 +390,31 @@ __global__ void __launch_bounds__(kGradThreads, V <= 16 ? 3 : 2) grad_kernel(con
   griddep_enter();
   const T* logits = static_cast<const T*>(a.logits);
   T* out = static_cast<T*>(a.out);
-  const int step = gridDim.x * kGradWarps * kRows;
-  float next[V], gnext[kSlots];
-  int inext[kSlots];
-  int t = (blockIdx.x * kGradWarps + warp) * kRows + g;
-  bool live;
+  // one row per group: more CTAs hide the latencies better than rows loaded ahead, whose registers
+  // they need (16384 x 256 bf16: 10.3 us, loaded ahead 11.6)
+  const int t = (blockIdx.x * kGradWarps + warp) * kRows + g;
+  float v[V], gw[kSlots], sel[kSlots];
+  int id[kSlots];
+  bool on = t < a.T;
 #pragma unroll
-  for (int i = 0; i < V; ++i) next[i] = -INFINITY;
-  // row t, if there is one: loaded beside its mask, not after it
-  const auto fetch = [&] {
-    live = t < a.T;
+  for (int i = 0; i < V; ++i) v[i] = -INFINITY;
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-      inext[s] = -1;
-      gnext[s] = 0.f;
+  for (int s = 0; s < kSlots; ++s) {
+    id[s] = -1;
+    gw[s] = 0.f;
+  }
+  if (on) {   // the row beside its mask and its slots, not after them
+    load_row<T, G, V, VEC>(logits + t * a.ld, a.E, l, v);
+    if (a.gw != nullptr) {
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        if (l + G * s < a.k) {
+          id[s] = a.idx[static_cast<long long>(t) * a.k + l + G * s];
+          gw[s] = a.gw[static_cast<long long>(t) * a.k + l + G * s];
+        }
     }
-    if (live) {
-      load_row<T, G, V, VEC>(logits + t * a.ld, a.E, l, next);
-      if (a.gw != nullptr) {
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-          if (l + G * s < a.k) {
-            inext[s] = a.idx[static_cast<long long>(t) * a.k + l + G * s];
-            gnext[s] = a.gw[static_cast<long long>(t) * a.k + l + G * s];
-          }
-      }
-      if (a.mask != nullptr) live = a.mask[t] != 0;
-    }
-  };
-  fetch();
+    if (a.mask != nullptr) on = a.mask[t] != 0;
+  }
   float cb = 0.f, cz = 0.f;
   if (a.gl != nullptr) {
     const float inv = 1.f / max(a.counts[a.E], 1);
@@ -410,18 +424,7 @@ __global__ void __launch_bounds__(kGradThreads, V <= 16 ? 3 : 2) grad_kernel(con
     for (int e = threadIdx.x; e < a.E; e += kGradThreads) sm_f[e] = a.counts[e] * fk;
     __syncthreads();
   }
-  while (t - g < a.T) {   // (the same for the warp)
-    float v[V], gw[kSlots], sel[kSlots];
-    int id[kSlots];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = next[i];
-    const int here = t;
-    bool on = live;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-      id[s] = inext[s];
-      gw[s] = gnext[s];
-    }
+  {
     // the slots' logits are read before the row is written (it may be written in place)
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
@@ -430,57 +433,63 @@ __global__ void __launch_bounds__(kGradThreads, V <= 16 ? 3 : 2) grad_kernel(con
         gw[s] = 0.f;
       }
       sel[s] = id[s] < 0 ? -INFINITY
-                         : to_f32(logits[here * a.ld + id[s]]) + (a.bias != nullptr ? a.bias[id[s]] : 0.f);
+                         : to_f32(logits[t * a.ld + id[s]]) + (a.bias != nullptr ? a.bias[id[s]] : 0.f);
     }
-    t += step;
-    fetch();
     if (a.bias != nullptr) add_bias<G, V, VEC>(a.bias, a.E, l, v);
-    float m = row_max<G>(v);
+    // The row's reductions in two rounds, the maxima and the sums, those of a round side by side (a
+    // round is a chain of shuffles).  sum f p = (sum f exp) / (sum exp), and so for the weights.
+    float m = v[0], sm = sel[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = max_nan(m, v[i]);
+#pragma unroll
+    for (int q = 1; q < kSlots; ++q) sm = max_nan(sm, sel[q]);
+#pragma unroll
+    for (int d = G / 2; d; d >>= 1) {
+      m = max_nan(m, __shfl_xor_sync(~0u, m, d));
+      sm = max_nan(sm, __shfl_xor_sync(~0u, sm, d));
+    }
     on = on && m != -INFINITY;
     m = on ? m : 0.f;
-    const float s = exp_row<G>(v, m), r = 1.f / s;
-    if (a.gl != nullptr) {
-      const float lz = cz * (m + logf(s));
-      float dot = 0.f;
+    const bool none = sm == -INFINITY;   // no slot with a logit above -inf: no weights, no gradient
+    float s = 0.f, sf = 0.f, ws = 0.f, wg = 0.f, w[kSlots];
+    const float c = m * kLog2e;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = col<G, VEC>(l, i);
-        v[i] *= r;
-        if (e < a.E) dot = fmaf(v[i], sm_f[e], dot);
-      }
-      dot = group_sum<G>(dot);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = col<G, VEC>(l, i);
-        if (e < a.E) v[i] *= fmaf(cb, sm_f[e] - dot, lz);
-      }
+    for (int i = 0; i < V; ++i) {
+      const int e = col<G, VEC>(l, i);
+      v[i] = exp2f(fmaf(v[i], kLog2e, -c));
+      s += v[i];
+      if (a.gl != nullptr && e < a.E) sf = fmaf(v[i], sm_f[e], sf);
     }
-    if (!on || a.gl == nullptr) {   // (a row that is not live may hold anything)
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      w[q] = none ? 0.f : exp2f((sel[q] - sm) * kLog2e);
+      ws += w[q];
+      wg = fmaf(w[q], gw[q], wg);
+    }
+#pragma unroll
+    for (int d = G / 2; d; d >>= 1) {
+      s += __shfl_xor_sync(~0u, s, d);
+      sf += __shfl_xor_sync(~0u, sf, d);
+      ws += __shfl_xor_sync(~0u, ws, d);
+      wg += __shfl_xor_sync(~0u, wg, d);
+    }
+    if (on && a.gl != nullptr) {
+      const float r = 1.f / s, lz = cz * (m + logf(s)), dot = sf * r;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = col<G, VEC>(l, i);
+        if (e < a.E) v[i] *= r * fmaf(cb, sm_f[e] - dot, lz);
+      }
+    } else {   // (a row that is not live may hold anything)
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = 0.f;
     }
     if (a.gw != nullptr) {
-      float sm = sel[0];
-#pragma unroll
-      for (int q = 1; q < kSlots; ++q) sm = max_nan(sm, sel[q]);
-      sm = group_max_nan<G>(sm);
-      const bool none = sm == -INFINITY;   // no slot with a logit above -inf: no weights, no gradient
-      float w[kSlots], d[kSlots], ws = 0.f, wg = 0.f;
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        w[q] = none ? 0.f : exp2f((sel[q] - sm) * kLog2e);
-        ws += w[q];
-      }
-      ws = group_sum<G>(ws);
       const float wr = none ? 0.f : 1.f / ws;
+      wg *= wr;
+      float d[kSlots];
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        w[q] *= wr;
-        wg = fmaf(w[q], gw[q], wg);
-      }
-      wg = group_sum<G>(wg);
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q) d[q] = on && id[q] >= 0 ? w[q] * (gw[q] - wg) : 0.f;
+      for (int q = 0; q < kSlots; ++q) d[q] = on && id[q] >= 0 ? w[q] * wr * (gw[q] - wg) : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = col<G, VEC>(l, i);
@@ -528,8 +537,8 @@ __global__ void __launch_bounds__(kGradThreads, V <= 16 ? 3 : 2) grad_kernel(con
       }
       __syncwarp();
     }
-    if (here >= a.T) continue;
-    T* o = out + here * a.ldo;
+    if (t >= a.T) return;
+    T* o = out + t * a.ldo;
     if constexpr (VEC) {
 #pragma unroll
       for (int j = 0; j < V / 4; ++j) {
@@ -575,9 +584,8 @@ int warp_rows(int E) { return E <= 16 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1; }
 bool rows_vec(const void* p, long long ld, int E, int es) {
   return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * es) == 0;
 }
-// CTAs of the losses kernel, in clusters of one or four: one CTA while each warp takes up to four
+// CTAs of the losses kernel, in clusters of one or eight: one CTA while each warp takes up to four
 // turns of rows, then clusters of two turns, as many as the SMs hold.
-constexpr int kMaxClusters = 72;   // two CTAs on 144 of 152 SMs: what fits inside the units' borders
 struct LossGrid {
   int cluster, clusters;
 };
@@ -668,7 +676,7 @@ extern "C" lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dt
   const int turn = kGradWarps * warp_rows(E);   // rows of a CTA at a time
   const size_t smem = static_cast<size_t>(turn + 1) * E * 4;
   const bool vec = rows_vec(logits, ld_logits, E, es) && rows_vec(dlogits, ld_dlogits, E, es);
-  const int grid = std::max(1, std::min((E <= 512 ? 3 : 2) * sm_count(), (T + turn - 1) / turn));
+  const int grid = (T + turn - 1) / turn;
   const cudaError_t e = by_shape(f32, E, vec, [&](auto t, auto g, auto v, auto vc) {
     auto kern = grad_kernel<decltype(t), decltype(g)::value, decltype(v)::value, decltype(vc)::value>;
     const cudaError_t r = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
