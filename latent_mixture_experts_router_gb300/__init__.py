@@ -56,6 +56,7 @@ class LatentMoEBlock:
         self.L = g_pool.shape[0]
         self.I = (W_gate[0] if isinstance(W_gate, tuple) else W_gate).shape[1]
         self._ws = None
+        self._loss_ws = None
 
     def config(self, T: int, act_dtype="bf16", out_dtype="f32") -> Config:
         return Config(T, self.D, self.L, self.E, self.I, self.top_k, self.eps, act_dtype,
@@ -78,4 +79,43 @@ class LatentMoEBlock:
         fn = latent_moe_forward_ex if ex else latent_moe_forward
         fn(cfg, x, w["W_router"], w["W_pool"], w["g_pool"], w["W_gate"], w["W_up"], w["W_down"],
            w["g_expert"], w["W_unpool"], w["g_pre"], w["g_post"], self.top_k, out, ws, stream, **ex)
+        return out
+
+    def _routing(self, cfg: Config):
+        """Views of the logits [T, E] and expert ids [T, k] that a forward call of ``cfg`` left."""
+        if cfg.T > 0 and (self._ws is None or self._ws.numel() < lmoe_workspace_size(cfg)):
+            raise ValueError("no forward call of this configuration came before")
+        lay, T, ld = lmoe_get_workspace_layout(cfg), cfg.T, (self.E + 31) // 32 * 32
+        if T == 0:
+            dev = self.W["g_pre"].device
+            return (torch.empty(0, self.E, device=dev), torch.empty(0, self.top_k, dtype=torch.int32, device=dev))
+
+        def view(name, n, dtype):
+            return self._ws[lay[name]:lay[name] + 4 * n].view(dtype)
+        return (view("logits", T * ld, torch.float32).view(T, ld)[:, :self.E],
+                view("topk_idx", T * self.top_k, torch.int32).view(T, self.top_k))
+
+    def router_losses(self, cfg: Config, router_bias=None, row_mask=None, stream=None):
+        """(losses [2], mean_probs [E], counts [E + 1]) of the last forward call, which had ``cfg``
+        and ``router_bias``: the balance loss and the z loss, as lmoe_router_losses defines them.
+        ``row_mask`` [T]: tokens that are 0 (padding) are left out."""
+        logits, idx = self._routing(cfg)
+        dev = logits.device
+        n = lmoe_router_losses_workspace_size(cfg.T, self.E)
+        if self._loss_ws is None or self._loss_ws.numel() < n:
+            self._loss_ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        losses, mean = torch.empty(2, device=dev), torch.empty(self.E, device=dev)
+        counts = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+        lmoe_router_losses(logits, idx, counts, mean, losses, self._loss_ws, router_bias, row_mask, stream)
+        return losses, mean, counts
+
+    def router_grad(self, cfg: Config, topk_w_grad=None, loss_grads=None, counts=None, router_bias=None,
+                    row_mask=None, out=None, stream=None):
+        """Gradient [T, E] fp32 of the last forward call's router logits from that of its routing
+        weights ``topk_w_grad`` [T, k] and of router_losses' two losses, ``loss_grads`` [2] (with
+        its ``counts``).  Summed over the tokens it is router_bias' gradient."""
+        logits, idx = self._routing(cfg)
+        if out is None:
+            out = torch.empty(logits.shape, device=logits.device)
+        lmoe_router_grad(logits, idx, counts, out, topk_w_grad, loss_grads, router_bias, row_mask, stream)
         return out
