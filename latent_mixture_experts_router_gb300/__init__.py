@@ -26,7 +26,7 @@ from ._lib import (Config, LmoeError, lmoe_workspace_size, lmoe_workspace_size_h
                    SINGLE_TOKEN_KERNEL, SINGLE_TOKEN_CHAIN,
                    lmoe_quantize_nvfp4, lmoe_nvfp4_block_scales, SCALES_ROW_MAJOR, SCALES_BLOCKED,
                    GUARD_BYTES, lmoe_workspace_guards, lmoe_validate_routing,
-                   lmoe_router_losses, lmoe_router_losses_workspace_size, lmoe_router_grad,
+                   lmoe_permute_noalloc, lmoe_router_losses, lmoe_router_losses_workspace_size, lmoe_router_grad,
                    lmoe_quantize_fp8_rows, lmoe_quantize_fp8_weight, lmoe_quantize_fp8_cols,
                    lmoe_fp8_padded_rows, lmoe_matmul_fp8, lmoe_matmul_fp8_wgrad)
 

@@ -12,10 +12,11 @@
 //
 // Both read each logit once; the memory traffic bounds them.  G lanes take a row, V values each in
 // registers (G V >= E), so a warp has 32 / G rows under way, and loads its next ones before it
-// works on the present ones.  exp is one FMA and ex2: exp2(l log2e - m log2e), exact in m's part
-// (it cancels in p).  The column sums of p stay in registers over a warp's rows, are added over the
-// CTA's warps and, through the cluster's shared memory, over eight CTAs, always in the same order;
-// one cluster finishes by itself, several leave a row of sums each for a second kernel.
+// works on the present ones.  exp(l - m) is exp2((l - m) log2e): the difference first, so that a row
+// of the type's lowest value, whose product with log2e overflows, still gets its probabilities.
+// The column sums of p stay in registers over a warp's rows, are added over the CTA's warps and,
+// through the cluster's shared memory, over eight CTAs, always in the same order; one cluster
+// finishes by itself, several leave a row of sums each for a second kernel.
 #include <algorithm>
 
 #include "../../include/latent_moe.h"
@@ -100,11 +101,10 @@ LMOE_DEV void add_bias(const float* bias, int E, int l, float (&v)[V]) {
 // v becomes exp(l - max); returns their sum over the row.  m: the row's maximum, not -inf.
 template <int G, int V>
 LMOE_DEV float exp_row(float (&v)[V], float m) {
-  const float c = m * kLog2e;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    v[i] = exp2f(fmaf(v[i], kLog2e, -c));
+    v[i] = exp2f((v[i] - m) * kLog2e);
     s += v[i];
   }
   return group_sum<G>(s);
@@ -452,11 +452,10 @@ __global__ void __launch_bounds__(kGradThreads, V <= 16 ? 4 : 2) grad_kernel(con
     m = on ? m : 0.f;
     const bool none = sm == -INFINITY;   // no slot with a logit above -inf: no weights, no gradient
     float s = 0.f, sf = 0.f, ws = 0.f, wg = 0.f, w[kSlots];
-    const float c = m * kLog2e;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = col<G, VEC>(l, i);
-      v[i] = exp2f(fmaf(v[i], kLog2e, -c));
+      v[i] = exp2f((v[i] - m) * kLog2e);
       s += v[i];
       if (a.gl != nullptr && e < a.E) sf = fmaf(v[i], sm_f[e], sf);
     }
@@ -661,10 +660,11 @@ extern "C" lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dt
                                         cudaStream_t stream) {
   const lmoe_status st = check_rows(logits, logits_dtype, ld_logits, router_bias, topk_idx, T, E, k);
   if (st != LMOE_OK) return st;
-  if (ld_dlogits < E || (loss_grads == nullptr && topk_w_grad == nullptr)) return LMOE_ERR_ARG;
+  if (ld_dlogits < E) return LMOE_ERR_ARG;
   if (logits == dlogits && ld_logits != ld_dlogits) return LMOE_ERR_ARG;
   if (loss_grads != nullptr && counts == nullptr) return LMOE_ERR_ARG;
-  if (T == 0) return LMOE_OK;
+  if (T == 0) return LMOE_OK;   // (an empty tensor's pointer may be NULL)
+  if (loss_grads == nullptr && topk_w_grad == nullptr) return LMOE_ERR_ARG;
   if (dlogits == nullptr || (topk_w_grad != nullptr && topk_idx == nullptr)) return LMOE_ERR_ARG;
   const bool f32 = logits_dtype == LMOE_F32;
   const int es = f32 ? 4 : 2;

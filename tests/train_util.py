@@ -78,17 +78,17 @@ def router_grad(logits, idx, counts, gw=None, gl=None, bias=None, mask=None):
         gb, gz = gl[0].double() * E / n, gl[1].double() * 2 / n
         dot = (p * f).sum(1, keepdim=True)
         part += p * (gb * (f - dot) + gz * lse)
-        # p and dot: the exponent's argument (twice |l - m| log2 e half steps, and twice those of the
-        # bias added), two ulps of exp2, sums over at most 32 + 5 terms a lane, a reciprocal and two
+        # p and dot: the exponent's argument (three roundings of |l - m| <= 2 top, and the bias added
+        # to l and to m), two ulps of exp2, sums over at most 32 + 5 terms a lane, a reciprocal and two
         # products; lse: five half steps of its largest logit and the sum's
-        rel = U * (2 * 2 * top + 2 * top + 4 + 37 + 37 + 8)
+        rel = U * (3 * 2 * top + 2 * top + 4 + 37 + 37 + 8)
         bound += p * (gb.abs() * (f + dot) * 3 + (gz * lse).abs() * 2) * rel + p * gz.abs() * U * (5 * top + 80)
     if gw is not None:
         w, ok = router_weights(lv, iv)
         g = torch.where(ok, gw[on].double(), 0.0)
         mean = (w * g).sum(1, keepdim=True)
         slots = w * (g - mean)
-        size = w * (g.abs() + (w * g.abs()).sum(1, keepdim=True)) * U * (4 * 2 * top + 4 * top + 60)
+        size = w * (g.abs() + (w * g.abs()).sum(1, keepdim=True)) * U * (2 * 3 * 2 * top + 4 * top + 60)
         ids = iv.long().clamp(0, E - 1)
         part.scatter_add_(1, ids, torch.where(ok, slots, 0.0))
         bound.scatter_add_(1, ids, torch.where(ok, size, 0.0))
@@ -118,9 +118,8 @@ def rule(x, axes, fmt, pow2=False):
 def blocks(x, dim):
     """x with ``dim`` padded by zeros to whole blocks of 128 and split in (blocks, 128)."""
     n = x.shape[dim]
-    pad = [0, 0] * x.dim()
-    pad[2 * (x.dim() - 1 - dim) + 1] = -n % 128
-    return torch.nn.functional.pad(x, pad).unflatten(dim, (-1, 128))
+    zeros = x.new_zeros(*x.shape[:dim], -n % 128, *x.shape[dim + 1:])
+    return torch.cat([x, zeros], dim).unflatten(dim, (-(-n // 128), 128))
 
 
 def gathered(src, index):
