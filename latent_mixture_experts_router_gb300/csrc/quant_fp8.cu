@@ -46,6 +46,21 @@ LMOE_DEV uint32_t cvt4(float a, float b, float c, float d) {
         "mov.b32 %0, {lo, hi};\n\t}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
+// four codes of v * s, the products two to an instruction: the conversions' issue slots are what the
+// gathered rows wait for (4096 x 4096 bf16 to 8 rows each: 40.3 us, one product an instruction 41.4; weights
+// 80.9 and 81.6; columns the same, fp32 ones 62.2 and 61.4: those keep single products)
+template <bool E5M2>
+LMOE_DEV uint32_t cvt4_scaled(float a, float b, float c, float d, float s) {
+  const auto mul = [&](float& x, float& y) {
+    asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %2};\n\t"
+        "mul.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(s));
+  };
+  mul(a, b);
+  mul(c, d);
+  return cvt4<E5M2>(a, b, c, d);
+}
 LMOE_DEV float scale_of(uint32_t amax_bits, const Fmt& f) {
   float s = __fdiv_rn(__uint_as_float(amax_bits), f.largest);
   if (s < 1.17549435e-38f) s = 1.17549435e-38f;
@@ -223,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) rows_kernel(
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      w[i] = cvt4<E5M2>(v[j].get(4 * i) * rj, v[j].get(4 * i + 1) * rj, v[j].get(4 * i + 2) * rj, v[j].get(4 * i + 3) * rj);
+      w[i] = cvt4_scaled<E5M2>(v[j].get(4 * i), v[j].get(4 * i + 1), v[j].get(4 * i + 2), v[j].get(4 * i + 3), rj);
     if (r0 + j < a.rows && in_k) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   }
 }
@@ -323,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kWeightCtas<T>) weight_kernel(const 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const Raw<T, 4>& x = v[4 * q + i];
-      w[i] = cvt4<E5M2>(x.get(0) * inv, x.get(1) * inv, x.get(2) * inv, x.get(3) * inv);
+      w[i] = cvt4_scaled<E5M2>(x.get(0), x.get(1), x.get(2), x.get(3), inv);
       if (n0 + 4 * q + i < a.N && k0 < a.K)
         *reinterpret_cast<uint32_t*>(a.codes + (g * a.N + n0 + 4 * q + i) * a.K + k0) = w[i];
     }
