@@ -424,7 +424,9 @@ lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dtype, long l
  *   code = nearest, ties to even, of v * (1 / s), saturating;   value = code * s
  * A block holding an infinity or NaN gets a scale that is not finite.  A K that is not a multiple
  * of 128 ends in a short block.  K is a multiple of 16 (the tensor memory accelerator's rows).
- * Codes are 16-byte aligned and contiguous, other pointers aligned to their elements.        */
+ * Codes are 16-byte aligned and contiguous, other pointers aligned to their elements.  Up to 2^24
+ * rows, N and K up to 2^20 (else LMOE_ERR_UNSUPPORTED).  No rows: nothing is launched or written,
+ * but for a weight gradient that is not accumulated, which becomes zeros.                    */
 typedef enum { LMOE_FP8_E4M3 = 0, LMOE_FP8_E5M2 = 1 } lmoe_fp8_format;
 
 /* Rows, a block is 128 elements of a row: codes [rows, K], scales [ceil(K/128), rows] fp32.

@@ -13,6 +13,12 @@
 // multiply-adds on the CUDA cores (128 a cycle) beside 128 x 256 x 128 on the tensor cores
 // (8192 a cycle): half the time.
 //
+// Measured: 8192 x 8192 x 16384 884 us (2.49 PFLOP/s), 32768 rows over 64 experts of 4096 x 4096 543 us (2.0;
+// an eighth are ragged tiles), 2560 rows over them 169 us (6.6 TB/s: the weights), 8 rows 26 us, weight
+// gradients of 8192 rows over 16 experts of 4096 x 2048 221 us.  Many rows: bound by the tensor cores'
+// reads of operands and the round trip of the two TMEM buffers.  Weight gradients: by the epilogue's
+// arithmetic and waits (without MMAs and loads 411 of 454 us at 16384 x 4096 x 4096) and its stores.
+//
 // Which operand is the MMA's 128 lanes ("lane operand") and which its columns:
 //   kRows   rows of a are lanes, rows of w columns (128 x 256 tiles): many rows per expert.  A thread
 //           holds one lane, so its scale as ws is one register for 128 columns.
@@ -931,7 +937,7 @@ cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, Fp8Args a, lo
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool known(lmoe_fp8_format f) { return f == LMOE_FP8_E4M3 || f == LMOE_FP8_E5M2; }
 constexpr int kSms = 152;
-constexpr int kRowsMin = 65;
+constexpr int kRowsMin = 55, kRowsMinOne = 65;
 
 }  // namespace
 }  // namespace lmoe
@@ -971,14 +977,16 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   g.status = status;
   g.budget = kDefaultWaitBudget;
   g.splits = 1;
-  // Up to 16 rows in all: 16-column tiles.  Then rows as lanes, unless an expert has fewer than
-  // kRowsMin rows on average or those tiles would leave three quarters of the SMs idle: then 64
-  // rows at a time, four of whose tiles cover one of the others.  Measured, rows as lanes against
-  // 64 at a time, K = N: 256 rows at 4096 18.4 and 12.6 us, 128 rows at 8192 31.6 and 21.8 us;
-  // above the limit, 256 rows at 8192, 34 us as lanes, and one SM's share of 64 at a time doubles.
+  // Up to 16 rows in all: 16-column tiles (8 rows of 64 experts, 4096 x 4096: 26 us, with 64 columns
+  // 66).  Then rows as lanes, unless an expert has fewer than kRowsMin rows on average (one matrix:
+  // kRowsMinOne) or those tiles would leave three quarters of the SMs idle: then 64 rows at a time,
+  // four of whose tiles cover one of the others.  Measured, rows as lanes against 64 at a time:
+  //   64 experts of 4096 x 4096 with 44, 52, 58, 64, 96 rows   183, 196, 194, 189, 202 us and 176, 192, 197, 207, 264
+  //   one matrix of 8192 x 16384 with 64 and 100 rows          41, 41 and 23, 40
+  //   256 rows by 4096 x 4096, 128 and 512 by 8192 x 8192      18.4, 31.6, 38 and 12.6, 21.9, 75
   const long long live = c->n_experts < c->rows ? c->n_experts : c->rows;
   const long long row_tiles = ((c->rows + 127) / 128 + live - 1) * ((c->N + 255) / 256);   // at most
-  const bool rows = c->rows / live >= kRowsMin && row_tiles * 4 > kSms;
+  const bool rows = c->rows / live >= (c->n_experts == 1 ? kRowsMinOne : kRowsMin) && row_tiles * 4 > kSms;
   const int bn = rows ? 256 : c->rows <= 16 ? 16 : 64;
   const unsigned long long K = c->K, N = c->N;
   const unsigned long long wd[3] = {K, N, static_cast<unsigned long long>(c->n_experts)}, wst[2] = {K, K * N};
@@ -1001,7 +1009,8 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
     g.fmt_p = c->b_format;
     g.fmt_q = c->a_format;
     const long long tiles = ((c->rows + bn - 1) / bn + live - 1) * wt;   // at most
-    // Few tiles: split the reduction among the CTAs of a cluster, at least four blocks each.
+    // Few tiles: split the reduction among the CTAs of a cluster, at least four blocks each (1 and 64
+    // rows by 4096 x 4096: 7.4 and 9.5 us, one CTA a tile 10.9 and 12.1; 16 by 8192 x 8192 12.2 and 17.9).
     while (g.splits < (bn == 16 ? 8 : 4) && tiles * g.splits * 2 <= kSms && g.num_kb / (g.splits * 2) >= 4) g.splits *= 2;
     if (g.splits > 1) e = bn == 16 ? launch_one<16, kSplit>(tw, ta, g, tiles, stream) : launch_one<64, kSplit>(tw, ta, g, tiles, stream);
     else e = bn == 16 ? launch_one<16, kCols>(tw, ta, g, tiles, stream) : launch_one<64, kCols>(tw, ta, g, tiles, stream);

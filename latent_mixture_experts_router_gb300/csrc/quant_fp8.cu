@@ -13,7 +13,10 @@
 // weight: [G][N, K], a block is 128 x 128; scales [N/128][K/128]; the transpose on request
 // cols:   [rows, K], a block is 128 rows of one column; codes transposed, [K][padded rows], each
 //         expert's rows padded to whole blocks; scales [blocks][K]
-// All three read and write each element once; the memory traffic bounds them.
+// All three read and write each element once; the memory traffic bounds them.  Measured: 16384 x 8192
+// bf16 rows 59.9 us (6.7 TB/s), 4096 x 4096 gathered to 8 rows each 40.3 us (issue slots: each row is
+// converted eight times); 8 x 4096 x 4096 bf16 weights, both orientations, 80.9 us (6.6 TB/s); columns of 16384 x
+// 4096 bf16 39.5 us (5.1 TB/s, issue slots at 65 %).
 #include <algorithm>
 
 #include "../../include/latent_moe.h"

