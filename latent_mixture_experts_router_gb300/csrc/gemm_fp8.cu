@@ -146,6 +146,17 @@ LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
 LMOE_DEV void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -429,7 +440,9 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
   const int r = quad * 32 + (lane >> 2);                // lanes r, + 8, + 16, + 24 of the tile
   const int c0 = half * C::kAcc, cl = (lane & 3) * 2;   // columns c0 + 8 g + cl, + 1
   const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-  constexpr int kChC = C::kAcc >= 32 ? 32 : 16;         // columns of one TMEM read
+  // columns of one TMEM read: as many as the registers hold (64 columns in reads of 64: 20.8 us for 128
+  // rows by 8192 x 8192, in reads of 32 21.4; a weight gradient's 128 sums leave room for 32)
+  constexpr int kChC = C::kAcc == 64 ? 64 : C::kAcc > 64 ? 32 : 16;
   constexpr int kG = kChC / 8, kN = C::kAcc / kChC * 2;
   uint8_t* so = stage_out + half * C::kOutBytes;
   int it = 0;
