@@ -14,7 +14,7 @@
 // (8192 a cycle): half the time.
 //
 // Measured: 8192 x 8192 x 16384 884 us (2.49 PFLOP/s), 32768 rows over 64 experts of 4096 x 4096 543 us (2.0;
-// an eighth are ragged tiles), 2560 rows over them 169 us (6.6 TB/s: the weights), 8 rows 26 us, weight
+// an eighth are ragged tiles), 2560 rows over them 170 us (6.5 TB/s: the weights), 8 rows 24.3 us, weight
 // gradients of 8192 rows over 16 experts of 4096 x 2048 221 us.  Many rows: bound by the tensor cores'
 // reads of operands and the round trip of the two TMEM buffers.  Weight gradients: by the epilogue's
 // arithmetic and waits (without MMAs and loads 411 of 454 us at 16384 x 4096 x 4096) and its stores.
@@ -956,7 +956,7 @@ cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, Fp8Args a, lo
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool known(lmoe_fp8_format f) { return f == LMOE_FP8_E4M3 || f == LMOE_FP8_E5M2; }
 constexpr int kSms = 152;
-constexpr int kRowsMin = 55, kRowsMinOne = 65;
+constexpr int kRowsMin = 55, kRowsMinOne = 65, kFewRows = 8;
 
 }  // namespace
 }  // namespace lmoe
@@ -996,8 +996,10 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   g.status = status;
   g.budget = kDefaultWaitBudget;
   g.splits = 1;
-  // Up to 16 rows in all: 16-column tiles (8 rows of 64 experts, 4096 x 4096: 26 us, with 64 columns
-  // 66).  Then rows as lanes, unless an expert has fewer than kRowsMin rows on average (one matrix:
+  // Up to 16 rows in all, or up to kFewRows for an expert on average: 16-column tiles.  Measured
+  // against 64 columns, 4096 x 4096: 1 row 6.8 us and 9.1, 8 and 24 rows of 64 experts 24.3, 45.5 and 26.0, 48.5, 480 rows
+  // of them 155 and 161; beyond the limit 800 and 1024 rows 164, 172 and 163, 163, 20 rows of 2 experts 18 and 12.
+  // Then rows as lanes, unless an expert has fewer than kRowsMin rows on average (one matrix:
   // kRowsMinOne) or those tiles would leave three quarters of the SMs idle: then 64 rows at a time,
   // four of whose tiles cover one of the others.  Measured, rows as lanes against 64 at a time:
   //   64 experts of 4096 x 4096 with 44, 52, 58, 64, 96 rows   183, 196, 194, 189, 202 us and 176, 192, 197, 207, 264
@@ -1006,7 +1008,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   const long long live = c->n_experts < c->rows ? c->n_experts : c->rows;
   const long long row_tiles = ((c->rows + 127) / 128 + live - 1) * ((c->N + 255) / 256);   // at most
   const bool rows = c->rows / live >= (c->n_experts == 1 ? kRowsMinOne : kRowsMin) && row_tiles * 4 > kSms;
-  const int bn = rows ? 256 : c->rows <= 16 ? 16 : 64;
+  const int bn = rows ? 256 : c->rows <= 16 || c->rows / live <= kFewRows ? 16 : 64;
   const unsigned long long K = c->K, N = c->N;
   const unsigned long long wd[3] = {K, N, static_cast<unsigned long long>(c->n_experts)}, wst[2] = {K, K * N};
   const unsigned long long ad[2] = {K, static_cast<unsigned long long>(c->rows)}, ast[1] = {K};

@@ -283,6 +283,20 @@ def test_rows_of_no_expert_are_left(lm, R, N):
         check_matmul(lm, *a, torch.tensor(offs, dtype=torch.int32, device="cuda"), torch.bfloat16, True)
 
 
+@pytest.mark.parametrize("R,E,N,K", [(5, 4, 131, 144), (33, 2, 257, 272), (60, 30, 130, 144), (70, 3, 131, 400), (500, 40, 136, 160)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_tiles_that_end_with_the_rows(lm, R, E, N, K, out):
+    # experts whose tiles reach past the last row start earlier and leave the rows before their own alone
+    a = matmul_case(R, E, N, K, E4M3, E4M3)
+    last = torch.full((E + 1,), R, dtype=torch.int32, device="cuda")
+    last[:-1] = torch.arange(E, device="cuda").int() + R - E          # one row each, the last rows
+    for offs in (split(R, E, 3, empty=0.0), last, torch.clamp(last, max=R - 1)):
+        check_matmul(lm, *a, offs, out, True)
+        buf = torch.full((3 + R * N,), 7.25, dtype=out, device="cuda")
+        check_matmul(lm, *a, offs, out, True, out=buf[3:].view(R, N))
+        assert bool((buf[:3] == 7.25).all())
+
+
 def test_matmul_bad_offsets_are_clamped(lm):
     for R, N in ((12, 256), (200, 700), (1200, 5000)):
         a = matmul_case(R, 2, N, 144, E4M3, E4M3)
