@@ -318,6 +318,11 @@ LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
   return t;
 }
 
+// Row tiles of `unit` rows that any split of `rows` among E experts takes at most (rows > 0).
+__host__ __device__ constexpr int most_tiles(int rows, int E, int unit) {
+  return (rows + unit - 1) / unit + (E < rows ? E : rows) - 1;
+}
+
 // What an epilogue thread needs to wait for the blocks of its tile.
 template <int BN, int MODE>
 struct Fp8Ring {
@@ -731,7 +736,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
   __syncthreads();
   if (warp == 0) {   // a run of groups per lane
     const int per = (args.E + 31) / 32, e0 = min(lane * per, args.E), e1 = min(e0 + per, args.E);
-    const int cap = MODE == kWgrad ? static_cast<int>(args.rows / 128) : 0x7fffffff;
+    // no more units than the launch has room for, whatever the offsets say (kSplit: one tile to a cluster)
+    const int rows = static_cast<int>(args.rows);
+    const int cap = MODE == kWgrad ? rows / 128 : most_tiles(rows, args.E, kUnit);
     int sum = 0;
     for (int e = e0; e < e1; ++e) sum += start[e];
     int run = sum;
@@ -1006,7 +1013,8 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   //   one matrix of 8192 x 16384 with 64 and 100 rows          41, 41 and 23, 40
   //   256 rows by 4096 x 4096, 128 and 512 by 8192 x 8192      18.4, 31.6, 38 and 12.6, 21.9, 75
   const long long live = c->n_experts < c->rows ? c->n_experts : c->rows;
-  const long long row_tiles = ((c->rows + 127) / 128 + live - 1) * ((c->N + 255) / 256);   // at most
+  const int R = static_cast<int>(c->rows);
+  const long long row_tiles = 1LL * most_tiles(R, c->n_experts, 128) * ((c->N + 255) / 256);
   const bool rows = c->rows / live >= (c->n_experts == 1 ? kRowsMinOne : kRowsMin) && row_tiles * 4 > kSms;
   const int bn = rows ? 256 : c->rows <= 16 || c->rows / live <= kFewRows ? 16 : 64;
   const unsigned long long K = c->K, N = c->N;
@@ -1030,7 +1038,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
     g.qs = a_scales;
     g.fmt_p = c->b_format;
     g.fmt_q = c->a_format;
-    const long long tiles = ((c->rows + bn - 1) / bn + live - 1) * wt;   // at most
+    const long long tiles = most_tiles(R, c->n_experts, bn) * wt;
     // Few tiles: split the reduction among the CTAs of a cluster, at least four blocks each (1 and 64
     // rows by 4096 x 4096: 7.4 and 9.5 us, one CTA a tile 10.9 and 12.1; 16 by 8192 x 8192 12.2 and 17.9).
     while (g.splits < (bn == 16 ? 8 : 4) && tiles * g.splits * 2 <= kSms && g.num_kb / (g.splits * 2) >= 4) g.splits *= 2;

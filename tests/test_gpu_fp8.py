@@ -306,6 +306,21 @@ def test_matmul_bad_offsets_are_clamped(lm):
             assert bool((y[R:] == 7.25).all())
 
 
+@pytest.mark.parametrize("R,N,K", [(3, 128, 4096), (12, 256, 4096), (200, 700, 2048), (1200, 5000, 144)])
+def test_matmul_offsets_that_go_back_end_in_bounds(lm, R, N, K):
+    # decreasing offsets name rows several times: the products are anyone's, but the call ends, reports
+    # nothing and writes rows 0 .. R - 1 only (the first two sizes split K over a cluster)
+    E = 6
+    a, a_s, w, w_s = matmul_case(R, E, N, K, E4M3, E4M3)
+    y = torch.full((R + 64, N), 7.25, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for offs in ([0, R, 0, R, 0, R, 0], [R, 0, R, 0, R, 0, R], [0, R, 1, R, 2, R, R]):
+        off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        lm.lmoe_matmul_fp8(a, a_s, w, w_s, y[:R], offsets=off, status=status)
+        torch.cuda.synchronize()
+        assert int(status) == 0 and bool((y[R:] == 7.25).all())
+
+
 @pytest.mark.parametrize("R,N,K", [(3, 264, 256), (50, 1000, 400), (600, 5000, 256)])
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_matmul_output_at_any_element(lm, R, N, K, out):
