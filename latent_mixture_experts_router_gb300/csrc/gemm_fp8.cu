@@ -209,6 +209,17 @@ LMOE_DEV void regs_inc() {
 LMOE_DEV void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same barrier, with whether every thread's `ok` is set.
+LMOE_DEV bool named_barrier_all(int id, int threads, bool ok) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<int>(ok))
+      : "memory");
+  return r != 0;
+}
 // Rows of group e, clamped into the rows there are, so that no offsets send a load or a store out
 // of range.
 LMOE_DEV void group_rows(const Fp8Args& a, int e, int& lo, int& hi) {
@@ -486,12 +497,12 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
       if (r + 8 * j < u.lanes) sp_next[j] = ps[8 * j];
   };
   if (MODE == kWgrad && ok && id0 < walk.total && t.kb0 < t.kb1) lane_scales(t, t.kb0);
-  for (int id = id0; ok && id < walk.total; id += step) {
+  for (int id = id0; id < walk.total; id += step) {
     // acc[g][j]: the column pair of group g, lane 8 j + l / 4 of the warp's 32
     uint64_t acc[C::kAcc / 8][4];
 #pragma unroll
     for (int i = 0; i < C::kAcc / 2; ++i) acc[i >> 2][i & 3] = 0;
-    for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+    for (int kb = t.kb0; ok && kb < t.kb1; ++kb, ++it) {
       ok = ring.wait(it);
       if (!ok) break;
       const uint32_t tb = tq + (it % C::kBufs) * BN;
@@ -566,12 +577,14 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
     const int skip = MODE == kWgrad ? 0 : t.skip;
     const int lanes = min(128, t.lanes);
     const long long base = t.out + static_cast<long long>(c0) * args.ldo;
-    const bool store = ok && rank == 0 && n > 0 && !(args.accumulate && t.kb0 == t.kb1);
+    const bool store = rank == 0 && n > 0 && !(args.accumulate && t.kb0 == t.kb1);
     // the next tile, and its first scales, before this one is stored
     if (id + step < walk.total) {
       if (ok) fetch(id + step);
       if (MODE == kWgrad && ok && t.kb0 < t.kb1) lane_scales(t, t.kb0);
     }
+    // Below, a wait that gave up in one warp ends the whole warpgroup at its next barrier, so that
+    // none of its warps stays at one.
     if (!store) continue;   // (the same for the warpgroup)
     const bool f32 = args.out_f32 || args.accumulate;   // (a bf16 sum is rounded once, after the addition)
     if (!f32) {
@@ -587,7 +600,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         }
         stmatrix_x4_trans(smem_u32(so + (8 * g + (lane & 7)) * 272 + (quad * 4 + (lane >> 3)) * 16), w);
       }
-      named_barrier(1 + half, 128);
+      if (!named_barrier_all(1 + half, 128, ok)) break;
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + base;
       if (args.out_vec) {
         // two columns to a store instruction, kBatch loads under way together
@@ -626,7 +639,8 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
             o[0] = x;
             o[132] = y;
           }
-        named_barrier(1 + half, 128);
+        ok = named_barrier_all(1 + half, 128, ok);
+        if (!ok) break;
         const long long o = base + static_cast<long long>(round * C::kOutCols) * args.ldo;
         if (args.out_vec && args.out_f32) {
           // a column to a store instruction, kBatch columns' loads under way together
@@ -666,6 +680,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         }
         named_barrier(1 + half, 128);   // (it is written again)
       }
+      if (!ok) break;
     }
     __syncwarp();
   }
