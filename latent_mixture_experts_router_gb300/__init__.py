@@ -101,8 +101,8 @@ class LatentMoEBlock:
         ``row_mask`` [T]: tokens that are 0 (padding) are left out."""
         logits, idx = self._routing(cfg)
         dev = logits.device
-        n = lmoe_router_losses_workspace_size(cfg.T, self.E)
-        if self._loss_ws is None or self._loss_ws.numel() < n:
+        if self._loss_ws is None:   # for any T: a captured call keeps its address
+            n = lmoe_router_losses_workspace_size(1 << 20, self.E)
             self._loss_ws = torch.empty(n, dtype=torch.uint8, device=dev)
         losses, mean = torch.empty(2, device=dev), torch.empty(self.E, device=dev)
         counts = torch.empty(self.E + 1, dtype=torch.int32, device=dev)

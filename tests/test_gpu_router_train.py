@@ -369,6 +369,30 @@ def test_block_methods(lm, T, shape):
     assert all(bool((t == 0).all()) for t in empty)
 
 
+def test_block_workspace_outlives_a_captured_call(lm):
+    # a call captured at a small T replays after one at a large T, whose losses need more workspace
+    import workloads
+    from gpu_util import run
+    w = workloads.Workload("rtcap", T=3000, D=256, L=128, E=24, I=128, k=3)
+    inp = workloads.make_inputs(w, torch.device("cuda:0"))
+    _, _, blk, big = run(inp)                       # (the block's own workspace has its full size from here on)
+    small = blk.config(40, "bf16" if inp.x.dtype == torch.bfloat16 else "f32")
+    x = inp.x[:40].contiguous()
+    blk.forward(x)
+    want = [t.clone() for t in blk.router_losses(small)]
+    ws = blk._loss_ws.data_ptr()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = blk.router_losses(small)
+    blk.forward(inp.x)
+    blk.router_losses(big)
+    assert blk._loss_ws.data_ptr() == ws and blk._loss_ws.numel() >= lm.lmoe_router_losses_workspace_size(1 << 20, 24)
+    blk.forward(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_refusals_on_the_device(lm):
     x = made(8, 16, 2)
     dev = dict(device="cuda")
