@@ -482,7 +482,8 @@ typedef struct {
  *  w [n_experts, N, K], w_scales [n_experts, ceil(N/128), ceil(K/128)]   (.._weight; for the input
  *  gradient the transposed pair, with N and K exchanged)
  *  out [rows, N].  Products of a block of 128 are summed by the tensor cores and added, scaled, to
- *  fp32 sums.  status (device, may be NULL): error word as lmoe_check_status reports it, a bit
+ *  fp32 sums; the product of a's and w's scale may lie outside fp32's range where the scaled sum does
+ *  not (likewise for the weight gradient).  status (device, may be NULL): error word as lmoe_check_status reports it, a bit
  *  is set if a device wait gives up; the caller zeroes it.                                  */
 lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* shape, const uint8_t* a, const float* a_scales,
                             const uint8_t* w, const float* w_scales, const int32_t* offsets,

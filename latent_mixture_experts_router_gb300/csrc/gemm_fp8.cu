@@ -79,6 +79,7 @@ struct Fp8Args {
   long long budget;
   int box;               // kCols, kSplit: rows of a that a tile loads
   int splits;            // kSplit: CTAs per tile (the cluster size)
+  float far;             // the largest as ws 2^64 (matmul), p s (wgrad) with which no sum times 2^64 leaves fp32's range
 };
 
 template <int BN, int MODE>
@@ -103,7 +104,9 @@ struct Fp8Cfg {
   static constexpr int kOutCols = kAcc >= 64 ? kAcc / 2 : kAcc;
   static constexpr int kOutBytes = MODE == kRows ? 128 * 272 : kAcc * 272 > kOutCols * 528 ? kAcc * 272 : kOutCols * 528;
   static constexpr int kTableBytes = (kMaxGroups + 4) * 4 + (MODE == kRows ? 16 * 16 : MODE == kWgrad ? 4 * 48 : 0);
-  static constexpr int kFixed = kRedBytes + kSlots * BN * 4 + kOutBytes * (kEpiWarps / 4) + kTableBytes + 512 + 1024;
+  // floats of one: columns' (lanes') scales, their mark, and (few columns) the scales as they are
+  static constexpr int kSlotLd = BN <= 64 ? 2 * BN + 4 : BN + 4;
+  static constexpr int kFixed = kRedBytes + kSlots * kSlotLd * 4 + kOutBytes * (kEpiWarps / 4) + kTableBytes + 512 + 1024;
   static constexpr int kStagesFit = ((kCtas == 2 ? 113 : 227) * 1024 - kFixed) / kStageBytes;
   // an odd number of stages, no more than the TMEM buffers, would break the MMA issuers' waits
   static constexpr int kStagesMost = kStagesFit > 11 ? 11 : kStagesFit;
@@ -187,6 +190,49 @@ LMOE_DEV uint64_t pack2(float lo, float hi) {
   return d;
 }
 LMOE_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+
+// Far scales.  A block's sum v is 0 or between 2^-32 and 2^39 in magnitude (the smallest and the largest
+// product of two codes, 128 of them), so v as ws may be a normal number where as ws is not: a block of
+// zeros has the scale 2^-126, tiny gradients come close to it.
+//
+// So sums are held lifted, times 2^64, and the factor staged for v is as ws 2^64 (wgrad: p 2^64 and s, one after
+// the other): it has all its bits from as ws = 2^-190 on, below which v as ws is less than the smallest
+// number.  Up to Fp8Args::far no lifted sum leaves the range at its other end.  A block with a larger
+// product has a mark beside its scales: matmul then finds them there as they are, and ws in the mark (wgrad:
+// always its largest s).  From a larger product on a sum is held as it is, or lowered by 2^64 if even that is too
+// large: a row's sums in kRows, a column's in kCols and kSplit, a lane's in wgrad, so that far scales of one
+// do not cost the others' small sums (its own blocks with small products then count down to 2^-111, or
+// 2^-47).  Sums are brought back when they are stored.
+// Measured with it and with as ws as one factor of sums as they are: 32768 rows over 64 experts of 4096 x 4096
+// 506 us and 506, 16384 rows by 8192 x 8192 888 and 891, 2560 rows over 64 experts 177.6 and 174.8, 100 rows by 8192 x
+// 8192 24.3 and 22.9, 8 rows over 64 experts 28.1 and 27.8.
+constexpr float kFarLane = 0x1p24f;   // wgrad: of p, so that v p 2^64 stays below 2^127
+constexpr float kLift = 0x1p64f, kFloatMax = 3.402823466e38f;
+// what a sum is held times, as the exponent field of a power of two: 2^64, 1, 2^-64
+enum Held : unsigned { kLifted = 127 + 64, kAsIs = 127, kLowered = 127 - 64 };
+LMOE_DEV float held_times(unsigned h) { return __uint_as_float(h << 23); }
+LMOE_DEV float held_back(unsigned h) { return __uint_as_float((254 - h) << 23); }
+// lowers h to `to` and returns what its sums are multiplied by
+LMOE_DEV float held_lower(unsigned& h, unsigned to) {
+  if (to >= h) return 1.f;
+  const float f = h - to == 64 ? 0x1p-64f : 0x1p-128f;
+  h = to;
+  return f;
+}
+LMOE_DEV bool finite(float v) { return fabsf(v) <= kFloatMax; }
+// matmul: as ws of a marked block in the unit h of its sums, which may be lowered for it: f is what they are
+// multiplied by.  Each multiple of 2 goes where it does not leave the range before the product does.
+LMOE_DEV float marked_product(float a, float b, unsigned& h, float far, float& f) {
+  const float p = fabsf(a) < 1.f ? (a * kLift) * b : a * (b * kLift);
+  f = 1.f;
+  if (!finite(a) || !finite(b)) return a * b;   // (infinities and NaN are what they are in any unit)
+  if (fabsf(p) > far) f = held_lower(h, fabsf(a * b) < 0x1p127f ? kAsIs : kLowered);
+  // (lowered, past 2^191: any factor so large brings any v but 0 out of range)
+  return h == kLifted ? p : h == kAsIs ? a * b : fminf(fmaxf((a * 0x1p-32f) * (b * 0x1p-32f), -kFloatMax), kFloatMax);
+}
+LMOE_DEV void scale_pair(uint64_t& d, float x, float y) {
+  asm volatile("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(pack2(x, y)));
+}
 // Stores four 8 x 8 matrices of 16-bit values transposed: thread l names the 16-byte row l % 8
 // of matrix l / 8; matrix m's elements (row t / 4, columns 2 (t % 4), + 1) are thread t's r[m].
 LMOE_DEV void stmatrix_x4_trans(uint32_t saddr, const uint32_t (&r)[4]) {
@@ -381,14 +427,24 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
     float acc[128];
 #pragma unroll
     for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+    unsigned held = kLifted;   // this thread's sums
     for (int kb = 0; kb < args.num_kb; ++kb, ++it) {
       ok = ring.wait(it);
       if (!ok) break;
       const uint32_t tb = tq + (it % C::kBufs) * BN;
       uint32_t v[2][32];
       tmem_ld_32cols(tb, v[0]);
-      const float s = sc[(it % C::kSlots) * BN + half * 128 + r];
+      float s = sc[(it % C::kSlots) * C::kSlotLd + half * 128 + r];
+      const float2 ws = *reinterpret_cast<const float2*>(sc + (it % C::kSlots) * C::kSlotLd + BN);   // the mark
       tmem_ld_wait();
+      if (ws.x != 0.f || ws.y != 0.f) {   // (the same for the CTA)
+        float f;
+        s = marked_product(s, half ? ws.y : ws.x, held, args.far, f);
+#pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] *= f;
+      } else {
+        s *= held_times(held) * 0x1p-64f;
+      }
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
         if (ch < 3) tmem_ld_32cols(tb + (ch + 1) * 32, v[(ch + 1) & 1]);
@@ -398,6 +454,7 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         if (ch < 3) tmem_ld_wait();
       }
     }
+    const float back = held_back(held);
     const Fp8Info t = infos[tile % kInfos];   // written before the tile's first scales
     const int n = min(128, t.ncols - half * 128);   // live columns (may be negative)
     if (ok && n > 0) {   // (the same for the warp)
@@ -413,15 +470,15 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float* a = acc + round * 64 + 4 * i;
-            *reinterpret_cast<float4*>(mine + lane * 272 + 16 * i) = make_float4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<float4*>(mine + lane * 272 + 16 * i) = make_float4(a[0] * back, a[1] * back, a[2] * back, a[3] * back);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float* a = acc + 8 * i;
             *reinterpret_cast<uint4*>(mine + lane * 272 + 16 * i) =
-                make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                           pack_bf16x2(a[6], a[7]));
+                make_uint4(pack_bf16x2(a[0] * back, a[1] * back), pack_bf16x2(a[2] * back, a[3] * back),
+                           pack_bf16x2(a[4] * back, a[5] * back), pack_bf16x2(a[6] * back, a[7] * back));
           }
         }
         __syncwarp();
@@ -502,6 +559,11 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
     uint64_t acc[C::kAcc / 8][4];
 #pragma unroll
     for (int i = 0; i < C::kAcc / 2; ++i) acc[i >> 2][i & 3] = 0;
+    // what the sums are held times, a byte each: wgrad four lanes, the others a column pair's two beside the next's
+    unsigned held[MODE == kWgrad ? 1 : (C::kAcc / 8 + 1) / 2];
+#pragma unroll
+    for (unsigned& h : held) h = kLifted * 0x01010101u;
+    bool lowered = false;   // any of them (not wgrad; the same for the warp)
     for (int kb = t.kb0; ok && kb < t.kb1; ++kb, ++it) {
       ok = ring.wait(it);
       if (!ok) break;
@@ -509,12 +571,52 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
       uint32_t v[2][kG * 4];
       tmem_ld_frag(tb, v[0]);
       uint64_t sp[4], s2[kG];
+      const float mark = sc[(it % C::kSlots) * C::kSlotLd + BN];
       if (MODE == kWgrad) {
+        float top = 0.f;   // (infinities and NaN are what they are in any unit)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sp[j] = pack2(sp_next[j], sp_next[j]);
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, finite(sp_next[j]) ? fabsf(sp_next[j]) : 0.f);
+        if (top * mark > args.far || top > kFarLane) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p = finite(sp_next[j]) ? fabsf(sp_next[j]) : 0.f;
+            if (!(p * mark > args.far || p > kFarLane)) continue;
+            unsigned h = held[0] >> (8 * j) & 0xff;
+            const float f = held_lower(h, p * mark < 0x1p127f && p < 0x1p88f ? kAsIs : kLowered);
+            held[0] = (held[0] & ~(0xffu << (8 * j))) | h << (8 * j);
+#pragma unroll
+            for (int g = 0; g < C::kAcc / 8; ++g) scale_pair(acc[g][j], f, f);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = sp_next[j] * held_times(held[0] >> (8 * j) & 0xff);
+          sp[j] = pack2(p, p);
+        }
+        __syncwarp();   // (the TMEM reads are the whole warp's)
         if (kb + 1 < t.kb1) lane_scales(t, kb + 1);
       }
-      const float* scs = sc + (it % C::kSlots) * BN + c0 + cl;
+      const float* scs = sc + (it % C::kSlots) * C::kSlotLd + c0 + cl;
+      const auto far_columns = [&] {   // scales of a marked block, or to sums that are not lifted any more
+        lowered = true;
+#pragma unroll
+        for (int g = 0; g < C::kAcc / 8; ++g) {
+          float x[2], f[2] = {1.f, 1.f};
+          unpack2(s2[g % kG], x[0], x[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int at = 8 * (2 * (g & 1) + i);
+            unsigned h = held[g / 2] >> at & 0xff;
+            if (mark != 0.f) x[i] = marked_product(scs[8 * g + i + BN + 4], mark, h, args.far, f[i]);
+            else x[i] *= held_times(h) * 0x1p-64f;
+            held[g / 2] = (held[g / 2] & ~(0xffu << at)) | h << at;
+          }
+          s2[g % kG] = pack2(x[0], x[1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) scale_pair(acc[g][j], f[0], f[1]);
+        }
+      };
+      static_assert(MODE == kWgrad || kN == 2, "all columns' scales at once");
       tmem_ld_wait();
 #pragma unroll
       for (int ch = 0; ch < kN; ++ch) {   // 16 lanes x kChC columns: lane half ch % 2
@@ -526,6 +628,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         if (h == 0) {
 #pragma unroll
           for (int g = 0; g < kG; ++g) s2[g] = *reinterpret_cast<const uint64_t*>(scs + (g0 + g) * 8);
+          if (MODE != kWgrad && (mark != 0.f || lowered)) far_columns();   // (the same for the warp)
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -538,6 +641,16 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         if (ch + 1 < kN) tmem_ld_wait();
       }
       ring.scales_read(it, lane);
+    }
+    float even = 0x1p-64f;   // what is left to be taken out of all sums, as they are stored (wgrad: a lane's own)
+    if (MODE != kWgrad && (MODE == kSplit || lowered)) {   // (the CTAs of a cluster may hold theirs otherwise)
+      even = 1.f;
+#pragma unroll
+      for (int g = 0; g < C::kAcc / 8; ++g) {
+        const unsigned h = held[g / 2] >> (16 * (g & 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) scale_pair(acc[g][j], held_back(h & 0xff), held_back(h >> 8 & 0xff));
+      }
     }
     if (MODE == kSplit) {
       // one tile per cluster: the sums of ranks 1.. go to rank 0 (the i-th four of thread x at
@@ -573,6 +686,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         }
       }
     }
+    const auto back = [&](int j) { return MODE == kWgrad ? held_back(held[0] >> (8 * j) & 0xff) : even; };
     const int n = min(C::kAcc, t.ncols - c0);   // columns to store: below n (may be negative), from skip on
     const int skip = MODE == kWgrad ? 0 : t.skip;
     const int lanes = min(128, t.lanes);
@@ -596,7 +710,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
         for (int j = 0; j < 4; ++j) {
           float x, y;
           unpack2(acc[g][j], x, y);
-          w[j] = pack_bf16x2(x, y);
+          w[j] = pack_bf16x2(x * back(j), y * back(j));
         }
         stmatrix_x4_trans(smem_u32(so + (8 * g + (lane & 7)) * 272 + (quad * 4 + (lane >> 3)) * 16), w);
       }
@@ -636,8 +750,8 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
             float x, y;
             unpack2(acc[round * (C::kOutCols / 8) + g][j], x, y);
             float* o = reinterpret_cast<float*>(so + (8 * g + cl) * 528 + (r + 8 * j) * 4);
-            o[0] = x;
-            o[132] = y;
+            o[0] = x * back(j);
+            o[132] = y * back(j);
           }
         ok = named_barrier_all(1 + half, 128, ok);
         if (!ok) break;
@@ -696,8 +810,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
                                              ~static_cast<uintptr_t>(1023));
   float* red = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
   uint8_t* stage_out = reinterpret_cast<uint8_t*>(red) + C::kRedBytes;
-  float* sc = reinterpret_cast<float*>(stage_out + C::kOutBytes * (C::kEpiWarps / 4));   // [kSlots][BN]
-  int* start = reinterpret_cast<int*>(sc + C::kSlots * BN);                              // [E + 1]
+  float* sc = reinterpret_cast<float*>(stage_out + C::kOutBytes * (C::kEpiWarps / 4));   // [kSlots][kSlotLd]
+  int* start = reinterpret_cast<int*>(sc + C::kSlots * C::kSlotLd);                      // [E + 1]
   Fp8Info* infos = reinterpret_cast<Fp8Info*>(start + kMaxGroups + 4);                   // [kInfos] (kRows)
   Fp8Tile* tiles = reinterpret_cast<Fp8Tile*>(start + kMaxGroups + 4);                   // [kTileRing] (kWgrad)
   uint64_t* full = MODE == kWgrad ? reinterpret_cast<uint64_t*>(tiles + kTileRing)
@@ -867,7 +981,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
     } else if (warp == 2) {
       // ---- scales, the loads of several blocks in flight at a time.  kRows: as[row] ws[half] for
       // the 128 lanes of each column half; kCols, kSplit: as ws of each column; wgrad: of each column
-      constexpr int kPer = (BN + 31) / 32, kBatch = BN >= 128 ? 2 : 4;
+      constexpr int kPer = (BN + 31) / 32, kOwn = MODE == kRows ? 4 : kPer, kBatch = BN >= 128 ? 2 : 4;
       int it = 0, tile = 0;
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
@@ -898,7 +1012,6 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
             const bool in = kb + j < t.kb1;
             u[j][0] = MODE == kWgrad ? 1.f : (in ? w[kb + j] : 0.f);
             u[j][1] = two && in ? w[args.num_kb + kb + j] : u[j][0];
-            constexpr int kOwn = MODE == kRows ? 4 : kPer;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
               v[j][i] = in && lane + 32 * i < live ? q[(kb + j) * ldq + 32 * i] : 0.f;
@@ -919,9 +1032,46 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
               told = true;
               ++tile;
             }
+            float* at = sc + s * C::kSlotLd;
+            if (MODE == kWgrad) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (lane + 32 * i < BN) sc[s * BN + lane + 32 * i] = v[j][i] * u[j][i / 4 & 1];
+              for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i < BN) at[lane + 32 * i] = v[j][i];
+              float top = 0.f;
+#pragma unroll
+              for (int i = 0; i < kPer; ++i) top = fmaxf(top, finite(v[j][i]) ? fabsf(v[j][i]) : 0.f);
+              top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
+              if (lane == 0) at[BN] = top;
+            } else if (MODE == kRows) {
+              const float b0 = u[j][0] * kLift, b1 = u[j][1] * kLift;
+              float top = fabsf(v[j][0]);   // this lane's largest scale (a NaN is left out, and staged as it is)
+#pragma unroll
+              for (int i = 0; i < kPer; ++i) {
+                if (i > 0 && i < kOwn) top = fmaxf(top, fabsf(v[j][i]));
+                if (lane + 32 * i < BN) at[lane + 32 * i] = v[j][i] * (i / 4 & 1 ? b1 : b0);
+              }
+              // (a zero of ws: the mark stays zero, and so do the products)
+              const bool far = !__all_sync(~0u, top * fmaxf(fabsf(b0), fabsf(b1)) <= args.far) && (u[j][0] != 0.f || u[j][1] != 0.f);
+              if (far) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                  if (lane + 32 * i < BN) at[lane + 32 * i] = v[j][i];
+              }
+              if (lane == 0) *reinterpret_cast<float2*>(at + BN) = far ? make_float2(u[j][0], u[j][1]) : make_float2(0.f, 0.f);
+            } else {
+              // the mark without a vote, which a small tile's start would wait for (2560 rows over 64 experts of
+              // 4096 x 4096: 178.6 us, with a vote as above 183)
+              if (lane == 0) at[BN] = 0.f;
+              __syncwarp();
+              const float b0 = u[j][0] * kLift;
+#pragma unroll
+              for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i < BN) {
+                  at[lane + 32 * i] = v[j][i] * b0;
+                  at[BN + 4 + lane + 32 * i] = v[j][i];
+                  if (!(fabsf(v[j][i]) * fabsf(b0) <= args.far) && u[j][0] != 0.f) at[BN] = u[j][0];
+                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sfull[s]);
             ++it;
@@ -977,6 +1127,11 @@ cudaError_t launch_one(const CUtensorMap& p, const CUtensorMap& q, Fp8Args a, lo
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool known(lmoe_fp8_format f) { return f == LMOE_FP8_E4M3 || f == LMOE_FP8_E5M2; }
+// the largest sum of a block's 128 products of codes
+double largest_sum(const lmoe_fp8_matmul& c) {
+  const auto largest = [](lmoe_fp8_format f) { return f == LMOE_FP8_E5M2 ? 57344.0 : 448.0; };
+  return 128.0 * largest(c.a_format) * largest(c.b_format);
+}
 constexpr int kSms = 152;
 constexpr int kRowsMin = 55, kRowsMinOne = 65, kFewRows = 8;
 
@@ -1018,6 +1173,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   g.status = status;
   g.budget = kDefaultWaitBudget;
   g.splits = 1;
+  g.far = static_cast<float>(0x1p126 / (g.num_kb * largest_sum(*c)));
   // Up to 16 rows in all, or up to kFewRows for an expert on average: 16-column tiles.  Measured
   // against 64 columns, 4096 x 4096: 1 row 6.8 us and 9.1, 8 and 24 rows of 64 experts 24.3, 45.5 and 26.0, 48.5, 480 rows
   // of them 155 and 161; beyond the limit 800 and 1024 rows 164, 172 and 163, 163, 20 rows of 2 experts 18 and 12.
@@ -1105,6 +1261,7 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   g.status = status;
   g.budget = kDefaultWaitBudget;
   g.splits = 1;
+  g.far = static_cast<float>(0x1p62 / (c->rows / 128 * largest_sum(*c)));
   const unsigned long long R = static_cast<unsigned long long>(c->rows);
   CUtensorMap tp, tq;
   const unsigned long long pd[2] = {R, static_cast<unsigned long long>(c->K)};
