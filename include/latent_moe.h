@@ -466,13 +466,15 @@ lmoe_status lmoe_quantize_fp8_cols(const void* src, lmoe_dtype src_dtype, long l
  *  N, K       a weight is [N, K]        n_experts  1..1024
  *  a_format, b_format  formats of the first and of the second operand
  *  out_dtype  LMOE_F32 or LMOE_BF16 (one rounding, at the end)
- *  accumulate wgrad: nonzero adds to what dw holds (matmul: must be 0)                      */
+ *  accumulate wgrad: nonzero adds to what dw holds (matmul: must be 0)
+ *  wait_budget_cycles  SM clock cycles a device wait may spin before it gives up (0: default)  */
 typedef struct {
   long long rows;
   int N, K, n_experts;
   lmoe_fp8_format a_format, b_format;
   lmoe_dtype out_dtype;
   int accumulate;
+  long long wait_budget_cycles;
 } lmoe_fp8_matmul;
 
 /* out[r, n] = sum_k a[r, k] w[e, n, k] for the rows offsets[e] <= r < offsets[e+1] of each expert

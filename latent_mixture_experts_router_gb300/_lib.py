@@ -70,7 +70,7 @@ _LAYOUT_FIELDS_NVFP4 = ["xq", "xq_scale", "xq_rowscale", "xe_rowscale", "h_scale
 class lmoe_fp8_matmul(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_longlong), ("N", ctypes.c_int), ("K", ctypes.c_int), ("n_experts", ctypes.c_int),
                 ("a_format", ctypes.c_int), ("b_format", ctypes.c_int), ("out_dtype", ctypes.c_int),
-                ("accumulate", ctypes.c_int)]
+                ("accumulate", ctypes.c_int), ("wait_budget_cycles", ctypes.c_longlong)]
 
 
 class lmoe_workspace_layout(ctypes.Structure):

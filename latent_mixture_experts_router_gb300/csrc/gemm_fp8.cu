@@ -266,6 +266,11 @@ LMOE_DEV bool named_barrier_all(int id, int threads, bool ok) {
       : "memory");
   return r != 0;
 }
+// mbar_wait of a whole warp, with one outcome: its lanes' own waits may give up one by one, and TMEM reads,
+// votes and warp barriers follow that need all of them.
+LMOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, long long budget) {
+  return __all_sync(~0u, mbar_wait(bar, parity, budget));
+}
 // Rows of group e, clamped into the rows there are, so that no offsets send a load or a store out
 // of range.
 LMOE_DEV void group_rows(const Fp8Args& a, int e, int& lo, int& hi) {
@@ -389,9 +394,8 @@ struct Fp8Ring {
   long long budget;
   // the block's products are in their buffer, and its scales staged (the MMA issuer waits for them)
   LMOE_DEV bool wait(int it) const {
-    const bool ok = mbar_wait(&acc_full[it % C::kBufs], (it / C::kBufs) & 1, budget);
+    const bool ok = warp_wait(&acc_full[it % C::kBufs], (it / C::kBufs) & 1, budget);
     if (!ok && status) atomicOr(status, kErrWaitEpilogue);
-    __syncwarp();   // (the TMEM reads that follow are the whole warp's)
     tc_fence_after();
     return ok;
   }
@@ -532,18 +536,21 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
   int tile = 0;
   const auto fetch = [&](int id) {   // the next tile (of the ring: this warp's turn with it ends here)
     if constexpr (MODE == kWgrad) {
-      const int i = tile++ % kTileRing;
-      ok = mbar_wait(&tfull[i], ((tile - 1) / kTileRing) & 1, ring.budget);
-      if (!ok) {
+      if (ok) {
+        const int i = tile % kTileRing;
+        ok = warp_wait(&tfull[i], (tile / kTileRing) & 1, ring.budget);
+        ++tile;
+        if (ok) {
+          t = tiles[i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[i]);
+          return;
+        }
         if (args.status) atomicOr(args.status, kErrWaitEpilogue);
-        return;
       }
-      t = tiles[i];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[i]);
-    } else {
-      t = tile_at<BN, MODE>(walk, args, id, rank);
     }
+    // (wgrad: also once a wait has given up, so that all warps know the same tiles and meet at the same barriers)
+    t = tile_at<BN, MODE>(walk, args, id, rank);
   };
   if (id0 < walk.total) fetch(id0);
   float sp_next[4] = {};   // wgrad: scales of this thread's four lanes in the next block
@@ -694,7 +701,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
     const bool store = rank == 0 && n > 0 && !(args.accumulate && t.kb0 == t.kb1);
     // the next tile, and its first scales, before this one is stored
     if (id + step < walk.total) {
-      if (ok) fetch(id + step);
+      fetch(id + step);
       if (MODE == kWgrad && ok && t.kb0 < t.kb1) lane_scales(t, t.kb0);
     }
     // Below, a wait that gave up in one warp ends the whole warpgroup at its next barrier, so that
@@ -995,7 +1002,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
         const bool two = MODE == kRows && b0 + 1 < nb;
         bool told = false;
         if (MODE == kWgrad) {
-          if (!mbar_wait(&tempty[tile % kTileRing], ((tile / kTileRing) & 1) ^ 1, budget)) {
+          if (!warp_wait(&tempty[tile % kTileRing], ((tile / kTileRing) & 1) ^ 1, budget)) {
             if (args.status) atomicOr(args.status, kErrWaitProducer);
             break;
           }
@@ -1022,7 +1029,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
           for (int j = 0; j < kBatch; ++j) {
             if (!ok || kb + j >= t.kb1) break;
             const int s = it % C::kSlots;
-            if (!mbar_wait(&sempty[s], ((it / C::kSlots) & 1) ^ 1, budget)) {
+            if (!warp_wait(&sempty[s], ((it / C::kSlots) & 1) ^ 1, budget)) {
               if (args.status) atomicOr(args.status, kErrWaitProducer);
               ok = false;
               break;
@@ -1143,7 +1150,7 @@ using namespace lmoe;
 extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* a, const float* a_scales,
                                        const uint8_t* w, const float* w_scales, const int32_t* offsets, void* out,
                                        uint32_t* status, cudaStream_t stream) {
-  if (c == nullptr || c->rows < 0 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
+  if (c == nullptr || c->wait_budget_cycles < 0 || c->rows < 0 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
   if (!known(c->a_format) || !known(c->b_format)) return LMOE_ERR_ARG;
   if (c->accumulate) return LMOE_ERR_ARG;
   if (offsets == nullptr && c->n_experts != 1) return LMOE_ERR_ARG;
@@ -1171,7 +1178,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   g.out_f32 = c->out_dtype == LMOE_F32;
   g.out_vec = aligned(out, 16) && c->N % (g.out_f32 ? 4 : 8) == 0;
   g.status = status;
-  g.budget = kDefaultWaitBudget;
+  g.budget = c->wait_budget_cycles > 0 ? c->wait_budget_cycles : kDefaultWaitBudget;
   g.splits = 1;
   g.far = static_cast<float>(0x1p126 / (g.num_kb * largest_sum(*c)));
   // Up to 16 rows in all, or up to kFewRows for an expert on average: 16-column tiles.  Measured
@@ -1222,7 +1229,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
 extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uint8_t* dy_t, const float* dy_scales,
                                              const uint8_t* x_t, const float* x_scales, const int32_t* offsets,
                                              void* dw, uint32_t* status, cudaStream_t stream) {
-  if (c == nullptr || c->rows < 0 || c->rows % 128 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
+  if (c == nullptr || c->wait_budget_cycles < 0 || c->rows < 0 || c->rows % 128 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
   if (!known(c->a_format) || !known(c->b_format)) return LMOE_ERR_ARG;
   if (offsets == nullptr && c->n_experts != 1) return LMOE_ERR_ARG;
   if (c->out_dtype != LMOE_F32 && c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
@@ -1259,7 +1266,7 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   g.fmt_p = c->b_format;
   g.fmt_q = c->a_format;
   g.status = status;
-  g.budget = kDefaultWaitBudget;
+  g.budget = c->wait_budget_cycles > 0 ? c->wait_budget_cycles : kDefaultWaitBudget;
   g.splits = 1;
   g.far = static_cast<float>(0x1p62 / (c->rows / 128 * largest_sum(*c)));
   const unsigned long long R = static_cast<unsigned long long>(c->rows);
