@@ -485,11 +485,22 @@ typedef struct {
  *  gradient the transposed pair, with N and K exchanged)
  *  out [rows, N].  Products of a block of 128 are summed by the tensor cores and added, scaled, to
  *  fp32 sums; the product of a's and w's scale may lie outside fp32's range where the scaled sum does
- *  not (likewise for the weight gradient).  status (device, may be NULL): error word as lmoe_check_status reports it, a bit
- *  is set if a device wait gives up; the caller zeroes it.                                  */
+ *  not (likewise for the weight gradient).
+ *  status (device): error word as lmoe_check_status reports it, a bit is set if a device wait gives
+ *  up and leaves the product unfinished; the caller zeroes it.  NULL: the device's own word, which
+ *  lmoe_fp8_check_status reads.                                                             */
 lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* shape, const uint8_t* a, const float* a_scales,
                             const uint8_t* w, const float* w_scales, const int32_t* offsets,
                             void* out, uint32_t* status, cudaStream_t stream);
+
+/* Reads (synchronising `stream`) and clears the current device's own error word of the 8-bit
+ * products, in which calls without a status word leave waits that gave up: LMOE_OK, or
+ * LMOE_ERR_TIMEOUT if any did since the last check; *detail (host, may be NULL) receives the word.
+ * One word for all streams: calls whose streams are not ordered before `stream` may still be
+ * running.  Not capturable.                                                                */
+lmoe_status lmoe_fp8_check_status(cudaStream_t stream, uint32_t* detail);
+/* lmoe_wait_selftest for that word: lmoe_fp8_check_status then reports LMOE_ERR_TIMEOUT. */
+lmoe_status lmoe_fp8_wait_selftest(long long budget_cycles, cudaStream_t stream);
 
 /* dw[e, n, k] (+)= sum over expert e's rows r of dy[r, n] x[r, k], from the column-quantised
  * dy_t [N, rows], dy_scales [rows/128, N] (a_format) and x_t [K, rows], x_scales [rows/128, K]

@@ -28,7 +28,8 @@ from ._lib import (Config, LmoeError, lmoe_workspace_size, lmoe_workspace_size_h
                    GUARD_BYTES, lmoe_workspace_guards, lmoe_validate_routing,
                    lmoe_permute_noalloc, lmoe_router_losses, lmoe_router_losses_workspace_size, lmoe_router_grad,
                    lmoe_quantize_fp8_rows, lmoe_quantize_fp8_weight, lmoe_quantize_fp8_cols,
-                   lmoe_fp8_padded_rows, lmoe_matmul_fp8, lmoe_matmul_fp8_wgrad)
+                   lmoe_fp8_padded_rows, lmoe_matmul_fp8, lmoe_matmul_fp8_wgrad,
+                   lmoe_fp8_check_status, lmoe_fp8_wait_selftest)
 
 load()
 

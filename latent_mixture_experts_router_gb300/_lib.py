@@ -123,7 +123,9 @@ def _lib():
         for name in ("lmoe_matmul_fp8", "lmoe_matmul_fp8_wgrad"):
             getattr(L, name).argtypes = [ctypes.POINTER(lmoe_fp8_matmul), _P, _P, _P, _P, _P, _P, _P, _P]
             getattr(L, name).restype = ctypes.c_int
-        for name in ("lmoe_router_losses_workspace_size", "lmoe_router_losses", "lmoe_router_grad",
+        L.lmoe_fp8_check_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
+        L.lmoe_fp8_wait_selftest.argtypes = [LL, _P]
+        for name in ("lmoe_fp8_check_status", "lmoe_fp8_wait_selftest", "lmoe_router_losses_workspace_size", "lmoe_router_losses", "lmoe_router_grad",
                      "lmoe_quantize_fp8_rows", "lmoe_quantize_fp8_weight", "lmoe_quantize_fp8_cols"):
             getattr(L, name).restype = ctypes.c_int
         L.lmoe_kernel_launches.restype = ctypes.c_ulonglong
@@ -560,10 +562,31 @@ def _fp8_product(fn, where, dev, stream, rows, N, K, E, a, a_scales, b, b_scales
           b_scales.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(status))
 
 
+def _on_device(device, stream, fn):
+    with torch.cuda.device(device):   # (None: the current one)
+        return fn(_stream(stream))
+
+
+def lmoe_fp8_check_status(device=None, stream=None) -> tuple[int, int]:
+    """(status, error word) of the 8-bit products on ``device`` that were given no ``status`` word since the
+    last check: LMOE_ERR_TIMEOUT if a device wait gave up and left a product unfinished.  Synchronises the
+    stream."""
+    word = ctypes.c_uint32()
+    st = _on_device(device, stream, lambda s: _lib().lmoe_fp8_check_status(s, ctypes.byref(word)))
+    return st, word.value
+
+
+def lmoe_fp8_wait_selftest(budget_cycles: int, device=None, stream=None):
+    """Run the wait-timeout diagnostic; lmoe_fp8_check_status() then reports the timeout."""
+    _check(_on_device(device, stream, lambda s: _lib().lmoe_fp8_wait_selftest(int(budget_cycles), s)),
+           "lmoe_fp8_wait_selftest")
+
+
 def lmoe_matmul_fp8(a, a_scales, w, w_scales, out, offsets=None, status=None, stream=None):
     """``out`` [rows, N] (fp32 or bf16) = ``a`` [rows, K] times ``w`` [N, K] transposed, or, with ``w`` [E, N,
     K] and ``offsets`` [E + 1] (int32), each expert's rows times its own; scales as
-    lmoe_quantize_fp8_rows and lmoe_quantize_fp8_weight write them."""
+    lmoe_quantize_fp8_rows and lmoe_quantize_fp8_weight write them.  ``status`` [1] (int32): error word, for a
+    device wait that gives up; None: the device's own word (lmoe_fp8_check_status)."""
     _need(a.dim() == 2 and w.dim() in (2, 3), "a [rows, K] and w [N, K] or [E, N, K]")
     dev, (rows, K), N, lead = a.get_device(), a.shape, w.shape[-2], w.shape[:-2]
     kb = -(-K // 128)
@@ -579,7 +602,8 @@ def lmoe_matmul_fp8(a, a_scales, w, w_scales, out, offsets=None, status=None, st
 def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate=False, status=None,
                           stream=None):
     """``dw`` [(E,) N, K] (fp32 or bf16) (+)= each expert's rows of dy transposed times its rows of x, from
-    ``dy_t`` [N, P] and ``x_t`` [K, P] as lmoe_quantize_fp8_cols writes them for ``offsets`` [E + 1]."""
+    ``dy_t`` [N, P] and ``x_t`` [K, P] as lmoe_quantize_fp8_cols writes them for ``offsets`` [E + 1].  ``status``
+    as in lmoe_matmul_fp8."""
     _need(dy_t.dim() == 2 and x_t.dim() == 2 and dw.dim() in (2, 3), "dy_t [N, P], x_t [K, P], dw [(E,) N, K]")
     dev, (N, P), K, lead = dy_t.get_device(), dy_t.shape, x_t.shape[0], dw.shape[:-2]
     _need(P % 128 == 0, "P must be a multiple of 128")

@@ -34,6 +34,8 @@
 // 32 (w % 4) .. (and column half (w - 4) / 4 with eight of them).  A finished tile passes
 // through shared memory on its way out, so that a store instruction writes whole rows (bulk copies of
 // single rows, 256 or 512 bytes, take the copy engine about 60 cycles each: 9000 cycles a tile).
+#include <mutex>
+
 #include "../../include/latent_moe.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -75,12 +77,19 @@ struct Fp8Args {
   int out_f32, accumulate;
   int out_vec;           // output rows start on 16 bytes: 16-byte stores
   unsigned fmt_p, fmt_q;   // 0 e4m3, 1 e5m2
-  unsigned* status;      // error word or nullptr
+  unsigned* status;      // error word, or nullptr: the device's own (g_status)
   long long budget;
   int box;               // kCols, kSplit: rows of a that a tile loads
   int splits;            // kSplit: CTAs per tile (the cluster size)
   float far;             // the largest as ws 2^64 (matmul), p s (wgrad) with which no sum times 2^64 leaves fp32's range
 };
+
+// What waits that gave up leave for lmoe_fp8_check_status where the caller has no word for it.
+__device__ unsigned g_status, g_status_taken;
+__global__ void take_status_kernel() {
+  griddep_enter();
+  g_status_taken = atomicExch(&g_status, 0u);
+}
 
 template <int BN, int MODE>
 struct Fp8Cfg {
@@ -395,7 +404,7 @@ struct Fp8Ring {
   // the block's products are in their buffer, and its scales staged (the MMA issuer waits for them)
   LMOE_DEV bool wait(int it) const {
     const bool ok = warp_wait(&acc_full[it % C::kBufs], (it / C::kBufs) & 1, budget);
-    if (!ok && status) atomicOr(status, kErrWaitEpilogue);
+    if (!ok) atomicOr(status, kErrWaitEpilogue);
     tc_fence_after();
     return ok;
   }
@@ -546,7 +555,7 @@ LMOE_DEV void epilogue_cols(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
           if (lane == 0) mbar_arrive(&tempty[i]);
           return;
         }
-        if (args.status) atomicOr(args.status, kErrWaitEpilogue);
+        atomicOr(ring.status, kErrWaitEpilogue);
       }
     }
     // (wgrad: also once a wait has given up, so that all warps know the same tiles and meet at the same barriers)
@@ -906,6 +915,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
   const int rank = static_cast<int>(blockIdx.x % S);
   const int id0 = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
   const long long budget = args.budget;
+  unsigned* const status = args.status != nullptr ? args.status : &g_status;
   if (MODE == kSplit) cluster_arrive();   // every CTA of the cluster has started (waited for below)
 
   if (warp < 4) {
@@ -922,7 +932,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % C::kStages;
           if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, budget)) {
-            if (args.status) atomicOr(args.status, kErrWaitProducer);
+            atomicOr(status, kErrWaitProducer);
             ok = false;
             break;
           }
@@ -941,7 +951,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
       // every copy of this thread lands before the CTA leaves
       for (int j = max(0, it - C::kStages); j < it; ++j)
         if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, kDrainBudget))
-          if (args.status) atomicOr(args.status, kErrDrain);
+          atomicOr(status, kErrDrain);
     } else if ((warp == 1 || warp == 3) && lane == 0) {
       // ---- MMA issuers: one block of 128 into one TMEM buffer, warp 1 the even blocks of the ring,
       // warp 3 the odd ones.  Issuing a block's MMAs and commits holds a thread for most of the time
@@ -969,7 +979,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
           if (!mbar_wait(&sfull[slot], (it / C::kSlots) & 1, budget) ||
               !mbar_wait(&acc_empty[buf], ((it / C::kBufs) & 1) ^ 1, budget) ||
               !mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
-            if (args.status) atomicOr(args.status, kErrWaitMma);
+            atomicOr(status, kErrWaitMma);
             ok = false;
             break;
           }
@@ -1003,7 +1013,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
         bool told = false;
         if (MODE == kWgrad) {
           if (!warp_wait(&tempty[tile % kTileRing], ((tile / kTileRing) & 1) ^ 1, budget)) {
-            if (args.status) atomicOr(args.status, kErrWaitProducer);
+            atomicOr(status, kErrWaitProducer);
             break;
           }
           if (lane == 0) {
@@ -1030,7 +1040,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
             if (!ok || kb + j >= t.kb1) break;
             const int s = it % C::kSlots;
             if (!warp_wait(&sempty[s], ((it / C::kSlots) & 1) ^ 1, budget)) {
-              if (args.status) atomicOr(args.status, kErrWaitProducer);
+              atomicOr(status, kErrWaitProducer);
               ok = false;
               break;
             }
@@ -1088,7 +1098,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
     }
   } else {
     if constexpr (C::kInc > 0) regs_inc<C::kInc>();
-    const Fp8Ring<BN, MODE> ring = {acc_full, acc_empty, sempty, args.status, budget};
+    const Fp8Ring<BN, MODE> ring = {acc_full, acc_empty, sempty, status, budget};
     if constexpr (MODE == kRows) epilogue_rows<BN>(args, walk, ring, sc, infos, stage_out, tmem, id0, step);
     else epilogue_cols<BN, MODE>(args, walk, ring, sc, red, stage_out, tmem, id0, step, rank, tiles, tfull, tempty);
   }
@@ -1105,7 +1115,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
   // ---- teardown: all MMAs of this CTA have completed before the columns are released
   if (warp == 1 && lane == 0)
     if (!mbar_wait(mma_done, 0, kDrainBudget))
-      if (args.status) atomicOr(args.status, kErrDrain);
+      atomicOr(status, kErrDrain);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1277,4 +1287,23 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   if (!encode_u8_swizzled(&tp, x_t, 2, pd, st, box) || !encode_u8_swizzled(&tq, dy_t, 2, qd, st, box))
     return LMOE_ERR_CUDA;
   return launch_one<128, kWgrad>(tp, tq, g, tiles, stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+}
+
+extern "C" lmoe_status lmoe_fp8_check_status(cudaStream_t stream, uint32_t* detail) {
+  static std::mutex mu;   // (one landing place for the word)
+  std::lock_guard<std::mutex> lock(mu);
+  uint32_t word = 0;
+  if (launch_pdl(take_status_kernel, dim3(1), dim3(1), 0, stream) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&word, g_status_taken, 4, 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return LMOE_ERR_CUDA;
+  if (detail != nullptr) *detail = word;
+  return word == 0 ? LMOE_OK : LMOE_ERR_TIMEOUT;
+}
+
+extern "C" lmoe_status lmoe_fp8_wait_selftest(long long budget_cycles, cudaStream_t stream) {
+  const long long b = budget_cycles < 1 ? 1 : budget_cycles > kDefaultWaitBudget ? kDefaultWaitBudget : budget_cycles;
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, g_status) != cudaSuccess) return LMOE_ERR_CUDA;
+  return launch_wait_selftest(b, static_cast<unsigned*>(word), stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }

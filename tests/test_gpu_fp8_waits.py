@@ -89,6 +89,30 @@ def test_wgrad_waits_that_give_up(lm, R, E, N, K, out, accumulate):
         at += n
 
 
+def test_calls_without_a_status_word_report_too(lm):
+    assert lm.lmoe_fp8_check_status()[0] in (0, -6)          # (whatever came before: cleared now)
+    a, w = integers((300, 256), E4M3, 1), integers((5000, 256), E4M3, 2)
+    one, y = torch.ones(2, 300, device="cuda"), torch.zeros(300, 5000, device="cuda")
+    lm.lmoe_matmul_fp8(a, one, w, torch.ones(40, 2, device="cuda"), y)
+    assert lm.lmoe_fp8_check_status() == (0, 0)
+    s = torch.cuda.Stream()
+    lm.lmoe_fp8_wait_selftest(100_000, stream=s)             # a wait that gives up
+    st, word = lm.lmoe_fp8_check_status(stream=s)
+    assert st == -6 and word & WAITS and word & ~WAITS == 0
+    assert lm.lmoe_fp8_check_status() == (0, 0)              # read once
+    # a product of its own, with a budget that cannot do: no status word of the caller's
+    from latent_mixture_experts_router_gb300 import _lib
+    shape = _lib.lmoe_fp8_matmul(300, 5000, 256, 1, 0, 0, 0, 0, 1)
+    ws = torch.ones(40, 2, device="cuda")
+    for _ in range(3):
+        assert _lib._lib().lmoe_matmul_fp8(ctypes.byref(shape), a.data_ptr(), one.data_ptr(), w.data_ptr(), ws.data_ptr(), None,
+                                           y.data_ptr(), None, torch.cuda.current_stream().cuda_stream) == 0
+    assert lm.lmoe_fp8_check_status()[0] == -6
+    lm.lmoe_matmul_fp8(a, one, w, ws, y)
+    assert lm.lmoe_fp8_check_status() == (0, 0)
+    assert torch.equal(y, (a.double() @ w.double().t()).float())
+
+
 def test_budget_is_checked(lm):
     from latent_mixture_experts_router_gb300 import _lib
     t = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
