@@ -425,7 +425,7 @@ lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dtype, long l
  * A block holding an infinity or NaN gets a scale that is not finite.  A K that is not a multiple
  * of 128 ends in a short block.  K is a multiple of 16 (the tensor memory accelerator's rows).
  * Codes are 16-byte aligned and contiguous, other pointers aligned to their elements.  Up to 2^24
- * rows, N and K up to 2^20 (else LMOE_ERR_UNSUPPORTED).  No rows: nothing is launched or written,
+ * rows (padded ones for the weight gradient), N and K up to 2^20 (else LMOE_ERR_UNSUPPORTED).  No rows: nothing is launched or written,
  * but for a weight gradient that is not accumulated, which becomes zeros.                    */
 typedef enum { LMOE_FP8_E4M3 = 0, LMOE_FP8_E5M2 = 1 } lmoe_fp8_format;
 
@@ -467,7 +467,10 @@ lmoe_status lmoe_quantize_fp8_cols(const void* src, lmoe_dtype src_dtype, long l
  *  a_format, b_format  formats of the first and of the second operand
  *  out_dtype  LMOE_F32 or LMOE_BF16 (one rounding, at the end)
  *  accumulate wgrad: nonzero adds to what dw holds (matmul: must be 0)
- *  wait_budget_cycles  SM clock cycles a device wait may spin before it gives up (0: default)  */
+ *  wait_budget_cycles  SM clock cycles a device wait may spin before it gives up (0: default)
+ *  unpadded_rows  wgrad: the rows that were padded, lmoe_quantize_fp8_cols' `rows`, to which offsets
+ *             are clamped as they are there.  0: not given; offsets then have to lie within those
+ *             rows, or blocks that were never written are added (matmul: must be 0)         */
 typedef struct {
   long long rows;
   int N, K, n_experts;
@@ -475,6 +478,7 @@ typedef struct {
   lmoe_dtype out_dtype;
   int accumulate;
   long long wait_budget_cycles;
+  long long unpadded_rows;
 } lmoe_fp8_matmul;
 
 /* out[r, n] = sum_k a[r, k] w[e, n, k] for the rows offsets[e] <= r < offsets[e+1] of each expert
@@ -505,7 +509,7 @@ lmoe_status lmoe_fp8_wait_selftest(long long budget_cycles, cudaStream_t stream)
 /* dw[e, n, k] (+)= sum over expert e's rows r of dy[r, n] x[r, k], from the column-quantised
  * dy_t [N, rows], dy_scales [rows/128, N] (a_format) and x_t [K, rows], x_scales [rows/128, K]
  * (b_format) of lmoe_quantize_fp8_cols, rows = its padded rows, offsets the same as there (of
- * the rows before padding).  An expert without rows gets zeros (accumulate: is left as it was). */
+ * the rows before padding; see unpadded_rows).  An expert without rows gets zeros (accumulate: is left as it was). */
 lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* shape, const uint8_t* dy_t,
                                   const float* dy_scales, const uint8_t* x_t,
                                   const float* x_scales, const int32_t* offsets, void* dw,

@@ -70,7 +70,8 @@ _LAYOUT_FIELDS_NVFP4 = ["xq", "xq_scale", "xq_rowscale", "xe_rowscale", "h_scale
 class lmoe_fp8_matmul(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_longlong), ("N", ctypes.c_int), ("K", ctypes.c_int), ("n_experts", ctypes.c_int),
                 ("a_format", ctypes.c_int), ("b_format", ctypes.c_int), ("out_dtype", ctypes.c_int),
-                ("accumulate", ctypes.c_int), ("wait_budget_cycles", ctypes.c_longlong)]
+                ("accumulate", ctypes.c_int), ("wait_budget_cycles", ctypes.c_longlong),
+                ("unpadded_rows", ctypes.c_longlong)]
 
 
 class lmoe_workspace_layout(ctypes.Structure):
@@ -552,12 +553,14 @@ def lmoe_quantize_fp8_cols(src, codes_t, scales_t, offsets=None, row_index=None,
           1 if pow2_scales else 0, codes_t.data_ptr(), scales_t.data_ptr())
 
 
-def _fp8_product(fn, where, dev, stream, rows, N, K, E, a, a_scales, b, b_scales, offsets, out, accumulate, status):
+def _fp8_product(fn, where, dev, stream, rows, N, K, E, a, a_scales, b, b_scales, offsets, out, accumulate, status,
+                 unpadded=0):
     if offsets is not None:
         _want(offsets, "offsets", torch.int32, (E + 1,), dev)
     if status is not None:
         _want(status, "status", (torch.int32, torch.uint32), (1,), dev)
-    shape = lmoe_fp8_matmul(rows, N, K, E, _FP8[a.dtype], _FP8[b.dtype], _DENSE[out.dtype], 1 if accumulate else 0)
+    shape = lmoe_fp8_matmul(rows, N, K, E, _FP8[a.dtype], _FP8[b.dtype], _DENSE[out.dtype], 1 if accumulate else 0, 0,
+                            unpadded)
     _call(fn, where, dev, stream, ctypes.byref(shape), a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
           b_scales.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(status))
 
@@ -600,10 +603,11 @@ def lmoe_matmul_fp8(a, a_scales, w, w_scales, out, offsets=None, status=None, st
 
 
 def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate=False, status=None,
-                          stream=None):
+                          stream=None, rows=None):
     """``dw`` [(E,) N, K] (fp32 or bf16) (+)= each expert's rows of dy transposed times its rows of x, from
-    ``dy_t`` [N, P] and ``x_t`` [K, P] as lmoe_quantize_fp8_cols writes them for ``offsets`` [E + 1].  ``status``
-    as in lmoe_matmul_fp8."""
+    ``dy_t`` [N, P] and ``x_t`` [K, P] as lmoe_quantize_fp8_cols writes them for ``offsets`` [E + 1].  ``rows``: how
+    many rows were padded there, to which offsets are clamped; None: offsets must lie within them, or blocks that were
+    never written are added.  ``status`` as in lmoe_matmul_fp8."""
     _need(dy_t.dim() == 2 and x_t.dim() == 2 and dw.dim() in (2, 3), "dy_t [N, P], x_t [K, P], dw [(E,) N, K]")
     dev, (N, P), K, lead = dy_t.get_device(), dy_t.shape, x_t.shape[0], dw.shape[:-2]
     _need(P % 128 == 0, "P must be a multiple of 128")
@@ -613,4 +617,4 @@ def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accu
     _want(x_scales, "x_scales", torch.float32, (P // 128, K), dev)
     _want(dw, "dw", _DENSE, (*lead, N, K), dev)
     _fp8_product(_lib().lmoe_matmul_fp8_wgrad, "lmoe_matmul_fp8_wgrad", dev, stream, P, N, K, lead[0] if lead else 1,
-                 dy_t, dy_scales, x_t, x_scales, offsets, dw, accumulate, status)
+                 dy_t, dy_scales, x_t, x_scales, offsets, dw, accumulate, status, 0 if rows is None else int(rows))

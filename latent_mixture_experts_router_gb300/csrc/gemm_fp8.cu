@@ -79,6 +79,7 @@ struct Fp8Args {
   unsigned fmt_p, fmt_q;   // 0 e4m3, 1 e5m2
   unsigned* status;      // error word, or nullptr: the device's own (g_status)
   long long budget;
+  int cap;               // rows that offsets are clamped to
   int box;               // kCols, kSplit: rows of a that a tile loads
   int splits;            // kSplit: CTAs per tile (the cluster size)
   float far;             // the largest as ws 2^64 (matmul), p s (wgrad) with which no sum times 2^64 leaves fp32's range
@@ -283,7 +284,7 @@ LMOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, long long budget) {
 // Rows of group e, clamped into the rows there are, so that no offsets send a load or a store out
 // of range.
 LMOE_DEV void group_rows(const Fp8Args& a, int e, int& lo, int& hi) {
-  const int cap = static_cast<int>(a.rows);
+  const int cap = a.cap;
   lo = 0;
   hi = cap;
   if (a.offsets != nullptr) {
@@ -1162,7 +1163,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
                                        uint32_t* status, cudaStream_t stream) {
   if (c == nullptr || c->wait_budget_cycles < 0 || c->rows < 0 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
   if (!known(c->a_format) || !known(c->b_format)) return LMOE_ERR_ARG;
-  if (c->accumulate) return LMOE_ERR_ARG;
+  if (c->accumulate || c->unpadded_rows != 0) return LMOE_ERR_ARG;
   if (offsets == nullptr && c->n_experts != 1) return LMOE_ERR_ARG;
   if (c->out_dtype != LMOE_F32 && c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
   if (c->n_experts > kMaxGroups || c->K % 16 || c->K > (1 << 20) || c->N > (1 << 20) || c->rows > (1LL << 24))
@@ -1190,6 +1191,7 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   g.status = status;
   g.budget = c->wait_budget_cycles > 0 ? c->wait_budget_cycles : kDefaultWaitBudget;
   g.splits = 1;
+  g.cap = static_cast<int>(c->rows);
   g.far = static_cast<float>(0x1p126 / (g.num_kb * largest_sum(*c)));
   // Up to 16 rows in all, or up to kFewRows for an expert on average: 16-column tiles.  Measured
   // against 64 columns, 4096 x 4096: 1 row 6.8 us and 9.1, 8 and 24 rows of 64 experts 24.3, 45.5 and 26.0, 48.5, 480 rows
@@ -1242,6 +1244,8 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   if (c == nullptr || c->wait_budget_cycles < 0 || c->rows < 0 || c->rows % 128 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
   if (!known(c->a_format) || !known(c->b_format)) return LMOE_ERR_ARG;
   if (offsets == nullptr && c->n_experts != 1) return LMOE_ERR_ARG;
+  if (c->unpadded_rows < 0 || (c->unpadded_rows > 0 && lmoe_fp8_padded_rows(c->unpadded_rows, c->n_experts) != c->rows))
+    return LMOE_ERR_ARG;
   if (c->out_dtype != LMOE_F32 && c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
   if (c->n_experts > kMaxGroups || c->K > (1 << 20) || c->N > (1 << 20) || c->rows > (1LL << 24))
     return LMOE_ERR_UNSUPPORTED;
@@ -1278,6 +1282,7 @@ extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uin
   g.status = status;
   g.budget = c->wait_budget_cycles > 0 ? c->wait_budget_cycles : kDefaultWaitBudget;
   g.splits = 1;
+  g.cap = static_cast<int>(c->unpadded_rows > 0 ? c->unpadded_rows : c->rows);
   g.far = static_cast<float>(0x1p62 / (c->rows / 128 * largest_sum(*c)));
   const unsigned long long R = static_cast<unsigned long long>(c->rows);
   CUtensorMap tp, tq;
