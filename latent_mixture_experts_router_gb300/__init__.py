@@ -16,6 +16,8 @@ arguments.  Importing it fails if the library has not been built.
 """
 from __future__ import annotations
 
+import dataclasses
+
 import torch
 
 from ._lib import (Config, LmoeError, lmoe_workspace_size, lmoe_workspace_size_host_io,  # noqa: F401
@@ -57,6 +59,7 @@ class LatentMoEBlock:
         self.L = g_pool.shape[0]
         self.I = (W_gate[0] if isinstance(W_gate, tuple) else W_gate).shape[1]
         self._ws = None
+        self._ran = None   # the configuration whose call left its routing in the workspace
         self._loss_ws = None
 
     def config(self, T: int, act_dtype="bf16", out_dtype="f32") -> Config:
@@ -67,6 +70,7 @@ class LatentMoEBlock:
         n = lmoe_workspace_size_host_io(cfg) if host_io else lmoe_workspace_size(cfg)
         if self._ws is None or self._ws.numel() < n:
             self._ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.W["g_pre"].device)
+            self._ran = None
         return self._ws
 
     def forward(self, x: torch.Tensor, out_dtype="f32", out=None, stream=None, **ex) -> torch.Tensor:
@@ -78,14 +82,18 @@ class LatentMoEBlock:
         ws = self.workspace(cfg)
         w = self.W
         fn = latent_moe_forward_ex if ex else latent_moe_forward
+        self._ran = None
         fn(cfg, x, w["W_router"], w["W_pool"], w["g_pool"], w["W_gate"], w["W_up"], w["W_down"],
            w["g_expert"], w["W_unpool"], w["g_pre"], w["g_post"], self.top_k, out, ws, stream, **ex)
+        self._ran = cfg
         return out
 
     def _routing(self, cfg: Config):
-        """Views of the logits [T, E] and expert ids [T, k] that a forward call of ``cfg`` left."""
-        if cfg.T > 0 and (self._ws is None or self._ws.numel() < lmoe_workspace_size(cfg)):
-            raise ValueError("no forward call of this configuration came before")
+        """Views of the logits [T, E] and expert ids [T, k] that the last forward call, of ``cfg``, left."""
+        # where they are depends on all of it but the types of x and out
+        if cfg.T > 0 and (self._ran is None or cfg != dataclasses.replace(
+                self._ran, act_dtype=cfg.act_dtype, out_dtype=cfg.out_dtype)):
+            raise ValueError("the last forward call was not one of this configuration")
         lay, T, ld = lmoe_get_workspace_layout(cfg), cfg.T, (self.E + 31) // 32 * 32
         if T == 0:
             dev = self.W["g_pre"].device
