@@ -16,6 +16,7 @@ arguments.  Importing it fails if the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import torch
@@ -43,6 +44,10 @@ class LatentMoEBlock:
     W_unpool [D, L]; gammas g_pre [D], g_pool [L], g_expert [E, L], g_post [D] (fp32).
     NVFP4 weights are (codes, row-major E4M3 scales, tensor scale) triples; their scales are
     converted once into the block layout the kernels read.
+
+    What a method allocates (its results, workspaces) belongs to the stream it is given, or the
+    current one.  The forward calls of a block share its workspace, and the router methods read it:
+    calls on several streams must be ordered by the caller.
     """
 
     def __init__(self, W_router, W_pool, g_pool, W_gate, W_up, W_down, g_expert, W_unpool, g_pre,
@@ -60,26 +65,64 @@ class LatentMoEBlock:
         self.I = (W_gate[0] if isinstance(W_gate, tuple) else W_gate).shape[1]
         self._ws = None
         self._ran = None   # the configuration whose call left its routing in the workspace
-        self._loss_ws = None
+        self._loss_ws = self._loss_stream = None
+        # the workspace's stream, an event behind its zeroing (None: waited for), other streams that used it
+        self._ws_stream = self._ws_zeroed = None
+        self._ws_users = []
 
     def config(self, T: int, act_dtype="bf16", out_dtype="f32") -> Config:
         return Config(T, self.D, self.L, self.E, self.I, self.top_k, self.eps, act_dtype,
                       self.weight_dtype, out_dtype)
 
-    def workspace(self, cfg: Config, host_io: bool = False) -> torch.Tensor:
+    def _device(self) -> torch.device:
+        return self.W["g_pre"].device
+
+    def _on(self, stream):
+        """A context in which torch allocates on ``stream`` (a torch stream or a raw handle; None: the current)."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self._device())
+        return torch.cuda.stream(stream)
+
+    def _current(self):
+        return torch.cuda.current_stream(self._device()) if self._device().type == "cuda" else None
+
+    def _capturing(self) -> bool:
+        return self._device().type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+    def _use_workspace(self):
+        """The current stream is about to use the workspace."""
+        cur = self._current()
+        if self._ws is None or cur == self._ws_stream or self._capturing():
+            return
+        if self._ws_zeroed is not None:
+            cur.wait_event(self._ws_zeroed)
+            self._ws_zeroed = None
+        if cur not in self._ws_users:
+            self._ws_users.append(cur)
+
+    def workspace(self, cfg: Config, host_io: bool = False, stream=None) -> torch.Tensor:
         n = lmoe_workspace_size_host_io(cfg) if host_io else lmoe_workspace_size(cfg)
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.W["g_pre"].device)
-            self._ran = None
+        with self._on(stream):
+            if self._ws is None or self._ws.numel() < n:
+                for s in self._ws_users:   # the old one is free once they are done with it
+                    self._ws.record_stream(s)
+                self._ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self._device())
+                self._ran = None
+                self._ws_stream, self._ws_users = self._current(), []
+                self._ws_zeroed = None if self._ws_stream is None or self._capturing() else self._ws_stream.record_event()
+            self._use_workspace()
         return self._ws
 
     def forward(self, x: torch.Tensor, out_dtype="f32", out=None, stream=None, **ex) -> torch.Tensor:
         act = "f32" if x.dtype == torch.float32 else "bf16"
         cfg = self.config(x.shape[0], act, out_dtype)
         if out is None:
-            out = torch.empty(x.shape, dtype=torch.float32 if out_dtype == "f32" else torch.bfloat16,
-                              device=x.device)
-        ws = self.workspace(cfg)
+            with self._on(stream):
+                out = torch.empty(x.shape, dtype=torch.float32 if out_dtype == "f32" else torch.bfloat16,
+                                  device=x.device)
+        ws = self.workspace(cfg, stream=stream)
         w = self.W
         fn = latent_moe_forward_ex if ex else latent_moe_forward
         self._ran = None
@@ -110,13 +153,25 @@ class LatentMoEBlock:
         ``row_mask`` [T]: tokens that are 0 (padding) are left out."""
         logits, idx = self._routing(cfg)
         dev = logits.device
-        if self._loss_ws is None:   # for any T: a captured call keeps its address
-            n = lmoe_router_losses_workspace_size(1 << 20, self.E)
-            self._loss_ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        losses, mean = torch.empty(2, device=dev), torch.empty(self.E, device=dev)
-        counts = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
-        lmoe_router_losses(logits, idx, counts, mean, losses, self._loss_ws, router_bias, row_mask, stream)
+        with self._on(stream):
+            self._use_workspace()
+            ws = self._loss_workspace(cfg.T)
+            losses, mean = torch.empty(2, device=dev), torch.empty(self.E, device=dev)
+            counts = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+        lmoe_router_losses(logits, idx, counts, mean, losses, ws, router_bias, row_mask, stream)
         return losses, mean, counts
+
+    def _loss_workspace(self, T: int):
+        """Workspace of the losses of T tokens: one that is kept, for any T, on the stream that first asked; another
+        stream's, and a captured call's (in its graph's memory), is its own, so that none of them overlap."""
+        cur = self._current()
+        if not self._capturing():
+            if self._loss_ws is None:
+                n = lmoe_router_losses_workspace_size(1 << 20, self.E)
+                self._loss_ws, self._loss_stream = torch.empty(n, dtype=torch.uint8, device=self._device()), cur
+            if cur == self._loss_stream:
+                return self._loss_ws
+        return torch.empty(lmoe_router_losses_workspace_size(T, self.E), dtype=torch.uint8, device=self._device())
 
     def router_grad(self, cfg: Config, topk_w_grad=None, loss_grads=None, counts=None, router_bias=None,
                     row_mask=None, out=None, stream=None):
@@ -124,7 +179,9 @@ class LatentMoEBlock:
         weights ``topk_w_grad`` [T, k] and of router_losses' two losses, ``loss_grads`` [2] (with
         its ``counts``).  Summed over the tokens it is router_bias' gradient."""
         logits, idx = self._routing(cfg)
-        if out is None:
-            out = torch.empty(logits.shape, device=logits.device)
+        with self._on(stream):
+            self._use_workspace()
+            if out is None:
+                out = torch.empty(logits.shape, device=logits.device)
         lmoe_router_grad(logits, idx, counts, out, topk_w_grad, loss_grads, router_bias, row_mask, stream)
         return out
