@@ -47,7 +47,8 @@ class LatentMoEBlock:
 
     What a method allocates (its results, workspaces) belongs to the stream it is given, or the
     current one.  The forward calls of a block share its workspace, and the router methods read it:
-    calls on several streams must be ordered by the caller.
+    calls on several streams must be ordered by the caller.  A workspace that a captured call uses
+    lives as long as the block, so graphs stay valid when a larger call replaces it.
     """
 
     def __init__(self, W_router, W_pool, g_pool, W_gate, W_up, W_down, g_expert, W_unpool, g_pre,
@@ -69,6 +70,7 @@ class LatentMoEBlock:
         # the workspace's stream, an event behind its zeroing (None: waited for), other streams that used it
         self._ws_stream = self._ws_zeroed = None
         self._ws_users = []
+        self._ws_captured, self._ws_of_graph, self._kept = False, False, []
 
     def config(self, T: int, act_dtype="bf16", out_dtype="f32") -> Config:
         return Config(T, self.D, self.L, self.E, self.I, self.top_k, self.eps, act_dtype,
@@ -94,7 +96,10 @@ class LatentMoEBlock:
     def _use_workspace(self):
         """The current stream is about to use the workspace."""
         cur = self._current()
-        if self._ws is None or cur == self._ws_stream or self._capturing():
+        if self._ws is not None and self._capturing():
+            self._ws_captured = True
+            return
+        if self._ws is None or cur == self._ws_stream:
             return
         if self._ws_zeroed is not None:
             cur.wait_event(self._ws_zeroed)
@@ -105,13 +110,19 @@ class LatentMoEBlock:
     def workspace(self, cfg: Config, host_io: bool = False, stream=None) -> torch.Tensor:
         n = lmoe_workspace_size_host_io(cfg) if host_io else lmoe_workspace_size(cfg)
         with self._on(stream):
-            if self._ws is None or self._ws.numel() < n:
-                for s in self._ws_users:   # the old one is free once they are done with it
-                    self._ws.record_stream(s)
+            capturing = self._capturing()
+            # (one allocated by a captured call is zeroed when its graph runs, and no other call's)
+            if self._ws is None or self._ws.numel() < n or (self._ws_of_graph and not capturing):
+                if self._ws is not None and (self._ws_captured or capturing):
+                    self._kept.append(self._ws)
+                else:
+                    for s in self._ws_users:   # the old one is free once they are done with it
+                        self._ws.record_stream(s)
                 self._ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self._device())
                 self._ran = None
                 self._ws_stream, self._ws_users = self._current(), []
-                self._ws_zeroed = None if self._ws_stream is None or self._capturing() else self._ws_stream.record_event()
+                self._ws_captured, self._ws_of_graph = False, capturing
+                self._ws_zeroed = None if self._ws_stream is None or capturing else self._ws_stream.record_event()
             self._use_workspace()
         return self._ws
 

@@ -1,5 +1,7 @@
 """What LatentMoEBlock keeps from call to call, on the host: its forward call is replaced by nothing, its tensors
 are in host memory (the router methods then end at the library's check for CUDA tensors)."""
+import weakref
+
 import pytest
 import torch
 
@@ -70,6 +72,41 @@ def test_routing_after_a_larger_workspace_is_refused(blk):
     blk.forward(x(40))
     blk.workspace(blk.config(4000))       # a new one: nothing has run in it
     refused(blk.router_losses, blk.config(40))
+
+
+def test_workspace_of_a_captured_call_is_kept(blk, monkeypatch):
+    capturing = [False]
+    monkeypatch.setattr(blk, "_capturing", lambda: capturing[0], raising=False)
+    blk.forward(x(40))
+    blk.forward(x(400))                      # the first one was in no graph: gone
+    assert not getattr(blk, "_kept", [])
+    capturing[0] = True
+    blk.forward(x(40))
+    capturing[0] = False
+    used = weakref.ref(blk._ws)
+    blk.forward(x(4000))
+    assert used() is not None and used() is not blk._ws
+    # the router methods' views count as well
+    blk.forward(x(4000))
+    capturing[0] = True
+    taken(blk.router_losses, blk.config(4000))
+    capturing[0] = False
+    again = weakref.ref(blk._ws)
+    blk.forward(x(6000))
+    assert again() is not None and used() is not None
+
+
+def test_workspace_made_by_a_captured_call_is_its_own(blk, monkeypatch):
+    # zeroed only when the graph runs: an eager call takes another
+    capturing = [True]
+    monkeypatch.setattr(blk, "_capturing", lambda: capturing[0], raising=False)
+    blk.forward(x(40))
+    first = weakref.ref(blk._ws)
+    blk.forward(x(40))                       # (the same capture goes on with it)
+    assert blk._ws is first()
+    capturing[0] = False
+    blk.forward(x(40))
+    assert blk._ws is not first() and first() is not None
 
 
 def test_views_are_the_layouts(lm, blk):

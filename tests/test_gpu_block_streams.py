@@ -147,3 +147,52 @@ def test_two_captured_graphs_of_the_losses_at_once(setup):
     torch.cuda.synchronize()
     for a, b in zip(outs, want):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_captured_calls_survive_a_larger_workspace(setup):
+    inp, make_block = setup
+    x = inp.x[:40].contiguous()
+    ref = make_block(inp)
+    want = [ref.forward(x).clone(), *(t.clone() for t in ref.router_losses(ref.config(40)))]
+    blk = make_block(inp)
+    cfg = blk.config(40)
+    blk.forward(x)
+    blk.router_losses(cfg)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [blk.forward(x), *blk.router_losses(cfg)]
+    small = blk._ws
+    size, ptr = small.numel(), small.data_ptr()
+    del small
+    big = blk.forward(inp.x)                     # replaces the workspace
+    big_l = [t.clone() for t in blk.router_losses(blk.config(3000))]
+    assert blk._ws.data_ptr() != ptr
+    junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]   # takes what was freed
+    assert all(t.data_ptr() != ptr for t in junk)
+    for t in got:
+        t.fill_(3)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(bool((t == 255).all()) for t in junk)      # the replays wrote their own workspace only
+    assert torch.equal(blk.forward(inp.x), big)
+    assert all(torch.equal(a, b) for a, b in zip(blk.router_losses(blk.config(3000)), big_l))
+
+
+def test_a_block_whose_first_call_is_captured(setup):
+    # (other blocks have run these kernels before: a library call's first set-up is not part of the capture)
+    inp, make_block = setup
+    ref = make_block(inp)
+    want = [ref.forward(inp.x).clone(), *(t.clone() for t in ref.router_losses(ref.config(3000)))]
+    blk = make_block(inp)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [blk.forward(inp.x), *blk.router_losses(blk.config(3000))]
+    eager = [blk.forward(inp.x), *blk.router_losses(blk.config(3000))]
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip(eager, want))
