@@ -922,8 +922,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
   if (warp < 4) {
     if constexpr (C::kDec > 0) regs_dec<C::kDec>();
     if (warp == 0 && lane == 0) {
-      // ---- TMA producer (narrow tiles: few rows, each weight is read about once)
-      const uint64_t pol_p = BN == 256 ? policy_evict_normal() : policy_evict_first();
+      // ---- TMA producer.  Tiles of few rows read each weight about once: those leave L2 first (8 rows over 64
+      // experts of 4096 x 4096 28.6 us, otherwise 33.4; 512 rows, 256 of them one expert's, whose 16 tiles
+      // side by side read the same weights, 193 and 200).  The weight gradient reads its lane operand
+      // again in every column of tiles (32768 rows over 64 experts of 4096 x 2048 811 us, leaving first 908).
+      const uint64_t pol_p = MODE == kCols || MODE == kSplit ? policy_evict_first() : policy_evict_normal();
       const uint64_t pol_q = policy_evict_normal();
       const uint32_t tx = C::kPBytes + (MODE == kCols || MODE == kSplit ? args.box : BN) * 128;
       int it = 0;
@@ -1196,6 +1199,8 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
   // Up to 16 rows in all, or up to kFewRows for an expert on average: 16-column tiles.  Measured
   // against 64 columns, 4096 x 4096: 1 row 6.8 us and 9.1, 8 and 24 rows of 64 experts 24.3, 45.5 and 26.0, 48.5, 480 rows
   // of them 155 and 161; beyond the limit 800 and 1024 rows 164, 172 and 163, 163, 20 rows of 2 experts 18 and 12.
+  // (The average says nothing of the split, which is known to the device alone: 512 rows of 64 experts even 168 and
+  // 172, with 64, 128, 256, 448 rows of one of them 172, 182, 190, 210 and 172, 171, 175, 185.)
   // Then rows as lanes, unless an expert has fewer than kRowsMin rows on average (one matrix:
   // kRowsMinOne) or those tiles would leave three quarters of the SMs idle: then 64 rows at a time,
   // four of whose tiles cover one of the others.  Measured, rows as lanes against 64 at a time:
