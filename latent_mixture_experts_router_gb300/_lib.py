@@ -611,6 +611,7 @@ def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accu
     _need(dy_t.dim() == 2 and x_t.dim() == 2 and dw.dim() in (2, 3), "dy_t [N, P], x_t [K, P], dw [(E,) N, K]")
     dev, (N, P), K, lead = dy_t.get_device(), dy_t.shape, x_t.shape[0], dw.shape[:-2]
     _need(P % 128 == 0, "P must be a multiple of 128")
+    _need(rows is None or rows != 0 or P == 0, f"rows 0, but {P} padded ones")   # (0 is "not given" to the library)
     _want(dy_t, "dy_t", _FP8, (N, P), dev)
     _want(dy_scales, "dy_scales", torch.float32, (P // 128, N), dev)
     _want(x_t, "x_t", _FP8, (K, P), dev)

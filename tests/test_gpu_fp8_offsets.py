@@ -61,6 +61,8 @@ def test_rows_are_checked(lm):
     for rows in (128, 257, -1):      # padded, those are not 256
         with pytest.raises(lm.LmoeError):
             lm.lmoe_matmul_fp8_wgrad(dy, ds, x, xs, dw, offsets=off, rows=rows)
+    with pytest.raises(ValueError, match="rows 0"):
+        lm.lmoe_matmul_fp8_wgrad(dy, ds, x, xs, dw, offsets=off, rows=0)
     from latent_mixture_experts_router_gb300 import _lib
     shape = _lib.lmoe_fp8_matmul(128, 16, 128, 1, 0, 0, 0, 0, 0, 128)   # a product of rows has no padding
     p = dy.data_ptr()
