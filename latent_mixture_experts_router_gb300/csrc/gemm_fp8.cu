@@ -7,17 +7,19 @@
 //           with expert e's rows padded to whole blocks of 128
 //
 // The scales are arbitrary fp32 numbers, which the tensor cores' own block scaling (powers of
-// two per 32) does not take.  So the tensor cores compute one block of 128 at a time into one of
+// two per 32) does not take; scales that are powers of two go the same way.  So the tensor cores compute one block of 128 at a time into one of
 // several TMEM buffers, and the epilogue warps add buffer x scales to fp32 accumulators in
 // registers while the next block's MMAs run.  Adding a 128 x 256 block takes 128 x 256 fused
 // multiply-adds on the CUDA cores (128 a cycle) beside 128 x 256 x 128 on the tensor cores
 // (8192 a cycle): half the time.
 //
-// Measured: 8192 x 8192 x 16384 884 us (2.49 PFLOP/s), 32768 rows over 64 experts of 4096 x 4096 543 us (2.0;
-// an eighth are ragged tiles), 2560 rows over them 170 us (6.5 TB/s: the weights), 8 rows 24.3 us, weight
-// gradients of 8192 rows over 16 experts of 4096 x 2048 221 us.  Many rows: bound by the tensor cores'
-// reads of operands and the round trip of the two TMEM buffers.  Weight gradients: by the epilogue's
-// arithmetic and waits (without MMAs and loads 411 of 454 us at 16384 x 4096 x 4096) and its stores.
+// Measured on normally distributed operands, other inputs in each call: 32768 rows over 64 experts of 4096 x 4096
+// 592 us (1.86 PFLOP/s; an eighth are ragged tiles; 506 with small codes, which take less power), 2047 x 8192 x
+// 4096 to fp32 78.6 us (1.75), 8 rows over 64 experts 24.1 us, weight gradients of 8192 rows over 16
+// experts of 4096 x 2048 223 us, of 1000 rows by 4096 x 8192 78.0 us.  Small codes: 8192 x 8192 x 16384 888 us,
+// 2560 rows over 64 experts 178.6 us (6.2 TB/s: the weights).  Many rows: bound by the tensor cores' reads of
+// operands and the round trip of the two TMEM buffers.  Weight gradients: by the epilogue's arithmetic and
+// waits (without MMAs and loads 411 of 454 us at 16384 x 4096 x 4096) and its stores.
 //
 // Which operand is the MMA's 128 lanes ("lane operand") and which its columns:
 //   kRows   rows of a are lanes, rows of w columns (128 x 256 tiles): many rows per expert.  A thread

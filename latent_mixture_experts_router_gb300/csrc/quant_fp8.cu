@@ -14,9 +14,9 @@
 // cols:   [rows, K], a block is 128 rows of one column; codes transposed, [K][padded rows], each
 //         expert's rows padded to whole blocks; scales [blocks][K]
 // All three read and write each element once; the memory traffic bounds them.  Measured: 16384 x 8192
-// bf16 rows 59.9 us (6.7 TB/s), 4096 x 4096 gathered to 8 rows each 40.3 us (issue slots: each row is
-// converted eight times); 8 x 4096 x 4096 bf16 weights, both orientations, 80.9 us (6.6 TB/s); columns of 16384 x
-// 4096 bf16 39.5 us (5.1 TB/s, issue slots at 65 %).
+// bf16 rows 59.9 us (6.7 TB/s), 4096 x 4096 gathered to 8 rows each 43.1 us (issue slots: each row is
+// converted eight times); 8 x 4096 x 4096 bf16 weights, both orientations, 81.7 us (6.6 TB/s); columns of 16384 x
+// 4096 bf16 41.3 us (4.9 TB/s, issue slots at 65 %).
 #include <algorithm>
 
 #include "../../include/latent_moe.h"
@@ -50,8 +50,8 @@ LMOE_DEV uint32_t cvt4(float a, float b, float c, float d) {
   return r;
 }
 // four codes of v * s, the products two to an instruction: the conversions' issue slots are what the
-// gathered rows wait for (4096 x 4096 bf16 to 8 rows each: 40.3 us, one product an instruction 41.4; weights
-// 80.9 and 81.6; columns the same, fp32 ones 62.2 and 61.4: those keep single products)
+// gathered rows wait for (4096 x 4096 bf16 to 8 rows each, the same inputs in each call: 40.3 us, one product an instruction 41.4;
+// weights 80.9 and 81.6; columns the same, fp32 ones 62.2 and 61.4: those keep single products)
 template <bool E5M2>
 LMOE_DEV uint32_t cvt4_scaled(float a, float b, float c, float d, float s) {
   const auto mul = [&](float& x, float& y) {
