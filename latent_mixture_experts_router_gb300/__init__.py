@@ -17,7 +17,6 @@ arguments.  Importing it fails if the library has not been built.
 from __future__ import annotations
 
 import contextlib
-import dataclasses
 
 import torch
 
@@ -32,7 +31,7 @@ from ._lib import (Config, LmoeError, lmoe_workspace_size, lmoe_workspace_size_h
                    lmoe_permute_noalloc, lmoe_router_losses, lmoe_router_losses_workspace_size, lmoe_router_grad,
                    lmoe_quantize_fp8_rows, lmoe_quantize_fp8_weight, lmoe_quantize_fp8_cols,
                    lmoe_fp8_padded_rows, lmoe_matmul_fp8, lmoe_matmul_fp8_wgrad,
-                   lmoe_fp8_check_status, lmoe_fp8_wait_selftest)
+                   lmoe_fp8_check_status, lmoe_fp8_wait_selftest, _raw_stream)
 
 load()
 
@@ -64,66 +63,70 @@ class LatentMoEBlock:
         self.E, self.D = W_router.shape
         self.L = g_pool.shape[0]
         self.I = (W_gate[0] if isinstance(W_gate, tuple) else W_gate).shape[1]
+        self._device = g_pre.device
         self._ws = None
         self._ran = None   # the configuration whose call left its routing in the workspace
+        self._routed = None   # it, and the views of that routing
         self._loss_ws = self._loss_stream = None
-        # the workspace's stream, an event behind its zeroing (None: waited for), other streams that used it
+        # the workspace's stream (handles), an event behind its zeroing (None: waited for), other streams that used it
         self._ws_stream = self._ws_zeroed = None
-        self._ws_users = []
+        self._ws_users = {}
         self._ws_captured, self._ws_of_graph, self._kept = False, False, []
 
     def config(self, T: int, act_dtype="bf16", out_dtype="f32") -> Config:
         return Config(T, self.D, self.L, self.E, self.I, self.top_k, self.eps, act_dtype,
                       self.weight_dtype, out_dtype)
 
-    def _device(self) -> torch.device:
-        return self.W["g_pre"].device
-
     def _on(self, stream):
         """A context in which torch allocates on ``stream`` (a torch stream or a raw handle; None: the current)."""
         if stream is None:
             return contextlib.nullcontext()
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self._device())
+            stream = torch.cuda.ExternalStream(int(stream), device=self._device)
         return torch.cuda.stream(stream)
 
-    def _current(self):
-        return torch.cuda.current_stream(self._device()) if self._device().type == "cuda" else None
+    def _current(self) -> int:
+        """The current stream's handle."""
+        return _raw_stream(self._device.index) if self._device.type == "cuda" else 0
 
     def _capturing(self) -> bool:
-        return self._device().type == "cuda" and torch.cuda.is_current_stream_capturing()
+        return self._device.type == "cuda" and torch.cuda.is_current_stream_capturing()
 
-    def _use_workspace(self):
-        """The current stream is about to use the workspace."""
-        cur = self._current()
-        if self._ws is not None and self._capturing():
+    def _use_workspace(self, cur: int, capturing: bool):
+        """The current stream ``cur`` is about to use the workspace."""
+        if self._ws is None:
+            return
+        if capturing:
             self._ws_captured = True
             return
-        if self._ws is None or cur == self._ws_stream:
+        if cur == self._ws_stream:
             return
         if self._ws_zeroed is not None:
-            cur.wait_event(self._ws_zeroed)
+            torch.cuda.current_stream(self._device).wait_event(self._ws_zeroed)
             self._ws_zeroed = None
         if cur not in self._ws_users:
-            self._ws_users.append(cur)
+            self._ws_users[cur] = torch.cuda.current_stream(self._device)
 
     def workspace(self, cfg: Config, host_io: bool = False, stream=None) -> torch.Tensor:
         n = lmoe_workspace_size_host_io(cfg) if host_io else lmoe_workspace_size(cfg)
         with self._on(stream):
-            capturing = self._capturing()
+            cur, capturing = self._current(), self._capturing()
             # (one allocated by a captured call is zeroed when its graph runs, and no other call's)
             if self._ws is None or self._ws.numel() < n or (self._ws_of_graph and not capturing):
                 if self._ws is not None and (self._ws_captured or capturing):
                     self._kept.append(self._ws)
                 else:
-                    for s in self._ws_users:   # the old one is free once they are done with it
+                    for s in self._ws_users.values():   # the old one is free once they are done with it
                         self._ws.record_stream(s)
-                self._ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self._device())
-                self._ran = None
-                self._ws_stream, self._ws_users = self._current(), []
+                self._ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self._device)
+                self._ran = self._routed = None
+                self._ws_stream, self._ws_users = cur, {}
                 self._ws_captured, self._ws_of_graph = False, capturing
-                self._ws_zeroed = None if self._ws_stream is None or capturing else self._ws_stream.record_event()
-            self._use_workspace()
+                if not capturing and self._device.type == "cuda":
+                    self._ws_zeroed = torch.cuda.current_stream(self._device).record_event()
+                else:
+                    self._ws_zeroed = None
+            self._use_workspace(cur, capturing)
         return self._ws
 
     def forward(self, x: torch.Tensor, out_dtype="f32", out=None, stream=None, **ex) -> torch.Tensor:
@@ -145,18 +148,23 @@ class LatentMoEBlock:
     def _routing(self, cfg: Config):
         """Views of the logits [T, E] and expert ids [T, k] that the last forward call, of ``cfg``, left."""
         # where they are depends on all of it but the types of x and out
-        if cfg.T > 0 and (self._ran is None or cfg != dataclasses.replace(
-                self._ran, act_dtype=cfg.act_dtype, out_dtype=cfg.out_dtype)):
+        def shape(c):
+            return c.T, c.d_model, c.d_latent, c.n_experts, c.d_ff, c.top_k, c.eps, c.weight_dtype
+        if cfg.T > 0 and (self._ran is None or shape(cfg) != shape(self._ran)):
             raise ValueError("the last forward call was not one of this configuration")
-        lay, T, ld = lmoe_get_workspace_layout(cfg), cfg.T, (self.E + 31) // 32 * 32
+        T, ld = cfg.T, (self.E + 31) // 32 * 32
         if T == 0:
-            dev = self.W["g_pre"].device
+            dev = self._device
             return (torch.empty(0, self.E, device=dev), torch.empty(0, self.top_k, dtype=torch.int32, device=dev))
+        if self._routed is not None and self._routed[0] == shape(cfg):
+            return self._routed[1:]
+        lay = lmoe_get_workspace_layout(cfg)
 
         def view(name, n, dtype):
             return self._ws[lay[name]:lay[name] + 4 * n].view(dtype)
-        return (view("logits", T * ld, torch.float32).view(T, ld)[:, :self.E],
-                view("topk_idx", T * self.top_k, torch.int32).view(T, self.top_k))
+        self._routed = (shape(cfg), view("logits", T * ld, torch.float32).view(T, ld)[:, :self.E],
+                        view("topk_idx", T * self.top_k, torch.int32).view(T, self.top_k))
+        return self._routed[1:]
 
     def router_losses(self, cfg: Config, router_bias=None, row_mask=None, stream=None):
         """(losses [2], mean_probs [E], counts [E + 1]) of the last forward call, which had ``cfg``
@@ -165,24 +173,24 @@ class LatentMoEBlock:
         logits, idx = self._routing(cfg)
         dev = logits.device
         with self._on(stream):
-            self._use_workspace()
-            ws = self._loss_workspace(cfg.T)
+            cur, capturing = self._current(), self._capturing()
+            self._use_workspace(cur, capturing)
+            ws = self._loss_workspace(cfg.T, cur, capturing)
             losses, mean = torch.empty(2, device=dev), torch.empty(self.E, device=dev)
             counts = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
         lmoe_router_losses(logits, idx, counts, mean, losses, ws, router_bias, row_mask, stream)
         return losses, mean, counts
 
-    def _loss_workspace(self, T: int):
+    def _loss_workspace(self, T: int, cur: int, capturing: bool):
         """Workspace of the losses of T tokens: one that is kept, for any T, on the stream that first asked; another
         stream's, and a captured call's (in its graph's memory), is its own, so that none of them overlap."""
-        cur = self._current()
-        if not self._capturing():
+        if not capturing:
             if self._loss_ws is None:
                 n = lmoe_router_losses_workspace_size(1 << 20, self.E)
-                self._loss_ws, self._loss_stream = torch.empty(n, dtype=torch.uint8, device=self._device()), cur
+                self._loss_ws, self._loss_stream = torch.empty(n, dtype=torch.uint8, device=self._device), cur
             if cur == self._loss_stream:
                 return self._loss_ws
-        return torch.empty(lmoe_router_losses_workspace_size(T, self.E), dtype=torch.uint8, device=self._device())
+        return torch.empty(lmoe_router_losses_workspace_size(T, self.E), dtype=torch.uint8, device=self._device)
 
     def router_grad(self, cfg: Config, topk_w_grad=None, loss_grads=None, counts=None, router_bias=None,
                     row_mask=None, out=None, stream=None):
@@ -191,7 +199,7 @@ class LatentMoEBlock:
         its ``counts``).  Summed over the tokens it is router_bias' gradient."""
         logits, idx = self._routing(cfg)
         with self._on(stream):
-            self._use_workspace()
+            self._use_workspace(self._current(), self._capturing())
             if out is None:
                 out = torch.empty(logits.shape, device=logits.device)
         lmoe_router_grad(logits, idx, counts, out, topk_w_grad, loss_grads, router_bias, row_mask, stream)

@@ -72,13 +72,11 @@ def test_results_are_not_taken_from_the_current_stream(setup, which):
 def test_a_larger_workspace_on_another_stream(setup):
     # the first call's workspace is used by s and replaced on the current stream while s is still at work
     inp, make_block = setup
-    blk = make_block(inp)
     x = inp.x[:500].contiguous()
     want = make_block(inp).forward(x).clone()
     torch.cuda.synchronize()
     for _ in range(3):
-        blk._ws, blk._ran = None, None
-        blk._ws_users, blk._ws_zeroed = [], None
+        blk = make_block(inp)
         s = torch.cuda.Stream()
         blk.workspace(blk.config(500))            # zeroed on the current stream,
         with torch.cuda.stream(s):
