@@ -425,8 +425,9 @@ lmoe_status lmoe_router_grad(const void* logits, lmoe_dtype logits_dtype, long l
  * A block holding an infinity or NaN gets a scale that is not finite.  A K that is not a multiple
  * of 128 ends in a short block.  K is a multiple of 16 (the tensor memory accelerator's rows).
  * Codes are 16-byte aligned and contiguous, other pointers aligned to their elements.  Up to 2^24
- * rows (padded ones for the weight gradient), N and K up to 2^20 (else LMOE_ERR_UNSUPPORTED).  No rows: nothing is launched or written,
- * but for a weight gradient that is not accumulated, which becomes zeros.                    */
+ * rows (padded ones for the weight gradient), N and K up to 2^20 (else LMOE_ERR_UNSUPPORTED).  No
+ * rows: nothing is launched or written, but for a weight gradient that is not accumulated, which
+ * becomes zeros.                                                                            */
 typedef enum { LMOE_FP8_E4M3 = 0, LMOE_FP8_E5M2 = 1 } lmoe_fp8_format;
 
 /* Rows, a block is 128 elements of a row: codes [rows, K], scales [ceil(K/128), rows] fp32.
@@ -489,7 +490,9 @@ typedef struct {
  *  gradient the transposed pair, with N and K exchanged)
  *  out [rows, N].  Products of a block of 128 are summed by the tensor cores and added, scaled, to
  *  fp32 sums; the product of a's and w's scale may lie outside fp32's range where the scaled sum does
- *  not (likewise for the weight gradient).
+ *  not (likewise for the weight gradient).  In a row of out (a row k of all dw[e, n, k]) that meets a
+ *  product of scales above 2^62 / (128 M_a M_b blocks) (4096 elements of E4M3: 2^32; the weight gradient:
+ *  or an x scale above 2^24), terms below 2^-46 may be lost.
  *  status (device): error word as lmoe_check_status reports it, a bit is set if a device wait gives
  *  up and leaves the product unfinished; the caller zeroes it.  NULL: the device's own word, which
  *  lmoe_fp8_check_status reads.                                                             */
@@ -509,7 +512,8 @@ lmoe_status lmoe_fp8_wait_selftest(long long budget_cycles, cudaStream_t stream)
 /* dw[e, n, k] (+)= sum over expert e's rows r of dy[r, n] x[r, k], from the column-quantised
  * dy_t [N, rows], dy_scales [rows/128, N] (a_format) and x_t [K, rows], x_scales [rows/128, K]
  * (b_format) of lmoe_quantize_fp8_cols, rows = its padded rows, offsets the same as there (of
- * the rows before padding; see unpadded_rows).  An expert without rows gets zeros (accumulate: is left as it was). */
+ * the rows before padding; see unpadded_rows).  An expert without rows gets zeros (accumulate: is
+ * left as it was).                                                                          */
 lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* shape, const uint8_t* dy_t,
                                   const float* dy_scales, const uint8_t* x_t,
                                   const float* x_scales, const int32_t* offsets, void* dw,

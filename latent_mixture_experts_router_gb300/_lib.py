@@ -126,7 +126,8 @@ def _lib():
             getattr(L, name).restype = ctypes.c_int
         L.lmoe_fp8_check_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
         L.lmoe_fp8_wait_selftest.argtypes = [LL, _P]
-        for name in ("lmoe_fp8_check_status", "lmoe_fp8_wait_selftest", "lmoe_router_losses_workspace_size", "lmoe_router_losses", "lmoe_router_grad",
+        for name in ("lmoe_fp8_check_status", "lmoe_fp8_wait_selftest",
+                     "lmoe_router_losses_workspace_size", "lmoe_router_losses", "lmoe_router_grad",
                      "lmoe_quantize_fp8_rows", "lmoe_quantize_fp8_weight", "lmoe_quantize_fp8_cols"):
             getattr(L, name).restype = ctypes.c_int
         L.lmoe_kernel_launches.restype = ctypes.c_ulonglong
