@@ -6,12 +6,12 @@
 //   wgrad   dw[e, n, k] = sum_{b of e} dys[b, n] xs[b, k] sum_{r in block b} dy[n, r] x[k, r]
 //           with expert e's rows padded to whole blocks of 128
 //
-// The scales are arbitrary fp32 numbers, which the tensor cores' own block scaling (powers of
-// two per 32) does not take; scales that are powers of two go the same way.  So the tensor cores compute one block of 128 at a time into one of
-// several TMEM buffers, and the epilogue warps add buffer x scales to fp32 accumulators in
-// registers while the next block's MMAs run.  Adding a 128 x 256 block takes 128 x 256 fused
-// multiply-adds on the CUDA cores (128 a cycle) beside 128 x 256 x 128 on the tensor cores
-// (8192 a cycle): half the time.
+// The scales are arbitrary fp32 numbers, which the tensor cores' own block scaling (powers of two per 32)
+// does not take; scales that are powers of two go the same way.  So the tensor cores compute one block of
+// 128 at a time into one of several TMEM buffers, and the epilogue warps add buffer x scales to fp32
+// accumulators in registers while the next block's MMAs run.  Adding a 128 x 256 block takes 128 x 256 fused
+// multiply-adds on the CUDA cores (128 a cycle) beside 128 x 256 x 128 on the tensor cores (8192 a cycle):
+// half the time.
 //
 // Measured on normally distributed operands, other inputs in each call: 32768 rows over 64 experts of 4096 x 4096
 // 592 us (1.86 PFLOP/s; an eighth are ragged tiles; 506 with small codes, which take less power), 2047 x 8192 x
@@ -487,7 +487,8 @@ LMOE_DEV void epilogue_rows(const Fp8Args& args, const Fp8Walk& walk, const Fp8R
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float* a = acc + round * 64 + 4 * i;
-            *reinterpret_cast<float4*>(mine + lane * 272 + 16 * i) = make_float4(a[0] * back, a[1] * back, a[2] * back, a[3] * back);
+            *reinterpret_cast<float4*>(mine + lane * 272 + 16 * i) =
+                make_float4(a[0] * back, a[1] * back, a[2] * back, a[3] * back);
           }
         } else {
 #pragma unroll
@@ -1075,13 +1076,15 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, MODE>::kThreads, Fp8Cfg<BN, MODE>::
                 if (lane + 32 * i < BN) at[lane + 32 * i] = v[j][i] * (i / 4 & 1 ? b1 : b0);
               }
               // (a zero of ws: the mark stays zero, and so do the products)
-              const bool far = !__all_sync(~0u, top * fmaxf(fabsf(b0), fabsf(b1)) <= args.far) && (u[j][0] != 0.f || u[j][1] != 0.f);
+              const bool near = __all_sync(~0u, top * fmaxf(fabsf(b0), fabsf(b1)) <= args.far);
+              const bool far = !near && (u[j][0] != 0.f || u[j][1] != 0.f);
               if (far) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i)
                   if (lane + 32 * i < BN) at[lane + 32 * i] = v[j][i];
               }
-              if (lane == 0) *reinterpret_cast<float2*>(at + BN) = far ? make_float2(u[j][0], u[j][1]) : make_float2(0.f, 0.f);
+              if (lane == 0)
+                *reinterpret_cast<float2*>(at + BN) = far ? make_float2(u[j][0], u[j][1]) : make_float2(0.f, 0.f);
             } else {
               // the mark without a vote, which a small tile's start would wait for (2560 rows over 64 experts of
               // 4096 x 4096: 178.6 us, with a vote as above 183)
@@ -1167,7 +1170,8 @@ using namespace lmoe;
 extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* a, const float* a_scales,
                                        const uint8_t* w, const float* w_scales, const int32_t* offsets, void* out,
                                        uint32_t* status, cudaStream_t stream) {
-  if (c == nullptr || c->wait_budget_cycles < 0 || c->rows < 0 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
+  if (c == nullptr || c->rows < 0 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
+  if (c->wait_budget_cycles < 0) return LMOE_ERR_ARG;
   if (!known(c->a_format) || !known(c->b_format)) return LMOE_ERR_ARG;
   if (c->accumulate || c->unpadded_rows != 0) return LMOE_ERR_ARG;
   if (offsets == nullptr && c->n_experts != 1) return LMOE_ERR_ARG;
@@ -1249,7 +1253,8 @@ extern "C" lmoe_status lmoe_matmul_fp8(const lmoe_fp8_matmul* c, const uint8_t* 
 extern "C" lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* c, const uint8_t* dy_t, const float* dy_scales,
                                              const uint8_t* x_t, const float* x_scales, const int32_t* offsets,
                                              void* dw, uint32_t* status, cudaStream_t stream) {
-  if (c == nullptr || c->wait_budget_cycles < 0 || c->rows < 0 || c->rows % 128 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
+  if (c == nullptr || c->rows < 0 || c->rows % 128 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0) return LMOE_ERR_ARG;
+  if (c->wait_budget_cycles < 0) return LMOE_ERR_ARG;
   if (!known(c->a_format) || !known(c->b_format)) return LMOE_ERR_ARG;
   if (offsets == nullptr && c->n_experts != 1) return LMOE_ERR_ARG;
   if (c->unpadded_rows < 0 || (c->unpadded_rows > 0 && lmoe_fp8_padded_rows(c->unpadded_rows, c->n_experts) != c->rows))
