@@ -243,8 +243,7 @@ def run(state):
         dy2, dw2 = (st["dy"][1], st["dw"][1]) if st["pairs"] == 2 else (None, None)
         lm.lmoe_matmul_bf16_wgrad(st["dy"][0], st["x"], st["dw"][0], offsets=st["offsets"], dy2=dy2, dw2=dw2)
         return st["dw"]
-    lm.lmoe_grad_norm(st["grads"], st["norm"], st["ws"])
-    lm.lmoe_grad_clip(st["grads"], st["norm"], st["max_norm"], out=st["outs"])
+    lm.lmoe_clip_grad_norm(st["grads"], st["norm"], st["max_norm"], st["ws"], out=st["outs"])
     return [st["norm"]] + st["out"]
 
 
