@@ -519,6 +519,93 @@ lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* shape, const uint8_t* d
                                   const float* x_scales, const int32_t* offsets, void* dw,
                                   uint32_t* status, cudaStream_t stream);
 
+/* ---- Training the experts in bf16 -----------------------------------------------------------
+ * A gated feed-forward block over expert-contiguous rows (lmoe_permute_noalloc's offsets), forward and
+ * backward, and the products that go with it.  Operands are bf16, sums fp32, each result is rounded once,
+ * where it is stored.  One training step of experts with weights w_gate, w_up [E, I, L] and w_down [E, L, I]:
+ *   forward    lmoe_gated_ffn (h, gate, up), lmoe_matmul_bf16 (y = h w_down^T)
+ *   backward   lmoe_gated_ffn_grad (dgate, dup from dy), lmoe_matmul_bf16 with transposed weights and two pairs (dx =
+ *              dgate w_gate + dup w_up), lmoe_matmul_bf16_wgrad (w_gate and w_up together; w_down from dy and h)
+ *   update     lmoe_clip_grad_norm
+ * One token uses the same calls; few rows stream the weights of the experts that have any.
+ *
+ * Shape of a call.
+ *  rows       rows of a and of the result, up to 2^24
+ *  N, K       the result has N columns and is reduced over K (wgrad: dw is [N, K], reduced over an expert's
+ *             rows); multiples of 8 up to 2^20          n_experts  1..1024
+ *  out_dtype  LMOE_F32 or LMOE_BF16 (the two gated calls: LMOE_BF16)
+ *  transposed lmoe_matmul_bf16: the weights are [n_experts, K, N] (else 0)
+ *  accumulate wgrad: nonzero adds to what dw holds, rounded once after the addition (else 0)
+ *  wait_budget_cycles  SM clock cycles a device wait may spin before it gives up (0: default)
+ * offsets [n_experts + 1] int32 device, non-decreasing, clamped into [0, rows]; NULL with n_experts = 1: all rows.
+ * Rows of no expert are neither read nor written.  What a masked (padded) row holds does not reach other
+ * rows; in a weight gradient, rows of no expert or of another one do not count, whatever they hold.
+ * Matrices are contiguous and 16-byte aligned, offsets and status 4-byte.  A result may not share memory with an
+ * operand, but for dgate = gate and dup = up.  status (device): error word, a bit is set if a device wait
+ * gives up and leaves the result unfinished; the caller zeroes it.  NULL: the device's own word
+ * (lmoe_bf16_check_status).  No rows: nothing is launched or written, but for a weight gradient that is not
+ * accumulated, which becomes zeros.                                                          */
+typedef struct {
+  long long rows;
+  int N, K, n_experts;
+  lmoe_dtype out_dtype;
+  int transposed;
+  int accumulate;
+  long long wait_budget_cycles;
+} lmoe_bf16_matmul;
+
+/* h = silu(g) u, g = x w_gate[e]^T, u = x w_up[e]^T, in one kernel: x [rows, K], w_gate and w_up [n_experts, N, K],
+ * h [rows, N].  gate, up [rows, N] (both or neither): g and u, for the gradient.               */
+lmoe_status lmoe_gated_ffn(const lmoe_bf16_matmul* shape, const void* x, const void* w_gate, const void* w_up,
+                           const int32_t* offsets, void* h, void* gate, void* up, uint32_t* status,
+                           cudaStream_t stream);
+
+/* The gradient through the down projection and the gated product, in one kernel: dh = dy w_down[e] stays in fp32,
+ *   dgate = dh u s (1 + g (1 - s)), dup = dh g s, s = sigmoid(g).
+ * dy [rows, K], w_down [n_experts, K, N] (as the block has it: N = d_ff), gate, up, dgate, dup [rows, N]. */
+lmoe_status lmoe_gated_ffn_grad(const lmoe_bf16_matmul* shape, const void* dy, const void* w_down, const void* gate,
+                                const void* up, const int32_t* offsets, void* dgate, void* dup, uint32_t* status,
+                                cudaStream_t stream);
+
+/* out = a w[e]^T with w [n_experts, N, K], or a w[e] with w [n_experts, K, N] (transposed); with a2, w2 (both or
+ * neither, of the same shapes) plus the second pair's product, in one sum.                   */
+lmoe_status lmoe_matmul_bf16(const lmoe_bf16_matmul* shape, const void* a, const void* w, const void* a2,
+                             const void* w2, const int32_t* offsets, void* out, uint32_t* status,
+                             cudaStream_t stream);
+
+/* dw[e] (+)= sum over expert e's rows r of dy[r]^T x[r]: dy [rows, N], x [rows, K], dw [n_experts, N, K]; with dy2,
+ * dw2 (both or neither) also the second weight's, from the same x.  An expert without rows gets zeros
+ * (accumulate: is left as it was).                                                           */
+lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* shape, const void* dy, const void* x, const void* dy2,
+                                   const int32_t* offsets, void* dw, void* dw2, uint32_t* status,
+                                   cudaStream_t stream);
+
+/* lmoe_fp8_check_status and lmoe_fp8_wait_selftest for the device's own word of these calls.    */
+lmoe_status lmoe_bf16_check_status(cudaStream_t stream, uint32_t* detail);
+lmoe_status lmoe_bf16_wait_selftest(long long budget_cycles, cudaStream_t stream);
+
+/* ---- The norm over all gradients, and clipping ------------------------------------------------
+ * norm = sqrt(sum over all tensors of g^2) (fp32, computed in fp64 where squares leave fp32's range; beyond
+ * fp32's range itself: infinity), out = g f with f = min(1, max_norm / (norm + 1e-6)).  As the formula says: with a norm
+ * of infinity f is 0 (and infinite elements become NaN), with a NaN everything becomes NaN.
+ * Host arrays of `count` (up to 2^20, copied before the call returns): grads, out (device pointers, aligned to
+ * their elements; out = grads: in place), sizes (elements, 0 allowed: such a tensor is skipped), dtypes (LMOE_F32 or
+ * LMOE_BF16).  An output may be its own gradient, but overlap no other tensor (LMOE_ERR_ARG).
+ *  norm [1] fp32 device; max_norm >= 0
+ *  workspace  lmoe_grad_norm_workspace_size() bytes, 8-byte aligned, nothing to be set or kept
+ * Sums are taken in a fixed order: the same tensors give the same bits (copies that start otherwise within 16
+ * bytes may differ in the last).
+ * lmoe_grad_norm: the norm alone; lmoe_grad_clip: from a norm that is there (of several devices, say);
+ * lmoe_clip_grad_norm: both.                                                                 */
+lmoe_status lmoe_grad_norm_workspace_size(int count, size_t* bytes);
+lmoe_status lmoe_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes, int count, float* norm,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+lmoe_status lmoe_grad_clip(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes,
+                           int count, const float* norm, float max_norm, cudaStream_t stream);
+lmoe_status lmoe_clip_grad_norm(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes,
+                                int count, float* norm, float max_norm, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
 /* Number of kernels this library has launched in this process (all devices, all calls). */
 unsigned long long lmoe_kernel_launches(void);
 

@@ -31,7 +31,9 @@ from ._lib import (Config, LmoeError, lmoe_workspace_size, lmoe_workspace_size_h
                    lmoe_permute_noalloc, lmoe_router_losses, lmoe_router_losses_workspace_size, lmoe_router_grad,
                    lmoe_quantize_fp8_rows, lmoe_quantize_fp8_weight, lmoe_quantize_fp8_cols,
                    lmoe_fp8_padded_rows, lmoe_matmul_fp8, lmoe_matmul_fp8_wgrad,
-                   lmoe_fp8_check_status, lmoe_fp8_wait_selftest, _raw_stream)
+                   lmoe_fp8_check_status, lmoe_fp8_wait_selftest, lmoe_gated_ffn, lmoe_gated_ffn_grad,
+                   lmoe_matmul_bf16, lmoe_matmul_bf16_wgrad, lmoe_bf16_check_status, lmoe_bf16_wait_selftest,
+                   lmoe_grad_norm_workspace_size, lmoe_grad_norm, lmoe_grad_clip, lmoe_clip_grad_norm, _raw_stream)
 
 load()
 

@@ -7,6 +7,7 @@ it fails loudly (there is no fallback path).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -74,6 +75,12 @@ class lmoe_fp8_matmul(ctypes.Structure):
                 ("unpadded_rows", ctypes.c_longlong)]
 
 
+class lmoe_bf16_matmul(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("N", ctypes.c_int), ("K", ctypes.c_int), ("n_experts", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("transposed", ctypes.c_int), ("accumulate", ctypes.c_int),
+                ("wait_budget_cycles", ctypes.c_longlong)]
+
+
 class lmoe_workspace_layout(ctypes.Structure):
     _fields_ = ([(f, ctypes.c_longlong) for f in _LAYOUT_FIELDS + _LAYOUT_FIELDS_NVFP4]
                 + [("xa_cols", ctypes.c_int), ("grouped_splits", ctypes.c_longlong)])
@@ -126,7 +133,21 @@ def _lib():
             getattr(L, name).restype = ctypes.c_int
         L.lmoe_fp8_check_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
         L.lmoe_fp8_wait_selftest.argtypes = [LL, _P]
-        for name in ("lmoe_fp8_check_status", "lmoe_fp8_wait_selftest",
+        S = ctypes.POINTER(lmoe_bf16_matmul)
+        L.lmoe_gated_ffn.argtypes = [S, _P, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.lmoe_gated_ffn_grad.argtypes = [S, _P, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.lmoe_matmul_bf16.argtypes = [S, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.lmoe_matmul_bf16_wgrad.argtypes = [S, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.lmoe_bf16_check_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
+        L.lmoe_bf16_wait_selftest.argtypes = [LL, _P]
+        L.lmoe_grad_norm_workspace_size.argtypes = [I, ctypes.POINTER(ctypes.c_size_t)]
+        L.lmoe_grad_norm.argtypes = [_P, _P, _P, I, _P, _P, ctypes.c_size_t, _P]
+        L.lmoe_grad_clip.argtypes = [_P, _P, _P, _P, I, _P, ctypes.c_float, _P]
+        L.lmoe_clip_grad_norm.argtypes = [_P, _P, _P, _P, I, _P, ctypes.c_float, _P, ctypes.c_size_t, _P]
+        for name in ("lmoe_gated_ffn", "lmoe_gated_ffn_grad", "lmoe_matmul_bf16", "lmoe_matmul_bf16_wgrad",
+                     "lmoe_bf16_check_status", "lmoe_bf16_wait_selftest", "lmoe_grad_norm_workspace_size",
+                     "lmoe_grad_norm", "lmoe_grad_clip", "lmoe_clip_grad_norm",
+                     "lmoe_fp8_check_status", "lmoe_fp8_wait_selftest",
                      "lmoe_router_losses_workspace_size", "lmoe_router_losses", "lmoe_router_grad",
                      "lmoe_quantize_fp8_rows", "lmoe_quantize_fp8_weight", "lmoe_quantize_fp8_cols"):
             getattr(L, name).restype = ctypes.c_int
@@ -620,3 +641,180 @@ def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accu
     _want(dw, "dw", _DENSE, (*lead, N, K), dev)
     _fp8_product(_lib().lmoe_matmul_fp8_wgrad, "lmoe_matmul_fp8_wgrad", dev, stream, P, N, K, lead[0] if lead else 1,
                  dy_t, dy_scales, x_t, x_scales, offsets, dw, accumulate, status, 0 if rows is None else int(rows))
+
+
+# ------------------------------------------------------------------ training the experts in bf16
+def _bf16_call(fn, where, dev, stream, rows, N, K, E, offsets, status, *operands, out_dtype=LMOE_BF16, transposed=False,
+               accumulate=False):
+    if offsets is not None:
+        _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+    if status is not None:
+        _want(status, "status", (torch.int32, torch.uint32), (1,), dev)
+    shape = lmoe_bf16_matmul(rows, N, K, E, out_dtype, 1 if transposed else 0, 1 if accumulate else 0, 0)
+    _call(fn, where, dev, stream, ctypes.byref(shape), *operands, _ptr(status))
+
+
+def _weight_shape(t, name, what):
+    _need(t.dim() in (2, 3), f"{name} {what}")
+    lead = t.shape[:-2]
+    return lead, lead[0] if lead else 1
+
+
+def lmoe_gated_ffn(x, w_gate, w_up, h, gate=None, up=None, offsets=None, status=None, stream=None):
+    """``h`` [rows, N] = silu(x w_gate^T) * (x w_up^T) for ``x`` [rows, K] and weights [N, K], or, with
+    weights [E, N, K] and ``offsets`` [E + 1] (int32), each expert's rows times its own; all bf16.  ``gate``, ``up``
+    [rows, N]: both products are stored too, for lmoe_gated_ffn_grad.  ``status`` [1] (int32): error word, for a device
+    wait that gives up; None: the device's own word (lmoe_bf16_check_status)."""
+    lead, E = _weight_shape(w_gate, "w_gate", "[N, K] or [E, N, K]")
+    _need(x.dim() == 2, "x [rows, K]")
+    dev, (rows, K), N = x.get_device(), x.shape, w_gate.shape[-2]
+    _want(x, "x", torch.bfloat16, (rows, K), dev)
+    _want(w_gate, "w_gate", torch.bfloat16, (*lead, N, K), dev)
+    _want(w_up, "w_up", torch.bfloat16, (*lead, N, K), dev)
+    _want(h, "h", torch.bfloat16, (rows, N), dev)
+    _need((gate is None) == (up is None), "gate and up: both or neither")
+    if gate is not None:
+        _want(gate, "gate", torch.bfloat16, (rows, N), dev)
+        _want(up, "up", torch.bfloat16, (rows, N), dev)
+    _bf16_call(_lib().lmoe_gated_ffn, "lmoe_gated_ffn", dev, stream, rows, N, K, E, offsets, status, x.data_ptr(),
+               w_gate.data_ptr(), w_up.data_ptr(), _ptr(offsets), h.data_ptr(), _ptr(gate), _ptr(up))
+
+
+def lmoe_gated_ffn_grad(dy, w_down, gate, up, dgate, dup, offsets=None, status=None, stream=None):
+    """``dgate``, ``dup`` [rows, N]: gradients of lmoe_gated_ffn's ``gate`` and ``up`` (which they may be) from
+    ``dy`` [rows, K], the gradient of the down projection's result, through ``w_down`` [K, N] or [E, K, N]; all
+    bf16.  ``offsets``, ``status`` as in lmoe_gated_ffn."""
+    lead, E = _weight_shape(w_down, "w_down", "[K, N] or [E, K, N]")
+    _need(dy.dim() == 2, "dy [rows, K]")
+    dev, (rows, K), N = dy.get_device(), dy.shape, w_down.shape[-1]
+    _want(dy, "dy", torch.bfloat16, (rows, K), dev)
+    _want(w_down, "w_down", torch.bfloat16, (*lead, K, N), dev)
+    for t, name in ((gate, "gate"), (up, "up"), (dgate, "dgate"), (dup, "dup")):
+        _want(t, name, torch.bfloat16, (rows, N), dev)
+    _bf16_call(_lib().lmoe_gated_ffn_grad, "lmoe_gated_ffn_grad", dev, stream, rows, N, K, E, offsets, status,
+               dy.data_ptr(), w_down.data_ptr(), gate.data_ptr(), up.data_ptr(), _ptr(offsets), dgate.data_ptr(),
+               dup.data_ptr())
+
+
+def lmoe_matmul_bf16(a, w, out, offsets=None, a2=None, w2=None, transposed=False, status=None, stream=None):
+    """``out`` [rows, N] (fp32 or bf16) = ``a`` [rows, K] (bf16) times ``w`` [N, K] transposed, or, with ``transposed``,
+    times ``w`` [K, N] as it is; with ``a2``, ``w2`` of the same shapes plus their product.  Weights with a leading E
+    and ``offsets`` [E + 1] (int32): each expert's rows times its own.  ``status`` as in lmoe_gated_ffn."""
+    lead, E = _weight_shape(w, "w", "[N, K] or [E, N, K]")
+    _need(a.dim() == 2, "a [rows, K]")
+    dev, (rows, K), N = a.get_device(), a.shape, w.shape[-1 if transposed else -2]
+    shape = (*lead, K, N) if transposed else (*lead, N, K)
+    _want(a, "a", torch.bfloat16, (rows, K), dev)
+    _want(w, "w", torch.bfloat16, shape, dev)
+    _want(out, "out", _DENSE, (rows, N), dev)
+    _need((a2 is None) == (w2 is None), "a2 and w2: both or neither")
+    if a2 is not None:
+        _want(a2, "a2", torch.bfloat16, (rows, K), dev)
+        _want(w2, "w2", torch.bfloat16, shape, dev)
+    _bf16_call(_lib().lmoe_matmul_bf16, "lmoe_matmul_bf16", dev, stream, rows, N, K, E, offsets, status, a.data_ptr(),
+               w.data_ptr(), _ptr(a2), _ptr(w2), _ptr(offsets), out.data_ptr(), out_dtype=_DENSE[out.dtype],
+               transposed=transposed)
+
+
+def lmoe_matmul_bf16_wgrad(dy, x, dw, offsets=None, dy2=None, dw2=None, accumulate=False, status=None, stream=None):
+    """``dw`` [(E,) N, K] (fp32 or bf16) (+)= each expert's rows of ``dy`` [rows, N] transposed times its rows of ``x``
+    [rows, K] (bf16); with ``dy2``, ``dw2`` of the same shapes also the second weight's, from the same x.
+    ``offsets``, ``status`` as in lmoe_gated_ffn."""
+    lead, E = _weight_shape(dw, "dw", "[N, K] or [E, N, K]")
+    _need(dy.dim() == 2 and x.dim() == 2, "dy [rows, N] and x [rows, K]")
+    dev, (rows, N), K = dy.get_device(), dy.shape, x.shape[1]
+    _want(dy, "dy", torch.bfloat16, (rows, N), dev)
+    _want(x, "x", torch.bfloat16, (rows, K), dev)
+    _want(dw, "dw", _DENSE, (*lead, N, K), dev)
+    _need((dy2 is None) == (dw2 is None), "dy2 and dw2: both or neither")
+    if dy2 is not None:
+        _want(dy2, "dy2", torch.bfloat16, (rows, N), dev)
+        _want(dw2, "dw2", dw.dtype, dw.shape, dev)
+    _bf16_call(_lib().lmoe_matmul_bf16_wgrad, "lmoe_matmul_bf16_wgrad", dev, stream, rows, N, K, E, offsets, status,
+               dy.data_ptr(), x.data_ptr(), _ptr(dy2), _ptr(offsets), dw.data_ptr(), _ptr(dw2),
+               out_dtype=_DENSE[dw.dtype], accumulate=accumulate)
+
+
+def lmoe_bf16_check_status(device=None, stream=None) -> tuple[int, int]:
+    """lmoe_fp8_check_status for the bf16 calls that were given no ``status`` word."""
+    word = ctypes.c_uint32()
+    st = _on_device(device, stream, lambda s: _lib().lmoe_bf16_check_status(s, ctypes.byref(word)))
+    return st, word.value
+
+
+def lmoe_bf16_wait_selftest(budget_cycles: int, device=None, stream=None):
+    """Run the wait-timeout diagnostic; lmoe_bf16_check_status() then reports the timeout."""
+    _check(_on_device(device, stream, lambda s: _lib().lmoe_bf16_wait_selftest(int(budget_cycles), s)),
+           "lmoe_bf16_wait_selftest")
+
+
+# ------------------------------------------------------------------ the norm over all gradients, clipping
+def lmoe_grad_norm_workspace_size(count: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib().lmoe_grad_norm_workspace_size(int(count), ctypes.byref(n)), "lmoe_grad_norm_workspace_size")
+    return n.value
+
+
+def _grad_list(ts, name, device):
+    """(addresses, sizes, dtypes) of contiguous CUDA tensors on one device, fp32 or bf16."""
+    _need({t.get_device() for t in ts} <= {device}, f"{name}: all tensors must be on cuda:{device}")
+    _need(all([t.is_contiguous() for t in ts]), f"{name}: tensors must be contiguous")
+    try:
+        kinds = array.array("i", [_DENSE[t.dtype] for t in ts])
+    except KeyError:
+        raise ValueError(f"{name}: tensors must be float32 or bfloat16") from None
+    return array.array("Q", [t.data_ptr() for t in ts]), array.array("q", [t.numel() for t in ts]), kinds
+
+
+def _grad_device(norm):
+    dev = norm.get_device()
+    _want(norm, "norm", torch.float32, (1,), dev)
+    return dev
+
+
+def _grad_args(grads, norm):
+    dev = _grad_device(norm)
+    return dev, *_grad_list(grads, "grads", dev)
+
+
+def _grad_out(out, dev, ptrs, sizes, kinds):
+    if out is None:
+        return ptrs
+    _need(len(out) == len(ptrs), "out: as many tensors as grads")
+    optrs, osizes, okinds = _grad_list(out, "out", dev)
+    _need(osizes == sizes and okinds == kinds, "out: sizes and dtypes of grads")
+    return optrs
+
+
+def _at(a):
+    return a.buffer_info()[0]
+
+
+def _workspace(workspace, dev):
+    _need(workspace.get_device() == dev and workspace.is_contiguous(), f"workspace must be contiguous on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def lmoe_grad_norm(grads, norm, workspace, stream=None):
+    """``norm`` [1] (fp32) = the 2-norm over all elements of the tensors ``grads`` (contiguous, fp32 or bf16, any
+    sizes).  ``workspace``: at least lmoe_grad_norm_workspace_size(len(grads)) bytes."""
+    dev, ptrs, sizes, kinds = _grad_args(grads, norm)
+    _call(_lib().lmoe_grad_norm, "lmoe_grad_norm", dev, stream, _at(ptrs), _at(sizes), _at(kinds), len(ptrs),
+          norm.data_ptr(), *_workspace(workspace, dev))
+
+
+def lmoe_grad_clip(grads, norm, max_norm, out=None, stream=None):
+    """``out`` (None: ``grads`` themselves) = ``grads`` times min(1, max_norm / (norm + 1e-6)), with a ``norm`` [1]
+    (fp32, on the device) that is there."""
+    dev, ptrs, sizes, kinds = _grad_args(grads, norm)
+    optrs = _grad_out(out, dev, ptrs, sizes, kinds)
+    _call(_lib().lmoe_grad_clip, "lmoe_grad_clip", dev, stream, _at(ptrs), _at(optrs), _at(sizes), _at(kinds), len(ptrs),
+          norm.data_ptr(), float(max_norm))
+
+
+def lmoe_clip_grad_norm(grads, norm, max_norm, workspace, out=None, stream=None):
+    """lmoe_grad_norm and lmoe_grad_clip in one call."""
+    dev, ptrs, sizes, kinds = _grad_args(grads, norm)
+    optrs = _grad_out(out, dev, ptrs, sizes, kinds)
+    _call(_lib().lmoe_clip_grad_norm, "lmoe_clip_grad_norm", dev, stream, _at(ptrs), _at(optrs), _at(sizes), _at(kinds),
+          len(ptrs), norm.data_ptr(), float(max_norm), *_workspace(workspace, dev))

@@ -1,0 +1,788 @@
+// gemm_bf16.cu — products of bf16 rows sorted by expert with their expert's weights, and what a
+// gated feed-forward block makes of them, forward and backward, on the 5th-generation tensor
+// cores, persistent.  For the rows r of expert e (offsets[e] <= r < offsets[e + 1]), or of one matrix:
+//
+//   kGated      g = x Wg^T, u = x Wu^T, h = silu(g) u         (g and u stored too if asked for)
+//   kGatedGrad  dh = dy Wd; dg = dh u s (1 + g (1 - s)), du = dh g s, s = sigmoid(g)
+//   kProduct    out = a W^T (+ a2 W2^T)
+//   kProductT   out = a W (+ a2 W2), W [k, n]
+//   kWgrad      dw[e] (+)= dy^T x over e's rows (and dw2 from dy2)
+//
+// Operands are bf16, sums fp32 in tensor memory, each result rounded once where it is stored.  The lane
+// operand (a, or dy transposed) gives an MMA its rows, the column operand (the weights, or x) its
+// columns.  An operand whose reduction is its rows' own dimension lies in shared memory as boxes of 64 of
+// them (128 bytes, swizzled) by its rows; the weights of kGatedGrad and kProductT and both operands of
+// kWgrad are reduced along their other dimension and lie there as boxes of 64 columns by 64 of the reduction,
+// which the tensor cores read as they are (MN-major), so nothing is transposed in memory.
+//
+// An expert's rows rarely fill kWgrad's last block of 64.  What lies behind them is another expert's (maybe
+// infinities or NaN, which a product with zero would keep), so a warp clears those rows of both operands in
+// shared memory before the tensor cores read them, up to the next 16; steps of 16 behind that are left out.
+//
+// Roles of a CTA: warp 0 lane 0 TMA producer, warp 1 lane 0 MMA issuer (warp 1 owns the TMEM), warp 2 the
+// clearing of kWgrad, warps 4..7 epilogue, warp w on TMEM lanes 32 (w % 4) ..  Two accumulator buffers: a
+// tile is stored while the next one is computed.  A warp's 32 x 32 block passes through its own shared
+// memory on the way out, so that a store instruction writes whole segments of four rows.
+#include <mutex>
+
+#include "../../include/latent_moe.h"
+#include "groups.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace lmoe {
+namespace {
+
+enum Bf16Mode : int { kGated = 0, kGatedGrad = 1, kProduct = 2, kProductT = 3, kWgrad = 4 };
+constexpr int kRaster = 8;       // row tiles that take turns before the next column of tiles
+constexpr int kLdStage = 36;     // floats of a staged row of 32: rows four apart share no banks
+constexpr int kLdSplit = 132;    // floats of a row of 128 partial sums
+
+struct Bf16Args {
+  FastDiv by_others, by_group;   // tiles across; kRaster rows of them
+  FastDiv by_tiles;              // kWgrad: tiles of an expert
+  long long rows;                // rows of a (kWgrad: of dy and x)
+  int n, k;                      // out is [rows, n], reduced over k (kWgrad: dw is [n, k])
+  int num_kb;                    // blocks of 64 of k (0: kWgrad)
+  int pairs;                     // pairs of operands that are summed (kWgrad: weights)
+  int E;
+  const int32_t* offsets;        // [E + 1], or nullptr: one group of all rows
+  int box;                       // rows of a that a load brings (tiles of few rows)
+  int splits;                    // CTAs (a cluster) that share a tile's reduction
+  const __nv_bfloat16 *gate, *up;   // kGatedGrad
+  void *out, *out2, *out3;       // h, gate, up; dgate, dup; out; dw, dw2
+  int out_f32, accumulate;
+  unsigned* status;              // error word, or nullptr: the device's own (g_status)
+  long long budget;
+};
+
+// What waits that gave up leave for lmoe_bf16_check_status where the caller has no word for it.
+__device__ unsigned g_status, g_status_taken;
+__global__ void take_status_kernel() {
+  griddep_enter();
+  g_status_taken = atomicExch(&g_status, 0u);
+}
+
+// UNIT: rows of a tile of one CTA.
+template <int MODE, int UNIT>
+struct Bf16Cfg {
+  static constexpr bool kLanesMn = MODE == kWgrad;
+  static constexpr bool kColsMn = MODE == kWgrad || MODE == kGatedGrad || MODE == kProductT;
+  static constexpr int kLanes = UNIT;                             // that a CTA loads
+  static constexpr int kBN = 128;                                 // accumulator columns
+  static constexpr int kOutCols = MODE == kGated ? kBN / 2 : kBN;  // columns of a tile
+  static constexpr int kThreads = 256;
+  static constexpr int kABytes = kLanes * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
+  static constexpr int kStagingBytes = 4 * 32 * kLdStage * 4;
+  static constexpr int kTableBytes = 2 * (kMaxGroups + 4) * 4;
+  static constexpr int kFixed = kStagingBytes + kTableBytes + 512 + 1024;
+  static constexpr int kFit = (227 * 1024 - kFixed) / kStageBytes;
+  static constexpr int kStages = kFit > 12 ? 12 : kFit;
+  static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
+  static constexpr uint32_t kTmemCols = 2 * kBN;
+  static constexpr int kSplitMost = kStages * kStageBytes / (kLdSplit * 4);   // rows of partial sums that fit
+  static_assert((3 * kStages + 2 * 2 + 1) * 8 + 8 <= 512, "barriers");
+  // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
+  static_assert(kStageBytes >= 128 * 128, "lane operand");
+};
+
+// Shared-memory descriptor of an MN-major operand tile with 128-byte swizzle: boxes of 64 columns (128 bytes) by 64
+// of the reduction, the next 64 columns 8192 bytes on (leading offset), the next 8 of the reduction 1024
+// (stride offset).  16 of the reduction are 2048 bytes.
+LMOE_DEV uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+LMOE_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 1 / (1 + exp(-g)); exp may reach infinity, its reciprocal is 0 then (an approximation with subnormal
+// results: __fdividef would give 0 from 2^126 on).
+LMOE_DEV float sigmoid(float g) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+  return r;
+}
+
+// A tile as one CTA sees it.
+struct Bf16Tile {
+  int e, p0, q0;      // first lane (row of a; kWgrad: row of dw), first column
+  int skip, live;     // lanes [skip, live) are the tile's
+  int kb0, kb1;       // blocks of the reduction
+  int r0, rows;       // kWgrad: the expert's rows
+  int second;         // kWgrad: of dw2
+};
+
+LMOE_DEV int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
+
+// off: offsets, clamped into the rows there are, so that no offsets send a load or a store out of range;
+// start[e]: first row tile of group e (not kWgrad)
+struct Bf16Walk {
+  const int *off, *start;
+  int total;
+};
+
+template <int MODE, int UNIT>
+LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank) {
+  using C = Bf16Cfg<MODE, UNIT>;
+  Bf16Tile t = {};
+  int i, rows;   // tile i of `rows` row tiles by by_others.d
+  if (MODE == kWgrad) {
+    t.e = a.by_tiles.div(id);
+    i = id - t.e * static_cast<int>(a.by_tiles.d);
+    rows = (a.n + UNIT - 1) / UNIT;
+    const int one = rows * static_cast<int>(a.by_others.d);
+    t.second = i >= one;
+    if (t.second) i -= one;
+  } else {
+    int l = 0, h = a.E;   // the last e with start[e] * others <= id
+    const int s = a.by_others.div(id);
+    while (h - l > 1) {
+      const int m = (l + h) >> 1;
+      if (w.start[m] <= s) l = m;
+      else h = m;
+    }
+    t.e = l;
+    i = id - w.start[l] * static_cast<int>(a.by_others.d);
+    rows = w.start[l + 1] - w.start[l];
+  }
+  const int g = a.by_group.div(i), first = g * kRaster, gm = min(kRaster, rows - first);
+  const int local = i - g * static_cast<int>(a.by_group.d), other = local / gm;
+  const int rt = first + local - other * gm;
+  const int lo = w.off[t.e], hi = max(w.off[t.e + 1], lo);
+  t.q0 = other * C::kOutCols;
+  if (MODE == kWgrad) {
+    t.p0 = rt * UNIT;
+    t.live = min(a.n - t.p0, C::kLanes);
+    t.r0 = lo;
+    t.rows = hi - lo;
+    t.kb1 = (hi - lo + kBK - 1) / kBK;
+  } else {
+    // Tiles of few rows: no row behind the last is asked for (a box filled with zeros past the end costs the
+    // copy engine more than rows); a tile near the end starts earlier and skips the lanes before its own.
+    const int p0 = lo + rt * UNIT;
+    t.p0 = min(p0, static_cast<int>(a.rows) - a.box);
+    t.skip = p0 - t.p0;
+    t.live = t.skip + min(UNIT, hi - p0);
+    const int blocks = a.num_kb * a.pairs;
+    t.kb1 = blocks;
+    if (a.splits > 1) {
+      t.kb0 = blocks * rank / a.splits;
+      t.kb1 = blocks * (rank + 1) / a.splits;
+    }
+  }
+  return t;
+}
+
+// ---- epilogue
+// Four values of a row, as they are stored.
+LMOE_DEV void store4(void* out, long long at, float4 v, bool f32) {
+  if (f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+LMOE_DEV float4 load4_bf16(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+LMOE_DEV float4 load4(const void* p, long long at, bool f32) {
+  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+  return load4_bf16(static_cast<const __nv_bfloat16*>(p) + at);
+}
+LMOE_DEV void gated_grad(float dh, float g, float u, float& dg, float& du) {
+  const float s = sigmoid(g);
+  dg = dh * u * (s * (1.f + g * (1.f - s)));
+  du = dh * (g * s);
+}
+LMOE_DEV float4 silu_mul(float4 g, float4 u) {
+  return make_float4(g.x * sigmoid(g.x) * u.x, g.y * sigmoid(g.y) * u.y, g.z * sigmoid(g.z) * u.z,
+                     g.w * sigmoid(g.w) * u.w);
+}
+// Four sums v of out's element `at` (kGated: of gate and up) to where they belong.
+template <int MODE>
+LMOE_DEV void finish4(const Bf16Args& a, void* out, long long at, float4 v, float4 v2) {
+  if (MODE == kGated) {
+    store4(a.out, at, silu_mul(v, v2), false);
+    if (a.out2 != nullptr) {
+      store4(a.out2, at, v, false);
+      store4(a.out3, at, v2, false);
+    }
+  } else if (MODE == kGatedGrad) {
+    const float4 g = load4_bf16(a.gate + at), u = load4_bf16(a.up + at);
+    float4 dg, du;
+    gated_grad(v.x, g.x, u.x, dg.x, du.x);
+    gated_grad(v.y, g.y, u.y, dg.y, du.y);
+    gated_grad(v.z, g.z, u.z, dg.z, du.z);
+    gated_grad(v.w, g.w, u.w, dg.w, du.w);
+    store4(a.out, at, dg, false);
+    store4(a.out2, at, du, false);
+  } else {
+    if (MODE == kWgrad && a.accumulate) {
+      const float4 o = load4(out, at, a.out_f32);
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    store4(out, at, v, a.out_f32);
+  }
+}
+
+// A warp's 32 lanes by 32 columns, a lane to a thread, into rows of shared memory; then thread l has columns
+// 4 (l % 8) .. of rows l / 8, + 4, ...
+LMOE_DEV void put32(float* st, int lane, const uint32_t (&v)[32]) {
+  float4* o = reinterpret_cast<float4*>(st + lane * kLdStage);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    o[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                       __uint_as_float(v[4 * i + 3]));
+}
+LMOE_DEV void get32(const float* st, int lane, float4 (&q)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    q[i] = *reinterpret_cast<const float4*>(st + (4 * i + (lane >> 3)) * kLdStage + (lane & 7) * 4);
+}
+
+template <int MODE, int UNIT>
+LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, float* staging, uint64_t* acc_full,
+                       uint64_t* acc_empty, unsigned* status, uint32_t tmem, int id0, int step, int rank) {
+  using C = Bf16Cfg<MODE, UNIT>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3;
+  float* st = staging + quad * 32 * kLdStage;
+  int tc = 0;
+  for (int id = id0; id < walk.total; id += step) {
+    const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
+    const bool any = t.kb0 < t.kb1;   // (kWgrad: an expert without rows has no blocks, and gets zeros)
+    const int buf = tc & 1;
+    if (any) {
+      if (!warp_wait(&acc_full[buf], (tc >> 1) & 1, args.budget)) {
+        atomicOr(status, kErrWaitEpilogue);
+        return;
+      }
+      tc_fence_after();
+      ++tc;
+    }
+    const int from = max(t.skip - quad * 32, 0), to = min(t.live - quad * 32, 32);   // lanes of this warp
+    const int width = MODE == kWgrad ? args.k : args.n;
+    const long long ld = width;
+    void* out = MODE == kWgrad && t.second ? args.out2 : args.out;
+    const long long row = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0 + quad * 32;
+    const int c4 = (lane & 7) * 4, r4 = lane >> 3;
+    const uint32_t tq = tmem + buf * C::kBN + (static_cast<uint32_t>(quad * 32) << 16);
+    if (from < to && (any || !args.accumulate)) {   // (the same for the warp)
+#pragma unroll 1
+      for (int c = 0; c < C::kOutCols; c += 32) {
+        if (t.q0 + c >= width) break;
+        float4 q[8], q2[8];
+        if (any) {
+          uint32_t v[32], v2[32];
+          tmem_ld_32cols(tq + c, v);
+          if (MODE == kGated) tmem_ld_32cols(tq + C::kBN / 2 + c, v2);
+          tmem_ld_wait();
+          put32(st, lane, v);
+          __syncwarp();
+          get32(st, lane, q);
+          __syncwarp();
+          if (MODE == kGated) {
+            put32(st, lane, v2);
+            __syncwarp();
+            get32(st, lane, q2);
+            __syncwarp();
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const int col = t.q0 + c + c4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + r4;
+          if (r >= from && r < to && col < width) finish4<MODE>(args, out, (row + r) * ld + col, q[i], q2[i]);
+        }
+      }
+    }
+    if (any) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+    }
+  }
+}
+
+template <int MODE, int UNIT>
+__global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT>::kThreads, 1)
+    gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
+                     const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
+                     const Bf16Args args) {
+  using C = Bf16Cfg<MODE, UNIT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* staging = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
+  int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(staging) + C::kStagingBytes);   // [E + 1]
+  int* start = off + kMaxGroups + 4;                                                           // [E + 1]
+  uint64_t* full = reinterpret_cast<uint64_t*>(start + kMaxGroups + 4);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tail = empty + C::kStages;       // kWgrad: a block with rows to be cleared has landed
+  uint64_t* acc_full = tail + C::kStages;    // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2]
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
+    }
+    mbar_init(mma_done, 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    if (args.pairs > 1) prefetch_tmap(&tmA2);
+    if (MODE == kGated || (MODE != kWgrad && args.pairs > 1)) prefetch_tmap(&tmB2);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  griddep_enter();
+
+  const int cap = static_cast<int>(args.rows);
+  for (int e = threadIdx.x; e <= args.E; e += C::kThreads)
+    off[e] = args.offsets != nullptr ? clamp_to(args.offsets[e], 0, cap) : e * cap;
+  __syncthreads();
+  if (MODE != kWgrad && warp == 0) {   // start[]: exclusive prefix sum of the row tiles, a run of groups per lane
+    const int per = (args.E + 31) / 32, e0 = min(lane * per, args.E), e1 = min(e0 + per, args.E);
+    // no more than the launch has room for, whatever the offsets say
+    const int most = most_tiles(cap, args.E, UNIT);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += (max(off[e + 1] - off[e], 0) + UNIT - 1) / UNIT;
+    int run = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(~0u, run, d);
+      if (lane >= d) run += up;
+    }
+    const int tot = __shfl_sync(~0u, run, 31);
+    run -= sum;
+    for (int e = e0; e < e1; ++e) {
+      start[e] = min(run, most);
+      run += (max(off[e + 1] - off[e], 0) + UNIT - 1) / UNIT;
+    }
+    if (lane == 0) start[args.E] = min(tot, most);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Bf16Walk walk;
+  walk.off = off;
+  walk.start = start;
+  walk.total = MODE == kWgrad ? args.E * static_cast<int>(args.by_tiles.d)
+                              : start[args.E] * static_cast<int>(args.by_others.d);
+  const int S = MODE == kWgrad ? 1 : args.splits;
+  const int rank = static_cast<int>(blockIdx.x % S);
+  const int id0 = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
+  const long long budget = args.budget;
+  unsigned* const status = args.status != nullptr ? args.status : &g_status;
+
+  if (warp == 0 && lane == 0) {
+    // ---- TMA producer
+    const uint64_t pol = policy_evict_normal();
+    const uint32_t tx = (MODE == kWgrad ? C::kABytes : args.box * 128) + C::kBBytes;
+    int it = 0;
+    uint32_t cleared = 0, phases = 0;   // stages whose last block went by its tail barrier; those barriers' parities
+    bool ok = true;
+    for (int id = id0; ok && id < walk.total; id += step) {
+      const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const int s = it % C::kStages;
+        if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, budget)) {
+          atomicOr(status, kErrWaitProducer);
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + s * C::kStageBytes;
+        uint8_t* sb = sa + C::kABytes;
+        const bool fix = MODE == kWgrad && kb + 1 == t.kb1 && t.rows % 16 != 0;   // cleared before it is full
+        uint64_t* bar = fix ? &tail[s] : &full[s];
+        cleared = (cleared & ~(1u << s)) | (fix ? 1u << s : 0u);
+        phases ^= fix ? 1u << s : 0u;
+        mbar_arrive_expect_tx(bar, tx);
+        // (the maps' innermost coordinates are bytes)
+        if (MODE == kWgrad) {
+          const CUtensorMap* ma = t.second ? &tmA2 : &tmA;
+          const int r = t.r0 + kb * kBK;
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            tma_load_2d_hint(sa + b * 8192, ma, bar, (t.p0 + b * 64) * 2, r, pol);
+            tma_load_2d_hint(sb + b * 8192, &tmB, bar, (t.q0 + b * 64) * 2, r, pol);
+          }
+        } else {
+          const bool two = kb >= args.num_kb;   // of the second pair
+          const int k0 = (two ? kb - args.num_kb : kb) * kBK;
+          tma_load_2d_hint(sa, two ? &tmA2 : &tmA, bar, k0 * 2, t.p0, pol);
+          const CUtensorMap* mb = two ? &tmB2 : &tmB;
+          if (MODE == kGated) {
+            tma_load_3d_hint(sb, &tmB, bar, k0 * 2, t.q0, t.e, pol);
+            tma_load_3d_hint(sb + 8192, &tmB2, bar, k0 * 2, t.q0, t.e, pol);
+          } else if (C::kColsMn) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) tma_load_3d_hint(sb + b * 8192, mb, bar, (t.q0 + b * 64) * 2, k0, t.e, pol);
+          } else {
+            tma_load_3d_hint(sb, mb, bar, k0 * 2, t.q0, t.e, pol);
+          }
+        }
+      }
+    }
+    // every copy of this thread lands before the CTA leaves
+    for (int j = max(0, it - C::kStages); j < it; ++j) {
+      const int s = j % C::kStages;
+      const bool landed = cleared >> s & 1 ? mbar_wait(&tail[s], (phases >> s & 1) ^ 1, kDrainBudget)
+                                           : mbar_wait(&full[s], (j / C::kStages) & 1, kDrainBudget);
+      if (!landed) atomicOr(status, kErrDrain);
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ---- MMA issuer
+    constexpr uint32_t idesc = idesc_bf16_f32(kBM, C::kBN) | (C::kLanesMn ? 1u << 15 : 0u) | (C::kColsMn ? 1u << 16 : 0u);
+    int it = 0, tc = 0;
+    bool ok = true;
+    for (int id = id0; ok && id < walk.total; id += step) {
+      const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
+      if (t.kb0 >= t.kb1) continue;
+      const int buf = tc & 1;
+      if (!mbar_wait(&acc_empty[buf], ((tc >> 1) & 1) ^ 1, budget)) {
+        atomicOr(status, kErrWaitMma);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * C::kBN;
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const int s = it % C::kStages;
+        if (!mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
+          atomicOr(status, kErrWaitMma);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(smem + s * C::kStageBytes), b0 = a0 + C::kABytes;
+        const uint64_t ad = C::kLanesMn ? sw128_mnmajor_desc(a0) : sw128_kmajor_desc(a0);
+        const uint64_t bd = C::kColsMn ? sw128_mnmajor_desc(b0) : sw128_kmajor_desc(b0);
+        const int left = MODE == kWgrad ? t.rows - kb * kBK : args.k - (kb >= args.num_kb ? kb - args.num_kb : kb) * kBK;
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk) {   // 16 on: 32 bytes, or 2048, in the descriptors' 16-byte addresses
+          if (kk * 16 < left)
+            mma_bf16(acc, ad + (C::kLanesMn ? 128 : 2) * kk, bd + (C::kColsMn ? 128 : 2) * kk, idesc,
+                     kb > t.kb0 || kk > 0);
+        }
+        mma_commit(&empty[s]);
+      }
+      mma_commit(&acc_full[buf]);
+      ++tc;
+    }
+    mma_commit(mma_done);
+  } else if (MODE == kWgrad && warp == 2) {
+    // ---- rows behind an expert's last, cleared in both operands
+    int it = 0;
+    uint32_t phases = 0;
+    for (int id = id0; id < walk.total; id += step) {
+      const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
+      it += t.kb1 - t.kb0;
+      if (t.rows % 16 == 0) continue;
+      const int s = (it - 1) % C::kStages;
+      if (!warp_wait(&tail[s], phases >> s & 1, budget)) {
+        atomicOr(status, kErrWaitProducer);
+        break;
+      }
+      phases ^= 1u << s;
+      const int r = (t.rows - 1) % kBK + 1, end = (r + 15) / 16 * 16;   // rows [r, end) of each of the four boxes
+      uint8_t* at = smem + s * C::kStageBytes;
+      for (int i = lane; i < (end - r) * 32; i += 32) {
+        const int box = i >> 3 & 3, k = r + (i >> 5);
+        *reinterpret_cast<uint4*>(at + box * 8192 + k * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+    }
+  } else if (warp >= 4 && S == 1) {
+    epilogue<MODE, UNIT>(args, walk, staging, acc_full, acc_empty, status, tmem, id0, step, rank);
+  }
+
+  if constexpr (MODE != kWgrad) {
+    if (S > 1) {
+      // One tile per cluster.  Every CTA's sums go to the first one's stages (free once its own MMAs are done), which
+      // adds them in rank order.  All threads pass the cluster barriers, whatever their role.
+      const bool mine = warp >= 4 && id0 < walk.total;
+      const int quad = warp & 3;
+      Bf16Tile t = {};
+      if (mine) {
+        t = tile_at<MODE, UNIT>(walk, args, id0, rank);
+        if (!warp_wait(&acc_full[0], 0, budget)) atomicOr(status, kErrWaitEpilogue);
+        tc_fence_after();
+      }
+      cluster_sync();
+      if (mine && quad * 32 < args.box) {
+        const int r = quad * 32 + lane;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t dst = cluster_map(smem_u32(smem), 0) + (rank * args.box + r) * kLdSplit * 4;
+#pragma unroll 1
+        for (int c = 0; c < C::kBN; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32cols(tq + c, v);
+          tmem_ld_wait();
+          if (r < args.box) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              cluster_store(dst + (c + 4 * i) * 4,
+                            make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                        __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+          }
+        }
+      }
+      cluster_sync();
+      if (mine && rank == 0) {
+        constexpr int kC4 = C::kOutCols / 4;
+        const float* red = reinterpret_cast<const float*>(smem);
+        for (int i = threadIdx.x & 127; i < (t.live - t.skip) * kC4; i += 128) {
+          const int r = t.skip + i / kC4, c = i % kC4 * 4, col = t.q0 + c;
+          if (col >= args.n) continue;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f), v2 = v;
+          for (int q = 0; q < S; ++q) {
+            const float* src = red + (q * args.box + r) * kLdSplit + c;
+            const float4 o = *reinterpret_cast<const float4*>(src);
+            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            if (MODE == kGated) {
+              const float4 p = *reinterpret_cast<const float4*>(src + C::kBN / 2);
+              v2 = make_float4(v2.x + p.x, v2.y + p.y, v2.z + p.z, v2.w + p.w);
+            }
+          }
+          finish4<MODE>(args, args.out, static_cast<long long>(t.p0 + r) * args.n + col, v, v2);
+        }
+      }
+    }
+  }
+  // ---- teardown: all MMAs of this CTA have completed before the columns are released
+  if (warp == 1 && lane == 0)
+    if (!mbar_wait(mma_done, 0, kDrainBudget)) atomicOr(status, kErrDrain);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int MODE, int UNIT>
+cudaError_t launch_one(const CUtensorMap (&m)[4], Bf16Args a, cudaStream_t s) {
+  using C = Bf16Cfg<MODE, UNIT>;
+  const unsigned others = ((MODE == kWgrad ? a.k : a.n) + C::kOutCols - 1) / C::kOutCols;
+  const long long row_tiles = MODE == kWgrad ? (a.n + UNIT - 1) / UNIT : most_tiles(static_cast<int>(a.rows), a.E, UNIT);
+  a.by_others = FastDiv::of(others);
+  a.by_group = FastDiv::of(others * kRaster);
+  a.by_tiles = FastDiv::of(static_cast<unsigned>(MODE == kWgrad ? row_tiles * others * a.pairs : 1));
+  const long long tiles = row_tiles * others * (MODE == kWgrad ? 1LL * a.E * a.pairs : 1);
+  auto kern = gemm_bf16_kernel<MODE, UNIT>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  if (a.splits > 1)
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * a.splits)), dim3(C::kThreads), C::kSmemBytes, s,
+                              a.splits, m[0], m[1], m[2], m[3], a);
+  const long long sms = sm_count();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(C::kThreads), C::kSmemBytes, s,
+                    m[0], m[1], m[2], m[3], a);
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+constexpr int kSms = 152;
+constexpr int kFewRows = 16;
+
+// [rows, cols] bf16, boxes of 64 columns by `high` rows; and [E, rows, cols]
+bool map_rows(CUtensorMap* m, const void* p, long long rows, int cols, int high) {
+  const unsigned long long d[2] = {2ull * cols, static_cast<unsigned long long>(rows)}, st[1] = {2ull * cols};
+  const unsigned box[2] = {128, static_cast<unsigned>(high)};
+  return encode_u8_swizzled(m, p, 2, d, st, box);
+}
+bool map_weights(CUtensorMap* m, const void* p, int E, int rows, int cols, int high) {
+  const unsigned long long d[3] = {2ull * cols, static_cast<unsigned long long>(rows), static_cast<unsigned long long>(E)};
+  const unsigned long long st[2] = {2ull * cols, 2ull * cols * rows};
+  const unsigned box[3] = {128, static_cast<unsigned>(high), 1};
+  return encode_u8_swizzled(m, p, 3, d, st, box);
+}
+
+// What all four entry points check of a shape.
+lmoe_status check_shape(const lmoe_bf16_matmul* c, const int32_t* offsets) {
+  if (c == nullptr || c->rows < 0 || c->N <= 0 || c->K <= 0 || c->n_experts <= 0 || c->wait_budget_cycles < 0)
+    return LMOE_ERR_ARG;
+  if (offsets == nullptr && c->n_experts != 1) return LMOE_ERR_ARG;
+  if (c->out_dtype != LMOE_F32 && c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
+  if (c->n_experts > kMaxGroups || c->K % 8 || c->N % 8 || c->K > (1 << 20) || c->N > (1 << 20) || c->rows > (1LL << 24))
+    return LMOE_ERR_UNSUPPORTED;
+  return LMOE_OK;
+}
+Bf16Args args_of(const lmoe_bf16_matmul* c, const int32_t* offsets, uint32_t* status) {
+  Bf16Args g = {};
+  g.rows = c->rows;
+  g.n = c->N;
+  g.k = c->K;
+  g.num_kb = (c->K + kBK - 1) / kBK;
+  g.pairs = 1;
+  g.E = c->n_experts;
+  g.offsets = offsets;
+  g.splits = 1;
+  g.out_f32 = c->out_dtype == LMOE_F32;
+  g.status = status;
+  g.budget = c->wait_budget_cycles > 0 ? c->wait_budget_cycles : kDefaultWaitBudget;
+  return g;
+}
+
+// One of the modes that take rows of a: which tile, and the launch.  A pair is (a, w).
+template <int MODE>
+lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a2, const void* w2, cudaStream_t stream) {
+  const int R = static_cast<int>(g.rows), live = g.E < R ? g.E : R;
+  const bool few = R / live <= kFewRows;
+  const int unit = few ? 32 : 128;
+  g.box = R < unit ? R : unit;
+  const int across = MODE == kGated ? 64 : 128;
+  const long long tiles = 1LL * most_tiles(R, g.E, unit) * ((g.n + across - 1) / across);
+  if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
+  const int most = few ? Bf16Cfg<MODE, 32>::kSplitMost : Bf16Cfg<MODE, 128>::kSplitMost;
+  while (g.splits < 8 && tiles * g.splits * 2 <= kSms && g.num_kb * g.pairs / (g.splits * 2) >= 4 &&
+         g.splits * 2 * g.box <= most)
+    g.splits *= 2;
+  constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
+  const int high = mn || MODE == kGated ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
+  CUtensorMap m[4];
+  if (!map_rows(&m[0], a, R, g.k, g.box) || !map_weights(&m[2], w, g.E, wr, wc, high)) return LMOE_ERR_CUDA;
+  m[1] = m[0];
+  m[3] = m[2];
+  if ((a2 != nullptr && !map_rows(&m[1], a2, R, g.k, g.box)) || (w2 != nullptr && !map_weights(&m[3], w2, g.E, wr, wc, high)))
+    return LMOE_ERR_CUDA;
+  const cudaError_t e = few ? launch_one<MODE, 32>(m, g, stream) : launch_one<MODE, 128>(m, g, stream);
+  return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace lmoe
+
+using namespace lmoe;
+
+extern "C" lmoe_status lmoe_gated_ffn(const lmoe_bf16_matmul* c, const void* x, const void* w_gate, const void* w_up,
+                                      const int32_t* offsets, void* h, void* gate, void* up, uint32_t* status,
+                                      cudaStream_t stream) {
+  const lmoe_status st = check_shape(c, offsets);
+  if (st != LMOE_OK) return st;
+  if (c->transposed || c->accumulate || (gate == nullptr) != (up == nullptr)) return LMOE_ERR_ARG;
+  if (c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
+  if (c->rows == 0) return LMOE_OK;
+  if (x == nullptr || w_gate == nullptr || w_up == nullptr || h == nullptr) return LMOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(h, 16) || !aligned(gate, 16) ||
+      !aligned(up, 16) || !aligned(offsets, 4) || !aligned(status, 4))
+    return LMOE_ERR_ALIGN;
+  Bf16Args g = args_of(c, offsets, status);
+  g.out = h;
+  g.out2 = gate;
+  g.out3 = up;
+  return rows_product<kGated>(g, x, w_gate, nullptr, w_up, stream);
+}
+
+extern "C" lmoe_status lmoe_gated_ffn_grad(const lmoe_bf16_matmul* c, const void* dy, const void* w_down,
+                                           const void* gate, const void* up, const int32_t* offsets, void* dgate,
+                                           void* dup, uint32_t* status, cudaStream_t stream) {
+  const lmoe_status st = check_shape(c, offsets);
+  if (st != LMOE_OK) return st;
+  if (c->transposed || c->accumulate) return LMOE_ERR_ARG;
+  if (c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
+  if (c->rows == 0) return LMOE_OK;
+  if (dy == nullptr || w_down == nullptr || gate == nullptr || up == nullptr || dgate == nullptr || dup == nullptr)
+    return LMOE_ERR_ARG;
+  if (!aligned(dy, 16) || !aligned(w_down, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(dgate, 16) ||
+      !aligned(dup, 16) || !aligned(offsets, 4) || !aligned(status, 4))
+    return LMOE_ERR_ALIGN;
+  Bf16Args g = args_of(c, offsets, status);
+  g.gate = static_cast<const __nv_bfloat16*>(gate);
+  g.up = static_cast<const __nv_bfloat16*>(up);
+  g.out = dgate;
+  g.out2 = dup;
+  return rows_product<kGatedGrad>(g, dy, w_down, nullptr, nullptr, stream);
+}
+
+extern "C" lmoe_status lmoe_matmul_bf16(const lmoe_bf16_matmul* c, const void* a, const void* w, const void* a2,
+                                        const void* w2, const int32_t* offsets, void* out, uint32_t* status,
+                                        cudaStream_t stream) {
+  const lmoe_status st = check_shape(c, offsets);
+  if (st != LMOE_OK) return st;
+  if (c->accumulate || (a2 == nullptr) != (w2 == nullptr)) return LMOE_ERR_ARG;
+  if (c->rows == 0) return LMOE_OK;
+  if (a == nullptr || w == nullptr || out == nullptr) return LMOE_ERR_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a2, 16) || !aligned(w2, 16) || !aligned(out, 16) ||
+      !aligned(offsets, 4) || !aligned(status, 4))
+    return LMOE_ERR_ALIGN;
+  Bf16Args g = args_of(c, offsets, status);
+  g.pairs = a2 != nullptr ? 2 : 1;
+  g.out = out;
+  return c->transposed ? rows_product<kProductT>(g, a, w, a2, w2, stream) : rows_product<kProduct>(g, a, w, a2, w2, stream);
+}
+
+extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const void* dy, const void* x,
+                                              const void* dy2, const int32_t* offsets, void* dw, void* dw2,
+                                              uint32_t* status, cudaStream_t stream) {
+  const lmoe_status st = check_shape(c, offsets);
+  if (st != LMOE_OK) return st;
+  if (c->transposed || dw == nullptr) return LMOE_ERR_ARG;
+  if (c->rows > 0 && (dy == nullptr || x == nullptr || (dy2 == nullptr) != (dw2 == nullptr))) return LMOE_ERR_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dy2, 16) || !aligned(dw, 16) || !aligned(dw2, 16) ||
+      !aligned(offsets, 4) || !aligned(status, 4))
+    return LMOE_ERR_ALIGN;
+  if (c->rows == 0) {
+    if (c->accumulate) return LMOE_OK;
+    const size_t bytes = static_cast<size_t>(c->n_experts) * c->N * c->K * (c->out_dtype == LMOE_F32 ? 4 : 2);
+    if (cudaMemsetAsync(dw, 0, bytes, stream) != cudaSuccess) return LMOE_ERR_CUDA;
+    if (dw2 != nullptr && cudaMemsetAsync(dw2, 0, bytes, stream) != cudaSuccess) return LMOE_ERR_CUDA;
+    return LMOE_OK;
+  }
+  Bf16Args g = args_of(c, offsets, status);
+  g.num_kb = 0;
+  g.pairs = dy2 != nullptr ? 2 : 1;
+  g.out = dw;
+  g.out2 = dw2;
+  g.accumulate = c->accumulate != 0;
+  const long long tiles = 1LL * ((c->N + 127) / 128) * ((c->K + 127) / 128) * c->n_experts * g.pairs;
+  if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
+  CUtensorMap m[4];
+  if (!map_rows(&m[0], dy, c->rows, c->N, kBK) || !map_rows(&m[2], x, c->rows, c->K, kBK)) return LMOE_ERR_CUDA;
+  m[1] = m[0];
+  m[3] = m[2];
+  if (dy2 != nullptr && !map_rows(&m[1], dy2, c->rows, c->N, kBK)) return LMOE_ERR_CUDA;
+  return launch_one<kWgrad, 128>(m, g, stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+}
+
+extern "C" lmoe_status lmoe_bf16_check_status(cudaStream_t stream, uint32_t* detail) {
+  static std::mutex mu;   // (one landing place for the word)
+  std::lock_guard<std::mutex> lock(mu);
+  uint32_t word = 0;
+  if (launch_pdl(take_status_kernel, dim3(1), dim3(1), 0, stream) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&word, g_status_taken, 4, 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return LMOE_ERR_CUDA;
+  if (detail != nullptr) *detail = word;
+  return word == 0 ? LMOE_OK : LMOE_ERR_TIMEOUT;
+}
+
+extern "C" lmoe_status lmoe_bf16_wait_selftest(long long budget_cycles, cudaStream_t stream) {
+  const long long b = budget_cycles < 1 ? 1 : budget_cycles > kDefaultWaitBudget ? kDefaultWaitBudget : budget_cycles;
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, g_status) != cudaSuccess) return LMOE_ERR_CUDA;
+  return launch_wait_selftest(b, static_cast<unsigned*>(word), stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+}

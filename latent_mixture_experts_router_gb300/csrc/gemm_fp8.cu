@@ -39,6 +39,7 @@
 #include <mutex>
 
 #include "../../include/latent_moe.h"
+#include "groups.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -46,24 +47,7 @@ namespace lmoe {
 namespace {
 
 enum Fp8Mode : int { kCols = 0, kWgrad = 1, kSplit = 2, kRows = 3 };
-constexpr int kMaxGroups = 1024;
 constexpr int kMaxSplit = 8;
-
-// Division of n < 2^31 by a fixed d, by a multiplication (Granlund and Montgomery 1994): the walk of
-// the tiles divides several times for each, and a division takes a thread beside busy ones hundreds
-// of cycles.
-struct FastDiv {
-  unsigned d, mul, shift;
-  __host__ static FastDiv of(unsigned d) {
-    unsigned shift = 0;
-    while ((1ull << shift) < d) ++shift;
-    return {d, static_cast<unsigned>(((1ull << 32) * ((1ull << shift) - d)) / d + 1), shift};
-  }
-  __device__ __forceinline__ int div(int n) const {
-    return static_cast<int>((__umulhi(static_cast<unsigned>(n), mul) + static_cast<unsigned>(n)) >> shift);
-  }
-  __device__ __forceinline__ int mod(int n) const { return n - div(n) * static_cast<int>(d); }
-};
 
 struct Fp8Args {
   FastDiv by_others, by_group, by_E;   // tiles across; kRasterGroup rows of them; experts
@@ -141,14 +125,6 @@ LMOE_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-LMOE_DEV void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
-                               uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
 // 16 lanes x 8 N columns: thread l gets, per 8 columns, columns 2 (l % 4), + 1 of lanes l / 4
@@ -279,11 +255,6 @@ LMOE_DEV bool named_barrier_all(int id, int threads, bool ok) {
       : "memory");
   return r != 0;
 }
-// mbar_wait of a whole warp, with one outcome: its lanes' own waits may give up one by one, and TMEM reads,
-// votes and warp barriers follow that need all of them.
-LMOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, long long budget) {
-  return __all_sync(~0u, mbar_wait(bar, parity, budget));
-}
 // Rows of group e, clamped into the rows there are, so that no offsets send a load or a store out
 // of range.
 LMOE_DEV void group_rows(const Fp8Args& a, int e, int& lo, int& hi) {
@@ -391,11 +362,6 @@ LMOE_DEV Fp8Tile tile_at(const Fp8Walk& w, const Fp8Args& a, int id, int rank) {
     }
   }
   return t;
-}
-
-// Row tiles of `unit` rows that any split of `rows` among E experts takes at most (rows > 0).
-__host__ __device__ constexpr int most_tiles(int rows, int E, int unit) {
-  return (rows + unit - 1) / unit + (E < rows ? E : rows) - 1;
 }
 
 // What an epilogue thread needs to wait for the blocks of its tile.
