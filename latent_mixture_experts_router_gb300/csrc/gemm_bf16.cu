@@ -37,6 +37,13 @@ enum Bf16Mode : int { kGated = 0, kGatedGrad = 1, kProduct = 2, kProductT = 3, k
 constexpr int kRaster = 8;       // row tiles that take turns before the next column of tiles
 constexpr int kLdStage = 36;     // floats of a staged row of 32: rows four apart share no banks
 constexpr int kLdSplit = 132;    // floats of a row of 128 partial sums
+// Tensor memory's fp32 sums are cut, not rounded, at each addition: 4096 products in a row leave 4.4e-6 of the result (2-norm),
+// in proportion to their number.  bf16 results do not show it; for fp32 results a sum in TMEM ends after kChunk
+// blocks of 64, and the epilogue adds those in registers (5e-7).
+constexpr int kChunk = 8;
+// Budget of the waits for a CTA's own copies and MMAs at its end: they take microseconds.  (In a pair whose second CTA gave
+// up, the first one waits that long for copies that never started.)
+constexpr long long kDrain = 20000000;
 
 struct Bf16Args {
   FastDiv by_others, by_group;   // tiles across; kRaster rows of them
@@ -63,24 +70,27 @@ __global__ void take_status_kernel() {
   g_status_taken = atomicExch(&g_status, 0u);
 }
 
-// UNIT: rows of a tile of one CTA.
-template <int MODE, int UNIT>
+// UNIT: rows of a tile; 256: a pair of CTAs, 128 rows and half of the column operand's tile each.
+// F32: fp32 results of long reductions, see kChunk.
+template <int MODE, int UNIT, bool F32>
 struct Bf16Cfg {
+  static constexpr bool kPair = UNIT == 256;
   static constexpr bool kLanesMn = MODE == kWgrad;
   static constexpr bool kColsMn = MODE == kWgrad || MODE == kGatedGrad || MODE == kProductT;
-  static constexpr int kLanes = UNIT;                             // that a CTA loads
-  static constexpr int kBN = 128;                                 // accumulator columns
+  static constexpr int kLanes = kPair ? 128 : UNIT;               // that a CTA loads
+  static constexpr int kBN = kPair ? 256 : 128;                   // accumulator columns
   static constexpr int kOutCols = MODE == kGated ? kBN / 2 : kBN;  // columns of a tile
-  static constexpr int kThreads = 256;
+  static constexpr int kEpiWarps = kPair ? 8 : 4;
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kABytes = kLanes * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
-  static constexpr int kStagingBytes = 4 * 32 * kLdStage * 4;
+  static constexpr int kStagingBytes = kEpiWarps * 32 * kLdStage * 4;
   static constexpr int kTableBytes = 2 * (kMaxGroups + 4) * 4;
   static constexpr int kFixed = kStagingBytes + kTableBytes + 512 + 1024;
   static constexpr int kFit = (227 * 1024 - kFixed) / kStageBytes;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
   static constexpr uint32_t kTmemCols = 2 * kBN;
-  static constexpr int kSplitMost = kStages * kStageBytes / (kLdSplit * 4);   // rows of partial sums that fit
+  static constexpr int kChunkBlocks = F32 ? kChunk : 1 << 30;
   static_assert((3 * kStages + 2 * 2 + 1) * 8 + 8 <= 512, "barriers");
   // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
   static_assert(kStageBytes >= 128 * 128, "lane operand");
@@ -97,6 +107,77 @@ LMOE_DEV uint64_t sw128_mnmajor_desc(uint32_t saddr) {
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
+}
+
+// ---- pairs of CTAs (cta_group::2): both hold their halves of the operands at the same place, the first one's thread
+// issues for both, and barriers that it waits for are the first one's.
+LMOE_DEV void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+LMOE_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+LMOE_DEV void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on this barrier of both CTAs.
+LMOE_DEV void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// Loads into this CTA's shared memory that are counted by the barrier at cluster address `bar`.
+LMOE_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+LMOE_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+LMOE_DEV void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait for a barrier on which another CTA's threads arrive.
+LMOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, long long budget) {
+  const uint32_t a = smem_u32(bar);
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(kWaitSleepNs)
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > budget) return false;
+  }
+}
+// Registers of a warpgroup: 4 x 32 x 56 + 8 x 32 x 224 = 384 x 168, what the block was launched with.
+template <int N>
+LMOE_DEV void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+LMOE_DEV void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 LMOE_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -127,9 +208,9 @@ struct Bf16Walk {
   int total;
 };
 
-template <int MODE, int UNIT>
+template <int MODE, int UNIT, bool F32>
 LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank) {
-  using C = Bf16Cfg<MODE, UNIT>;
+  using C = Bf16Cfg<MODE, UNIT, F32>;
   Bf16Tile t = {};
   int i, rows;   // tile i of `rows` row tiles by by_others.d
   if (MODE == kWgrad) {
@@ -157,11 +238,15 @@ LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank
   const int lo = w.off[t.e], hi = max(w.off[t.e + 1], lo);
   t.q0 = other * C::kOutCols;
   if (MODE == kWgrad) {
-    t.p0 = rt * UNIT;
+    t.p0 = rt * UNIT + (C::kPair ? rank * 128 : 0);
     t.live = min(a.n - t.p0, C::kLanes);
     t.r0 = lo;
     t.rows = hi - lo;
     t.kb1 = (hi - lo + kBK - 1) / kBK;
+  } else if (C::kPair) {
+    t.p0 = lo + rt * UNIT + rank * 128;
+    t.live = min(hi - t.p0, 128);
+    t.kb1 = a.num_kb * a.pairs;
   } else {
     // Tiles of few rows: no row behind the last is asked for (a box filled with zeros past the end costs the
     // copy engine more than rows); a tile near the end starts earlier and skips the lanes before its own.
@@ -235,12 +320,10 @@ LMOE_DEV void finish4(const Bf16Args& a, void* out, long long at, float4 v, floa
 
 // A warp's 32 lanes by 32 columns, a lane to a thread, into rows of shared memory; then thread l has columns
 // 4 (l % 8) .. of rows l / 8, + 4, ...
-LMOE_DEV void put32(float* st, int lane, const uint32_t (&v)[32]) {
+LMOE_DEV void put32(float* st, int lane, const float* v) {
   float4* o = reinterpret_cast<float4*>(st + lane * kLdStage);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    o[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                       __uint_as_float(v[4 * i + 3]));
+  for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 LMOE_DEV void get32(const float* st, int lane, float4 (&q)[8]) {
 #pragma unroll
@@ -248,78 +331,135 @@ LMOE_DEV void get32(const float* st, int lane, float4 (&q)[8]) {
     q[i] = *reinterpret_cast<const float4*>(st + (4 * i + (lane >> 3)) * kLdStage + (lane & 7) * 4);
 }
 
-template <int MODE, int UNIT>
-LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, float* staging, uint64_t* acc_full,
-                       uint64_t* acc_empty, unsigned* status, uint32_t tmem, int id0, int step, int rank) {
-  using C = Bf16Cfg<MODE, UNIT>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3;
-  float* st = staging + quad * 32 * kLdStage;
+// Where an epilogue warp waits for sums, and gives their buffers back.
+struct Bf16Ring {
+  uint64_t* acc_full;
+  uint32_t acc_empty;   // cluster address where the MMA issuer's barriers are (its own CTA's)
+  unsigned* status;
+  long long budget;
+  LMOE_DEV bool wait(int tc) const {
+    const bool ok = warp_wait(&acc_full[tc & 1], (tc >> 1) & 1, budget);
+    if (!ok) atomicOr(status, kErrWaitEpilogue);
+    tc_fence_after();
+    return ok;
+  }
+  LMOE_DEV void release(int tc, int lane) const {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(acc_empty + (tc & 1) * 8);
+  }
+};
+// The sums of a tile over all its chunks, 128 columns of this thread's lane from column c0 on, in registers; false if a
+// wait gave up.
+template <int BN>
+LMOE_DEV bool gather_sums(const Bf16Ring& ring, uint32_t tmem, int c0, int chunks, int& tc, int lane, int quad,
+                          float (&acc)[128]) {
+  for (int ch = 0; ch < chunks; ++ch, ++tc) {
+    if (!ring.wait(tc)) return false;
+    const uint32_t tq = tmem + (tc & 1) * BN + c0 + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[32];
+      tmem_ld_32cols(tq + c * 32, v);
+      tmem_ld_wait();
+      if (ch == 0) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = __uint_as_float(v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c * 32 + i] += __uint_as_float(v[i]);
+      }
+    }
+    ring.release(tc, lane);
+  }
+  return true;
+}
+
+template <int MODE, int UNIT, bool F32>
+LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Ring& ring, float* staging, uint32_t tmem,
+                       int id0, int step, int rank) {
+  using C = Bf16Cfg<MODE, UNIT, F32>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = (warp - 4) >> 2;
+  constexpr int kCols = C::kOutCols * 4 / C::kEpiWarps;   // of this warp
+  float* st = staging + (warp - 4) * 32 * kLdStage;
+  const int c4 = (lane & 7) * 4, r4 = lane >> 3;
+  const int width = MODE == kWgrad ? args.k : args.n;
   int tc = 0;
   for (int id = id0; id < walk.total; id += step) {
-    const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
-    const bool any = t.kb0 < t.kb1;   // (kWgrad: an expert without rows has no blocks, and gets zeros)
-    const int buf = tc & 1;
-    if (any) {
-      if (!warp_wait(&acc_full[buf], (tc >> 1) & 1, args.budget)) {
-        atomicOr(status, kErrWaitEpilogue);
-        return;
-      }
-      tc_fence_after();
-      ++tc;
-    }
+    const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+    const int blocks = t.kb1 - t.kb0;   // (kWgrad: an expert without rows has none, and gets zeros)
     const int from = max(t.skip - quad * 32, 0), to = min(t.live - quad * 32, 32);   // lanes of this warp
-    const int width = MODE == kWgrad ? args.k : args.n;
-    const long long ld = width;
     void* out = MODE == kWgrad && t.second ? args.out2 : args.out;
     const long long row = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0 + quad * 32;
-    const int c4 = (lane & 7) * 4, r4 = lane >> 3;
-    const uint32_t tq = tmem + buf * C::kBN + (static_cast<uint32_t>(quad * 32) << 16);
-    if (from < to && (any || !args.accumulate)) {   // (the same for the warp)
+    const int q0 = t.q0 + half * kCols;
+    // four rows to a store instruction
+    const auto store = [&](int c, const float4(&q)[8], const float4(&q2)[8]) {
+      const int col = q0 + c + c4;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + r4;
+        if (r >= from && r < to && col < width) finish4<MODE>(args, out, (row + r) * width + col, q[i], q2[i]);
+      }
+    };
+    if (F32 && blocks > 0) {
+      float acc[128];
+      const int chunks = (blocks + C::kChunkBlocks - 1) / C::kChunkBlocks;
+      if (!gather_sums<C::kBN>(ring, tmem, half * kCols, chunks, tc, lane, quad, acc)) return;
+      if (from >= to) continue;   // (the same for the warp)
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        if (q0 + c >= width) break;
+        float4 q[8];
+        put32(st, lane, acc + c);
+        __syncwarp();
+        get32(st, lane, q);
+        __syncwarp();
+        store(c, q, q);
+      }
+      continue;
+    }
+    if (blocks > 0) {
+      if (!ring.wait(tc)) return;
+      const uint32_t tq = tmem + (tc & 1) * C::kBN + half * kCols + (static_cast<uint32_t>(quad * 32) << 16);
+      if (from < to) {
 #pragma unroll 1
-      for (int c = 0; c < C::kOutCols; c += 32) {
-        if (t.q0 + c >= width) break;
-        float4 q[8], q2[8];
-        if (any) {
+        for (int c = 0; c < kCols; c += 32) {
+          if (q0 + c >= width) break;
+          float4 q[8], q2[8];
           uint32_t v[32], v2[32];
           tmem_ld_32cols(tq + c, v);
           if (MODE == kGated) tmem_ld_32cols(tq + C::kBN / 2 + c, v2);
           tmem_ld_wait();
-          put32(st, lane, v);
+          put32(st, lane, reinterpret_cast<const float*>(v));
           __syncwarp();
           get32(st, lane, q);
           __syncwarp();
           if (MODE == kGated) {
-            put32(st, lane, v2);
+            put32(st, lane, reinterpret_cast<const float*>(v2));
             __syncwarp();
             get32(st, lane, q2);
             __syncwarp();
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        const int col = t.q0 + c + c4;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + r4;
-          if (r >= from && r < to && col < width) finish4<MODE>(args, out, (row + r) * ld + col, q[i], q2[i]);
+          store(c, q, q2);
         }
       }
-    }
-    if (any) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      ring.release(tc, lane);
+      ++tc;
+    } else if (from < to && !args.accumulate) {
+      float4 q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < kCols; c += 32) store(c, q, q);
     }
   }
 }
 
-template <int MODE, int UNIT>
-__global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT>::kThreads, 1)
+template <int MODE, int UNIT, bool F32>
+__global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
     gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
                      const Bf16Args args) {
-  using C = Bf16Cfg<MODE, UNIT>;
+  using C = Bf16Cfg<MODE, UNIT, F32>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -337,13 +477,13 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], C::kPair && MODE == kWgrad ? 2 : 1);
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4);
+      mbar_init(&acc_empty[b], C::kEpiWarps * (C::kPair ? 2 : 1));
     }
     mbar_init(mma_done, 1);
     fence_mbar_init();
@@ -353,8 +493,12 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT>::kThreads, 1)
     if (MODE == kGated || (MODE != kWgrad && args.pairs > 1)) prefetch_tmap(&tmB2);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
-    tmem_relinquish();
+    if (C::kPair) {
+      tmem_alloc_pair(tmem_slot, C::kTmemCols);
+    } else {
+      tmem_alloc(tmem_slot, C::kTmemCols);
+      tmem_relinquish();
+    }
   }
   griddep_enter();
 
@@ -384,6 +528,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (C::kPair) cluster_sync();   // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Bf16Walk walk;
@@ -391,165 +536,191 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT>::kThreads, 1)
   walk.start = start;
   walk.total = MODE == kWgrad ? args.E * static_cast<int>(args.by_tiles.d)
                               : start[args.E] * static_cast<int>(args.by_others.d);
-  const int S = MODE == kWgrad ? 1 : args.splits;
+  const int S = C::kPair ? 2 : MODE == kWgrad ? 1 : args.splits;   // CTAs of a cluster
   const int rank = static_cast<int>(blockIdx.x % S);
   const int id0 = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
   const long long budget = args.budget;
   unsigned* const status = args.status != nullptr ? args.status : &g_status;
 
-  if (warp == 0 && lane == 0) {
-    // ---- TMA producer
-    const uint64_t pol = policy_evict_normal();
-    const uint32_t tx = (MODE == kWgrad ? C::kABytes : args.box * 128) + C::kBBytes;
-    int it = 0;
-    uint32_t cleared = 0, phases = 0;   // stages whose last block went by its tail barrier; those barriers' parities
-    bool ok = true;
-    for (int id = id0; ok && id < walk.total; id += step) {
-      const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        const int s = it % C::kStages;
-        if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, budget)) {
-          atomicOr(status, kErrWaitProducer);
-          ok = false;
-          break;
-        }
-        uint8_t* sa = smem + s * C::kStageBytes;
-        uint8_t* sb = sa + C::kABytes;
-        const bool fix = MODE == kWgrad && kb + 1 == t.kb1 && t.rows % 16 != 0;   // cleared before it is full
-        uint64_t* bar = fix ? &tail[s] : &full[s];
-        cleared = (cleared & ~(1u << s)) | (fix ? 1u << s : 0u);
-        phases ^= fix ? 1u << s : 0u;
-        mbar_arrive_expect_tx(bar, tx);
-        // (the maps' innermost coordinates are bytes)
-        if (MODE == kWgrad) {
-          const CUtensorMap* ma = t.second ? &tmA2 : &tmA;
-          const int r = t.r0 + kb * kBK;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            tma_load_2d_hint(sa + b * 8192, ma, bar, (t.p0 + b * 64) * 2, r, pol);
-            tma_load_2d_hint(sb + b * 8192, &tmB, bar, (t.q0 + b * 64) * 2, r, pol);
+  const Bf16Ring ring = {acc_full, C::kPair ? cluster_map(smem_u32(acc_empty), 0) : smem_u32(acc_empty), status, budget};
+  if (warp < 4) {
+    if constexpr (C::kPair && F32) regs_dec<56>();
+    if (warp == 0 && lane == 0) {
+      // ---- TMA producer
+      const uint64_t pol = policy_evict_normal();
+      const uint32_t tx = (MODE == kWgrad || C::kPair ? C::kABytes : args.box * 128) + C::kBBytes;
+      int it = 0;
+      uint32_t cleared = 0, phases = 0;   // stages whose last block went by its tail barrier; those barriers' parities
+      bool ok = true;
+      for (int id = id0; ok && id < walk.total; id += step) {
+        const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+        const int qb = t.q0 + (C::kPair && MODE != kGated ? rank * 128 : 0);   // the column operand's part of this CTA
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const int s = it % C::kStages;
+          if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, budget)) {
+            atomicOr(status, kErrWaitProducer);
+            ok = false;
+            break;
           }
-        } else {
-          const bool two = kb >= args.num_kb;   // of the second pair
-          const int k0 = (two ? kb - args.num_kb : kb) * kBK;
-          tma_load_2d_hint(sa, two ? &tmA2 : &tmA, bar, k0 * 2, t.p0, pol);
-          const CUtensorMap* mb = two ? &tmB2 : &tmB;
-          if (MODE == kGated) {
-            tma_load_3d_hint(sb, &tmB, bar, k0 * 2, t.q0, t.e, pol);
-            tma_load_3d_hint(sb + 8192, &tmB2, bar, k0 * 2, t.q0, t.e, pol);
-          } else if (C::kColsMn) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) tma_load_3d_hint(sb + b * 8192, mb, bar, (t.q0 + b * 64) * 2, k0, t.e, pol);
+          uint8_t* sa = smem + s * C::kStageBytes;
+          uint8_t* sb = sa + C::kABytes;
+          const bool fix = MODE == kWgrad && kb + 1 == t.kb1 && t.rows % 16 != 0;   // cleared before it is full
+          cleared = (cleared & ~(1u << s)) | (fix ? 1u << s : 0u);
+          phases ^= fix ? 1u << s : 0u;
+          uint64_t* bar = fix ? &tail[s] : &full[s];
+          const uint32_t there = C::kPair ? cluster_map(smem_u32(&full[s]), 0) : 0;
+          if (fix || !C::kPair) mbar_arrive_expect_tx(bar, tx);
+          else if (rank == 0) mbar_arrive_expect_tx(bar, 2 * tx);
+          else if (MODE == kWgrad) mbar_arrive_cluster(there);
+          // (the maps' innermost coordinates are bytes)
+          const auto load2 = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
+            if (C::kPair && !fix) tma_load_2d_pair(dst, m, there, c0, c1, pol);
+            else tma_load_2d_hint(dst, m, bar, c0, c1, pol);
+          };
+          const auto load3 = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
+            if (C::kPair) tma_load_3d_pair(dst, m, there, c0, c1, t.e, pol);
+            else tma_load_3d_hint(dst, m, bar, c0, c1, t.e, pol);
+          };
+          if (MODE == kWgrad) {
+            const CUtensorMap* ma = t.second ? &tmA2 : &tmA;
+            const int r = t.r0 + kb * kBK;
+  #pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              load2(sa + b * 8192, ma, (t.p0 + b * 64) * 2, r);
+              load2(sb + b * 8192, &tmB, (qb + b * 64) * 2, r);
+            }
           } else {
-            tma_load_3d_hint(sb, mb, bar, k0 * 2, t.q0, t.e, pol);
+            const bool two = kb >= args.num_kb;   // of the second pair
+            const int k0 = (two ? kb - args.num_kb : kb) * kBK;
+            load2(sa, two ? &tmA2 : &tmA, k0 * 2, t.p0);
+            const CUtensorMap* mb = two ? &tmB2 : &tmB;
+            if (MODE == kGated) {
+              if (C::kPair) {   // gate's rows here, up's in the other CTA
+                load3(sb, rank == 0 ? &tmB : &tmB2, k0 * 2, qb);
+              } else {
+                load3(sb, &tmB, k0 * 2, qb);
+                load3(sb + 8192, &tmB2, k0 * 2, qb);
+              }
+            } else if (C::kColsMn) {
+  #pragma unroll
+              for (int b = 0; b < 2; ++b) load3(sb + b * 8192, mb, (qb + b * 64) * 2, k0);
+            } else {
+              load3(sb, mb, k0 * 2, qb);
+            }
           }
         }
       }
-    }
-    // every copy of this thread lands before the CTA leaves
-    for (int j = max(0, it - C::kStages); j < it; ++j) {
-      const int s = j % C::kStages;
-      const bool landed = cleared >> s & 1 ? mbar_wait(&tail[s], (phases >> s & 1) ^ 1, kDrainBudget)
-                                           : mbar_wait(&full[s], (j / C::kStages) & 1, kDrainBudget);
-      if (!landed) atomicOr(status, kErrDrain);
-    }
-  } else if (warp == 1 && lane == 0) {
-    // ---- MMA issuer
-    constexpr uint32_t idesc = idesc_bf16_f32(kBM, C::kBN) | (C::kLanesMn ? 1u << 15 : 0u) | (C::kColsMn ? 1u << 16 : 0u);
-    int it = 0, tc = 0;
-    bool ok = true;
-    for (int id = id0; ok && id < walk.total; id += step) {
-      const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
-      if (t.kb0 >= t.kb1) continue;
-      const int buf = tc & 1;
-      if (!mbar_wait(&acc_empty[buf], ((tc >> 1) & 1) ^ 1, budget)) {
-        atomicOr(status, kErrWaitMma);
-        break;
+      // every copy of this thread lands before the CTA leaves (a pair's are counted by the first CTA, and neither leaves
+      // before the other)
+      for (int j = max(0, it - C::kStages); j < it; ++j) {
+        const int s = j % C::kStages;
+        const bool tail_bar = cleared >> s & 1;
+        if (C::kPair && rank != 0 && !tail_bar) continue;
+        const bool landed = tail_bar ? mbar_wait(&tail[s], (phases >> s & 1) ^ 1, kDrain)
+                                     : mbar_wait(&full[s], (j / C::kStages) & 1, kDrain);
+        if (!landed) atomicOr(status, kErrDrain);
       }
-      tc_fence_after();
-      const uint32_t acc = tmem + buf * C::kBN;
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        const int s = it % C::kStages;
-        if (!mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
-          atomicOr(status, kErrWaitMma);
-          ok = false;
+    } else if (warp == 1 && lane == 0 && (!C::kPair || rank == 0)) {
+      // ---- MMA issuer
+      constexpr uint32_t idesc = idesc_bf16_f32(C::kPair ? 256 : 128, C::kBN) | (C::kLanesMn ? 1u << 15 : 0u) |
+                                 (C::kColsMn ? 1u << 16 : 0u);
+      const auto commit = [](uint64_t* bar) {
+        if (C::kPair) mma_commit_pair(bar);
+        else mma_commit(bar);
+      };
+      int it = 0, tc = 0;
+      bool ok = true;
+      for (int id = id0; ok && id < walk.total; id += step) {
+        const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+        for (int c0 = t.kb0; ok && c0 < t.kb1; c0 += C::kChunkBlocks, ++tc) {
+          const int buf = tc & 1, c1 = min(t.kb1 - c0, C::kChunkBlocks) + c0;
+          if (!mbar_wait_cluster(&acc_empty[buf], ((tc >> 1) & 1) ^ 1, budget)) {
+            atomicOr(status, kErrWaitMma);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t acc = tmem + buf * C::kBN;
+          for (int kb = c0; kb < c1; ++kb, ++it) {
+            const int s = it % C::kStages;
+            if (!(MODE == kWgrad && C::kPair ? mbar_wait_cluster(&full[s], (it / C::kStages) & 1, budget)
+                                             : mbar_wait(&full[s], (it / C::kStages) & 1, budget))) {
+              atomicOr(status, kErrWaitMma);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(smem + s * C::kStageBytes), b0 = a0 + C::kABytes;
+            const uint64_t ad = C::kLanesMn ? sw128_mnmajor_desc(a0) : sw128_kmajor_desc(a0);
+            const uint64_t bd = C::kColsMn ? sw128_mnmajor_desc(b0) : sw128_kmajor_desc(b0);
+            const int left = MODE == kWgrad ? t.rows - kb * kBK
+                                            : args.k - (kb >= args.num_kb ? kb - args.num_kb : kb) * kBK;
+  #pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) {   // 16 on: 32 bytes, or 2048, in the descriptors' 16-byte addresses
+              if (kk * 16 >= left) break;
+              const uint64_t ak = ad + (C::kLanesMn ? 128 : 2) * kk, bk = bd + (C::kColsMn ? 128 : 2) * kk;
+              if (C::kPair) mma_bf16_pair(acc, ak, bk, idesc, kb > c0 || kk > 0);
+              else mma_bf16(acc, ak, bk, idesc, kb > c0 || kk > 0);
+            }
+            commit(&empty[s]);
+          }
+          commit(&acc_full[buf]);
+        }
+      }
+      commit(mma_done);
+    } else if (MODE == kWgrad && warp == 2) {
+      // ---- rows behind an expert's last, cleared in both operands
+      int it = 0;
+      uint32_t phases = 0;
+      for (int id = id0; id < walk.total; id += step) {
+        const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+        it += t.kb1 - t.kb0;
+        if (t.rows % 16 == 0) continue;
+        const int s = (it - 1) % C::kStages;
+        if (!warp_wait(&tail[s], phases >> s & 1, budget)) {
+          atomicOr(status, kErrWaitProducer);
           break;
         }
-        tc_fence_after();
-        const uint32_t a0 = smem_u32(smem + s * C::kStageBytes), b0 = a0 + C::kABytes;
-        const uint64_t ad = C::kLanesMn ? sw128_mnmajor_desc(a0) : sw128_kmajor_desc(a0);
-        const uint64_t bd = C::kColsMn ? sw128_mnmajor_desc(b0) : sw128_kmajor_desc(b0);
-        const int left = MODE == kWgrad ? t.rows - kb * kBK : args.k - (kb >= args.num_kb ? kb - args.num_kb : kb) * kBK;
-#pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk) {   // 16 on: 32 bytes, or 2048, in the descriptors' 16-byte addresses
-          if (kk * 16 < left)
-            mma_bf16(acc, ad + (C::kLanesMn ? 128 : 2) * kk, bd + (C::kColsMn ? 128 : 2) * kk, idesc,
-                     kb > t.kb0 || kk > 0);
+        phases ^= 1u << s;
+        const int r = (t.rows - 1) % kBK + 1, end = (r + 15) / 16 * 16;   // rows [r, end) of each of the four boxes
+        uint8_t* at = smem + s * C::kStageBytes;
+        for (int i = lane; i < (end - r) * 32; i += 32) {
+          const int box = i >> 3 & 3, k = r + (i >> 5);
+          *reinterpret_cast<uint4*>(at + box * 8192 + k * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
-        mma_commit(&empty[s]);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(C::kPair ? cluster_map(smem_u32(&full[s]), 0) : smem_u32(&full[s]));
       }
-      mma_commit(&acc_full[buf]);
-      ++tc;
     }
-    mma_commit(mma_done);
-  } else if (MODE == kWgrad && warp == 2) {
-    // ---- rows behind an expert's last, cleared in both operands
-    int it = 0;
-    uint32_t phases = 0;
-    for (int id = id0; id < walk.total; id += step) {
-      const Bf16Tile t = tile_at<MODE, UNIT>(walk, args, id, rank);
-      it += t.kb1 - t.kb0;
-      if (t.rows % 16 == 0) continue;
-      const int s = (it - 1) % C::kStages;
-      if (!warp_wait(&tail[s], phases >> s & 1, budget)) {
-        atomicOr(status, kErrWaitProducer);
-        break;
-      }
-      phases ^= 1u << s;
-      const int r = (t.rows - 1) % kBK + 1, end = (r + 15) / 16 * 16;   // rows [r, end) of each of the four boxes
-      uint8_t* at = smem + s * C::kStageBytes;
-      for (int i = lane; i < (end - r) * 32; i += 32) {
-        const int box = i >> 3 & 3, k = r + (i >> 5);
-        *reinterpret_cast<uint4*>(at + box * 8192 + k * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-      }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
-    }
-  } else if (warp >= 4 && S == 1) {
-    epilogue<MODE, UNIT>(args, walk, staging, acc_full, acc_empty, status, tmem, id0, step, rank);
+  } else {
+    if constexpr (C::kPair && F32) regs_inc<224>();
+    if (C::kPair || S == 1) epilogue<MODE, UNIT, F32>(args, walk, ring, staging, tmem, id0, step, rank);
   }
 
-  if constexpr (MODE != kWgrad) {
+  if constexpr (MODE != kWgrad && !C::kPair) {
     if (S > 1) {
       // One tile per cluster.  Every CTA's sums go to the first one's stages (free once its own MMAs are done), which
       // adds them in rank order.  All threads pass the cluster barriers, whatever their role.
       const bool mine = warp >= 4 && id0 < walk.total;
       const int quad = warp & 3;
       Bf16Tile t = {};
+      float acc[128];
       if (mine) {
-        t = tile_at<MODE, UNIT>(walk, args, id0, rank);
-        if (!warp_wait(&acc_full[0], 0, budget)) atomicOr(status, kErrWaitEpilogue);
-        tc_fence_after();
+        t = tile_at<MODE, UNIT, F32>(walk, args, id0, rank);
+        int tc = 0;
+        const int chunks = F32 ? (t.kb1 - t.kb0 + kChunk - 1) / kChunk : 1;
+        if (!gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, quad, acc)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+        }
       }
       cluster_sync();
-      if (mine && quad * 32 < args.box) {
-        const int r = quad * 32 + lane;
-        const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t dst = cluster_map(smem_u32(smem), 0) + (rank * args.box + r) * kLdSplit * 4;
-#pragma unroll 1
-        for (int c = 0; c < C::kBN; c += 32) {
-          uint32_t v[32];
-          tmem_ld_32cols(tq + c, v);
-          tmem_ld_wait();
-          if (r < args.box) {
+      if (mine && quad * 32 + lane < args.box) {
+        const uint32_t dst = cluster_map(smem_u32(smem), 0) + (rank * args.box + quad * 32 + lane) * kLdSplit * 4;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              cluster_store(dst + (c + 4 * i) * 4,
-                            make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                        __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
-          }
-        }
+        for (int i = 0; i < 32; ++i)
+          cluster_store(dst + i * 16, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
       }
       cluster_sync();
       if (mine && rank == 0) {
@@ -575,38 +746,43 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT>::kThreads, 1)
   }
   // ---- teardown: all MMAs of this CTA have completed before the columns are released
   if (warp == 1 && lane == 0)
-    if (!mbar_wait(mma_done, 0, kDrainBudget)) atomicOr(status, kErrDrain);
+    if (!mbar_wait(mma_done, 0, kDrain)) atomicOr(status, kErrDrain);
   tc_fence_before();
-  __syncthreads();
+  if (C::kPair) cluster_sync();
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    if (C::kPair) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-template <int MODE, int UNIT>
+template <int MODE, int UNIT, bool F32>
 cudaError_t launch_one(const CUtensorMap (&m)[4], Bf16Args a, cudaStream_t s) {
-  using C = Bf16Cfg<MODE, UNIT>;
+  using C = Bf16Cfg<MODE, UNIT, F32>;
   const unsigned others = ((MODE == kWgrad ? a.k : a.n) + C::kOutCols - 1) / C::kOutCols;
   const long long row_tiles = MODE == kWgrad ? (a.n + UNIT - 1) / UNIT : most_tiles(static_cast<int>(a.rows), a.E, UNIT);
   a.by_others = FastDiv::of(others);
   a.by_group = FastDiv::of(others * kRaster);
   a.by_tiles = FastDiv::of(static_cast<unsigned>(MODE == kWgrad ? row_tiles * others * a.pairs : 1));
   const long long tiles = row_tiles * others * (MODE == kWgrad ? 1LL * a.E * a.pairs : 1);
-  auto kern = gemm_bf16_kernel<MODE, UNIT>;
+  auto kern = gemm_bf16_kernel<MODE, UNIT, F32>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if (a.splits > 1)
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * a.splits)), dim3(C::kThreads), C::kSmemBytes, s,
                               a.splits, m[0], m[1], m[2], m[3], a);
   const long long sms = sm_count();
+  if (C::kPair)
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles < sms / 2 ? tiles : sms / 2) * 2), dim3(C::kThreads),
+                              C::kSmemBytes, s, 2, m[0], m[1], m[2], m[3], a);
   return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(C::kThreads), C::kSmemBytes, s,
                     m[0], m[1], m[2], m[3], a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int kSms = 152;
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 16, kPairRows = 96;
 
 // [rows, cols] bf16, boxes of 64 columns by `high` rows; and [E, rows, cols]
 bool map_rows(CUtensorMap* m, const void* p, long long rows, int cols, int high) {
@@ -648,28 +824,35 @@ Bf16Args args_of(const lmoe_bf16_matmul* c, const int32_t* offsets, uint32_t* st
 }
 
 // One of the modes that take rows of a: which tile, and the launch.  A pair is (a, w).
-template <int MODE>
+template <int MODE, bool F32>
 lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a2, const void* w2, cudaStream_t stream) {
   const int R = static_cast<int>(g.rows), live = g.E < R ? g.E : R;
-  const bool few = R / live <= kFewRows;
-  const int unit = few ? 32 : 128;
+  const int unit = R / live <= kFewRows ? 32 : R / live < kPairRows ? 128 : 256;
   g.box = R < unit ? R : unit;
-  const int across = MODE == kGated ? 64 : 128;
+  const int across = (MODE == kGated ? 64 : 128) * (unit == 256 ? 2 : 1);
   const long long tiles = 1LL * most_tiles(R, g.E, unit) * ((g.n + across - 1) / across);
   if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
-  const int most = few ? Bf16Cfg<MODE, 32>::kSplitMost : Bf16Cfg<MODE, 128>::kSplitMost;
-  while (g.splits < 8 && tiles * g.splits * 2 <= kSms && g.num_kb * g.pairs / (g.splits * 2) >= 4 &&
-         g.splits * 2 * g.box <= most)
-    g.splits *= 2;
+  if (unit < 256) {
+    using Few = Bf16Cfg<MODE, 32, F32>;
+    using Wide = Bf16Cfg<MODE, 128, F32>;
+    // rows of partial sums that fit
+    const int most = (unit == 32 ? Few::kStages * Few::kStageBytes : Wide::kStages * Wide::kStageBytes) / (kLdSplit * 4);
+    while (g.splits < 8 && tiles * g.splits * 2 <= kSms && g.num_kb * g.pairs / (g.splits * 2) >= 4 &&
+           g.splits * 2 * g.box <= most)
+      g.splits *= 2;
+  }
   constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
-  const int high = mn || MODE == kGated ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
+  const int high = mn || (MODE == kGated && unit < 256) ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
+  const int rows = unit == 256 ? 128 : g.box;
   CUtensorMap m[4];
-  if (!map_rows(&m[0], a, R, g.k, g.box) || !map_weights(&m[2], w, g.E, wr, wc, high)) return LMOE_ERR_CUDA;
+  if (!map_rows(&m[0], a, R, g.k, rows) || !map_weights(&m[2], w, g.E, wr, wc, high)) return LMOE_ERR_CUDA;
   m[1] = m[0];
   m[3] = m[2];
-  if ((a2 != nullptr && !map_rows(&m[1], a2, R, g.k, g.box)) || (w2 != nullptr && !map_weights(&m[3], w2, g.E, wr, wc, high)))
+  if ((a2 != nullptr && !map_rows(&m[1], a2, R, g.k, rows)) || (w2 != nullptr && !map_weights(&m[3], w2, g.E, wr, wc, high)))
     return LMOE_ERR_CUDA;
-  const cudaError_t e = few ? launch_one<MODE, 32>(m, g, stream) : launch_one<MODE, 128>(m, g, stream);
+  const cudaError_t e = unit == 32    ? launch_one<MODE, 32, F32>(m, g, stream)
+                        : unit == 128 ? launch_one<MODE, 128, F32>(m, g, stream)
+                                      : launch_one<MODE, 256, F32>(m, g, stream);
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
@@ -694,7 +877,7 @@ extern "C" lmoe_status lmoe_gated_ffn(const lmoe_bf16_matmul* c, const void* x, 
   g.out = h;
   g.out2 = gate;
   g.out3 = up;
-  return rows_product<kGated>(g, x, w_gate, nullptr, w_up, stream);
+  return rows_product<kGated, false>(g, x, w_gate, nullptr, w_up, stream);
 }
 
 extern "C" lmoe_status lmoe_gated_ffn_grad(const lmoe_bf16_matmul* c, const void* dy, const void* w_down,
@@ -715,7 +898,7 @@ extern "C" lmoe_status lmoe_gated_ffn_grad(const lmoe_bf16_matmul* c, const void
   g.up = static_cast<const __nv_bfloat16*>(up);
   g.out = dgate;
   g.out2 = dup;
-  return rows_product<kGatedGrad>(g, dy, w_down, nullptr, nullptr, stream);
+  return rows_product<kGatedGrad, false>(g, dy, w_down, nullptr, nullptr, stream);
 }
 
 extern "C" lmoe_status lmoe_matmul_bf16(const lmoe_bf16_matmul* c, const void* a, const void* w, const void* a2,
@@ -732,7 +915,11 @@ extern "C" lmoe_status lmoe_matmul_bf16(const lmoe_bf16_matmul* c, const void* a
   Bf16Args g = args_of(c, offsets, status);
   g.pairs = a2 != nullptr ? 2 : 1;
   g.out = out;
-  return c->transposed ? rows_product<kProductT>(g, a, w, a2, w2, stream) : rows_product<kProduct>(g, a, w, a2, w2, stream);
+  if (c->transposed)
+    return g.out_f32 ? rows_product<kProductT, true>(g, a, w, a2, w2, stream)
+                     : rows_product<kProductT, false>(g, a, w, a2, w2, stream);
+  return g.out_f32 ? rows_product<kProduct, true>(g, a, w, a2, w2, stream)
+                   : rows_product<kProduct, false>(g, a, w, a2, w2, stream);
 }
 
 extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const void* dy, const void* x,
@@ -765,7 +952,10 @@ extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const v
   m[1] = m[0];
   m[3] = m[2];
   if (dy2 != nullptr && !map_rows(&m[1], dy2, c->rows, c->N, kBK)) return LMOE_ERR_CUDA;
-  return launch_one<kWgrad, 128>(m, g, stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+  const bool pair = c->N > 128 && c->K > 128;
+  const cudaError_t e = g.out_f32 ? (pair ? launch_one<kWgrad, 256, true>(m, g, stream) : launch_one<kWgrad, 128, true>(m, g, stream))
+                                  : (pair ? launch_one<kWgrad, 256, false>(m, g, stream) : launch_one<kWgrad, 128, false>(m, g, stream));
+  return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
 extern "C" lmoe_status lmoe_bf16_check_status(cudaStream_t stream, uint32_t* detail) {
