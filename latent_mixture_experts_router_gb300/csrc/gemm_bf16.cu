@@ -150,25 +150,11 @@ LMOE_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar, in
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
+// (Of CTA scope: what it orders are TMEM reads and shared memory that this CTA's own tensor cores read.  A release at cluster
+// scope would wait for the epilogue's global stores, an acquire cost the MMA issuer several hundred cycles a block:
+// weight gradients 650 instead of TFLOP/s.)
 LMOE_DEV void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// mbar_wait for a barrier on which another CTA's threads arrive.
-LMOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, long long budget) {
-  const uint32_t a = smem_u32(bar);
-  const long long t0 = clock64();
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(a), "r"(parity), "r"(kWaitSleepNs)
-        : "memory");
-    if (ok) return true;
-    if (clock64() - t0 > budget) return false;
-  }
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Registers of a warpgroup: 4 x 32 x 56 + 8 x 32 x 224 = 384 x 168, what the block was launched with.
 template <int N>
@@ -430,6 +416,7 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
           tmem_ld_32cols(tq + c, v);
           if (MODE == kGated) tmem_ld_32cols(tq + C::kBN / 2 + c, v2);
           tmem_ld_wait();
+          if (c + 32 >= min(kCols, width - q0)) ring.release(tc, lane);   // (all of it has been read)
           put32(st, lane, reinterpret_cast<const float*>(v));
           __syncwarp();
           get32(st, lane, q);
@@ -443,7 +430,7 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
           store(c, q, q2);
         }
       }
-      ring.release(tc, lane);
+      if (from >= to || q0 >= width) ring.release(tc, lane);
       ++tc;
     } else if (from < to && !args.accumulate) {
       float4 q[8];
@@ -634,7 +621,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
         const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
         for (int c0 = t.kb0; ok && c0 < t.kb1; c0 += C::kChunkBlocks, ++tc) {
           const int buf = tc & 1, c1 = min(t.kb1 - c0, C::kChunkBlocks) + c0;
-          if (!mbar_wait_cluster(&acc_empty[buf], ((tc >> 1) & 1) ^ 1, budget)) {
+          if (!mbar_wait(&acc_empty[buf], ((tc >> 1) & 1) ^ 1, budget)) {
             atomicOr(status, kErrWaitMma);
             ok = false;
             break;
@@ -643,8 +630,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
           const uint32_t acc = tmem + buf * C::kBN;
           for (int kb = c0; kb < c1; ++kb, ++it) {
             const int s = it % C::kStages;
-            if (!(MODE == kWgrad && C::kPair ? mbar_wait_cluster(&full[s], (it / C::kStages) & 1, budget)
-                                             : mbar_wait(&full[s], (it / C::kStages) & 1, budget))) {
+            if (!mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
               atomicOr(status, kErrWaitMma);
               ok = false;
               break;
