@@ -135,21 +135,61 @@ LMOE_DEV void mma_commit_pair(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-// Loads into this CTA's shared memory that are counted by the barrier at cluster address `bar`.
-LMOE_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
-      : "memory");
+// ---- loads into this CTA's shared memory (addresses, not pointers: a producer thread's own instructions are what
+// bounds it).  In a pair they are counted by the barrier at cluster address `bar`.
+template <bool PAIR>
+LMOE_DEV void load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, uint64_t policy) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+        : "memory");
 }
-LMOE_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
-      : "memory");
+template <bool PAIR>
+LMOE_DEV void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, uint64_t policy) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
 }
+LMOE_DEV void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+LMOE_DEV bool wait_at(uint32_t bar, uint32_t parity, long long budget) {   // mbar_wait
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
+    if (clock64() - t0 > budget) return false;
+  }
+  return true;
+}
+// A place in the ring of stages.
+template <int STAGES>
+struct RingAt {
+  uint32_t s = 0, phase = 0;
+  LMOE_DEV void next() {
+    if (++s == STAGES) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // (Of CTA scope: what it orders are TMEM reads and shared memory that this CTA's own tensor cores read.  A release at cluster
 // scope would wait for the epilogue's global stores, an acquire cost the MMA issuer several hundred cycles a block:
 // weight gradients 650 instead of TFLOP/s.)
@@ -532,90 +572,103 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
   const Bf16Ring ring = {acc_full, C::kPair ? cluster_map(smem_u32(acc_empty), 0) : smem_u32(acc_empty), status, budget};
   if (warp < 4) {
     if constexpr (C::kPair && F32) regs_dec<56>();
-    if (warp == 0 && lane == 0) {
-      // ---- TMA producer
+    const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty), tail0 = smem_u32(tail);
+    const uint32_t lead0 = C::kPair ? cluster_map(full0, 0) : full0;   // the barriers that the MMA issuer waits for
+    if ((warp == 0 || warp == 3) && lane == 0) {
+      // ---- TMA producers, warp 0 of the lane operand, warp 3 of the column operand
+      const bool lanes = warp == 0;
       const uint64_t pol = policy_evict_normal();
-      const uint32_t tx = (MODE == kWgrad || C::kPair ? C::kABytes : args.box * 128) + C::kBBytes;
-      int it = 0;
+      const uint32_t tx = ((MODE == kWgrad || C::kPair ? C::kABytes : args.box * 128) + C::kBBytes);
+      RingAt<C::kStages> at;
+      int issued = 0;
       uint32_t cleared = 0, phases = 0;   // stages whose last block went by its tail barrier; those barriers' parities
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
         const int qb = t.q0 + (C::kPair && MODE != kGated ? rank * 128 : 0);   // the column operand's part of this CTA
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const int s = it % C::kStages;
-          if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, budget)) {
+        const CUtensorMap* map = lanes ? (MODE == kWgrad && t.second ? &tmA2 : &tmA)
+                                       : (MODE == kGated && C::kPair && rank != 0 ? &tmB2 : &tmB);
+        int k0 = (MODE == kWgrad ? t.r0 : 0) + t.kb0 * kBK;   // of the reduction
+        for (int kb = t.kb0; kb < t.kb1; ++kb, k0 += kBK) {
+          if (MODE != kGated && MODE != kWgrad && kb == args.num_kb) {   // on to the second pair
+            map = lanes ? &tmA2 : &tmB2;
+            k0 = 0;
+          } else if (MODE != kGated && MODE != kWgrad && kb == t.kb0 && kb > args.num_kb) {
+            map = lanes ? &tmA2 : &tmB2;
+            k0 = (kb - args.num_kb) * kBK;
+          }
+          const uint32_t s = at.s;
+          if (!wait_at(empty0 + s * 8, at.phase ^ 1, budget)) {
             atomicOr(status, kErrWaitProducer);
             ok = false;
             break;
           }
-          uint8_t* sa = smem + s * C::kStageBytes;
-          uint8_t* sb = sa + C::kABytes;
           const bool fix = MODE == kWgrad && kb + 1 == t.kb1 && t.rows % 16 != 0;   // cleared before it is full
-          cleared = (cleared & ~(1u << s)) | (fix ? 1u << s : 0u);
-          phases ^= fix ? 1u << s : 0u;
-          uint64_t* bar = fix ? &tail[s] : &full[s];
-          const uint32_t there = C::kPair ? cluster_map(smem_u32(&full[s]), 0) : 0;
-          if (fix || !C::kPair) mbar_arrive_expect_tx(bar, tx);
-          else if (rank == 0) mbar_arrive_expect_tx(bar, 2 * tx);
-          else if (MODE == kWgrad) mbar_arrive_cluster(there);
-          // (the maps' innermost coordinates are bytes)
-          const auto load2 = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
-            if (C::kPair && !fix) tma_load_2d_pair(dst, m, there, c0, c1, pol);
-            else tma_load_2d_hint(dst, m, bar, c0, c1, pol);
-          };
-          const auto load3 = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
-            if (C::kPair) tma_load_3d_pair(dst, m, there, c0, c1, t.e, pol);
-            else tma_load_3d_hint(dst, m, bar, c0, c1, t.e, pol);
-          };
+          const uint32_t bar = fix ? tail0 + s * 8 : lead0 + s * 8;
+          const uint32_t dst = stages + s * C::kStageBytes + (lanes ? 0 : C::kABytes);
           if (MODE == kWgrad) {
-            const CUtensorMap* ma = t.second ? &tmA2 : &tmA;
-            const int r = t.r0 + kb * kBK;
-  #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              load2(sa + b * 8192, ma, (t.p0 + b * 64) * 2, r);
-              load2(sb + b * 8192, &tmB, (qb + b * 64) * 2, r);
-            }
-          } else {
-            const bool two = kb >= args.num_kb;   // of the second pair
-            const int k0 = (two ? kb - args.num_kb : kb) * kBK;
-            load2(sa, two ? &tmA2 : &tmA, k0 * 2, t.p0);
-            const CUtensorMap* mb = two ? &tmB2 : &tmB;
-            if (MODE == kGated) {
-              if (C::kPair) {   // gate's rows here, up's in the other CTA
-                load3(sb, rank == 0 ? &tmB : &tmB2, k0 * 2, qb);
-              } else {
-                load3(sb, &tmB, k0 * 2, qb);
-                load3(sb + 8192, &tmB2, k0 * 2, qb);
-              }
-            } else if (C::kColsMn) {
-  #pragma unroll
-              for (int b = 0; b < 2; ++b) load3(sb + b * 8192, mb, (qb + b * 64) * 2, k0);
-            } else {
-              load3(sb, mb, k0 * 2, qb);
-            }
+            cleared = (cleared & ~(1u << s)) | (fix ? 1u << s : 0u);
+            phases ^= fix ? 1u << s : 0u;
           }
+          if (lanes) {
+            if (fix || !C::kPair) arrive_expect_tx(fix ? bar : full0 + s * 8, tx);
+            else if (rank == 0) arrive_expect_tx(full0 + s * 8, 2 * tx);
+            else if (MODE == kWgrad) mbar_arrive_cluster(bar);
+          }
+          // (the maps' innermost coordinates are bytes)
+          if (MODE == kWgrad) {
+            const int c = (lanes ? t.p0 : qb) * 2;
+            if (fix) {
+              load_2d<false>(dst, map, bar, c, k0, pol);
+              load_2d<false>(dst + 8192, map, bar, c + 128, k0, pol);
+            } else {
+              load_2d<C::kPair>(dst, map, bar, c, k0, pol);
+              load_2d<C::kPair>(dst + 8192, map, bar, c + 128, k0, pol);
+            }
+          } else if (lanes) {
+            load_2d<C::kPair>(dst, map, bar, k0 * 2, t.p0, pol);
+          } else if (C::kColsMn) {
+            load_3d<C::kPair>(dst, map, bar, qb * 2, k0, t.e, pol);
+            load_3d<C::kPair>(dst + 8192, map, bar, qb * 2 + 128, k0, t.e, pol);
+          } else {   // (kGated: a pair's gate rows here, up's in the other CTA)
+            load_3d<C::kPair>(dst, map, bar, k0 * 2, qb, t.e, pol);
+            if (MODE == kGated && !C::kPair) load_3d<false>(dst + 8192, &tmB2, bar, k0 * 2, qb, t.e, pol);
+          }
+          at.next();
+          ++issued;
         }
       }
-      // every copy of this thread lands before the CTA leaves (a pair's are counted by the first CTA, and neither leaves
-      // before the other)
-      for (int j = max(0, it - C::kStages); j < it; ++j) {
+      // Every copy lands before the CTA leaves.  A pair's are counted by the first CTA, and neither leaves before the other; a
+      // second CTA that gave up may have copies that the first one did not count, which land within this millisecond.
+      for (int j = max(0, issued - C::kStages); j < issued; ++j) {
         const int s = j % C::kStages;
-        const bool tail_bar = cleared >> s & 1;
+        const bool tail_bar = MODE == kWgrad && (cleared >> s & 1);
         if (C::kPair && rank != 0 && !tail_bar) continue;
-        const bool landed = tail_bar ? mbar_wait(&tail[s], (phases >> s & 1) ^ 1, kDrain)
-                                     : mbar_wait(&full[s], (j / C::kStages) & 1, kDrain);
-        if (!landed) atomicOr(status, kErrDrain);
+        const bool landed = tail_bar ? wait_at(tail0 + s * 8, (phases >> s & 1) ^ 1, kDrain)
+                                     : wait_at(full0 + s * 8, (j / C::kStages) & 1, kDrain);
+        if (!landed) {
+          atomicOr(status, kErrDrain);
+          break;
+        }
       }
+      if (C::kPair && rank != 0 && !ok) wait_at(full0, 0, kDrain / 10);   // (a barrier that nothing arrives on)
     } else if (warp == 1 && lane == 0 && (!C::kPair || rank == 0)) {
       // ---- MMA issuer
       constexpr uint32_t idesc = idesc_bf16_f32(C::kPair ? 256 : 128, C::kBN) | (C::kLanesMn ? 1u << 15 : 0u) |
                                  (C::kColsMn ? 1u << 16 : 0u);
+      constexpr int kStepA = C::kLanesMn ? 128 : 2, kStepB = C::kColsMn ? 128 : 2;   // 16 on, in 16-byte addresses
+      const uint64_t ad0 = C::kLanesMn ? sw128_mnmajor_desc(stages) : sw128_kmajor_desc(stages);
+      const uint64_t bd0 = C::kColsMn ? sw128_mnmajor_desc(stages + C::kABytes) : sw128_kmajor_desc(stages + C::kABytes);
       const auto commit = [](uint64_t* bar) {
         if (C::kPair) mma_commit_pair(bar);
         else mma_commit(bar);
       };
-      int it = 0, tc = 0;
+      const auto mma = [](uint32_t acc, uint64_t a, uint64_t b, bool add) {
+        if (C::kPair) mma_bf16_pair(acc, a, b, idesc, add);
+        else mma_bf16(acc, a, b, idesc, add);
+      };
+      RingAt<C::kStages> at;
+      int tc = 0;
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
@@ -626,29 +679,26 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
             ok = false;
             break;
           }
-          tc_fence_after();
           const uint32_t acc = tmem + buf * C::kBN;
-          for (int kb = c0; kb < c1; ++kb, ++it) {
-            const int s = it % C::kStages;
-            if (!mbar_wait(&full[s], (it / C::kStages) & 1, budget)) {
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!wait_at(full0 + at.s * 8, at.phase, budget)) {
               atomicOr(status, kErrWaitMma);
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t a0 = smem_u32(smem + s * C::kStageBytes), b0 = a0 + C::kABytes;
-            const uint64_t ad = C::kLanesMn ? sw128_mnmajor_desc(a0) : sw128_kmajor_desc(a0);
-            const uint64_t bd = C::kColsMn ? sw128_mnmajor_desc(b0) : sw128_kmajor_desc(b0);
-            const int left = MODE == kWgrad ? t.rows - kb * kBK
-                                            : args.k - (kb >= args.num_kb ? kb - args.num_kb : kb) * kBK;
-  #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {   // 16 on: 32 bytes, or 2048, in the descriptors' 16-byte addresses
-              if (kk * 16 >= left) break;
-              const uint64_t ak = ad + (C::kLanesMn ? 128 : 2) * kk, bk = bd + (C::kColsMn ? 128 : 2) * kk;
-              if (C::kPair) mma_bf16_pair(acc, ak, bk, idesc, kb > c0 || kk > 0);
-              else mma_bf16(acc, ak, bk, idesc, kb > c0 || kk > 0);
+            const uint64_t ad = ad0 + at.s * (C::kStageBytes / 16), bd = bd0 + at.s * (C::kStageBytes / 16);
+            mma(acc, ad, bd, kb > c0);
+            // of the reduction, 64 in all but its last blocks
+            const int left = MODE == kWgrad ? t.rows - kb * kBK : args.k - (kb >= args.num_kb ? kb - args.num_kb : kb) * kBK;
+            if (left >= kBK) {
+#pragma unroll
+              for (int kk = 1; kk < kBK / 16; ++kk) mma(acc, ad + kStepA * kk, bd + kStepB * kk, true);
+            } else {
+              for (int kk = 1; kk * 16 < left; ++kk) mma(acc, ad + kStepA * kk, bd + kStepB * kk, true);
             }
-            commit(&empty[s]);
+            commit(&empty[at.s]);
+            at.next();
           }
           commit(&acc_full[buf]);
         }
