@@ -35,7 +35,6 @@ namespace {
 
 enum Bf16Mode : int { kGated = 0, kGatedGrad = 1, kProduct = 2, kProductT = 3, kWgrad = 4 };
 constexpr int kRaster = 8;       // row tiles that take turns before the next column of tiles
-constexpr int kLdStage = 36;     // floats of a staged row of 32: rows four apart share no banks
 constexpr int kLdSplit = 132;    // floats of a row of 128 partial sums
 // Tensor memory's fp32 sums are cut, not rounded, at each addition: 4096 products in a row leave 4.4e-6 of the result (2-norm),
 // in proportion to their number.  bf16 results do not show it; for fp32 results a sum in TMEM ends after kChunk
@@ -59,6 +58,7 @@ struct Bf16Args {
   const __nv_bfloat16 *gate, *up;   // kGatedGrad
   void *out, *out2, *out3;       // h, gate, up; dgate, dup; out; dw, dw2
   int out_f32, accumulate;
+  int whole;                     // whole groups of 32 rows leave by tensor stores
   unsigned* status;              // error word, or nullptr: the device's own (g_status)
   long long budget;
 };
@@ -80,10 +80,12 @@ struct Bf16Cfg {
   static constexpr int kLanes = kPair ? 128 : UNIT;               // that a CTA loads
   static constexpr int kBN = kPair ? 256 : 128;                   // accumulator columns
   static constexpr int kOutCols = MODE == kGated ? kBN / 2 : kBN;  // columns of a tile
-  static constexpr int kEpiWarps = kPair ? 8 : 4;
+  static constexpr int kEpiWarps = kPair && F32 ? 8 : 4;
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kABytes = kLanes * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
-  static constexpr int kStagingBytes = kEpiWarps * 32 * kLdStage * 4;
+  // a warp's 32 rows of 128 bytes on their way out (kGatedGrad: and in, of gate and of up)
+  static constexpr int kWarpBytes = 4096 * (MODE == kGatedGrad ? 3 : 1);
+  static constexpr int kStagingBytes = kEpiWarps * kWarpBytes;
   static constexpr int kTableBytes = 2 * (kMaxGroups + 4) * 4;
   static constexpr int kFixed = kStagingBytes + kTableBytes + 512 + 1024;
   static constexpr int kFit = (227 * 1024 - kFixed) / kStageBytes;
@@ -91,7 +93,7 @@ struct Bf16Cfg {
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
   static constexpr uint32_t kTmemCols = 2 * kBN;
   static constexpr int kChunkBlocks = F32 ? kChunk : 1 << 30;
-  static_assert((3 * kStages + 2 * 2 + 1) * 8 + 8 <= 512, "barriers");
+  static_assert((3 * kStages + 2 * 2 + 1 + 4) * 8 + 8 <= 512, "barriers");
   // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
   static_assert(kStageBytes >= 128 * 128, "lane operand");
 };
@@ -177,6 +179,14 @@ LMOE_DEV bool wait_at(uint32_t bar, uint32_t parity, long long budget) {   // mb
     if (clock64() - t0 > budget) return false;
   }
   return true;
+}
+// One thread of a converged warp.  (As the condition of what issues copies and MMAs: the compiler knows then that one
+// thread runs it, and needs no loops over the warp for their uniform operands; with lane == 0 16384 x 8192 x 8192 took
+// 1264 us, so 1162.)
+LMOE_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // A place in the ring of stages.
 template <int STAGES>
@@ -291,14 +301,6 @@ LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank
 }
 
 // ---- epilogue
-// Four values of a row, as they are stored.
-LMOE_DEV void store4(void* out, long long at, float4 v, bool f32) {
-  if (f32)
-    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
-        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
 LMOE_DEV float4 load4_bf16(const __nv_bfloat16* p) {
   const uint2 w = *reinterpret_cast<const uint2*>(p);
   return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
@@ -308,20 +310,24 @@ LMOE_DEV float4 load4(const void* p, long long at, bool f32) {
   if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
   return load4_bf16(static_cast<const __nv_bfloat16*>(p) + at);
 }
+LMOE_DEV void store4(void* out, long long at, float4 v, bool f32) {
+  if (f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
 LMOE_DEV void gated_grad(float dh, float g, float u, float& dg, float& du) {
   const float s = sigmoid(g);
   dg = dh * u * (s * (1.f + g * (1.f - s)));
   du = dh * (g * s);
 }
-LMOE_DEV float4 silu_mul(float4 g, float4 u) {
-  return make_float4(g.x * sigmoid(g.x) * u.x, g.y * sigmoid(g.y) * u.y, g.z * sigmoid(g.z) * u.z,
-                     g.w * sigmoid(g.w) * u.w);
-}
-// Four sums v of out's element `at` (kGated: of gate and up) to where they belong.
+LMOE_DEV float silu_mul(float g, float u) { return g * sigmoid(g) * u; }
+// Four sums v of out's element `at` (kGated: of gate and up) to where they belong (tiles shared by a cluster).
 template <int MODE>
-LMOE_DEV void finish4(const Bf16Args& a, void* out, long long at, float4 v, float4 v2) {
+LMOE_DEV void finish4(const Bf16Args& a, long long at, float4 v, float4 v2) {
   if (MODE == kGated) {
-    store4(a.out, at, silu_mul(v, v2), false);
+    store4(a.out, at, make_float4(silu_mul(v.x, v2.x), silu_mul(v.y, v2.y), silu_mul(v.z, v2.z), silu_mul(v.w, v2.w)), false);
     if (a.out2 != nullptr) {
       store4(a.out2, at, v, false);
       store4(a.out3, at, v2, false);
@@ -336,25 +342,92 @@ LMOE_DEV void finish4(const Bf16Args& a, void* out, long long at, float4 v, floa
     store4(a.out, at, dg, false);
     store4(a.out2, at, du, false);
   } else {
-    if (MODE == kWgrad && a.accumulate) {
-      const float4 o = load4(out, at, a.out_f32);
-      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-    }
-    store4(out, at, v, a.out_f32);
+    store4(a.out, at, v, a.out_f32);
   }
 }
 
-// A warp's 32 lanes by 32 columns, a lane to a thread, into rows of shared memory; then thread l has columns
-// 4 (l % 8) .. of rows l / 8, + 4, ...
-LMOE_DEV void put32(float* st, int lane, const float* v) {
-  float4* o = reinterpret_cast<float4*>(st + lane * kLdStage);
+// A warp's 32 rows of 128 bytes in shared memory, one to a thread: their 16-byte parts swizzled as the tensor
+// copies have them (part j of row r at j ^ (r % 8)), which is free of bank conflicts by rows and by columns.
+LMOE_DEV uint4* part_of(uint8_t* st, int r, int j) { return reinterpret_cast<uint4*>(st + r * 128 + ((j ^ (r & 7)) << 4)); }
+LMOE_DEV void put_row(uint8_t* st, int lane, const uint32_t* w) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  for (int j = 0; j < 8; ++j) *part_of(st, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
-LMOE_DEV void get32(const float* st, int lane, float4 (&q)[8]) {
+LMOE_DEV void get_row(uint8_t* st, int lane, uint32_t (&w)[32]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    q[i] = *reinterpret_cast<const float4*>(st + (4 * i + (lane >> 3)) * kLdStage + (lane & 7) * 4);
+  for (int j = 0; j < 8; ++j) {
+    const uint4 q = *part_of(st, lane, j);
+    w[4 * j] = q.x;
+    w[4 * j + 1] = q.y;
+    w[4 * j + 2] = q.z;
+    w[4 * j + 3] = q.w;
+  }
+}
+template <bool THREE>
+LMOE_DEV void tensor_store(const CUtensorMap* m, const void* src, int c0, int c1, int c2) {
+  if constexpr (THREE)
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// What an epilogue warp writes: rows [from, to) of 32 from row `row` of out (ld bytes each) on, `limit` bytes of each.
+struct Bf16Rows {
+  uint8_t* st;
+  int lane, from, to;
+  bool whole;        // by tensor stores
+  long long row, ld;
+  int limit;
+  int r0, e;         // kWgrad: the first row of expert e's matrix
+};
+// The staged rows have been read (by whichever way the last ones left): they may be written again.
+LMOE_DEV void staging_free() {
+  if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+// 128 bytes of each row, from byte `col` on, one row to a thread.
+template <int MODE>
+LMOE_DEV void emit(const Bf16Rows& o, const CUtensorMap* m, void* out, int col, const uint32_t* w) {
+  staging_free();
+  put_row(o.st, o.lane, w);
+  if (o.whole) {
+    fence_async_shared();
+    __syncwarp();
+    if (elect_one()) tensor_store<MODE == kWgrad>(m, o.st, col, MODE == kWgrad ? o.r0 : static_cast<int>(o.row), o.e);
+  } else {
+    __syncwarp();
+    const int j = o.lane & 7;
+    uint8_t* p = static_cast<uint8_t*>(out) + (o.row + (o.lane >> 3)) * o.ld + col + j * 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, p += 4 * o.ld) {
+      const int r = 4 * i + (o.lane >> 3);
+      const uint4 q = *part_of(o.st, r, j);
+      if (r >= o.from && r < o.to && col + j * 16 < o.limit) *reinterpret_cast<uint4*>(p) = q;
+    }
+  }
+}
+// 32 columns of sums, added to what the rows hold.
+LMOE_DEV void emit_added(const Bf16Rows& o, void* out, int width, int col, bool f32, const uint32_t* w) {
+  __syncwarp();
+  put_row(o.st, o.lane, w);
+  __syncwarp();
+  const int j = o.lane & 7, c = col + j * 4;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (o.lane >> 3);
+    const float4 q = *reinterpret_cast<const float4*>(part_of(o.st, r, j));
+    if (r >= o.from && r < o.to && c < width) {
+      const long long at = (o.row + r) * width + c;
+      const float4 p = load4(out, at, f32);
+      store4(out, at, make_float4(q.x + p.x, q.y + p.y, q.z + p.z, q.w + p.w), f32);
+    }
+  }
 }
 
 // Where an epilogue warp waits for sums, and gives their buffers back.
@@ -401,105 +474,185 @@ LMOE_DEV bool gather_sums(const Bf16Ring& ring, uint32_t tmem, int c0, int chunk
   return true;
 }
 
+// 64 columns of bf16 from two reads of 32.
+LMOE_DEV void pack32(const uint32_t (&v)[32], uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
+
+struct Bf16Maps {
+  const CUtensorMap *out, *out2, *out3, *gate, *up;
+};
+
 template <int MODE, int UNIT, bool F32>
-LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Ring& ring, float* staging, uint32_t tmem,
-                       int id0, int step, int rank) {
+LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Ring& ring, const Bf16Maps& maps,
+                       uint8_t* staging, uint64_t* landed, uint32_t tmem, int id0, int step, int rank) {
   using C = Bf16Cfg<MODE, UNIT, F32>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = (warp - 4) >> 2;
   constexpr int kCols = C::kOutCols * 4 / C::kEpiWarps;   // of this warp
-  float* st = staging + (warp - 4) * 32 * kLdStage;
-  const int c4 = (lane & 7) * 4, r4 = lane >> 3;
+  constexpr int kEs = F32 ? 4 : 2;
   const int width = MODE == kWgrad ? args.k : args.n;
-  int tc = 0;
+  uint8_t* st = staging + (warp - 4) * C::kWarpBytes;
+  uint8_t* in = st + 4096;   // kGatedGrad: gate's rows, and up's behind them
+  int tc = 0, loads = 0;
   for (int id = id0; id < walk.total; id += step) {
     const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
     const int blocks = t.kb1 - t.kb0;   // (kWgrad: an expert without rows has none, and gets zeros)
-    const int from = max(t.skip - quad * 32, 0), to = min(t.live - quad * 32, 32);   // lanes of this warp
-    void* out = MODE == kWgrad && t.second ? args.out2 : args.out;
-    const long long row = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0 + quad * 32;
     const int q0 = t.q0 + half * kCols;
-    // four rows to a store instruction
-    const auto store = [&](int c, const float4(&q)[8], const float4(&q2)[8]) {
-      const int col = q0 + c + c4;
+    Bf16Rows o;
+    o.st = st;
+    o.lane = lane;
+    o.from = max(t.skip - quad * 32, 0);
+    o.to = min(t.live - quad * 32, 32);
+    o.row = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0 + quad * 32;
+    o.ld = static_cast<long long>(width) * kEs;
+    o.limit = width * kEs;
+    o.r0 = t.p0 + quad * 32;
+    o.e = t.e;
+    // (kWgrad's tensors end with an expert's rows; elsewhere the rows behind may be another expert's)
+    o.whole = args.whole && (MODE == kWgrad || (o.from == 0 && o.to == 32));
+    void* out = MODE == kWgrad && t.second ? args.out2 : args.out;
+    const CUtensorMap* map = MODE == kWgrad && t.second ? maps.out2 : maps.out;
+    const bool any = o.from < o.to && q0 < width;   // (the same for the warp)
+    if (blocks == 0) {
+      uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + r4;
-        if (r >= from && r < to && col < width) finish4<MODE>(args, out, (row + r) * width + col, q[i], q2[i]);
-      }
-    };
-    if (F32 && blocks > 0) {
+      for (int i = 0; i < 32; ++i) w[i] = 0;
+      if (any && !args.accumulate)
+        for (int c = 0; c < kCols && q0 + c < width; c += 128 / kEs) emit<MODE>(o, map, out, (q0 + c) * kEs, w);
+      continue;
+    }
+    if constexpr (F32) {
       float acc[128];
       const int chunks = (blocks + C::kChunkBlocks - 1) / C::kChunkBlocks;
-      if (!gather_sums<C::kBN>(ring, tmem, half * kCols, chunks, tc, lane, quad, acc)) return;
-      if (from >= to) continue;   // (the same for the warp)
+      if (!gather_sums<C::kBN>(ring, tmem, half * kCols, chunks, tc, lane, quad, acc)) break;
+      if (!any) continue;
 #pragma unroll
       for (int c = 0; c < kCols; c += 32) {
         if (q0 + c >= width) break;
-        float4 q[8];
-        put32(st, lane, acc + c);
-        __syncwarp();
-        get32(st, lane, q);
-        __syncwarp();
-        store(c, q, q);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(acc + c);
+        if (MODE == kWgrad && args.accumulate) emit_added(o, out, width, q0 + c, true, w);
+        else emit<MODE>(o, map, out, (q0 + c) * 4, w);
       }
-      continue;
-    }
-    if (blocks > 0) {
-      if (!ring.wait(tc)) return;
-      const uint32_t tq = tmem + (tc & 1) * C::kBN + half * kCols + (static_cast<uint32_t>(quad * 32) << 16);
-      if (from < to) {
-#pragma unroll 1
-        for (int c = 0; c < kCols; c += 32) {
-          if (q0 + c >= width) break;
-          float4 q[8], q2[8];
-          uint32_t v[32], v2[32];
-          tmem_ld_32cols(tq + c, v);
-          if (MODE == kGated) tmem_ld_32cols(tq + C::kBN / 2 + c, v2);
-          tmem_ld_wait();
-          if (c + 32 >= min(kCols, width - q0)) ring.release(tc, lane);   // (all of it has been read)
-          put32(st, lane, reinterpret_cast<const float*>(v));
+    } else {
+      const auto load_gate = [&](int c) {   // 64 columns of gate and up
+        if constexpr (MODE == kGatedGrad) {
           __syncwarp();
-          get32(st, lane, q);
-          __syncwarp();
-          if (MODE == kGated) {
-            put32(st, lane, reinterpret_cast<const float*>(v2));
-            __syncwarp();
-            get32(st, lane, q2);
-            __syncwarp();
+          if (elect_one()) {
+            const uint32_t bar = smem_u32(landed + quad);
+            arrive_expect_tx(bar, 8192);
+            load_2d<false>(smem_u32(in), maps.gate, bar, (q0 + c) * 2, t.p0 + quad * 32, policy_evict_normal());
+            load_2d<false>(smem_u32(in + 4096), maps.up, bar, (q0 + c) * 2, t.p0 + quad * 32, policy_evict_normal());
           }
-          store(c, q, q2);
+          __syncwarp();
         }
-      }
-      if (from >= to || q0 >= width) ring.release(tc, lane);
-      ++tc;
-    } else if (from < to && !args.accumulate) {
-      float4 q[8];
+      };
+      if (any) load_gate(0);
+      bool ok = ring.wait(tc);
+      if (any && ok) {
+        const uint32_t tq = tmem + (tc & 1) * C::kBN + half * kCols + (static_cast<uint32_t>(quad * 32) << 16);
+        const int end = min(kCols, width - q0);
+#pragma unroll 1
+        for (int c = 0; c < end; c += 64) {
+          const bool last = c + 64 >= end;
+          uint32_t v[2][32];
+          if constexpr (MODE == kGated) {
+            uint32_t h[32], g[32], u[32];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < kCols; c += 32) store(c, q, q);
+            for (int b = 0; b < 2; ++b) {
+              tmem_ld_32cols(tq + c + b * 32, v[0]);
+              tmem_ld_32cols(tq + C::kBN / 2 + c + b * 32, v[1]);
+              tmem_ld_wait();
+              if (b == 1 && last) ring.release(tc, lane);   // (all of it has been read)
+              pack32(v[0], g + b * 16);
+              pack32(v[1], u + b * 16);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                v[0][i] = __float_as_uint(silu_mul(__uint_as_float(v[0][i]), __uint_as_float(v[1][i])));
+              pack32(v[0], h + b * 16);
+            }
+            emit<MODE>(o, maps.out, args.out, (q0 + c) * 2, h);
+            if (args.out2 != nullptr) {
+              emit<MODE>(o, maps.out2, args.out2, (q0 + c) * 2, g);
+              emit<MODE>(o, maps.out3, args.out3, (q0 + c) * 2, u);
+            }
+          } else {
+            tmem_ld_32cols(tq + c, v[0]);
+            tmem_ld_32cols(tq + c + 32, v[1]);
+            tmem_ld_wait();
+            if (last) ring.release(tc, lane);
+            uint32_t w[32];
+            if constexpr (MODE == kGatedGrad) {
+              uint32_t g[32], u[32];
+              ok = warp_wait(landed + quad, loads & 1, ring.budget);
+              if (!ok) {
+                atomicOr(ring.status, kErrWaitEpilogue);
+                break;
+              }
+              ++loads;
+              get_row(in, lane, g);
+              get_row(in + 4096, lane, u);
+              if (!last) load_gate(c + 64);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float dg[2], du[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  const uint32_t gi = b ? g[i] & 0xffff0000u : g[i] << 16, ui = b ? u[i] & 0xffff0000u : u[i] << 16;
+                  gated_grad(__uint_as_float(v[i / 16][2 * (i % 16) + b]), __uint_as_float(gi), __uint_as_float(ui), dg[b], du[b]);
+                }
+                w[i] = pack_bf16x2(dg[0], dg[1]);
+                u[i] = pack_bf16x2(du[0], du[1]);
+              }
+              emit<MODE>(o, maps.out, args.out, (q0 + c) * 2, w);
+              emit<MODE>(o, maps.out2, args.out2, (q0 + c) * 2, u);
+            } else if (MODE == kWgrad && args.accumulate) {
+              emit_added(o, out, width, q0 + c, false, v[0]);
+              if (q0 + c + 32 < width) emit_added(o, out, width, q0 + c + 32, false, v[1]);
+            } else {
+              pack32(v[0], w);
+              pack32(v[1], w + 16);
+              emit<MODE>(o, map, out, (q0 + c) * 2, w);
+            }
+          }
+        }
+      } else if (ok) {
+        ring.release(tc, lane);
+      }
+      if (!ok) {
+        if (MODE == kGatedGrad && any) warp_wait(landed + quad, loads & 1, kDrain);   // (what was asked for lands here)
+        break;
+      }
+      ++tc;
     }
   }
+  // what this warp stored is there before the CTA leaves
+  if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncwarp();
 }
 
 template <int MODE, int UNIT, bool F32>
 __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
     gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
-                     const Bf16Args args) {
+                     const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmO2,
+                     const __grid_constant__ CUtensorMap tmO3, const __grid_constant__ CUtensorMap tmGate,
+                     const __grid_constant__ CUtensorMap tmUp, const Bf16Args args) {
   using C = Bf16Cfg<MODE, UNIT, F32>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* staging = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
-  int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(staging) + C::kStagingBytes);   // [E + 1]
-  int* start = off + kMaxGroups + 4;                                                           // [E + 1]
+  uint8_t* staging = smem + C::kStages * C::kStageBytes;
+  int* off = reinterpret_cast<int*>(staging + C::kStagingBytes);   // [E + 1]
+  int* start = off + kMaxGroups + 4;                               // [E + 1]
   uint64_t* full = reinterpret_cast<uint64_t*>(start + kMaxGroups + 4);
   uint64_t* empty = full + C::kStages;
   uint64_t* tail = empty + C::kStages;       // kWgrad: a block with rows to be cleared has landed
   uint64_t* acc_full = tail + C::kStages;    // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2]
   uint64_t* mma_done = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* landed = mma_done + 1;           // [4] kGatedGrad: a warp's rows of gate and up
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -513,6 +666,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       mbar_init(&acc_empty[b], C::kEpiWarps * (C::kPair ? 2 : 1));
     }
     mbar_init(mma_done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&landed[i], 1);
     fence_mbar_init();
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
@@ -574,7 +728,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
     if constexpr (C::kPair && F32) regs_dec<56>();
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty), tail0 = smem_u32(tail);
     const uint32_t lead0 = C::kPair ? cluster_map(full0, 0) : full0;   // the barriers that the MMA issuer waits for
-    if ((warp == 0 || warp == 3) && lane == 0) {
+    if ((warp == 0 || warp == 3) && elect_one()) {
       // ---- TMA producers, warp 0 of the lane operand, warp 3 of the column operand
       const bool lanes = warp == 0;
       const uint64_t pol = policy_evict_normal();
@@ -652,7 +806,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
         }
       }
       if (C::kPair && rank != 0 && !ok) wait_at(full0, 0, kDrain / 10);   // (a barrier that nothing arrives on)
-    } else if (warp == 1 && lane == 0 && (!C::kPair || rank == 0)) {
+    } else if (warp == 1 && (!C::kPair || rank == 0) && elect_one()) {
       // ---- MMA issuer
       constexpr uint32_t idesc = idesc_bf16_f32(C::kPair ? 256 : 128, C::kBN) | (C::kLanesMn ? 1u << 15 : 0u) |
                                  (C::kColsMn ? 1u << 16 : 0u);
@@ -731,7 +885,10 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
     }
   } else {
     if constexpr (C::kPair && F32) regs_inc<224>();
-    if (C::kPair || S == 1) epilogue<MODE, UNIT, F32>(args, walk, ring, staging, tmem, id0, step, rank);
+    if (C::kPair || S == 1) {
+      const Bf16Maps maps = {&tmO, &tmO2, &tmO3, &tmGate, &tmUp};
+      epilogue<MODE, UNIT, F32>(args, walk, ring, maps, staging, landed, tmem, id0, step, rank);
+    }
   }
 
   if constexpr (MODE != kWgrad && !C::kPair) {
@@ -775,7 +932,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
               v2 = make_float4(v2.x + p.x, v2.y + p.y, v2.z + p.z, v2.w + p.w);
             }
           }
-          finish4<MODE>(args, args.out, static_cast<long long>(t.p0 + r) * args.n + col, v, v2);
+          finish4<MODE>(args, static_cast<long long>(t.p0 + r) * args.n + col, v, v2);
         }
       }
     }
@@ -794,7 +951,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
 }
 
 template <int MODE, int UNIT, bool F32>
-cudaError_t launch_one(const CUtensorMap (&m)[4], Bf16Args a, cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap (&m)[9], Bf16Args a, cudaStream_t s) {
   using C = Bf16Cfg<MODE, UNIT, F32>;
   const unsigned others = ((MODE == kWgrad ? a.k : a.n) + C::kOutCols - 1) / C::kOutCols;
   const long long row_tiles = MODE == kWgrad ? (a.n + UNIT - 1) / UNIT : most_tiles(static_cast<int>(a.rows), a.E, UNIT);
@@ -807,13 +964,13 @@ cudaError_t launch_one(const CUtensorMap (&m)[4], Bf16Args a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (a.splits > 1)
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * a.splits)), dim3(C::kThreads), C::kSmemBytes, s,
-                              a.splits, m[0], m[1], m[2], m[3], a);
+                              a.splits, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], m[8], a);
   const long long sms = sm_count();
   if (C::kPair)
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles < sms / 2 ? tiles : sms / 2) * 2), dim3(C::kThreads),
-                              C::kSmemBytes, s, 2, m[0], m[1], m[2], m[3], a);
+                              C::kSmemBytes, s, 2, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], m[8], a);
   return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(C::kThreads), C::kSmemBytes, s,
-                    m[0], m[1], m[2], m[3], a);
+                    m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], m[8], a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -880,10 +1037,18 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
   constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
   const int high = mn || (MODE == kGated && unit < 256) ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
   const int rows = unit == 256 ? 128 : g.box;
-  CUtensorMap m[4];
+  CUtensorMap m[9];
   if (!map_rows(&m[0], a, R, g.k, rows) || !map_weights(&m[2], w, g.E, wr, wc, high)) return LMOE_ERR_CUDA;
-  m[1] = m[0];
-  m[3] = m[2];
+  for (int i = 1; i < 9; ++i)   // (some are not used)
+    if (i != 2) m[i] = m[i == 3 ? 2 : 0];
+  g.whole = unit > 32 && g.splits == 1;
+  if (g.whole) {
+    const int es = F32 ? 2 : 1;   // (in 16-bit columns)
+    if (!map_rows(&m[4], g.out, R, g.n * es, 32) || (g.out2 != nullptr && !map_rows(&m[5], g.out2, R, g.n * es, 32)) ||
+        (g.out3 != nullptr && !map_rows(&m[6], g.out3, R, g.n * es, 32)))
+      return LMOE_ERR_CUDA;
+  }
+  if (MODE == kGatedGrad && (!map_rows(&m[7], g.gate, R, g.n, 32) || !map_rows(&m[8], g.up, R, g.n, 32))) return LMOE_ERR_CUDA;
   if ((a2 != nullptr && !map_rows(&m[1], a2, R, g.k, rows)) || (w2 != nullptr && !map_weights(&m[3], w2, g.E, wr, wc, high)))
     return LMOE_ERR_CUDA;
   const cudaError_t e = unit == 32    ? launch_one<MODE, 32, F32>(m, g, stream)
@@ -983,10 +1148,15 @@ extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const v
   g.accumulate = c->accumulate != 0;
   const long long tiles = 1LL * ((c->N + 127) / 128) * ((c->K + 127) / 128) * c->n_experts * g.pairs;
   if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
-  CUtensorMap m[4];
-  if (!map_rows(&m[0], dy, c->rows, c->N, kBK) || !map_rows(&m[2], x, c->rows, c->K, kBK)) return LMOE_ERR_CUDA;
-  m[1] = m[0];
-  m[3] = m[2];
+  CUtensorMap m[9];
+  const int es = g.out_f32 ? 2 : 1;   // (in 16-bit columns)
+  g.whole = !g.accumulate;
+  if (!map_rows(&m[0], dy, c->rows, c->N, kBK) || !map_rows(&m[2], x, c->rows, c->K, kBK) ||
+      !map_weights(&m[4], dw, g.E, g.n, g.k * es, 32))
+    return LMOE_ERR_CUDA;
+  for (int i = 1; i < 9; ++i)   // (some are not used)
+    if (i != 2 && i != 4) m[i] = m[0];
+  if (dw2 != nullptr && !map_weights(&m[5], dw2, g.E, g.n, g.k * es, 32)) return LMOE_ERR_CUDA;
   if (dy2 != nullptr && !map_rows(&m[1], dy2, c->rows, c->N, kBK)) return LMOE_ERR_CUDA;
   const bool pair = c->N > 128 && c->K > 128;
   const cudaError_t e = g.out_f32 ? (pair ? launch_one<kWgrad, 256, true>(m, g, stream) : launch_one<kWgrad, 128, true>(m, g, stream))
