@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 
@@ -755,15 +756,18 @@ def lmoe_grad_norm_workspace_size(count: int) -> int:
     return n.value
 
 
+_T = torch.Tensor
+
+
 def _grad_list(ts, name, device):
     """(addresses, sizes, dtypes) of contiguous CUDA tensors on one device, fp32 or bf16."""
-    _need({t.get_device() for t in ts} <= {device}, f"{name}: all tensors must be on cuda:{device}")
-    _need(all([t.is_contiguous() for t in ts]), f"{name}: tensors must be contiguous")
-    try:
-        kinds = array.array("i", [_DENSE[t.dtype] for t in ts])
-    except KeyError:
-        raise ValueError(f"{name}: tensors must be float32 or bfloat16") from None
-    return array.array("Q", [t.data_ptr() for t in ts]), array.array("q", [t.numel() for t in ts]), kinds
+    # (maps over whole lists: a call with hundreds of tensors is bound by this)
+    _need(set(map(_T.get_device, ts)) <= {device}, f"{name}: all tensors must be on cuda:{device}")
+    _need(False not in map(_T.is_contiguous, ts), f"{name}: tensors must be contiguous")
+    found = set(map(operator.attrgetter("dtype"), ts))
+    _need(found <= _DENSE.keys(), f"{name}: tensors must be float32 or bfloat16")
+    kinds = array.array("i", [_DENSE[found.pop()]]) * len(ts) if len(found) == 1 else array.array("i", [_DENSE[t.dtype] for t in ts])
+    return array.array("Q", map(_T.data_ptr, ts)), array.array("q", map(_T.numel, ts)), kinds
 
 
 def _grad_device(norm):

@@ -92,6 +92,9 @@ struct Bf16Cfg {
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
   static constexpr uint32_t kTmemCols = 2 * kBN;
+  // A pair's last tile of an expert, with no more than 128 rows: an MMA of 128 rows (64 of each CTA) takes half the time.
+  // Its sums lie with their first 128 columns in lanes 0..63 and the others in lanes 64..127.
+  static constexpr bool kShort = kPair && !F32 && MODE != kWgrad;
   static constexpr int kChunkBlocks = F32 ? kChunk : 1 << 30;
   static_assert((3 * kStages + 2 * 2 + 1 + 4) * 8 + 8 <= 512, "barriers");
   // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
@@ -233,6 +236,7 @@ struct Bf16Tile {
   int kb0, kb1;       // blocks of the reduction
   int r0, rows;       // kWgrad: the expert's rows
   int second;         // kWgrad: of dw2
+  bool brief;         // a short tile
 };
 
 LMOE_DEV int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
@@ -280,8 +284,11 @@ LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank
     t.rows = hi - lo;
     t.kb1 = (hi - lo + kBK - 1) / kBK;
   } else if (C::kPair) {
-    t.p0 = lo + rt * UNIT + rank * 128;
-    t.live = min(hi - t.p0, 128);
+    const int p0 = lo + rt * UNIT;
+    t.brief = C::kShort && hi - p0 <= 128;
+    const int mine = t.brief ? 64 : 128;   // rows of this CTA
+    t.p0 = p0 + rank * mine;
+    t.live = min(hi - t.p0, mine);
     t.kb1 = a.num_kb * a.pairs;
   } else {
     // Tiles of few rows: no row behind the last is asked for (a box filled with zeros past the end costs the
@@ -498,16 +505,18 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
   for (int id = id0; id < walk.total; id += step) {
     const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
     const int blocks = t.kb1 - t.kb0;   // (kWgrad: an expert without rows has none, and gets zeros)
-    const int q0 = t.q0 + half * kCols;
+    // (short tiles: 64 rows, whose other columns are two quadrants on)
+    const int rows0 = C::kShort && t.brief ? (quad & 1) * 32 : quad * 32;
+    const int q0 = t.q0 + half * kCols + (C::kShort && t.brief ? (quad >> 1) * (kCols / 2) : 0);
     Bf16Rows o;
     o.st = st;
     o.lane = lane;
-    o.from = max(t.skip - quad * 32, 0);
-    o.to = min(t.live - quad * 32, 32);
-    o.row = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0 + quad * 32;
+    o.from = max(t.skip - rows0, 0);
+    o.to = min(t.live - rows0, 32);
+    o.row = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0 + rows0;
     o.ld = static_cast<long long>(width) * kEs;
     o.limit = width * kEs;
-    o.r0 = t.p0 + quad * 32;
+    o.r0 = t.p0 + rows0;
     o.e = t.e;
     // (kWgrad's tensors end with an expert's rows; elsewhere the rows behind may be another expert's)
     o.whole = args.whole && (MODE == kWgrad || (o.from == 0 && o.to == 32));
@@ -541,8 +550,8 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
           if (elect_one()) {
             const uint32_t bar = smem_u32(landed + quad);
             arrive_expect_tx(bar, 8192);
-            load_2d<false>(smem_u32(in), maps.gate, bar, (q0 + c) * 2, t.p0 + quad * 32, policy_evict_normal());
-            load_2d<false>(smem_u32(in + 4096), maps.up, bar, (q0 + c) * 2, t.p0 + quad * 32, policy_evict_normal());
+            load_2d<false>(smem_u32(in), maps.gate, bar, (q0 + c) * 2, o.r0, policy_evict_normal());
+            load_2d<false>(smem_u32(in + 4096), maps.up, bar, (q0 + c) * 2, o.r0, policy_evict_normal());
           }
           __syncwarp();
         }
@@ -551,7 +560,7 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
       bool ok = ring.wait(tc);
       if (any && ok) {
         const uint32_t tq = tmem + (tc & 1) * C::kBN + half * kCols + (static_cast<uint32_t>(quad * 32) << 16);
-        const int end = min(kCols, width - q0);
+        const int end = min(C::kShort && t.brief ? kCols / 2 : kCols, width - q0);
 #pragma unroll 1
         for (int c = 0; c < end; c += 64) {
           const bool last = c + 64 >= end;
@@ -560,8 +569,9 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
             uint32_t h[32], g[32], u[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              tmem_ld_32cols(tq + c + b * 32, v[0]);
-              tmem_ld_32cols(tq + C::kBN / 2 + c + b * 32, v[1]);
+              // (64 columns of gate, then the same of up)
+              tmem_ld_32cols(tq + 2 * c + b * 32, v[0]);
+              tmem_ld_32cols(tq + 2 * c + 64 + b * 32, v[1]);
               tmem_ld_wait();
               if (b == 1 && last) ring.release(tc, lane);   // (all of it has been read)
               pack32(v[0], g + b * 16);
@@ -732,16 +742,16 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       // ---- TMA producers, warp 0 of the lane operand, warp 3 of the column operand
       const bool lanes = warp == 0;
       const uint64_t pol = policy_evict_normal();
-      const uint32_t tx = ((MODE == kWgrad || C::kPair ? C::kABytes : args.box * 128) + C::kBBytes);
+      const uint32_t tx = (MODE == kWgrad || C::kPair ? C::kABytes : args.box * 128) + C::kBBytes;
       RingAt<C::kStages> at;
       int issued = 0;
       uint32_t cleared = 0, phases = 0;   // stages whose last block went by its tail barrier; those barriers' parities
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
-        const int qb = t.q0 + (C::kPair && MODE != kGated ? rank * 128 : 0);   // the column operand's part of this CTA
-        const CUtensorMap* map = lanes ? (MODE == kWgrad && t.second ? &tmA2 : &tmA)
-                                       : (MODE == kGated && C::kPair && rank != 0 ? &tmB2 : &tmB);
+        // the column operand's part of this CTA
+        const int qb = t.q0 + (C::kPair ? rank * (C::kOutCols / 2) : 0);
+        const CUtensorMap* map = lanes ? (MODE == kWgrad && t.second ? &tmA2 : &tmA) : &tmB;
         int k0 = (MODE == kWgrad ? t.r0 : 0) + t.kb0 * kBK;   // of the reduction
         for (int kb = t.kb0; kb < t.kb1; ++kb, k0 += kBK) {
           if (MODE != kGated && MODE != kWgrad && kb == args.num_kb) {   // on to the second pair
@@ -766,7 +776,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
           }
           if (lanes) {
             if (fix || !C::kPair) arrive_expect_tx(fix ? bar : full0 + s * 8, tx);
-            else if (rank == 0) arrive_expect_tx(full0 + s * 8, 2 * tx);
+            else if (rank == 0) arrive_expect_tx(full0 + s * 8, 2 * (t.brief ? tx - 8192 : tx));
             else if (MODE == kWgrad) mbar_arrive_cluster(bar);
           }
           // (the maps' innermost coordinates are bytes)
@@ -780,13 +790,14 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
               load_2d<C::kPair>(dst + 8192, map, bar, c + 128, k0, pol);
             }
           } else if (lanes) {
-            load_2d<C::kPair>(dst, map, bar, k0 * 2, t.p0, pol);
+            load_2d<C::kPair>(dst, map, bar, k0 * 2, t.p0, pol);   // (a pair's: 64 rows at a time)
+            if (C::kPair && !t.brief) load_2d<C::kPair>(dst + 8192, map, bar, k0 * 2, t.p0 + 64, pol);
           } else if (C::kColsMn) {
             load_3d<C::kPair>(dst, map, bar, qb * 2, k0, t.e, pol);
             load_3d<C::kPair>(dst + 8192, map, bar, qb * 2 + 128, k0, t.e, pol);
-          } else {   // (kGated: a pair's gate rows here, up's in the other CTA)
+          } else {   // (kGated: 64 rows of gate and the same of up)
             load_3d<C::kPair>(dst, map, bar, k0 * 2, qb, t.e, pol);
-            if (MODE == kGated && !C::kPair) load_3d<false>(dst + 8192, &tmB2, bar, k0 * 2, qb, t.e, pol);
+            if (MODE == kGated) load_3d<C::kPair>(dst + 8192, &tmB2, bar, k0 * 2, qb, t.e, pol);
           }
           at.next();
           ++issued;
@@ -808,8 +819,9 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       if (C::kPair && rank != 0 && !ok) wait_at(full0, 0, kDrain / 10);   // (a barrier that nothing arrives on)
     } else if (warp == 1 && (!C::kPair || rank == 0) && elect_one()) {
       // ---- MMA issuer
-      constexpr uint32_t idesc = idesc_bf16_f32(C::kPair ? 256 : 128, C::kBN) | (C::kLanesMn ? 1u << 15 : 0u) |
-                                 (C::kColsMn ? 1u << 16 : 0u);
+      constexpr uint32_t kMajor = (C::kLanesMn ? 1u << 15 : 0u) | (C::kColsMn ? 1u << 16 : 0u);
+      constexpr uint32_t kWhole = idesc_bf16_f32(C::kPair ? 256 : 128, C::kBN) | kMajor;
+      constexpr uint32_t kBrief = idesc_bf16_f32(128, C::kBN) | kMajor;
       constexpr int kStepA = C::kLanesMn ? 128 : 2, kStepB = C::kColsMn ? 128 : 2;   // 16 on, in 16-byte addresses
       const uint64_t ad0 = C::kLanesMn ? sw128_mnmajor_desc(stages) : sw128_kmajor_desc(stages);
       const uint64_t bd0 = C::kColsMn ? sw128_mnmajor_desc(stages + C::kABytes) : sw128_kmajor_desc(stages + C::kABytes);
@@ -817,7 +829,8 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
         if (C::kPair) mma_commit_pair(bar);
         else mma_commit(bar);
       };
-      const auto mma = [](uint32_t acc, uint64_t a, uint64_t b, bool add) {
+      uint32_t idesc = kWhole;
+      const auto mma = [&](uint32_t acc, uint64_t a, uint64_t b, bool add) {
         if (C::kPair) mma_bf16_pair(acc, a, b, idesc, add);
         else mma_bf16(acc, a, b, idesc, add);
       };
@@ -826,6 +839,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
         const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+        if (C::kShort) idesc = t.brief ? kBrief : kWhole;
         for (int c0 = t.kb0; ok && c0 < t.kb1; c0 += C::kChunkBlocks, ++tc) {
           const int buf = tc & 1, c1 = min(t.kb1 - c0, C::kChunkBlocks) + c0;
           if (!mbar_wait(&acc_empty[buf], ((tc >> 1) & 1) ^ 1, budget)) {
@@ -1035,8 +1049,8 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
       g.splits *= 2;
   }
   constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
-  const int high = mn || (MODE == kGated && unit < 256) ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
-  const int rows = unit == 256 ? 128 : g.box;
+  const int high = mn || MODE == kGated ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
+  const int rows = unit == 256 ? 64 : g.box;
   CUtensorMap m[9];
   if (!map_rows(&m[0], a, R, g.k, rows) || !map_weights(&m[2], w, g.E, wr, wc, high)) return LMOE_ERR_CUDA;
   for (int i = 1; i < 9; ++i)   // (some are not used)
