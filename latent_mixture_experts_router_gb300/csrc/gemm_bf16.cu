@@ -38,8 +38,9 @@ constexpr int kRaster = 8;       // row tiles that take turns before the next co
 constexpr int kLdSplit = 132;    // floats of a row of 128 partial sums
 // Tensor memory's fp32 sums are cut, not rounded, at each addition: 4096 products in a row leave 4.4e-6 of the result (2-norm),
 // in proportion to their number.  bf16 results do not show it; for fp32 results a sum in TMEM ends after kChunk
-// blocks of 64, and the epilogue adds those in registers (5e-7).
-constexpr int kChunk = 8;
+// blocks of 64, and the epilogue adds those in registers (8e-7.  Sums of 8 blocks: 5e-7, but
+// experts of about 512 rows then take two: their weight gradients 246 us instead of 239).
+constexpr int kChunk = 12;
 // Budget of the waits for a CTA's own copies and MMAs at its end: they take microseconds.  (In a pair whose second CTA gave
 // up, the first one waits that long for copies that never started.)
 constexpr long long kDrain = 20000000;
@@ -86,7 +87,10 @@ struct Bf16Cfg {
   // a warp's 32 rows of 128 bytes on their way out (kGatedGrad: and in, of gate and of up)
   static constexpr int kWarpBytes = 4096 * (MODE == kGatedGrad ? 3 : 1);
   static constexpr int kStagingBytes = kEpiWarps * kWarpBytes;
-  static constexpr int kTableBytes = 2 * (kMaxGroups + 4) * 4;
+  // off[], and start[] (not kWgrad).  An fp32 kWgrad has room for a stage more than with all offsets: from kOffsets experts
+  // on they are read where they are (read there always, 16 experts' weight gradients to bf16 took 195 us, so 181).
+  static constexpr int kOffsets = F32 && MODE == kWgrad ? 320 : kMaxGroups + 4;
+  static constexpr int kTableBytes = kOffsets * 4 * (MODE == kWgrad ? 1 : 2);
   static constexpr int kFixed = kStagingBytes + kTableBytes + 512 + 1024;
   static constexpr int kFit = (227 * 1024 - kFixed) / kStageBytes;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
@@ -241,8 +245,12 @@ struct Bf16Tile {
 
 LMOE_DEV int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
-// off: offsets, clamped into the rows there are, so that no offsets send a load or a store out of range;
-// start[e]: first row tile of group e (not kWgrad)
+// Offset i, clamped into the rows there are, so that no offsets send a load or a store out of range.
+LMOE_DEV int offset_of(const Bf16Args& a, int i) {
+  const int cap = static_cast<int>(a.rows);
+  return a.offsets != nullptr ? clamp_to(__ldg(a.offsets + i), 0, cap) : i * cap;
+}
+// off: offsets (if they fit); start[e]: first row tile of group e (not kWgrad)
 struct Bf16Walk {
   const int *off, *start;
   int total;
@@ -275,7 +283,9 @@ LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank
   const int g = a.by_group.div(i), first = g * kRaster, gm = min(kRaster, rows - first);
   const int local = i - g * static_cast<int>(a.by_group.d), other = local / gm;
   const int rt = first + local - other * gm;
-  const int lo = w.off[t.e], hi = max(w.off[t.e + 1], lo);
+  const bool near = C::kOffsets > kMaxGroups || a.E < C::kOffsets;
+  const int lo = near ? w.off[t.e] : offset_of(a, t.e);
+  const int hi = max(near ? w.off[t.e + 1] : offset_of(a, t.e + 1), lo);
   t.q0 = other * C::kOutCols;
   if (MODE == kWgrad) {
     t.p0 = rt * UNIT + (C::kPair ? rank * 128 : 0);
@@ -654,8 +664,8 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* staging = smem + C::kStages * C::kStageBytes;
   int* off = reinterpret_cast<int*>(staging + C::kStagingBytes);   // [E + 1]
-  int* start = off + kMaxGroups + 4;                               // [E + 1]
-  uint64_t* full = reinterpret_cast<uint64_t*>(start + kMaxGroups + 4);
+  int* start = off + C::kOffsets;                                  // [E + 1] (not kWgrad)
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::kStagingBytes + C::kTableBytes);
   uint64_t* empty = full + C::kStages;
   uint64_t* tail = empty + C::kStages;       // kWgrad: a block with rows to be cleared has landed
   uint64_t* acc_full = tail + C::kStages;    // [2]
@@ -693,14 +703,13 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
   }
   griddep_enter();
 
-  const int cap = static_cast<int>(args.rows);
-  for (int e = threadIdx.x; e <= args.E; e += C::kThreads)
-    off[e] = args.offsets != nullptr ? clamp_to(args.offsets[e], 0, cap) : e * cap;
+  if (C::kOffsets > kMaxGroups || args.E < C::kOffsets)
+    for (int e = threadIdx.x; e <= args.E; e += C::kThreads) off[e] = offset_of(args, e);
   __syncthreads();
   if (MODE != kWgrad && warp == 0) {   // start[]: exclusive prefix sum of the row tiles, a run of groups per lane
     const int per = (args.E + 31) / 32, e0 = min(lane * per, args.E), e1 = min(e0 + per, args.E);
     // no more than the launch has room for, whatever the offsets say
-    const int most = most_tiles(cap, args.E, UNIT);
+    const int most = most_tiles(static_cast<int>(args.rows), args.E, UNIT);
     int sum = 0;
     for (int e = e0; e < e1; ++e) sum += (max(off[e + 1] - off[e], 0) + UNIT - 1) / UNIT;
     int run = sum;
