@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import operator
 import os
 from dataclasses import dataclass
@@ -645,20 +646,48 @@ def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accu
 
 
 # ------------------------------------------------------------------ training the experts in bf16
-def _bf16_call(fn, where, dev, stream, rows, N, K, E, offsets, status, *operands, out_dtype=LMOE_BF16, transposed=False,
-               accumulate=False):
+# (Small calls are bound by what happens here: a tensor that fits is passed over in one expression, and
+# _want says what is wrong with one that does not; shapes are kept as the library takes them.)
+_BF16 = torch.bfloat16
+
+
+def _bf16(t, name, shape, device):
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != device or not t.is_contiguous() or device < 0:
+        _want(t, name, _BF16, shape, device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bf16_shape(rows, N, K, E, out_dtype, transposed, accumulate):
+    return ctypes.byref(lmoe_bf16_matmul(rows, N, K, E, out_dtype, transposed, accumulate, 0))
+
+
+def _bf16_extra(offsets, status, E, device):
+    """Addresses of offsets and status (None: none)."""
+    at = st = None
     if offsets is not None:
-        _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+        if offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or offsets.get_device() != device or \
+                not offsets.is_contiguous():
+            _want(offsets, "offsets", torch.int32, (E + 1,), device)
+        at = offsets.data_ptr()
     if status is not None:
-        _want(status, "status", (torch.int32, torch.uint32), (1,), dev)
-    shape = lmoe_bf16_matmul(rows, N, K, E, out_dtype, 1 if transposed else 0, 1 if accumulate else 0, 0)
-    _call(fn, where, dev, stream, ctypes.byref(shape), *operands, _ptr(status))
+        _want(status, "status", (torch.int32, torch.uint32), (1,), device)
+        st = status.data_ptr()
+    return at, st
 
 
-def _weight_shape(t, name, what):
-    _need(t.dim() in (2, 3), f"{name} {what}")
-    lead = t.shape[:-2]
-    return lead, lead[0] if lead else 1
+def _rows_of(t, name, what):
+    shape = t.shape
+    _need(len(shape) == 2, f"{name} {what}")
+    return shape
+
+
+def _weight_of(t, name, what):
+    """(rows, columns, experts) of one matrix or of a stack of them."""
+    shape = t.shape
+    if len(shape) == 3:
+        return shape[1], shape[2], shape[0]
+    _need(len(shape) == 2, f"{name} {what}")
+    return shape[0], shape[1], 1
 
 
 def lmoe_gated_ffn(x, w_gate, w_up, h, gate=None, up=None, offsets=None, status=None, stream=None):
@@ -666,74 +695,84 @@ def lmoe_gated_ffn(x, w_gate, w_up, h, gate=None, up=None, offsets=None, status=
     weights [E, N, K] and ``offsets`` [E + 1] (int32), each expert's rows times its own; all bf16.  ``gate``, ``up``
     [rows, N]: both products are stored too, for lmoe_gated_ffn_grad.  ``status`` [1] (int32): error word, for a device
     wait that gives up; None: the device's own word (lmoe_bf16_check_status)."""
-    lead, E = _weight_shape(w_gate, "w_gate", "[N, K] or [E, N, K]")
-    _need(x.dim() == 2, "x [rows, K]")
-    dev, (rows, K), N = x.get_device(), x.shape, w_gate.shape[-2]
-    _want(x, "x", torch.bfloat16, (rows, K), dev)
-    _want(w_gate, "w_gate", torch.bfloat16, (*lead, N, K), dev)
-    _want(w_up, "w_up", torch.bfloat16, (*lead, N, K), dev)
-    _want(h, "h", torch.bfloat16, (rows, N), dev)
-    _need((gate is None) == (up is None), "gate and up: both or neither")
-    if gate is not None:
-        _want(gate, "gate", torch.bfloat16, (rows, N), dev)
-        _want(up, "up", torch.bfloat16, (rows, N), dev)
-    _bf16_call(_lib().lmoe_gated_ffn, "lmoe_gated_ffn", dev, stream, rows, N, K, E, offsets, status, x.data_ptr(),
-               w_gate.data_ptr(), w_up.data_ptr(), _ptr(offsets), h.data_ptr(), _ptr(gate), _ptr(up))
+    N, K, E = _weight_of(w_gate, "w_gate", "[N, K] or [E, N, K]")
+    rows, dev = _rows_of(x, "x", "[rows, K]")[0], x.get_device()
+    _bf16(x, "x", (rows, K), dev)
+    _bf16(w_gate, "w_gate", w_gate.shape, dev)
+    _bf16(w_up, "w_up", w_gate.shape, dev)
+    out = (rows, N)
+    _bf16(h, "h", out, dev)
+    g = u = None
+    if gate is not None or up is not None:
+        _need(gate is not None and up is not None, "gate and up: both or neither")
+        _bf16(gate, "gate", out, dev)
+        _bf16(up, "up", out, dev)
+        g, u = gate.data_ptr(), up.data_ptr()
+    off, st = _bf16_extra(offsets, status, E, dev)
+    _call(_lib().lmoe_gated_ffn, "lmoe_gated_ffn", dev, stream, _bf16_shape(rows, N, K, E, LMOE_BF16, 0, 0), x.data_ptr(),
+          w_gate.data_ptr(), w_up.data_ptr(), off, h.data_ptr(), g, u, st)
 
 
 def lmoe_gated_ffn_grad(dy, w_down, gate, up, dgate, dup, offsets=None, status=None, stream=None):
     """``dgate``, ``dup`` [rows, N]: gradients of lmoe_gated_ffn's ``gate`` and ``up`` (which they may be) from
     ``dy`` [rows, K], the gradient of the down projection's result, through ``w_down`` [K, N] or [E, K, N]; all
     bf16.  ``offsets``, ``status`` as in lmoe_gated_ffn."""
-    lead, E = _weight_shape(w_down, "w_down", "[K, N] or [E, K, N]")
-    _need(dy.dim() == 2, "dy [rows, K]")
-    dev, (rows, K), N = dy.get_device(), dy.shape, w_down.shape[-1]
-    _want(dy, "dy", torch.bfloat16, (rows, K), dev)
-    _want(w_down, "w_down", torch.bfloat16, (*lead, K, N), dev)
-    for t, name in ((gate, "gate"), (up, "up"), (dgate, "dgate"), (dup, "dup")):
-        _want(t, name, torch.bfloat16, (rows, N), dev)
-    _bf16_call(_lib().lmoe_gated_ffn_grad, "lmoe_gated_ffn_grad", dev, stream, rows, N, K, E, offsets, status,
-               dy.data_ptr(), w_down.data_ptr(), gate.data_ptr(), up.data_ptr(), _ptr(offsets), dgate.data_ptr(),
-               dup.data_ptr())
+    K, N, E = _weight_of(w_down, "w_down", "[K, N] or [E, K, N]")
+    rows, dev = _rows_of(dy, "dy", "[rows, K]")[0], dy.get_device()
+    _bf16(dy, "dy", (rows, K), dev)
+    _bf16(w_down, "w_down", w_down.shape, dev)
+    out = (rows, N)
+    _bf16(gate, "gate", out, dev)
+    _bf16(up, "up", out, dev)
+    _bf16(dgate, "dgate", out, dev)
+    _bf16(dup, "dup", out, dev)
+    off, st = _bf16_extra(offsets, status, E, dev)
+    _call(_lib().lmoe_gated_ffn_grad, "lmoe_gated_ffn_grad", dev, stream, _bf16_shape(rows, N, K, E, LMOE_BF16, 0, 0),
+          dy.data_ptr(), w_down.data_ptr(), gate.data_ptr(), up.data_ptr(), off, dgate.data_ptr(), dup.data_ptr(), st)
 
 
 def lmoe_matmul_bf16(a, w, out, offsets=None, a2=None, w2=None, transposed=False, status=None, stream=None):
     """``out`` [rows, N] (fp32 or bf16) = ``a`` [rows, K] (bf16) times ``w`` [N, K] transposed, or, with ``transposed``,
     times ``w`` [K, N] as it is; with ``a2``, ``w2`` of the same shapes plus their product.  Weights with a leading E
     and ``offsets`` [E + 1] (int32): each expert's rows times its own.  ``status`` as in lmoe_gated_ffn."""
-    lead, E = _weight_shape(w, "w", "[N, K] or [E, N, K]")
-    _need(a.dim() == 2, "a [rows, K]")
-    dev, (rows, K), N = a.get_device(), a.shape, w.shape[-1 if transposed else -2]
-    shape = (*lead, K, N) if transposed else (*lead, N, K)
-    _want(a, "a", torch.bfloat16, (rows, K), dev)
-    _want(w, "w", torch.bfloat16, shape, dev)
+    N, K, E = _weight_of(w, "w", "[N, K] or [E, N, K]")
+    if transposed:
+        N, K = K, N
+    rows, dev = _rows_of(a, "a", "[rows, K]")[0], a.get_device()
+    _bf16(a, "a", (rows, K), dev)
+    _bf16(w, "w", w.shape, dev)
     _want(out, "out", _DENSE, (rows, N), dev)
-    _need((a2 is None) == (w2 is None), "a2 and w2: both or neither")
-    if a2 is not None:
-        _want(a2, "a2", torch.bfloat16, (rows, K), dev)
-        _want(w2, "w2", torch.bfloat16, shape, dev)
-    _bf16_call(_lib().lmoe_matmul_bf16, "lmoe_matmul_bf16", dev, stream, rows, N, K, E, offsets, status, a.data_ptr(),
-               w.data_ptr(), _ptr(a2), _ptr(w2), _ptr(offsets), out.data_ptr(), out_dtype=_DENSE[out.dtype],
-               transposed=transposed)
+    p2 = q2 = None
+    if a2 is not None or w2 is not None:
+        _need(a2 is not None and w2 is not None, "a2 and w2: both or neither")
+        _bf16(a2, "a2", (rows, K), dev)
+        _bf16(w2, "w2", w.shape, dev)
+        p2, q2 = a2.data_ptr(), w2.data_ptr()
+    off, st = _bf16_extra(offsets, status, E, dev)
+    _call(_lib().lmoe_matmul_bf16, "lmoe_matmul_bf16", dev, stream,
+          _bf16_shape(rows, N, K, E, _DENSE[out.dtype], 1 if transposed else 0, 0), a.data_ptr(), w.data_ptr(), p2, q2, off,
+          out.data_ptr(), st)
 
 
 def lmoe_matmul_bf16_wgrad(dy, x, dw, offsets=None, dy2=None, dw2=None, accumulate=False, status=None, stream=None):
     """``dw`` [(E,) N, K] (fp32 or bf16) (+)= each expert's rows of ``dy`` [rows, N] transposed times its rows of ``x``
     [rows, K] (bf16); with ``dy2``, ``dw2`` of the same shapes also the second weight's, from the same x.
     ``offsets``, ``status`` as in lmoe_gated_ffn."""
-    lead, E = _weight_shape(dw, "dw", "[N, K] or [E, N, K]")
-    _need(dy.dim() == 2 and x.dim() == 2, "dy [rows, N] and x [rows, K]")
-    dev, (rows, N), K = dy.get_device(), dy.shape, x.shape[1]
-    _want(dy, "dy", torch.bfloat16, (rows, N), dev)
-    _want(x, "x", torch.bfloat16, (rows, K), dev)
-    _want(dw, "dw", _DENSE, (*lead, N, K), dev)
-    _need((dy2 is None) == (dw2 is None), "dy2 and dw2: both or neither")
-    if dy2 is not None:
-        _want(dy2, "dy2", torch.bfloat16, (rows, N), dev)
+    N, K, E = _weight_of(dw, "dw", "[N, K] or [E, N, K]")
+    rows, dev = _rows_of(dy, "dy", "[rows, N]")[0], dy.get_device()
+    _bf16(dy, "dy", (rows, N), dev)
+    _bf16(x, "x", (rows, K), dev)
+    _want(dw, "dw", _DENSE, dw.shape, dev)
+    p2 = q2 = None
+    if dy2 is not None or dw2 is not None:
+        _need(dy2 is not None and dw2 is not None, "dy2 and dw2: both or neither")
+        _bf16(dy2, "dy2", (rows, N), dev)
         _want(dw2, "dw2", dw.dtype, dw.shape, dev)
-    _bf16_call(_lib().lmoe_matmul_bf16_wgrad, "lmoe_matmul_bf16_wgrad", dev, stream, rows, N, K, E, offsets, status,
-               dy.data_ptr(), x.data_ptr(), _ptr(dy2), _ptr(offsets), dw.data_ptr(), _ptr(dw2),
-               out_dtype=_DENSE[dw.dtype], accumulate=accumulate)
+        p2, q2 = dy2.data_ptr(), dw2.data_ptr()
+    off, st = _bf16_extra(offsets, status, E, dev)
+    _call(_lib().lmoe_matmul_bf16_wgrad, "lmoe_matmul_bf16_wgrad", dev, stream,
+          _bf16_shape(rows, N, K, E, _DENSE[dw.dtype], 0, 1 if accumulate else 0), dy.data_ptr(), x.data_ptr(), p2, off,
+          dw.data_ptr(), q2, st)
 
 
 def lmoe_bf16_check_status(device=None, stream=None) -> tuple[int, int]:

@@ -1021,6 +1021,7 @@ lmoe_status check_shape(const lmoe_bf16_matmul* c, const int32_t* offsets) {
   if (c->out_dtype != LMOE_F32 && c->out_dtype != LMOE_BF16) return LMOE_ERR_UNSUPPORTED;
   if (c->n_experts > kMaxGroups || c->K % 8 || c->N % 8 || c->K > (1 << 20) || c->N > (1 << 20) || c->rows > (1LL << 24))
     return LMOE_ERR_UNSUPPORTED;
+  if ((c->rows / 128 + c->n_experts) * ((c->N + 63) / 64) > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;   // tiles of the narrowest
   return LMOE_OK;
 }
 Bf16Args args_of(const lmoe_bf16_matmul* c, const int32_t* offsets, uint32_t* status) {
@@ -1047,7 +1048,6 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
   g.box = R < unit ? R : unit;
   const int across = (MODE == kGated ? 64 : 128) * (unit == 256 ? 2 : 1);
   const long long tiles = 1LL * most_tiles(R, g.E, unit) * ((g.n + across - 1) / across);
-  if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
   if (unit < 256) {
     using Few = Bf16Cfg<MODE, 32, F32>;
     using Wide = Bf16Cfg<MODE, 128, F32>;
