@@ -612,6 +612,9 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
               ++loads;
               get_row(in, lane, g);
               get_row(in + 4096, lane, u);
+              // (the reads are done, not only issued, before the next rows may land on them: where the tensor cores fill
+              // shared memory's bandwidth they were overtaken)
+              fence_async_shared();
               if (!last) load_gate(c + 64);
 #pragma unroll
               for (int i = 0; i < 32; ++i) {

@@ -216,6 +216,44 @@ def test_gated_ffn_grad(lm, R, N, K, split, in_place):
     assert lm.lmoe_bf16_check_status() == (0, 0)
 
 
+def test_gated_ffn_grad_of_full_tiles_many_times(lm):
+    """Large tiles, where the tensor cores keep shared memory busy: the same bits each time, and the right ones."""
+    R, N, K, E = 8192, 2048, 2048, 8
+    off = xu.offsets_of([1300, 700, 1024, 100, 2000, 1024, 1500, 544])
+    dy, wd, g, u = normal((R, K), 1, 1e-2), normal((E, K, N), 2, N ** -0.5), normal((R, N), 3, 2), normal((R, N), 4)
+    (dg, tg), (du, tu) = xu.gated_grad(dy, wd, g, u, off)
+    for _ in range(25):
+        a, b = torch.zeros_like(g), torch.zeros_like(u)
+        lm.lmoe_gated_ffn_grad(dy, wd, g, u, a, b, offsets=off)
+        close(a, dg, tg, "dgate")
+        close(b, du, tu, "dup")
+
+
+def test_gated_ffn_of_full_tiles_many_times(lm):
+    R, N, K, E = 8192, 2048, 2048, 8
+    off = xu.offsets_of([1300, 700, 1024, 100, 2000, 1024, 1500, 544])
+    x, wg, wu = normal((R, K), 1), normal((E, N, K), 2, K ** -0.5), normal((E, N, K), 3, K ** -0.5)
+    want = xu.gated(x, wg, wu, off)
+    for _ in range(25):
+        bufs = [torch.zeros(R, N, dtype=BF16, device="cuda") for _ in range(3)]
+        lm.lmoe_gated_ffn(x, wg, wu, *bufs, offsets=off)
+        for got, (v, tol), name in zip(bufs, want, "hgu"):
+            close(got, v, tol, name)
+
+
+def test_products_of_full_tiles_many_times(lm):
+    R, N, K, E = 8192, 2048, 2048, 8
+    off = xu.offsets_of([1300, 700, 1024, 100, 2000, 1024, 1500, 544])
+    a, w, dy = ints((R, K), 1), ints((E, N, K), 2), ints((R, N), 3)
+    want, dw = xu.product(a, w, off)[0], xu.wgrad(dy, a, E, off)[0]
+    for out in (F32, BF16):
+        for _ in range(25):
+            y, d = torch.zeros(R, N, dtype=out, device="cuda"), torch.zeros(E, N, K, dtype=out, device="cuda")
+            lm.lmoe_matmul_bf16(a, w, y, offsets=off)
+            lm.lmoe_matmul_bf16_wgrad(dy, a, d, offsets=off)
+            assert torch.equal(y, want.float().to(out)) and torch.equal(d, dw.float().to(out))
+
+
 def test_gradient_is_that_of_the_block(lm):
     """dgate, dup against differences of the loss sum(dy . y) with the down projection behind the gated product."""
     R, N, K, h = 12, 24, 40, 2.0 ** -10
