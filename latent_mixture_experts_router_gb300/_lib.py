@@ -798,14 +798,19 @@ def lmoe_grad_norm_workspace_size(count: int) -> int:
 _T = torch.Tensor
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _grad_list(ts, name, device):
-    """(addresses, sizes, dtypes) of contiguous CUDA tensors on one device, fp32 or bf16."""
+    """(addresses, sizes, dtypes) of a list of contiguous CUDA tensors on one device, fp32 or bf16."""
     # (maps over whole lists: a call with hundreds of tensors is bound by this)
     _need(set(map(_T.get_device, ts)) <= {device}, f"{name}: all tensors must be on cuda:{device}")
     _need(False not in map(_T.is_contiguous, ts), f"{name}: tensors must be contiguous")
-    found = set(map(operator.attrgetter("dtype"), ts))
+    dtypes = list(map(_dtype_of, ts))
+    found = set(dtypes)
     _need(found <= _DENSE.keys(), f"{name}: tensors must be float32 or bfloat16")
-    kinds = array.array("i", [_DENSE[found.pop()]]) * len(ts) if len(found) == 1 else array.array("i", [_DENSE[t.dtype] for t in ts])
+    kinds = array.array("i", [_DENSE[found.pop()]]) * len(dtypes) if len(found) == 1 else \
+        array.array("i", [LMOE_BF16 if d is _BF16 else LMOE_F32 for d in dtypes])
     return array.array("Q", map(_T.data_ptr, ts)), array.array("q", map(_T.numel, ts)), kinds
 
 
@@ -817,12 +822,13 @@ def _grad_device(norm):
 
 def _grad_args(grads, norm):
     dev = _grad_device(norm)
-    return dev, *_grad_list(grads, "grads", dev)
+    return dev, *_grad_list(list(grads), "grads", dev)   # (any iterable, gone through several times)
 
 
 def _grad_out(out, dev, ptrs, sizes, kinds):
     if out is None:
         return ptrs
+    out = list(out)
     _need(len(out) == len(ptrs), "out: as many tensors as grads")
     optrs, osizes, okinds = _grad_list(out, "out", dev)
     _need(osizes == sizes and okinds == kinds, "out: sizes and dtypes of grads")

@@ -35,7 +35,6 @@ namespace {
 
 enum Bf16Mode : int { kGated = 0, kGatedGrad = 1, kProduct = 2, kProductT = 3, kWgrad = 4 };
 constexpr int kRaster = 8;       // row tiles that take turns before the next column of tiles
-constexpr int kLdSplit = 132;    // floats of a row of 128 partial sums
 // Tensor memory's fp32 sums are cut, not rounded, at each addition: 4096 products in a row leave 4.4e-6 of the result (2-norm),
 // in proportion to their number.  bf16 results do not show it; for fp32 results a sum in TMEM ends after kChunk
 // blocks of 64, and the epilogue adds those in registers (8e-7.  Sums of 8 blocks: 5e-7, but
@@ -103,6 +102,8 @@ struct Bf16Cfg {
   static_assert((3 * kStages + 2 * 2 + 1 + 4) * 8 + 8 <= 512, "barriers");
   // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
   static_assert(kStageBytes >= 128 * 128, "lane operand");
+  // sums of a tile shared by a cluster of up to 8: of each row 128, and 4 or 8 floats of padding for each CTA
+  static_assert(kPair || kStages * kStageBytes >= kLanes * (128 + 8 * 8) * 4, "partial sums");
 };
 
 // Shared-memory descriptor of an MN-major operand tile with 128-byte swizzle: boxes of 64 columns (128 bytes) by 64
@@ -237,7 +238,8 @@ LMOE_DEV float sigmoid(float g) {
 struct Bf16Tile {
   int e, p0, q0;      // first lane (row of a; kWgrad: row of dw), first column
   int skip, live;     // lanes [skip, live) are the tile's
-  int kb0, kb1;       // blocks of the reduction
+  int kb0, kb1;       // blocks of the reduction, of
+  int blocks;         // so many
   int r0, rows;       // kWgrad: the expert's rows
   int second;         // kWgrad: of dw2
   bool brief;         // a short tile
@@ -292,14 +294,14 @@ LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank
     t.live = min(a.n - t.p0, C::kLanes);
     t.r0 = lo;
     t.rows = hi - lo;
-    t.kb1 = (hi - lo + kBK - 1) / kBK;
+    t.blocks = (hi - lo + kBK - 1) / kBK;
   } else if (C::kPair) {
     const int p0 = lo + rt * UNIT;
     t.brief = C::kShort && hi - p0 <= 128;
     const int mine = t.brief ? 64 : 128;   // rows of this CTA
     t.p0 = p0 + rank * mine;
     t.live = min(hi - t.p0, mine);
-    t.kb1 = a.num_kb * a.pairs;
+    t.blocks = a.num_kb * a.pairs;
   } else {
     // Tiles of few rows: no row behind the last is asked for (a box filled with zeros past the end costs the
     // copy engine more than rows); a tile near the end starts earlier and skips the lanes before its own.
@@ -307,12 +309,12 @@ LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank
     t.p0 = min(p0, static_cast<int>(a.rows) - a.box);
     t.skip = p0 - t.p0;
     t.live = t.skip + min(UNIT, hi - p0);
-    const int blocks = a.num_kb * a.pairs;
-    t.kb1 = blocks;
-    if (a.splits > 1) {
-      t.kb0 = blocks * rank / a.splits;
-      t.kb1 = blocks * (rank + 1) / a.splits;
-    }
+    t.blocks = a.num_kb * a.pairs;
+  }
+  t.kb1 = t.blocks;
+  if (!C::kPair && a.splits > 1) {
+    t.kb0 = static_cast<int>(static_cast<long long>(t.blocks) * rank / a.splits);
+    t.kb1 = static_cast<int>(static_cast<long long>(t.blocks) * (rank + 1) / a.splits);
   }
   return t;
 }
@@ -342,7 +344,7 @@ LMOE_DEV void gated_grad(float dh, float g, float u, float& dg, float& du) {
 LMOE_DEV float silu_mul(float g, float u) { return g * sigmoid(g) * u; }
 // Four sums v of out's element `at` (kGated: of gate and up) to where they belong (tiles shared by a cluster).
 template <int MODE>
-LMOE_DEV void finish4(const Bf16Args& a, long long at, float4 v, float4 v2) {
+LMOE_DEV void finish4(const Bf16Args& a, void* out, long long at, float4 v, float4 v2) {
   if (MODE == kGated) {
     store4(a.out, at, make_float4(silu_mul(v.x, v2.x), silu_mul(v.y, v2.y), silu_mul(v.z, v2.z), silu_mul(v.w, v2.w)), false);
     if (a.out2 != nullptr) {
@@ -359,7 +361,11 @@ LMOE_DEV void finish4(const Bf16Args& a, long long at, float4 v, float4 v2) {
     store4(a.out, at, dg, false);
     store4(a.out2, at, du, false);
   } else {
-    store4(a.out, at, v, a.out_f32);
+    if (MODE == kWgrad && a.accumulate) {
+      const float4 o = load4(out, at, a.out_f32);
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    store4(out, at, v, a.out_f32);
   }
 }
 
@@ -739,7 +745,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
   walk.start = start;
   walk.total = MODE == kWgrad ? args.E * static_cast<int>(args.by_tiles.d)
                               : start[args.E] * static_cast<int>(args.by_others.d);
-  const int S = C::kPair ? 2 : MODE == kWgrad ? 1 : args.splits;   // CTAs of a cluster
+  const int S = C::kPair ? 2 : args.splits;   // CTAs of a cluster
   const int rank = static_cast<int>(blockIdx.x % S);
   const int id0 = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
   const long long budget = args.budget;
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
             ok = false;
             break;
           }
-          const bool fix = MODE == kWgrad && kb + 1 == t.kb1 && t.rows % 16 != 0;   // cleared before it is full
+          const bool fix = MODE == kWgrad && kb + 1 == t.blocks && t.rows % 16 != 0;   // cleared before it is full
           const uint32_t bar = fix ? tail0 + s * 8 : lead0 + s * 8;
           const uint32_t dst = stages + s * C::kStageBytes + (lanes ? 0 : C::kABytes);
           if (MODE == kWgrad) {
@@ -891,7 +897,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       for (int id = id0; id < walk.total; id += step) {
         const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
         it += t.kb1 - t.kb0;
-        if (t.rows % 16 == 0) continue;
+        if (t.rows % 16 == 0 || t.kb0 == t.kb1 || t.kb1 != t.blocks) continue;
         const int s = (it - 1) % C::kStages;
         if (!warp_wait(&tail[s], phases >> s & 1, budget)) {
           atomicOr(status, kErrWaitProducer);
@@ -917,48 +923,58 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
     }
   }
 
-  if constexpr (MODE != kWgrad && !C::kPair) {
+  if constexpr (!C::kPair) {
     if (S > 1) {
-      // One tile per cluster.  Every CTA's sums go to the first one's stages (free once its own MMAs are done), which
-      // adds them in rank order.  All threads pass the cluster barriers, whatever their role.
+      // One tile per cluster, each CTA with a part of the reduction.  CTA q finishes the q-th part of the columns: every CTA's
+      // sums of those go to its stages (free once its own MMAs are done), and it adds them in rank order.  All threads
+      // pass the cluster barriers, whatever their role.
       const bool mine = warp >= 4 && id0 < walk.total;
-      const int quad = warp & 3;
+      const int row = (warp & 3) * 32 + lane, rows = MODE == kWgrad ? 128 : args.box;
+      constexpr int kParts = C::kOutCols / 4;   // fours of columns of the result
+      const int shift = __ffs(kParts) - __ffs(S), part = 4 << shift;   // columns of a CTA
+      const int width = (MODE == kGated ? 2 * part : part) + 4;          // floats of a row of sums
       Bf16Tile t = {};
       float acc[128];
       if (mine) {
         t = tile_at<MODE, UNIT, F32>(walk, args, id0, rank);
         int tc = 0;
-        const int chunks = F32 ? (t.kb1 - t.kb0 + kChunk - 1) / kChunk : 1;
-        if (!gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, quad, acc)) {
+        const int n = t.kb1 - t.kb0, chunks = F32 ? (n + kChunk - 1) / kChunk : n > 0;
+        const bool ok = gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, warp & 3, acc);
+        if (!ok || chunks == 0) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) acc[i] = 0.f;
         }
       }
       cluster_sync();
-      if (mine && quad * 32 + lane < args.box) {
-        const uint32_t dst = cluster_map(smem_u32(smem), 0) + (rank * args.box + quad * 32 + lane) * kLdSplit * 4;
+      if (mine && row < rows) {
+        const uint32_t at = smem_u32(smem) + (rank * rows + row) * width * 4;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          cluster_store(dst + i * 16, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
+        for (int i = 0; i < 32; ++i) {   // (kGated: 16 of gate, 16 of up)
+          const int p = i % kParts, c = (p & ((1 << shift) - 1)) * 4 + (i < kParts ? 0 : part);
+          cluster_store(cluster_map(at, p >> shift) + c * 4,
+                        make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
+        }
       }
       cluster_sync();
-      if (mine && rank == 0) {
-        constexpr int kC4 = C::kOutCols / 4;
+      if (mine && !(MODE == kWgrad && args.accumulate && t.blocks == 0)) {
         const float* red = reinterpret_cast<const float*>(smem);
-        for (int i = threadIdx.x & 127; i < (t.live - t.skip) * kC4; i += 128) {
-          const int r = t.skip + i / kC4, c = i % kC4 * 4, col = t.q0 + c;
-          if (col >= args.n) continue;
+        const int ld = MODE == kWgrad ? args.k : args.n;
+        void* out = MODE == kWgrad && t.second ? args.out2 : args.out;
+        const long long row0 = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0;
+        for (int i = threadIdx.x & 127; i < (t.live - t.skip) << shift; i += 128) {
+          const int r = t.skip + (i >> shift), c = (i & ((1 << shift) - 1)) * 4, col = t.q0 + rank * part + c;
+          if (col >= ld) continue;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f), v2 = v;
           for (int q = 0; q < S; ++q) {
-            const float* src = red + (q * args.box + r) * kLdSplit + c;
+            const float* src = red + (q * rows + r) * width + c;
             const float4 o = *reinterpret_cast<const float4*>(src);
             v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
             if (MODE == kGated) {
-              const float4 p = *reinterpret_cast<const float4*>(src + C::kBN / 2);
+              const float4 p = *reinterpret_cast<const float4*>(src + part);
               v2 = make_float4(v2.x + p.x, v2.y + p.y, v2.z + p.z, v2.w + p.w);
             }
           }
-          finish4<MODE>(args, static_cast<long long>(t.p0 + r) * args.n + col, v, v2);
+          finish4<MODE>(args, out, (row0 + r) * ld + col, v, v2);
         }
       }
     }
@@ -1001,7 +1017,7 @@ cudaError_t launch_one(const CUtensorMap (&m)[9], Bf16Args a, cudaStream_t s) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int kSms = 152;
-constexpr int kFewRows = 16, kPairRows = 96;
+constexpr int kFewRows = 16, kFewTiles = 8, kPairRows = 96, kPairTiles = 46;
 
 // [rows, cols] bf16, boxes of 64 columns by `high` rows; and [E, rows, cols]
 bool map_rows(CUtensorMap* m, const void* p, long long rows, int cols, int high) {
@@ -1043,23 +1059,66 @@ Bf16Args args_of(const lmoe_bf16_matmul* c, const int32_t* offsets, uint32_t* st
   return g;
 }
 
+// Clusters of s such CTAs (one to an SM) that run side by side: fewer than the SMs' number divided by s, since a cluster keeps
+// to one GPC and those have any number of SMs (clusters of 8: 16 of them took 27 us for what 14 do in 16).
+int most_clusters(int s) {
+  static std::mutex mu;
+  static int known[9] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[s] == 0) {
+    using C = Bf16Cfg<kProduct, 32, false>;
+    auto kern = gemm_bf16_kernel<kProduct, 32, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = kSms / s;
+    }
+    known[s] = n;
+  }
+  return known[s];
+}
+// CTAs (a cluster) for each of few tiles: as long as all clusters run side by side, and with at least four blocks of the
+// reduction to a CTA.  Fewer than `from` blocks are not shared: the sums' way to the CTAs that finish them takes 2 to 3 us.
+int splits_for(long long tiles, long long blocks, int from) {
+  int s = 1;
+  while (s < 8 && blocks >= from && tiles * s * 2 <= kSms && blocks / (s * 2) >= 4 && tiles <= most_clusters(s * 2)) s *= 2;
+  return s;
+}
 // One of the modes that take rows of a: which tile, and the launch.  A pair is (a, w).
+//
+// Tiles of 32 rows up to kFewRows rows per expert on average, or where kFewTiles tiles of 128 rows or fewer would leave most
+// SMs idle; of 256 rows (a pair of CTAs) from kPairRows rows per expert and kPairTiles tiles on; else of 128.  Measured, us, 32 /
+// 128 / 256 rows:
+//   64 experts of 4096 x 4096 with 8, 16, 32, 48, 64, 96, 128, 160 rows   318 320 325 381 382 614 779 920 / 326 328 330 335 337
+//                                                                          342 345 483 / 333 335 338 341 343 348 353 376
+//   (all the same, as the measured splits were even; with uneven ones half the experts have more rows than the average)
+//   one matrix of 4096 x 4096 with 128, 256, 512, 768, 1024 rows          17 28 50 71 83 / 17 19 22 33 37 / 18 24 25 26 26
+//   one of 1024 x 4096 with 128, 256, 1024 rows                           11 14 28 / 16 16 19 / 17 24 24
+// A cluster shares the reduction where tiles are few: one row of 4096 x 4096 10.0, unshared 19; 100 rows by 2048 x 4096 13.2 and
+// 15.4, by 2048 x 1024 11.2 and 8.4; 16 rows by 2048 x 2048 8.5 and 10.7; weight gradients of 32768, 8000, 4000, 2000 rows,
+// 256 x 256: 24.5, 15.4, 13.8, 11.9 and (142), 22, 16.9, 11.4.
 template <int MODE, bool F32>
 lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a2, const void* w2, cudaStream_t stream) {
   const int R = static_cast<int>(g.rows), live = g.E < R ? g.E : R;
-  const int unit = R / live <= kFewRows ? 32 : R / live < kPairRows ? 128 : 256;
+  const auto tiles_of = [&](int unit) {
+    const int across = (MODE == kGated ? 64 : 128) * (unit == 256 ? 2 : 1);
+    return 1LL * most_tiles(R, g.E, unit) * ((g.n + across - 1) / across);
+  };
+  const bool few = R / live <= kFewRows || tiles_of(128) <= kFewTiles;
+  const int unit = few ? 32 : R / live < kPairRows || tiles_of(256) < kPairTiles ? 128 : 256;
   g.box = R < unit ? R : unit;
-  const int across = (MODE == kGated ? 64 : 128) * (unit == 256 ? 2 : 1);
-  const long long tiles = 1LL * most_tiles(R, g.E, unit) * ((g.n + across - 1) / across);
-  if (unit < 256) {
-    using Few = Bf16Cfg<MODE, 32, F32>;
-    using Wide = Bf16Cfg<MODE, 128, F32>;
-    // rows of partial sums that fit
-    const int most = (unit == 32 ? Few::kStages * Few::kStageBytes : Wide::kStages * Wide::kStageBytes) / (kLdSplit * 4);
-    while (g.splits < 8 && tiles * g.splits * 2 <= kSms && g.num_kb * g.pairs / (g.splits * 2) >= 4 &&
-           g.splits * 2 * g.box <= most)
-      g.splits *= 2;
-  }
+  if (unit < 256) g.splits = splits_for(tiles_of(unit), g.num_kb * g.pairs, MODE == kGatedGrad ? 8 : few ? 24 : 48);
   constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
   const int high = mn || MODE == kGated ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
   const int rows = unit == 256 ? 64 : g.box;
@@ -1176,7 +1235,9 @@ extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const v
   if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
   CUtensorMap m[9];
   const int es = g.out_f32 ? 2 : 1;   // (in 16-bit columns)
-  g.whole = !g.accumulate;
+  const bool pair = 1LL * ((c->N + 255) / 256) * ((c->K + 255) / 256) * c->n_experts * g.pairs >= kPairTiles;
+  if (!pair) g.splits = splits_for(tiles, c->rows / c->n_experts / kBK, 48);
+  g.whole = !g.accumulate && g.splits == 1;
   if (!map_rows(&m[0], dy, c->rows, c->N, kBK) || !map_rows(&m[2], x, c->rows, c->K, kBK) ||
       !map_weights(&m[4], dw, g.E, g.n, g.k * es, 32))
     return LMOE_ERR_CUDA;
@@ -1184,7 +1245,6 @@ extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const v
     if (i != 2 && i != 4) m[i] = m[0];
   if (dw2 != nullptr && !map_weights(&m[5], dw2, g.E, g.n, g.k * es, 32)) return LMOE_ERR_CUDA;
   if (dy2 != nullptr && !map_rows(&m[1], dy2, c->rows, c->N, kBK)) return LMOE_ERR_CUDA;
-  const bool pair = c->N > 128 && c->K > 128;
   const cudaError_t e = g.out_f32 ? (pair ? launch_one<kWgrad, 256, true>(m, g, stream) : launch_one<kWgrad, 128, true>(m, g, stream))
                                   : (pair ? launch_one<kWgrad, 256, false>(m, g, stream) : launch_one<kWgrad, 128, false>(m, g, stream));
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;

@@ -150,6 +150,19 @@ def test_nothing_to_clip(lm):
     assert torch.equal(g, keep)
 
 
+def test_any_iterable_of_tensors(lm):
+    grads = [normal(100, F32, i) for i in range(3)]
+    norm, again, ws = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda"), workspace(lm, 3)
+    lm.lmoe_grad_norm(grads, norm, ws)
+    lm.lmoe_grad_norm((g for g in grads), again, ws)
+    assert float(norm) > 0 and torch.equal(norm, again)
+    outs = [torch.zeros_like(g) for g in grads]
+    lm.lmoe_clip_grad_norm(iter(grads), again, 0.5, ws, out=iter(outs))
+    for g, o in zip(grads, outs):
+        v, tol = xu.clipped(g, norm, 0.5)
+        close(o, v, tol)
+
+
 def test_overlapping_outputs_are_refused(lm):
     flat = torch.ones(1000, device="cuda")
     norm, ws = torch.ones(1, device="cuda"), workspace(lm, 3)
