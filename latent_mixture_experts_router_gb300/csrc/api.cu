@@ -313,7 +313,7 @@ bool encode_u8_2d(CUtensorMap* m, const void* base, unsigned long long cols, uns
 
 namespace lmoe {
 bool encode_u8_swizzled(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
-                        const unsigned long long* strides, const unsigned* box) {
+                        const unsigned long long* strides, const unsigned* box, bool half) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr || rank < 2 || rank > 3) return false;
   cuuint64_t d[3], st[2];
@@ -325,8 +325,8 @@ bool encode_u8_swizzled(CUtensorMap* m, const void* base, int rank, const unsign
     if (i > 0) st[i - 1] = strides[i - 1];
   }
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, st, b, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_INTERLEAVE_NONE, half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t allow_smem(const void* kernel, int bytes) {

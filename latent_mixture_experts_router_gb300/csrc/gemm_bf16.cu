@@ -83,8 +83,9 @@ struct Bf16Cfg {
   static constexpr int kEpiWarps = kPair && F32 ? 8 : 4;
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kABytes = kLanes * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
-  // a warp's 32 rows of 128 bytes on their way out (kGatedGrad: and in, of gate and of up)
-  static constexpr int kWarpBytes = 4096 * (MODE == kGatedGrad ? 3 : 1);
+  // a warp's 32 rows of 128 bytes on their way out (kGatedGrad: of 64 bytes, and in, of gate and of up)
+  static constexpr int kRow = MODE == kGatedGrad ? 64 : 128;
+  static constexpr int kWarpBytes = 32 * kRow * (MODE == kGatedGrad ? 3 : 1);
   static constexpr int kStagingBytes = kEpiWarps * kWarpBytes;
   // off[], and start[] (not kWgrad).  An fp32 kWgrad has room for a stage more than with all offsets: from kOffsets experts
   // on they are read where they are (read there always, 16 experts' weight gradients to bf16 took 195 us, so 181).
@@ -369,17 +370,23 @@ LMOE_DEV void finish4(const Bf16Args& a, void* out, long long at, float4 v, floa
   }
 }
 
-// A warp's 32 rows of 128 bytes in shared memory, one to a thread: their 16-byte parts swizzled as the tensor
-// copies have them (part j of row r at j ^ (r % 8)), which is free of bank conflicts by rows and by columns.
-LMOE_DEV uint4* part_of(uint8_t* st, int r, int j) { return reinterpret_cast<uint4*>(st + r * 128 + ((j ^ (r & 7)) << 4)); }
+// A warp's 32 rows of ROW bytes (128, or 64) in shared memory, one to a thread: their 16-byte parts swizzled as the tensor
+// copies have them (part j of row r at j ^ (r % 8), or j ^ (r / 2 % 4)), which is free of bank conflicts by rows and by
+// columns.
+template <int ROW>
+LMOE_DEV uint4* part_of(uint8_t* st, int r, int j) {
+  return reinterpret_cast<uint4*>(st + r * ROW + ((j ^ (ROW == 128 ? r & 7 : r >> 1 & 3)) << 4));
+}
+template <int ROW>
 LMOE_DEV void put_row(uint8_t* st, int lane, const uint32_t* w) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) *part_of(st, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  for (int j = 0; j < ROW / 16; ++j) *part_of<ROW>(st, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
-LMOE_DEV void get_row(uint8_t* st, int lane, uint32_t (&w)[32]) {
+template <int ROW>
+LMOE_DEV void get_row(uint8_t* st, int lane, uint32_t (&w)[ROW / 4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint4 q = *part_of(st, lane, j);
+  for (int j = 0; j < ROW / 16; ++j) {
+    const uint4 q = *part_of<ROW>(st, lane, j);
     w[4 * j] = q.x;
     w[4 * j + 1] = q.y;
     w[4 * j + 2] = q.z;
@@ -414,23 +421,24 @@ LMOE_DEV void staging_free() {
   if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
 }
-// 128 bytes of each row, from byte `col` on, one row to a thread.
-template <int MODE>
+// ROW bytes of each row, from byte `col` on, one row to a thread.
+template <int MODE, int ROW>
 LMOE_DEV void emit(const Bf16Rows& o, const CUtensorMap* m, void* out, int col, const uint32_t* w) {
   staging_free();
-  put_row(o.st, o.lane, w);
+  put_row<ROW>(o.st, o.lane, w);
   if (o.whole) {
     fence_async_shared();
     __syncwarp();
     if (elect_one()) tensor_store<MODE == kWgrad>(m, o.st, col, MODE == kWgrad ? o.r0 : static_cast<int>(o.row), o.e);
   } else {
     __syncwarp();
-    const int j = o.lane & 7;
-    uint8_t* p = static_cast<uint8_t*>(out) + (o.row + (o.lane >> 3)) * o.ld + col + j * 16;
+    constexpr int kParts = ROW / 16, kAtOnce = 32 / kParts;   // rows to a store instruction
+    const int j = o.lane % kParts, r0 = o.lane / kParts;
+    uint8_t* p = static_cast<uint8_t*>(out) + (o.row + r0) * o.ld + col + j * 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i, p += 4 * o.ld) {
-      const int r = 4 * i + (o.lane >> 3);
-      const uint4 q = *part_of(o.st, r, j);
+    for (int i = 0; i < kParts; ++i, p += kAtOnce * o.ld) {
+      const int r = kAtOnce * i + r0;
+      const uint4 q = *part_of<ROW>(o.st, r, j);
       if (r >= o.from && r < o.to && col + j * 16 < o.limit) *reinterpret_cast<uint4*>(p) = q;
     }
   }
@@ -438,13 +446,13 @@ LMOE_DEV void emit(const Bf16Rows& o, const CUtensorMap* m, void* out, int col, 
 // 32 columns of sums, added to what the rows hold.
 LMOE_DEV void emit_added(const Bf16Rows& o, void* out, int width, int col, bool f32, const uint32_t* w) {
   __syncwarp();
-  put_row(o.st, o.lane, w);
+  put_row<128>(o.st, o.lane, w);
   __syncwarp();
   const int j = o.lane & 7, c = col + j * 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (o.lane >> 3);
-    const float4 q = *reinterpret_cast<const float4*>(part_of(o.st, r, j));
+    const float4 q = *reinterpret_cast<const float4*>(part_of<128>(o.st, r, j));
     if (r >= o.from && r < o.to && c < width) {
       const long long at = (o.row + r) * width + c;
       const float4 p = load4(out, at, f32);
@@ -516,14 +524,16 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
   constexpr int kEs = F32 ? 4 : 2;
   const int width = MODE == kWgrad ? args.k : args.n;
   uint8_t* st = staging + (warp - 4) * C::kWarpBytes;
-  uint8_t* in = st + 4096;   // kGatedGrad: gate's rows, and up's behind them
+  uint8_t* in = st + 32 * C::kRow;   // kGatedGrad: gate's rows, and up's behind them
+  uint64_t* mine = landed + (warp - 4);
   int tc = 0, loads = 0;
   for (int id = id0; id < walk.total; id += step) {
     const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
     const int blocks = t.kb1 - t.kb0;   // (kWgrad: an expert without rows has none, and gets zeros)
     // (short tiles: 64 rows, whose other columns are two quadrants on)
     const int rows0 = C::kShort && t.brief ? (quad & 1) * 32 : quad * 32;
-    const int q0 = t.q0 + half * kCols + (C::kShort && t.brief ? (quad >> 1) * (kCols / 2) : 0);
+    const int cols = C::kShort && t.brief ? kCols / 2 : kCols;
+    const int q0 = t.q0 + half * cols + (C::kShort && t.brief ? (quad >> 1) * (C::kOutCols / 2) : 0);
     Bf16Rows o;
     o.st = st;
     o.lane = lane;
@@ -544,7 +554,7 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = 0;
       if (any && !args.accumulate)
-        for (int c = 0; c < kCols && q0 + c < width; c += 128 / kEs) emit<MODE>(o, map, out, (q0 + c) * kEs, w);
+        for (int c = 0; c < kCols && q0 + c < width; c += C::kRow / kEs) emit<MODE, C::kRow>(o, map, out, (q0 + c) * kEs, w);
       continue;
     }
     if constexpr (F32) {
@@ -557,17 +567,17 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
         if (q0 + c >= width) break;
         const uint32_t* w = reinterpret_cast<const uint32_t*>(acc + c);
         if (MODE == kWgrad && args.accumulate) emit_added(o, out, width, q0 + c, true, w);
-        else emit<MODE>(o, map, out, (q0 + c) * 4, w);
+        else emit<MODE, C::kRow>(o, map, out, (q0 + c) * 4, w);
       }
     } else {
-      const auto load_gate = [&](int c) {   // 64 columns of gate and up
+      const auto load_gate = [&](int c) {   // 32 columns of gate and up
         if constexpr (MODE == kGatedGrad) {
           __syncwarp();
           if (elect_one()) {
-            const uint32_t bar = smem_u32(landed + quad);
-            arrive_expect_tx(bar, 8192);
+            const uint32_t bar = smem_u32(mine);
+            arrive_expect_tx(bar, 4096);
             load_2d<false>(smem_u32(in), maps.gate, bar, (q0 + c) * 2, o.r0, policy_evict_normal());
-            load_2d<false>(smem_u32(in + 4096), maps.up, bar, (q0 + c) * 2, o.r0, policy_evict_normal());
+            load_2d<false>(smem_u32(in + 2048), maps.up, bar, (q0 + c) * 2, o.r0, policy_evict_normal());
           }
           __syncwarp();
         }
@@ -575,11 +585,12 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
       if (any) load_gate(0);
       bool ok = ring.wait(tc);
       if (any && ok) {
-        const uint32_t tq = tmem + (tc & 1) * C::kBN + half * kCols + (static_cast<uint32_t>(quad * 32) << 16);
-        const int end = min(C::kShort && t.brief ? kCols / 2 : kCols, width - q0);
+        const uint32_t tq = tmem + (tc & 1) * C::kBN + half * cols + (static_cast<uint32_t>(quad * 32) << 16);
+        const int end = min(cols, width - q0);
+        constexpr int kStep = C::kRow / 2;
 #pragma unroll 1
-        for (int c = 0; c < end; c += 64) {
-          const bool last = c + 64 >= end;
+        for (int c = 0; c < end; c += kStep) {
+          const bool last = c + kStep >= end;
           uint32_t v[2][32];
           if constexpr (MODE == kGated) {
             uint32_t h[32], g[32], u[32];
@@ -597,51 +608,54 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
                 v[0][i] = __float_as_uint(silu_mul(__uint_as_float(v[0][i]), __uint_as_float(v[1][i])));
               pack32(v[0], h + b * 16);
             }
-            emit<MODE>(o, maps.out, args.out, (q0 + c) * 2, h);
+            emit<MODE, C::kRow>(o, maps.out, args.out, (q0 + c) * 2, h);
             if (args.out2 != nullptr) {
-              emit<MODE>(o, maps.out2, args.out2, (q0 + c) * 2, g);
-              emit<MODE>(o, maps.out3, args.out3, (q0 + c) * 2, u);
+              emit<MODE, C::kRow>(o, maps.out2, args.out2, (q0 + c) * 2, g);
+              emit<MODE, C::kRow>(o, maps.out3, args.out3, (q0 + c) * 2, u);
             }
+          } else if constexpr (MODE == kGatedGrad) {
+            tmem_ld_32cols(tq + c, v[0]);
+            tmem_ld_wait();
+            if (last) ring.release(tc, lane);
+            ok = warp_wait(mine, loads & 1, ring.budget);
+            if (!ok) {
+              atomicOr(ring.status, kErrWaitEpilogue);
+              break;
+            }
+            ++loads;
+            uint32_t g[16], u[16], w[16];
+            get_row<64>(in, lane, g);
+            get_row<64>(in + 2048, lane, u);
+            // (the reads are done, not only issued, before the next rows may land on them: where the tensor cores fill
+            // shared memory's bandwidth they were overtaken)
+            fence_async_shared();
+            if (!last) load_gate(c + 32);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float dg[2], du[2];
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const uint32_t gi = b ? g[i] & 0xffff0000u : g[i] << 16, ui = b ? u[i] & 0xffff0000u : u[i] << 16;
+                gated_grad(__uint_as_float(v[0][2 * i + b]), __uint_as_float(gi), __uint_as_float(ui), dg[b], du[b]);
+              }
+              w[i] = pack_bf16x2(dg[0], dg[1]);
+              u[i] = pack_bf16x2(du[0], du[1]);
+            }
+            emit<MODE, C::kRow>(o, maps.out, args.out, (q0 + c) * 2, w);
+            emit<MODE, C::kRow>(o, maps.out2, args.out2, (q0 + c) * 2, u);
           } else {
             tmem_ld_32cols(tq + c, v[0]);
             tmem_ld_32cols(tq + c + 32, v[1]);
             tmem_ld_wait();
             if (last) ring.release(tc, lane);
-            uint32_t w[32];
-            if constexpr (MODE == kGatedGrad) {
-              uint32_t g[32], u[32];
-              ok = warp_wait(landed + quad, loads & 1, ring.budget);
-              if (!ok) {
-                atomicOr(ring.status, kErrWaitEpilogue);
-                break;
-              }
-              ++loads;
-              get_row(in, lane, g);
-              get_row(in + 4096, lane, u);
-              // (the reads are done, not only issued, before the next rows may land on them: where the tensor cores fill
-              // shared memory's bandwidth they were overtaken)
-              fence_async_shared();
-              if (!last) load_gate(c + 64);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float dg[2], du[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const uint32_t gi = b ? g[i] & 0xffff0000u : g[i] << 16, ui = b ? u[i] & 0xffff0000u : u[i] << 16;
-                  gated_grad(__uint_as_float(v[i / 16][2 * (i % 16) + b]), __uint_as_float(gi), __uint_as_float(ui), dg[b], du[b]);
-                }
-                w[i] = pack_bf16x2(dg[0], dg[1]);
-                u[i] = pack_bf16x2(du[0], du[1]);
-              }
-              emit<MODE>(o, maps.out, args.out, (q0 + c) * 2, w);
-              emit<MODE>(o, maps.out2, args.out2, (q0 + c) * 2, u);
-            } else if (MODE == kWgrad && args.accumulate) {
+            if (MODE == kWgrad && args.accumulate) {
               emit_added(o, out, width, q0 + c, false, v[0]);
               if (q0 + c + 32 < width) emit_added(o, out, width, q0 + c + 32, false, v[1]);
             } else {
+              uint32_t w[32];
               pack32(v[0], w);
               pack32(v[1], w + 16);
-              emit<MODE>(o, map, out, (q0 + c) * 2, w);
+              emit<MODE, C::kRow>(o, map, out, (q0 + c) * 2, w);
             }
           }
         }
@@ -649,7 +663,7 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
         ring.release(tc, lane);
       }
       if (!ok) {
-        if (MODE == kGatedGrad && any) warp_wait(landed + quad, loads & 1, kDrain);   // (what was asked for lands here)
+        if (MODE == kGatedGrad && any) warp_wait(mine, loads & 1, kDrain);   // (what was asked for lands here)
         break;
       }
       ++tc;
@@ -1019,11 +1033,11 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 constexpr int kSms = 152;
 constexpr int kFewRows = 16, kFewTiles = 8, kPairRows = 96, kPairTiles = 46;
 
-// [rows, cols] bf16, boxes of 64 columns by `high` rows; and [E, rows, cols]
-bool map_rows(CUtensorMap* m, const void* p, long long rows, int cols, int high) {
+// [rows, cols] bf16, boxes of 64 columns (half: 32) by `high` rows; and [E, rows, cols]
+bool map_rows(CUtensorMap* m, const void* p, long long rows, int cols, int high, bool half = false) {
   const unsigned long long d[2] = {2ull * cols, static_cast<unsigned long long>(rows)}, st[1] = {2ull * cols};
-  const unsigned box[2] = {128, static_cast<unsigned>(high)};
-  return encode_u8_swizzled(m, p, 2, d, st, box);
+  const unsigned box[2] = {half ? 64u : 128u, static_cast<unsigned>(high)};
+  return encode_u8_swizzled(m, p, 2, d, st, box, half);
 }
 bool map_weights(CUtensorMap* m, const void* p, int E, int rows, int cols, int high) {
   const unsigned long long d[3] = {2ull * cols, static_cast<unsigned long long>(rows), static_cast<unsigned long long>(E)};
@@ -1129,11 +1143,13 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
   g.whole = unit > 32 && g.splits == 1;
   if (g.whole) {
     const int es = F32 ? 2 : 1;   // (in 16-bit columns)
-    if (!map_rows(&m[4], g.out, R, g.n * es, 32) || (g.out2 != nullptr && !map_rows(&m[5], g.out2, R, g.n * es, 32)) ||
+    constexpr bool half = MODE == kGatedGrad;
+    if (!map_rows(&m[4], g.out, R, g.n * es, 32, half) || (g.out2 != nullptr && !map_rows(&m[5], g.out2, R, g.n * es, 32, half)) ||
         (g.out3 != nullptr && !map_rows(&m[6], g.out3, R, g.n * es, 32)))
       return LMOE_ERR_CUDA;
   }
-  if (MODE == kGatedGrad && (!map_rows(&m[7], g.gate, R, g.n, 32) || !map_rows(&m[8], g.up, R, g.n, 32))) return LMOE_ERR_CUDA;
+  if (MODE == kGatedGrad && (!map_rows(&m[7], g.gate, R, g.n, 32, true) || !map_rows(&m[8], g.up, R, g.n, 32, true)))
+    return LMOE_ERR_CUDA;
   if ((a2 != nullptr && !map_rows(&m[1], a2, R, g.k, rows)) || (w2 != nullptr && !map_weights(&m[3], w2, g.E, wr, wc, high)))
     return LMOE_ERR_CUDA;
   const cudaError_t e = unit == 32    ? launch_one<MODE, 32, F32>(m, g, stream)

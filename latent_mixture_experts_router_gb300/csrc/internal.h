@@ -171,9 +171,9 @@ cudaError_t launch_swiglu_reduce_nvfp4(const float* partial, const int* splits_d
 // device; nothing to do up to 48 KB).
 cudaError_t allow_smem(const void* kernel, int bytes);
 // Tensor map of a byte matrix (rank 2 or 3, innermost dimension first; strides in bytes of the
-// dimensions after it) with 128-byte swizzled boxes; elements outside read as 0.
+// dimensions after it) with 128-byte (half: 64-byte) swizzled boxes; elements outside read as 0.
 bool encode_u8_swizzled(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
-                        const unsigned long long* strides, const unsigned* box);
+                        const unsigned long long* strides, const unsigned* box, bool half = false);
 
 // Counts every kernel launch of the library (lmoe_kernel_launches).
 void count_launch();
