@@ -19,10 +19,27 @@
 // infinities or NaN, which a product with zero would keep), so a warp clears those rows of both operands in
 // shared memory before the tensor cores read them, up to the next 16; steps of 16 behind that are left out.
 //
-// Roles of a CTA: warp 0 lane 0 TMA producer, warp 1 lane 0 MMA issuer (warp 1 owns the TMEM), warp 2 the
-// clearing of kWgrad, warps 4..7 epilogue, warp w on TMEM lanes 32 (w % 4) ..  Two accumulator buffers: a
-// tile is stored while the next one is computed.  A warp's 32 x 32 block passes through its own shared
-// memory on the way out, so that a store instruction writes whole segments of four rows.
+// Tiles (UNIT rows, see rows_product for which where and what was measured):
+//   256   a pair of CTAs (cta_group::2), 256 x 256 sums: each CTA loads 128 rows of the lane operand and half of the
+//         column operand's tile, 32 KB for 128 x 256 x 64 products, which shared memory can take in in the time of the MMAs
+//         (a single CTA's 128 x 128 tiles take in twice as much: 32768 rows over 64 experts of 4096 x 4096, gate and up 2568
+//         us, so 1360).  kGated: columns are 64 of gate, the same 64 of up, and so on.  An expert's last tile, if it has
+//         no more than 128 rows, goes by MMAs of half the height (612 and 412 rows in turn: 1600 us without, so 1480).
+//   128   one CTA, 128 x 128 sums: fewer rows per expert, or too few tiles of 256.
+//   32    the same with loads of up to 32 rows: a few tokens.  Bound by the stream of weights.
+// Few tiles with a long reduction are shared by a cluster of up to 8 CTAs.
+//
+// Roles of a CTA: one thread of warp 0 loads the lane operand, one of warp 3 the column operand (one thread for both: weight
+// gradients 267 us, so 245), one of warp 1 issues MMAs (in a pair the first CTA's, for both), warp 2 clears kWgrad's
+// rows, warps 4.. are the epilogue, warp w on TMEM lanes 32 (w % 4) ..  Two accumulator buffers: a tile is stored while
+// the next one is computed.  A warp's 32 rows of 128 bytes (kGatedGrad: 64, and gate and up come in the same way) pass
+// through its own shared memory and leave by tensor stores; where they are not all the tile's, by stores of whole segments.
+//
+// Measured (other inputs in each call, power-limited at 1.6 to 1.7 GHz where it is tensor-bound): 32768 uneven rows over 64 experts
+// of 4096 x 4096, g and u stored, 1790 us; the gradient of 16384 over 32 475 us; dx of 16384 over 32, two pairs, 917 us;
+// 16384 x 8192 x 8192 1100 us (2.0 PFLOP/s) cold, 1270 sustained; two weight gradients of 8192 rows over 16 to fp32 525 us
+// (4.5 TB/s); one token on 8 of 64 experts, gate and up, 79 us, 1024 rows over 64 experts 320 us (6.8 TB/s).  Tensor pipe busy 88 to
+// 95 % (gradient 78, weight gradient 56 beside 62 % of HBM's nominal rate) at 512 rows per expert.
 #include <mutex>
 
 #include "../../include/latent_moe.h"
@@ -211,7 +228,7 @@ struct RingAt {
 
 // (Of CTA scope: what it orders are TMEM reads and shared memory that this CTA's own tensor cores read.  A release at cluster
 // scope would wait for the epilogue's global stores, an acquire cost the MMA issuer several hundred cycles a block:
-// weight gradients 650 instead of TFLOP/s.)
+// weight gradients of 8192 rows, 16 experts, 509 us instead of 267.)
 LMOE_DEV void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -1112,16 +1129,21 @@ int splits_for(long long tiles, long long blocks, int from) {
 // One of the modes that take rows of a: which tile, and the launch.  A pair is (a, w).
 //
 // Tiles of 32 rows up to kFewRows rows per expert on average, or where kFewTiles tiles of 128 rows or fewer would leave most
-// SMs idle; of 256 rows (a pair of CTAs) from kPairRows rows per expert and kPairTiles tiles on; else of 128.  Measured, us, 32 /
-// 128 / 256 rows:
-//   64 experts of 4096 x 4096 with 8, 16, 32, 48, 64, 96, 128, 160 rows   318 320 325 381 382 614 779 920 / 326 328 330 335 337
-//                                                                          342 345 483 / 333 335 338 341 343 348 353 376
-//   (all the same, as the measured splits were even; with uneven ones half the experts have more rows than the average)
-//   one matrix of 4096 x 4096 with 128, 256, 512, 768, 1024 rows          17 28 50 71 83 / 17 19 22 33 37 / 18 24 25 26 26
-//   one of 1024 x 4096 with 128, 256, 1024 rows                           11 14 28 / 16 16 19 / 17 24 24
-// A cluster shares the reduction where tiles are few: one row of 4096 x 4096 10.0, unshared 19; 100 rows by 2048 x 4096 13.2 and
-// 15.4, by 2048 x 1024 11.2 and 8.4; 16 rows by 2048 x 2048 8.5 and 10.7; weight gradients of 32768, 8000, 4000, 2000 rows,
-// 256 x 256: 24.5, 15.4, 13.8, 11.9 and (142), 22, 16.9, 11.4.
+// SMs idle; of 256 rows from kPairRows rows per expert and kPairTiles tiles on; else of 128.  Measured in us, 32 / 128 / 256
+// rows each:
+//   64 experts of 4096 x 4096, even splits   8 rows   318 / 326 / 333      64 rows    382 / 337 / 343
+//                                            16       320 / 328 / 335      96         614 / 342 / 348
+//                                            32       325 / 330 / 338      128        779 / 345 / 353
+//                                            48       381 / 335 / 341      160        920 / 483 / 376
+//   (by the average: with uneven splits, which the device alone knows, half the experts have more rows)
+//   one matrix of 4096 x 4096                128      17 / 17 / 18         512        50 / 22 / 25
+//                                            256      28 / 19 / 24         1024       83 / 37 / 26
+//   one of 1024 x 4096                       128      11 / 16 / 17         1024       28 / 19 / 24
+// A cluster shares the reduction where tiles are few, from 24 blocks on for 32 rows, 48 for 128 and for weight gradients, 8 for
+// kGatedGrad (whose tiles a cluster finishes with more threads).  Shared and not: one row of 4096 x 4096 10.0 and 19 us, 16
+// rows of 2048 x 2048 8.5 and 10.7, of 1024 x 1024 8.4 and 8.1; 100 rows of 2048 x 4096 13.2 and 15.4, of 2048 x 2048 11.8 and 11.0;
+// kGatedGrad 16 rows of 1024 x 1024 9.4 and 13.8; weight gradients of 256 x 256 over 32768, 8000, 4000, 2000 rows 24.5, 15.4, 13.8,
+// 11.9 and (a pair's tile) 142, 22, 16.9, 11.4.
 template <int MODE, bool F32>
 lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a2, const void* w2, cudaStream_t stream) {
   const int R = static_cast<int>(g.rows), live = g.E < R ? g.E : R;
