@@ -1074,6 +1074,22 @@ lmoe_status check_shape(const lmoe_bf16_matmul* c, const int32_t* offsets) {
   if ((c->rows / 128 + c->n_experts) * ((c->N + 63) / 64) > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;   // tiles of the narrowest
   return LMOE_OK;
 }
+// A matrix in memory, or the offsets: where it begins, and its bytes.
+struct Span {
+  const void* p;
+  long long n;
+};
+// Whether no result (the first `results`) shares memory with another one or with an operand.
+template <int N>
+bool apart(const Span (&m)[N], int results) {
+  for (int i = 0; i < results; ++i)
+    for (int j = i + 1; j < N; ++j) {
+      if (m[i].p == nullptr || m[j].p == nullptr) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(m[i].p), b = reinterpret_cast<uintptr_t>(m[j].p);
+      if (a < b + m[j].n && b < a + m[i].n) return false;
+    }
+  return true;
+}
 Bf16Args args_of(const lmoe_bf16_matmul* c, const int32_t* offsets, uint32_t* status) {
   Bf16Args g = {};
   g.rows = c->rows;
@@ -1197,6 +1213,9 @@ extern "C" lmoe_status lmoe_gated_ffn(const lmoe_bf16_matmul* c, const void* x, 
   if (!aligned(x, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(h, 16) || !aligned(gate, 16) ||
       !aligned(up, 16) || !aligned(offsets, 4) || !aligned(status, 4))
     return LMOE_ERR_ALIGN;
+  const long long rn = 2LL * c->rows * c->N, w = 2LL * c->n_experts * c->N * c->K, o = 4LL * (c->n_experts + 1);
+  if (!apart<8>({{h, rn}, {gate, rn}, {up, rn}, {x, 2LL * c->rows * c->K}, {w_gate, w}, {w_up, w}, {offsets, o}, {status, 4}}, 3))
+    return LMOE_ERR_ARG;
   Bf16Args g = args_of(c, offsets, status);
   g.out = h;
   g.out2 = gate;
@@ -1217,6 +1236,11 @@ extern "C" lmoe_status lmoe_gated_ffn_grad(const lmoe_bf16_matmul* c, const void
   if (!aligned(dy, 16) || !aligned(w_down, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(dgate, 16) ||
       !aligned(dup, 16) || !aligned(offsets, 4) || !aligned(status, 4))
     return LMOE_ERR_ALIGN;
+  const long long rn = 2LL * c->rows * c->N, w = 2LL * c->n_experts * c->N * c->K, o = 4LL * (c->n_experts + 1);
+  const void* g_in = gate == dgate ? nullptr : gate;   // (in place)
+  const void* u_in = up == dup ? nullptr : up;
+  if (!apart<8>({{dgate, rn}, {dup, rn}, {g_in, rn}, {u_in, rn}, {dy, 2LL * c->rows * c->K}, {w_down, w}, {offsets, o}, {status, 4}}, 2))
+    return LMOE_ERR_ARG;
   Bf16Args g = args_of(c, offsets, status);
   g.gate = static_cast<const __nv_bfloat16*>(gate);
   g.up = static_cast<const __nv_bfloat16*>(up);
@@ -1230,12 +1254,16 @@ extern "C" lmoe_status lmoe_matmul_bf16(const lmoe_bf16_matmul* c, const void* a
                                         cudaStream_t stream) {
   const lmoe_status st = check_shape(c, offsets);
   if (st != LMOE_OK) return st;
-  if (c->accumulate || (a2 == nullptr) != (w2 == nullptr)) return LMOE_ERR_ARG;
-  if (c->rows == 0) return LMOE_OK;
+  if (c->accumulate) return LMOE_ERR_ARG;
+  if (c->rows == 0) return LMOE_OK;   // (an empty tensor's address may be null)
+  if ((a2 == nullptr) != (w2 == nullptr)) return LMOE_ERR_ARG;
   if (a == nullptr || w == nullptr || out == nullptr) return LMOE_ERR_ARG;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a2, 16) || !aligned(w2, 16) || !aligned(out, 16) ||
       !aligned(offsets, 4) || !aligned(status, 4))
     return LMOE_ERR_ALIGN;
+  const long long rk = 2LL * c->rows * c->K, wb = 2LL * c->n_experts * c->N * c->K, o = 4LL * (c->n_experts + 1);
+  const long long rn = (c->out_dtype == LMOE_F32 ? 4LL : 2LL) * c->rows * c->N;
+  if (!apart<7>({{out, rn}, {a, rk}, {a2, rk}, {w, wb}, {w2, wb}, {offsets, o}, {status, 4}}, 1)) return LMOE_ERR_ARG;
   Bf16Args g = args_of(c, offsets, status);
   g.pairs = a2 != nullptr ? 2 : 1;
   g.out = out;
@@ -1271,6 +1299,9 @@ extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const v
   g.accumulate = c->accumulate != 0;
   const long long tiles = 1LL * ((c->N + 127) / 128) * ((c->K + 127) / 128) * c->n_experts * g.pairs;
   if (tiles > 0x7fffffffLL) return LMOE_ERR_UNSUPPORTED;
+  const long long rn = 2LL * c->rows * c->N, o = 4LL * (c->n_experts + 1);
+  const long long wb = (g.out_f32 ? 4LL : 2LL) * c->n_experts * c->N * c->K;
+  if (!apart<7>({{dw, wb}, {dw2, wb}, {dy, rn}, {dy2, rn}, {x, 2LL * c->rows * c->K}, {offsets, o}, {status, 4}}, 2)) return LMOE_ERR_ARG;
   CUtensorMap m[9];
   const int es = g.out_f32 ? 2 : 1;   // (in 16-bit columns)
   const bool pair = 1LL * ((c->N + 255) / 256) * ((c->K + 255) / 256) * c->n_experts * g.pairs >= kPairTiles;

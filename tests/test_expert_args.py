@@ -101,6 +101,27 @@ def test_no_rows_launch_nothing(lm, C, name, args):
     assert lm.lmoe_kernel_launches() == n0
 
 
+G = 1 << 30   # apart from one another: 8 rows of 256 are 4 KB, the weights 64 KB
+FFN_APART = dict(FFN, x=P, wg=P + G, wu=P + 2 * G, offsets=P + 3 * G, h=P + 4 * G, gate=P + 5 * G, up=P + 6 * G)
+GRAD_APART = dict(FFN_GRAD, dy=P, wd=P + G, gate=P + 2 * G, up=P + 3 * G, offsets=P + 4 * G, dgate=P + 5 * G, dup=P + 6 * G)
+MATMUL_APART = dict(MATMUL, a=P, w=P + G, a2=P + 2 * G, w2=P + 3 * G, offsets=P + 4 * G, y=P + 5 * G)
+WGRAD_APART = dict(WGRAD, dy=P, x=P + G, dy2=P + 2 * G, offsets=P + 3 * G, dw=P + 4 * G, dw2=P + 5 * G)
+SHARED = [("lmoe_gated_ffn", FFN_APART, [("h", "x", 0), ("h", "wg", 65520), ("gate", "h", 0), ("up", "gate", 1008), ("up", "wu", 16),
+                                         ("h", "offsets", 0)]),
+          ("lmoe_gated_ffn_grad", GRAD_APART, [("dgate", "up", 0), ("dup", "gate", 0), ("dgate", "gate", 16), ("dup", "dgate", 0),
+                                               ("dgate", "dy", 4080), ("dup", "wd", 0)]),
+          ("lmoe_matmul_bf16", MATMUL_APART, [("y", "a", 0), ("y", "a2", 4080), ("y", "w", 0), ("y", "w2", 16)]),
+          ("lmoe_matmul_bf16_wgrad", WGRAD_APART, [("dw", "dy", 0), ("dw2", "x", 0), ("dw2", "dw", 16), ("dw", "dy2", 0)])]
+
+
+@pytest.mark.parametrize("name,args,result,other,at", [
+    pytest.param(n, a, *c, id=f"{n[5:]}-{c[0]}-in-{c[1]}+{c[2]}") for n, a, cases in SHARED for c in cases])
+def test_results_that_share_memory_are_refused(lm, C, name, args, result, other, at):
+    n0 = lm.lmoe_kernel_launches()
+    assert call(C, name, args, **{result: args[other] + at}) == ARG
+    assert lm.lmoe_kernel_launches() == n0
+
+
 def test_no_shape_is_refused(C):
     for name, args in (("lmoe_gated_ffn", FFN), ("lmoe_gated_ffn_grad", FFN_GRAD), ("lmoe_matmul_bf16", MATMUL),
                        ("lmoe_matmul_bf16_wgrad", WGRAD)):

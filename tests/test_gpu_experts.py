@@ -97,6 +97,30 @@ def test_matmul_of_random_operands(lm, R, N, K, E, transposed, out):
     close(y, want, xu.rounded(want, tol, out))
 
 
+def test_no_rows(lm):
+    N, K, E = 64, 128, 3
+    e = lambda n: torch.empty(0, n, dtype=BF16, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    w, wt = ints((E, N, K), 1), ints((E, K, N), 2)
+    n0 = lm.lmoe_kernel_launches()
+    lm.lmoe_gated_ffn(e(K), w, w, e(N), e(N), e(N), offsets=off)
+    lm.lmoe_gated_ffn_grad(e(K), wt, e(N), e(N), e(N), e(N), offsets=off)
+    lm.lmoe_matmul_bf16(e(K), w, e(N), offsets=off)
+    lm.lmoe_matmul_bf16(e(K), wt, e(N), offsets=off, a2=e(K), w2=wt, transposed=True)
+    for dtype in (F32, BF16):
+        dw, dw2 = (torch.full((E, N, K), 3.0, dtype=dtype, device="cuda") for _ in range(2))
+        lm.lmoe_matmul_bf16_wgrad(e(N), e(K), dw, offsets=off, dy2=e(N), dw2=dw2, accumulate=True)
+        assert bool((dw == 3).all()) and bool((dw2 == 3).all())
+        lm.lmoe_matmul_bf16_wgrad(e(N), e(K), dw, offsets=off, dy2=e(N), dw2=dw2)
+        assert bool((dw == 0).all()) and bool((dw2 == 0).all())
+    assert lm.lmoe_kernel_launches() == n0
+    # rows, but none of an expert
+    a, y, dw = ints((50, K), 3), torch.full((50, N), 7.25, device="cuda"), torch.full((E, N, K), 3.0, device="cuda")
+    lm.lmoe_matmul_bf16(a, w, y, offsets=off)
+    lm.lmoe_matmul_bf16_wgrad(ints((50, N), 4), a, dw, offsets=off)
+    assert bool((y == 7.25).all()) and bool((dw == 0).all())
+
+
 def test_rows_of_no_expert_and_wild_offsets(lm):
     R, N, K = 300, 136, 264
     a, w = ints((R, K), 1), ints((3, N, K), 2)
