@@ -1010,12 +1010,17 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       }
     }
   }
-  // ---- teardown: all MMAs of this CTA have completed before the columns are released
-  if (warp == 1 && lane == 0)
+  // ---- teardown: all MMAs of this CTA have completed before the columns are released.  (A pair's second CTA, whose warp 1 has had
+  // nothing to do so far, waits once the first one is done: the arrival here is then under way.)
+  const bool issuer = !C::kPair || rank == 0;
+  if (issuer && warp == 1 && lane == 0)
     if (!mbar_wait(mma_done, 0, kDrain)) atomicOr(status, kErrDrain);
   tc_fence_before();
   if (C::kPair) cluster_sync();
   else __syncthreads();
+  if (!issuer && warp == 1) {
+    if (!warp_wait(mma_done, 0, kDrain) && lane == 0) atomicOr(status, kErrDrain);
+  }
   if (warp == 1) {
     tc_fence_after();
     if (C::kPair) tmem_dealloc_pair(tmem, C::kTmemCols);

@@ -428,6 +428,25 @@ def test_calls_without_a_status_word_report_too(lm):
     assert torch.equal(y.double(), a.double() @ w.double().t())
 
 
+def test_long_calls_are_no_timeouts(lm):
+    """Calls of tens of milliseconds: no wait of theirs may take the whole for its own."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("not enough memory")
+    assert lm.lmoe_bf16_check_status()[0] in (0, -6)
+    a, w = normal((1 << 18, 8192), 1), normal((8192, 8192), 2)
+    y = torch.zeros(1 << 18, 8192, dtype=BF16, device="cuda")
+    dw = torch.zeros(8192, 8192, device="cuda")
+    lm.lmoe_matmul_bf16(a, w, y)
+    lm.lmoe_matmul_bf16_wgrad(a, a, dw)
+    assert lm.lmoe_bf16_check_status() == (0, 0)
+    rows = torch.tensor([0, 77777, (1 << 18) - 1], device="cuda")
+    want, tol = xu.product(a[rows], w)
+    close(y[rows], want, xu.rounded(want, tol, BF16))
+    d = a[:, :16].double()
+    want, tol = d.t() @ a[:, :64].double(), (d.abs().t() @ a[:, :64].double().abs()) * 2.0 ** -23 * 768
+    close(dw[:16, :64], want, tol)
+
+
 def test_two_streams_at_once(lm):
     """Calls on two streams share nothing: each gives what it gives alone."""
     made = []
