@@ -98,12 +98,15 @@ struct Bf16Cfg {
   static constexpr int kBN = kPair ? 256 : 128;                   // accumulator columns
   static constexpr int kOutCols = MODE == kGated ? kBN / 2 : kBN;  // columns of a tile
   static constexpr int kEpiWarps = kPair && F32 ? 8 : 4;
+  // few rows: the one warp that has them leaves the sums in shared memory (in two buffers by turns), and all four finish them
+  static constexpr bool kFlat = UNIT == 32;
+  static constexpr int kLdFlat = 132;                             // floats of a row of 128 sums
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kABytes = kLanes * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
   // a warp's 32 rows of 128 bytes on their way out (kGatedGrad: of 64 bytes, and in, of gate and of up)
   static constexpr int kRow = MODE == kGatedGrad ? 64 : 128;
   static constexpr int kWarpBytes = 32 * kRow * (MODE == kGatedGrad ? 3 : 1);
-  static constexpr int kStagingBytes = kEpiWarps * kWarpBytes;
+  static constexpr int kStagingBytes = kFlat ? 2 * 32 * kLdFlat * 4 : kEpiWarps * kWarpBytes;
   // off[], and start[] (not kWgrad).  An fp32 kWgrad has room for a stage more than with all offsets: from kOffsets experts
   // on they are read where they are (read there always, 16 experts' weight gradients to bf16 took 195 us, so 181).
   static constexpr int kOffsets = F32 && MODE == kWgrad ? 320 : kMaxGroups + 4;
@@ -384,6 +387,34 @@ LMOE_DEV void finish4(const Bf16Args& a, void* out, long long at, float4 v, floa
       v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
     }
     store4(out, at, v, a.out_f32);
+  }
+}
+
+// Finishes rows [skip, live) of a tile from the sums of `parts` CTAs: four columns of a row to a thread, of 4 << shift from
+// column col0 on; row r of CTA q's sums is at red + (q rows + r) ld (kGated: up's behind gate's).
+struct Bf16Sums {
+  const float* red;
+  int parts, rows, ld, shift, col0;
+};
+template <int MODE>
+LMOE_DEV void finish_sums(const Bf16Args& a, const Bf16Sums& s, const Bf16Tile& t) {
+  const int width = MODE == kWgrad ? a.k : a.n;
+  void* out = MODE == kWgrad && t.second ? a.out2 : a.out;
+  const long long row0 = (MODE == kWgrad ? static_cast<long long>(t.e) * a.n : 0) + t.p0;
+  for (int i = threadIdx.x & 127; i < (t.live - t.skip) << s.shift; i += 128) {
+    const int r = t.skip + (i >> s.shift), c = (i & ((1 << s.shift) - 1)) * 4, col = s.col0 + c;
+    if (col >= width) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), v2 = v;
+    for (int q = 0; q < s.parts; ++q) {
+      const float* src = s.red + (q * s.rows + r) * s.ld + c;
+      const float4 o = *reinterpret_cast<const float4*>(src);
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+      if (MODE == kGated) {
+        const float4 p = *reinterpret_cast<const float4*>(src + (4 << s.shift));
+        v2 = make_float4(v2.x + p.x, v2.y + p.y, v2.z + p.z, v2.w + p.w);
+      }
+    }
+    finish4<MODE>(a, out, (row0 + r) * width + col, v, v2);
   }
 }
 
@@ -691,6 +722,36 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
   __syncwarp();
 }
 
+// Epilogue of tiles of few rows.  What a tile takes here is what bounds short reductions: a warp's own way (rows by tensor or
+// segment stores, gate and up of 32 columns at a time) took 5.8 us a tile for kGatedGrad.
+template <int MODE, int UNIT, bool F32>
+LMOE_DEV void epilogue_flat(const Bf16Args& args, const Bf16Walk& walk, const Bf16Ring& ring, float* sums, uint32_t tmem, int id0,
+                            int step) {
+  using C = Bf16Cfg<MODE, UNIT, F32>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kShift = C::kOutCols == 128 ? 5 : 4;   // fours of columns
+  int tc = 0, turn = 0;
+  for (int id = id0; id < walk.total; id += step, turn ^= 1) {
+    const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, 0);
+    float* buf = sums + turn * 32 * C::kLdFlat;
+    bool ok = true;
+    if (warp == 4) {
+      float acc[128];
+      const int chunks = F32 ? (t.blocks + kChunk - 1) / kChunk : 1;
+      ok = gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, 0, acc);
+      if (ok && lane >= t.skip && lane < t.live) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          *reinterpret_cast<float4*>(buf + lane * C::kLdFlat + 4 * i) =
+              make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+      }
+    }
+    // (a buffer is written again after the next tile's barrier, which all reach when they are done with it)
+    if (!named_barrier_all(1, 128, ok)) break;
+    finish_sums<MODE>(args, {buf, 1, 32, C::kLdFlat, kShift, t.q0}, t);
+  }
+}
+
 template <int MODE, int UNIT, bool F32>
 __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
     gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
@@ -723,7 +784,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], C::kEpiWarps * (C::kPair ? 2 : 1));
+      mbar_init(&acc_empty[b], C::kFlat ? 1 : C::kEpiWarps * (C::kPair ? 2 : 1));
     }
     mbar_init(mma_done, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&landed[i], 1);
@@ -949,8 +1010,12 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
   } else {
     if constexpr (C::kPair && F32) regs_inc<224>();
     if (C::kPair || S == 1) {
-      const Bf16Maps maps = {&tmO, &tmO2, &tmO3, &tmGate, &tmUp};
-      epilogue<MODE, UNIT, F32>(args, walk, ring, maps, staging, landed, tmem, id0, step, rank);
+      if constexpr (C::kFlat) {
+        epilogue_flat<MODE, UNIT, F32>(args, walk, ring, reinterpret_cast<float*>(staging), tmem, id0, step);
+      } else {
+        const Bf16Maps maps = {&tmO, &tmO2, &tmO3, &tmGate, &tmUp};
+        epilogue<MODE, UNIT, F32>(args, walk, ring, maps, staging, landed, tmem, id0, step, rank);
+      }
     }
   }
 
@@ -970,7 +1035,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
         t = tile_at<MODE, UNIT, F32>(walk, args, id0, rank);
         int tc = 0;
         const int n = t.kb1 - t.kb0, chunks = F32 ? (n + kChunk - 1) / kChunk : n > 0;
-        const bool ok = gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, warp & 3, acc);
+        const bool ok = C::kFlat && warp != 4 ? true : gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, warp & 3, acc);
         if (!ok || chunks == 0) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -987,27 +1052,8 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
         }
       }
       cluster_sync();
-      if (mine && !(MODE == kWgrad && args.accumulate && t.blocks == 0)) {
-        const float* red = reinterpret_cast<const float*>(smem);
-        const int ld = MODE == kWgrad ? args.k : args.n;
-        void* out = MODE == kWgrad && t.second ? args.out2 : args.out;
-        const long long row0 = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0;
-        for (int i = threadIdx.x & 127; i < (t.live - t.skip) << shift; i += 128) {
-          const int r = t.skip + (i >> shift), c = (i & ((1 << shift) - 1)) * 4, col = t.q0 + rank * part + c;
-          if (col >= ld) continue;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f), v2 = v;
-          for (int q = 0; q < S; ++q) {
-            const float* src = red + (q * rows + r) * width + c;
-            const float4 o = *reinterpret_cast<const float4*>(src);
-            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-            if (MODE == kGated) {
-              const float4 p = *reinterpret_cast<const float4*>(src + part);
-              v2 = make_float4(v2.x + p.x, v2.y + p.y, v2.z + p.z, v2.w + p.w);
-            }
-          }
-          finish4<MODE>(args, out, (row0 + r) * ld + col, v, v2);
-        }
-      }
+      if (mine && !(MODE == kWgrad && args.accumulate && t.blocks == 0))
+        finish_sums<MODE>(args, {reinterpret_cast<const float*>(smem), S, rows, width, shift, t.q0 + rank * part}, t);
     }
   }
   // ---- teardown: all MMAs of this CTA have completed before the columns are released.  (A pair's second CTA, whose warp 1 has had
@@ -1053,7 +1099,7 @@ cudaError_t launch_one(const CUtensorMap (&m)[9], Bf16Args a, cudaStream_t s) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int kSms = 152;
-constexpr int kFewRows = 16, kFewTiles = 8, kPairRows = 96, kPairTiles = 46;
+constexpr int kFewRows = 16, kFewTiles = 8, kPairRows = 48, kPairRowsF32 = 128, kPairTiles = 46;
 
 // [rows, cols] bf16, boxes of 64 columns (half: 32) by `high` rows; and [E, rows, cols]
 bool map_rows(CUtensorMap* m, const void* p, long long rows, int cols, int high, bool half = false) {
@@ -1173,7 +1219,7 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
     return 1LL * most_tiles(R, g.E, unit) * ((g.n + across - 1) / across);
   };
   const bool few = R / live <= kFewRows || tiles_of(128) <= kFewTiles;
-  const int unit = few ? 32 : R / live < kPairRows || tiles_of(256) < kPairTiles ? 128 : 256;
+  const int unit = few ? 32 : R / live < (F32 ? kPairRowsF32 : kPairRows) || tiles_of(256) < kPairTiles ? 128 : 256;
   g.box = R < unit ? R : unit;
   if (unit < 256) g.splits = splits_for(tiles_of(unit), g.num_kb * g.pairs, MODE == kGatedGrad ? 8 : few ? 24 : 48);
   constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
@@ -1191,7 +1237,7 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
         (g.out3 != nullptr && !map_rows(&m[6], g.out3, R, g.n * es, 32)))
       return LMOE_ERR_CUDA;
   }
-  if (MODE == kGatedGrad && (!map_rows(&m[7], g.gate, R, g.n, 32, true) || !map_rows(&m[8], g.up, R, g.n, 32, true)))
+  if (MODE == kGatedGrad && unit > 32 && (!map_rows(&m[7], g.gate, R, g.n, 32, true) || !map_rows(&m[8], g.up, R, g.n, 32, true)))
     return LMOE_ERR_CUDA;
   if ((a2 != nullptr && !map_rows(&m[1], a2, R, g.k, rows)) || (w2 != nullptr && !map_weights(&m[3], w2, g.E, wr, wc, high)))
     return LMOE_ERR_CUDA;

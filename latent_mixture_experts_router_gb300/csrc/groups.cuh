@@ -34,6 +34,21 @@ LMOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, long long budget) {
   return __all_sync(~0u, mbar_wait(bar, parity, budget));
 }
 
+LMOE_DEV void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The same barrier, with whether every thread's `ok` is set.
+LMOE_DEV bool named_barrier_all(int id, int threads, bool ok) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<int>(ok))
+      : "memory");
+  return r != 0;
+}
+
 LMOE_DEV void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
                                uint64_t policy) {
   asm volatile(
