@@ -118,7 +118,7 @@ struct Bf16Cfg {
   static constexpr uint32_t kTmemCols = 2 * kBN;
   // A pair's last tile of an expert, with no more than 128 rows: an MMA of 128 rows (64 of each CTA) takes half the time.
   // Its sums lie with their first 128 columns in lanes 0..63 and the others in lanes 64..127.
-  static constexpr bool kShort = kPair && !F32 && MODE != kWgrad;
+  static constexpr bool kShort = kPair && MODE != kWgrad;
   static constexpr int kChunkBlocks = F32 ? kChunk : 1 << 30;
   static_assert((3 * kStages + 2 * 2 + 1 + 4) * 8 + 8 <= 512, "barriers");
   // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
@@ -527,16 +527,17 @@ struct Bf16Ring {
     if (lane == 0) mbar_arrive_cluster(acc_empty + (tc & 1) * 8);
   }
 };
-// The sums of a tile over all its chunks, 128 columns of this thread's lane from column c0 on, in registers; false if a
-// wait gave up.
+// The sums of a tile over all its chunks, `cols` (128 or 64) columns of this thread's lane from column c0 on, in registers;
+// false if a wait gave up.
 template <int BN>
-LMOE_DEV bool gather_sums(const Bf16Ring& ring, uint32_t tmem, int c0, int chunks, int& tc, int lane, int quad,
+LMOE_DEV bool gather_sums(const Bf16Ring& ring, uint32_t tmem, int c0, int cols, int chunks, int& tc, int lane, int quad,
                           float (&acc)[128]) {
   for (int ch = 0; ch < chunks; ++ch, ++tc) {
     if (!ring.wait(tc)) return false;
     const uint32_t tq = tmem + (tc & 1) * BN + c0 + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      if (c * 32 >= cols) break;
       uint32_t v[32];
       tmem_ld_32cols(tq + c * 32, v);
       tmem_ld_wait();
@@ -608,11 +609,11 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
     if constexpr (F32) {
       float acc[128];
       const int chunks = (blocks + C::kChunkBlocks - 1) / C::kChunkBlocks;
-      if (!gather_sums<C::kBN>(ring, tmem, half * kCols, chunks, tc, lane, quad, acc)) break;
+      if (!gather_sums<C::kBN>(ring, tmem, half * cols, cols, chunks, tc, lane, quad, acc)) break;
       if (!any) continue;
 #pragma unroll
       for (int c = 0; c < kCols; c += 32) {
-        if (q0 + c >= width) break;
+        if (c >= cols || q0 + c >= width) break;
         const uint32_t* w = reinterpret_cast<const uint32_t*>(acc + c);
         if (MODE == kWgrad && args.accumulate) emit_added(o, out, width, q0 + c, true, w);
         else emit<MODE, C::kRow>(o, map, out, (q0 + c) * 4, w);
@@ -738,7 +739,7 @@ LMOE_DEV void epilogue_flat(const Bf16Args& args, const Bf16Walk& walk, const Bf
     if (warp == 4) {
       float acc[128];
       const int chunks = F32 ? (t.blocks + kChunk - 1) / kChunk : 1;
-      ok = gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, 0, acc);
+      ok = gather_sums<C::kBN>(ring, tmem, 0, 128, chunks, tc, lane, 0, acc);
       if (ok && lane >= t.skip && lane < t.live) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -1035,7 +1036,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
         t = tile_at<MODE, UNIT, F32>(walk, args, id0, rank);
         int tc = 0;
         const int n = t.kb1 - t.kb0, chunks = F32 ? (n + kChunk - 1) / kChunk : n > 0;
-        const bool ok = C::kFlat && warp != 4 ? true : gather_sums<C::kBN>(ring, tmem, 0, chunks, tc, lane, warp & 3, acc);
+        const bool ok = C::kFlat && warp != 4 ? true : gather_sums<C::kBN>(ring, tmem, 0, 128, chunks, tc, lane, warp & 3, acc);
         if (!ok || chunks == 0) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -1099,7 +1100,7 @@ cudaError_t launch_one(const CUtensorMap (&m)[9], Bf16Args a, cudaStream_t s) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int kSms = 152;
-constexpr int kFewRows = 16, kFewTiles = 8, kPairRows = 48, kPairRowsF32 = 128, kPairTiles = 46;
+constexpr int kFewRows = 16, kFewTiles = 8, kPairRows = 96, kPairTiles = 46;
 
 // [rows, cols] bf16, boxes of 64 columns (half: 32) by `high` rows; and [E, rows, cols]
 bool map_rows(CUtensorMap* m, const void* p, long long rows, int cols, int high, bool half = false) {
@@ -1196,16 +1197,18 @@ int splits_for(long long tiles, long long blocks, int from) {
 // One of the modes that take rows of a: which tile, and the launch.  A pair is (a, w).
 //
 // Tiles of 32 rows up to kFewRows rows per expert on average, or where kFewTiles tiles of 128 rows or fewer would leave most
-// SMs idle; of 256 rows from kPairRows rows per expert and kPairTiles tiles on; else of 128.  Measured in us, 32 / 128 / 256
-// rows each:
-//   64 experts of 4096 x 4096, even splits   8 rows   318 / 326 / 333      64 rows    382 / 337 / 343
-//                                            16       320 / 328 / 335      96         614 / 342 / 348
-//                                            32       325 / 330 / 338      128        779 / 345 / 353
-//                                            48       381 / 335 / 341      160        920 / 483 / 376
-//   (by the average: with uneven splits, which the device alone knows, half the experts have more rows)
-//   one matrix of 4096 x 4096                128      17 / 17 / 18         512        50 / 22 / 25
-//                                            256      28 / 19 / 24         1024       83 / 37 / 26
-//   one of 1024 x 4096                       128      11 / 16 / 17         1024       28 / 19 / 24
+// SMs idle; of 256 rows from kPairTiles of them and kPairRows rows per expert on, or for fewer rows where the weights' rows are
+// no multiple of 128 bytes (a box then takes two lines for each of its rows, and the pair takes fewer boxes in); else of
+// 128.  Measured in us, 32 / 128 / 256 rows each:
+//   64 experts of 4096 x 4096, even splits     8 rows   318 / 326 / 333      64 rows    382 / 337 / 343
+//                                              16       320 / 328 / 335      128        779 / 345 / 353
+//                                              32       325 / 330 / 338      160        920 / 483 / 376
+//   uneven splits, by the average              16       322 / 330 / 335      64         464 / 345 / 346
+//                                              32       333 / 333 / 339      96         666 / 370 / 354
+//   20 experts of 6768 x 7800, uneven          20       381 / 531 / 401      80         897 / 598 / 428
+//   one matrix of 4096 x 4096                  128      17 / 17 / 18         512        50 / 22 / 25
+//                                              256      28 / 19 / 24         1024       83 / 37 / 26
+//   one of 1024 x 4096                         128      11 / 16 / 17         1024       28 / 19 / 24
 // A cluster shares the reduction where tiles are few, from 24 blocks on for 32 rows, 48 for 128 and for weight gradients, 8 for
 // kGatedGrad (whose tiles a cluster finishes with more threads).  Shared and not: one row of 4096 x 4096 10.0 and 19 us, 16
 // rows of 2048 x 2048 8.5 and 10.7, of 1024 x 1024 8.4 and 8.1; 100 rows of 2048 x 4096 13.2 and 15.4, of 2048 x 2048 11.8 and 11.0;
@@ -1219,11 +1222,13 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
     return 1LL * most_tiles(R, g.E, unit) * ((g.n + across - 1) / across);
   };
   const bool few = R / live <= kFewRows || tiles_of(128) <= kFewTiles;
-  const int unit = few ? 32 : R / live < (F32 ? kPairRowsF32 : kPairRows) || tiles_of(256) < kPairTiles ? 128 : 256;
+  constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
+  const int wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;   // a weight's rows and columns
+  const bool pair = tiles_of(256) >= kPairTiles && (wc % 64 != 0 || R / live >= kPairRows);
+  const int unit = few ? 32 : pair ? 256 : 128;
   g.box = R < unit ? R : unit;
   if (unit < 256) g.splits = splits_for(tiles_of(unit), g.num_kb * g.pairs, MODE == kGatedGrad ? 8 : few ? 24 : 48);
-  constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
-  const int high = mn || MODE == kGated ? 64 : 128, wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;
+  const int high = mn || MODE == kGated ? 64 : 128;
   const int rows = unit == 256 ? 64 : g.box;
   CUtensorMap m[9];
   if (!map_rows(&m[0], a, R, g.k, rows) || !map_weights(&m[2], w, g.E, wr, wc, high)) return LMOE_ERR_CUDA;
