@@ -1194,12 +1194,21 @@ int splits_for(long long tiles, long long blocks, int from) {
   while (s < 8 && blocks >= from && tiles * s * 2 <= kSms && blocks / (s * 2) >= 4 && tiles <= most_clusters(s * 2)) s *= 2;
   return s;
 }
+// Cycles, about, of tiles of 256 rows (in a pair a block of 64 takes 600, or 430 if none of them has more than 128 rows) and of 128
+// (575, shared by s CTAs), by their waves over the SMs; a pair takes 3000 longer to start and end, a cluster 5000.  (2811 rows of
+// 1000 x 8184: 60 us by pairs, 115 by tiles of 128 rows; 32 of 8192 x 1024 12.8 and 8.5.)
+long long pair_cycles(long long tiles, long long blocks, bool brief) {
+  return (tiles + kSms / 2 - 1) / (kSms / 2) * blocks * (brief ? 430 : 600) + 3000;
+}
+long long one_cycles(long long tiles, long long blocks, int s) {
+  return (tiles * s + kSms - 1) / kSms * blocks * 575 / s + (s > 1 ? 5000 : 0);
+}
 // One of the modes that take rows of a: which tile, and the launch.  A pair is (a, w).
 //
 // Tiles of 32 rows up to kFewRows rows per expert on average, or where kFewTiles tiles of 128 rows or fewer would leave most
 // SMs idle; of 256 rows from kPairTiles of them and kPairRows rows per expert on, or for fewer rows where the weights' rows are
 // no multiple of 128 bytes (a box then takes two lines for each of its rows, and the pair takes fewer boxes in); else of
-// 128.  Measured in us, 32 / 128 / 256 rows each:
+// 128.  One matrix, whose tiles are known: of 256 or 128 rows by the cycles they take.  Measured in us, 32 / 128 / 256 rows each:
 //   64 experts of 4096 x 4096, even splits     8 rows   318 / 326 / 333      64 rows    382 / 337 / 343
 //                                              16       320 / 328 / 335      128        779 / 345 / 353
 //                                              32       325 / 330 / 338      160        920 / 483 / 376
@@ -1224,10 +1233,13 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
   const bool few = R / live <= kFewRows || tiles_of(128) <= kFewTiles;
   constexpr bool mn = MODE == kGatedGrad || MODE == kProductT;
   const int wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;   // a weight's rows and columns
-  const bool pair = tiles_of(256) >= kPairTiles && (wc % 64 != 0 || R / live >= kPairRows);
+  const long long blocks = g.num_kb * g.pairs;
+  const int from = MODE == kGatedGrad ? 8 : few ? 24 : 48, shared = splits_for(tiles_of(few ? 32 : 128), blocks, from);
+  const bool pair = g.E == 1 ? pair_cycles(tiles_of(256), blocks, R <= 128) < one_cycles(tiles_of(128), blocks, shared)
+                             : tiles_of(256) >= kPairTiles && (wc % 64 != 0 || R / live >= kPairRows);
   const int unit = few ? 32 : pair ? 256 : 128;
   g.box = R < unit ? R : unit;
-  if (unit < 256) g.splits = splits_for(tiles_of(unit), g.num_kb * g.pairs, MODE == kGatedGrad ? 8 : few ? 24 : 48);
+  if (unit < 256) g.splits = shared;
   const int high = mn || MODE == kGated ? 64 : 128;
   const int rows = unit == 256 ? 64 : g.box;
   CUtensorMap m[9];
@@ -1360,8 +1372,13 @@ extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const v
   if (!apart<7>({{dw, wb}, {dw2, wb}, {dy, rn}, {dy2, rn}, {x, 2LL * c->rows * c->K}, {offsets, o}, {status, 4}}, 2)) return LMOE_ERR_ARG;
   CUtensorMap m[9];
   const int es = g.out_f32 ? 2 : 1;   // (in 16-bit columns)
-  const bool pair = 1LL * ((c->N + 255) / 256) * ((c->K + 255) / 256) * c->n_experts * g.pairs >= kPairTiles;
-  if (!pair) g.splits = splits_for(tiles, c->rows / c->n_experts / kBK, 48);
+  const long long wide = 1LL * ((c->N + 255) / 256) * ((c->K + 255) / 256) * c->n_experts * g.pairs;
+  const long long blocks = c->rows / c->n_experts / kBK + 1;
+  const int shared = splits_for(tiles, blocks, 48);
+  // (a tile's store takes as long as some 8 blocks; an expert of one row, 4096 x 4096: 21.0 us by pairs, 28.8 without this)
+  const long long least = blocks > 8 ? blocks : 8;
+  const bool pair = pair_cycles(wide, least, false) < one_cycles(tiles, least, shared);
+  if (!pair) g.splits = shared;
   g.whole = !g.accumulate && g.splits == 1;
   if (!map_rows(&m[0], dy, c->rows, c->N, kBK) || !map_rows(&m[2], x, c->rows, c->K, kBK) ||
       !map_weights(&m[4], dw, g.E, g.n, g.k * es, 32))
