@@ -7,14 +7,17 @@ it fails loudly (there is no fallback path).
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import functools
-import operator
 import os
 from dataclasses import dataclass
 
 import torch
+
+try:
+    from . import _tensors   # csrc/tensors.cpp
+except ImportError as e:
+    raise ImportError(f"{e}; run latent_mixture_experts_router_gb300.build.build()") from None
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblatent_moe.so")
@@ -646,14 +649,19 @@ def lmoe_matmul_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accu
 
 
 # ------------------------------------------------------------------ training the experts in bf16
-# (Small calls are bound by what happens here: a tensor that fits is passed over in one expression, and
-# _want says what is wrong with one that does not; shapes are kept as the library takes them.)
+# (Small calls are bound by what happens here: a tensor that fits is passed over in one native call, and _want says
+# what is wrong with one that does not; shapes are kept as the library takes them.)
 _BF16 = torch.bfloat16
+_bf16_at = _tensors.bf16_at
 
 
 def _bf16(t, name, shape, device):
-    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != device or not t.is_contiguous() or device < 0:
+    """The address of ``t``, contiguous bf16 of ``shape`` on device number ``device``."""
+    at = _bf16_at(t, shape, device)
+    if at < 0:
         _want(t, name, _BF16, shape, device)
+        raise ValueError(f"{name}: not a plain CUDA tensor")
+    return at
 
 
 @functools.lru_cache(maxsize=1024)
@@ -697,20 +705,18 @@ def lmoe_gated_ffn(x, w_gate, w_up, h, gate=None, up=None, offsets=None, status=
     wait that gives up; None: the device's own word (lmoe_bf16_check_status)."""
     N, K, E = _weight_of(w_gate, "w_gate", "[N, K] or [E, N, K]")
     rows, dev = _rows_of(x, "x", "[rows, K]")[0], x.get_device()
-    _bf16(x, "x", (rows, K), dev)
-    _bf16(w_gate, "w_gate", w_gate.shape, dev)
-    _bf16(w_up, "w_up", w_gate.shape, dev)
+    xp = _bf16(x, "x", (rows, K), dev)
+    wg = _bf16(w_gate, "w_gate", w_gate.shape, dev)
+    wu = _bf16(w_up, "w_up", w_gate.shape, dev)
     out = (rows, N)
-    _bf16(h, "h", out, dev)
+    hp = _bf16(h, "h", out, dev)
     g = u = None
     if gate is not None or up is not None:
         _need(gate is not None and up is not None, "gate and up: both or neither")
-        _bf16(gate, "gate", out, dev)
-        _bf16(up, "up", out, dev)
-        g, u = gate.data_ptr(), up.data_ptr()
+        g, u = _bf16(gate, "gate", out, dev), _bf16(up, "up", out, dev)
     off, st = _bf16_extra(offsets, status, E, dev)
-    _call(_lib().lmoe_gated_ffn, "lmoe_gated_ffn", dev, stream, _bf16_shape(rows, N, K, E, LMOE_BF16, 0, 0), x.data_ptr(),
-          w_gate.data_ptr(), w_up.data_ptr(), off, h.data_ptr(), g, u, st)
+    _call(_lib().lmoe_gated_ffn, "lmoe_gated_ffn", dev, stream, _bf16_shape(rows, N, K, E, LMOE_BF16, 0, 0), xp, wg, wu, off,
+          hp, g, u, st)
 
 
 def lmoe_gated_ffn_grad(dy, w_down, gate, up, dgate, dup, offsets=None, status=None, stream=None):
@@ -719,16 +725,13 @@ def lmoe_gated_ffn_grad(dy, w_down, gate, up, dgate, dup, offsets=None, status=N
     bf16.  ``offsets``, ``status`` as in lmoe_gated_ffn."""
     K, N, E = _weight_of(w_down, "w_down", "[K, N] or [E, K, N]")
     rows, dev = _rows_of(dy, "dy", "[rows, K]")[0], dy.get_device()
-    _bf16(dy, "dy", (rows, K), dev)
-    _bf16(w_down, "w_down", w_down.shape, dev)
     out = (rows, N)
-    _bf16(gate, "gate", out, dev)
-    _bf16(up, "up", out, dev)
-    _bf16(dgate, "dgate", out, dev)
-    _bf16(dup, "dup", out, dev)
+    dyp, wd = _bf16(dy, "dy", (rows, K), dev), _bf16(w_down, "w_down", w_down.shape, dev)
+    g, u = _bf16(gate, "gate", out, dev), _bf16(up, "up", out, dev)
+    dg, du = _bf16(dgate, "dgate", out, dev), _bf16(dup, "dup", out, dev)
     off, st = _bf16_extra(offsets, status, E, dev)
-    _call(_lib().lmoe_gated_ffn_grad, "lmoe_gated_ffn_grad", dev, stream, _bf16_shape(rows, N, K, E, LMOE_BF16, 0, 0),
-          dy.data_ptr(), w_down.data_ptr(), gate.data_ptr(), up.data_ptr(), off, dgate.data_ptr(), dup.data_ptr(), st)
+    _call(_lib().lmoe_gated_ffn_grad, "lmoe_gated_ffn_grad", dev, stream, _bf16_shape(rows, N, K, E, LMOE_BF16, 0, 0), dyp, wd,
+          g, u, off, dg, du, st)
 
 
 def lmoe_matmul_bf16(a, w, out, offsets=None, a2=None, w2=None, transposed=False, status=None, stream=None):
@@ -739,19 +742,15 @@ def lmoe_matmul_bf16(a, w, out, offsets=None, a2=None, w2=None, transposed=False
     if transposed:
         N, K = K, N
     rows, dev = _rows_of(a, "a", "[rows, K]")[0], a.get_device()
-    _bf16(a, "a", (rows, K), dev)
-    _bf16(w, "w", w.shape, dev)
+    ap, wp = _bf16(a, "a", (rows, K), dev), _bf16(w, "w", w.shape, dev)
     _want(out, "out", _DENSE, (rows, N), dev)
     p2 = q2 = None
     if a2 is not None or w2 is not None:
         _need(a2 is not None and w2 is not None, "a2 and w2: both or neither")
-        _bf16(a2, "a2", (rows, K), dev)
-        _bf16(w2, "w2", w.shape, dev)
-        p2, q2 = a2.data_ptr(), w2.data_ptr()
+        p2, q2 = _bf16(a2, "a2", (rows, K), dev), _bf16(w2, "w2", w.shape, dev)
     off, st = _bf16_extra(offsets, status, E, dev)
     _call(_lib().lmoe_matmul_bf16, "lmoe_matmul_bf16", dev, stream,
-          _bf16_shape(rows, N, K, E, _DENSE[out.dtype], 1 if transposed else 0, 0), a.data_ptr(), w.data_ptr(), p2, q2, off,
-          out.data_ptr(), st)
+          _bf16_shape(rows, N, K, E, _DENSE[out.dtype], 1 if transposed else 0, 0), ap, wp, p2, q2, off, out.data_ptr(), st)
 
 
 def lmoe_matmul_bf16_wgrad(dy, x, dw, offsets=None, dy2=None, dw2=None, accumulate=False, status=None, stream=None):
@@ -760,19 +759,17 @@ def lmoe_matmul_bf16_wgrad(dy, x, dw, offsets=None, dy2=None, dw2=None, accumula
     ``offsets``, ``status`` as in lmoe_gated_ffn."""
     N, K, E = _weight_of(dw, "dw", "[N, K] or [E, N, K]")
     rows, dev = _rows_of(dy, "dy", "[rows, N]")[0], dy.get_device()
-    _bf16(dy, "dy", (rows, N), dev)
-    _bf16(x, "x", (rows, K), dev)
+    dyp, xp = _bf16(dy, "dy", (rows, N), dev), _bf16(x, "x", (rows, K), dev)
     _want(dw, "dw", _DENSE, dw.shape, dev)
     p2 = q2 = None
     if dy2 is not None or dw2 is not None:
         _need(dy2 is not None and dw2 is not None, "dy2 and dw2: both or neither")
-        _bf16(dy2, "dy2", (rows, N), dev)
+        p2 = _bf16(dy2, "dy2", (rows, N), dev)
         _want(dw2, "dw2", dw.dtype, dw.shape, dev)
-        p2, q2 = dy2.data_ptr(), dw2.data_ptr()
+        q2 = dw2.data_ptr()
     off, st = _bf16_extra(offsets, status, E, dev)
     _call(_lib().lmoe_matmul_bf16_wgrad, "lmoe_matmul_bf16_wgrad", dev, stream,
-          _bf16_shape(rows, N, K, E, _DENSE[dw.dtype], 0, 1 if accumulate else 0), dy.data_ptr(), x.data_ptr(), p2, off,
-          dw.data_ptr(), q2, st)
+          _bf16_shape(rows, N, K, E, _DENSE[dw.dtype], 0, 1 if accumulate else 0), dyp, xp, p2, off, dw.data_ptr(), q2, st)
 
 
 def lmoe_bf16_check_status(device=None, stream=None) -> tuple[int, int]:
@@ -795,48 +792,21 @@ def lmoe_grad_norm_workspace_size(count: int) -> int:
     return n.value
 
 
-_T = torch.Tensor
-
-
-_dtype_of = operator.attrgetter("dtype")
-
-
-def _grad_list(ts, name, device):
-    """(addresses, sizes, dtypes) of a list of contiguous CUDA tensors on one device, fp32 or bf16."""
-    # (maps over whole lists: a call with hundreds of tensors is bound by this)
-    _need(set(map(_T.get_device, ts)) <= {device}, f"{name}: all tensors must be on cuda:{device}")
-    _need(False not in map(_T.is_contiguous, ts), f"{name}: tensors must be contiguous")
-    dtypes = list(map(_dtype_of, ts))
-    found = set(dtypes)
-    _need(found <= _DENSE.keys(), f"{name}: tensors must be float32 or bfloat16")
-    kinds = array.array("i", [_DENSE[found.pop()]]) * len(dtypes) if len(found) == 1 else \
-        array.array("i", [LMOE_BF16 if d is _BF16 else LMOE_F32 for d in dtypes])
-    return array.array("Q", map(_T.data_ptr, ts)), array.array("q", map(_T.numel, ts)), kinds
-
-
-def _grad_device(norm):
+def _grad_args(grads, norm):
+    """The device of ``norm``, and of the tensors ``grads`` (any iterable of contiguous fp32 or bf16 tensors on it) the addresses,
+    sizes and dtypes, packed, and their number."""
     dev = norm.get_device()
     _want(norm, "norm", torch.float32, (1,), dev)
-    return dev
-
-
-def _grad_args(grads, norm):
-    dev = _grad_device(norm)
-    return dev, *_grad_list(list(grads), "grads", dev)   # (any iterable, gone through several times)
+    return dev, *_tensors.gradients(grads, "grads", dev)
 
 
 def _grad_out(out, dev, ptrs, sizes, kinds):
     if out is None:
         return ptrs
-    out = list(out)
-    _need(len(out) == len(ptrs), "out: as many tensors as grads")
-    optrs, osizes, okinds = _grad_list(out, "out", dev)
+    optrs, osizes, okinds, count = _tensors.gradients(out, "out", dev)
+    _need(count * 8 == len(ptrs), "out: as many tensors as grads")
     _need(osizes == sizes and okinds == kinds, "out: sizes and dtypes of grads")
     return optrs
-
-
-def _at(a):
-    return a.buffer_info()[0]
 
 
 def _workspace(workspace, dev):
@@ -847,23 +817,23 @@ def _workspace(workspace, dev):
 def lmoe_grad_norm(grads, norm, workspace, stream=None):
     """``norm`` [1] (fp32) = the 2-norm over all elements of the tensors ``grads`` (contiguous, fp32 or bf16, any
     sizes).  ``workspace``: at least lmoe_grad_norm_workspace_size(len(grads)) bytes."""
-    dev, ptrs, sizes, kinds = _grad_args(grads, norm)
-    _call(_lib().lmoe_grad_norm, "lmoe_grad_norm", dev, stream, _at(ptrs), _at(sizes), _at(kinds), len(ptrs),
+    dev, ptrs, sizes, kinds, count = _grad_args(grads, norm)
+    _call(_lib().lmoe_grad_norm, "lmoe_grad_norm", dev, stream, ptrs, sizes, kinds, count,
           norm.data_ptr(), *_workspace(workspace, dev))
 
 
 def lmoe_grad_clip(grads, norm, max_norm, out=None, stream=None):
     """``out`` (None: ``grads`` themselves) = ``grads`` times min(1, max_norm / (norm + 1e-6)), with a ``norm`` [1]
     (fp32, on the device) that is there."""
-    dev, ptrs, sizes, kinds = _grad_args(grads, norm)
+    dev, ptrs, sizes, kinds, count = _grad_args(grads, norm)
     optrs = _grad_out(out, dev, ptrs, sizes, kinds)
-    _call(_lib().lmoe_grad_clip, "lmoe_grad_clip", dev, stream, _at(ptrs), _at(optrs), _at(sizes), _at(kinds), len(ptrs),
-          norm.data_ptr(), float(max_norm))
+    _call(_lib().lmoe_grad_clip, "lmoe_grad_clip", dev, stream, ptrs, optrs, sizes, kinds, count, norm.data_ptr(),
+          float(max_norm))
 
 
 def lmoe_clip_grad_norm(grads, norm, max_norm, workspace, out=None, stream=None):
     """lmoe_grad_norm and lmoe_grad_clip in one call."""
-    dev, ptrs, sizes, kinds = _grad_args(grads, norm)
+    dev, ptrs, sizes, kinds, count = _grad_args(grads, norm)
     optrs = _grad_out(out, dev, ptrs, sizes, kinds)
-    _call(_lib().lmoe_clip_grad_norm, "lmoe_clip_grad_norm", dev, stream, _at(ptrs), _at(optrs), _at(sizes), _at(kinds),
-          len(ptrs), norm.data_ptr(), float(max_norm), *_workspace(workspace, dev))
+    _call(_lib().lmoe_clip_grad_norm, "lmoe_clip_grad_norm", dev, stream, ptrs, optrs, sizes, kinds, count,
+          norm.data_ptr(), float(max_norm), *_workspace(workspace, dev))

@@ -4,6 +4,9 @@ Each translation unit compiles in its own nvcc process, in parallel; objects go
 to ``_build/`` next to this file.  A unit is recompiled when it or any header
 under csrc/ or include/ is newer than its object.
 
+The binding's extension _tensors.so (csrc/tensors.cpp, torch's and Python's headers, no CUDA) is compiled beside them by
+the host compiler.
+
 ``build(checked=True)`` makes the checked variant liblatent_moe_checked.so (objects
 in ``_build_checked/``): the same sources with -DLMOE_BOUNDS_CHECKS=1, whose forward
 validates the routing structures before any kernel indexes with them.  It is off by
@@ -13,15 +16,18 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblatent_moe.so")
+LIB_TENSORS = os.path.join(PKG, "_tensors.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "liblatent_moe_checked.so")
 
@@ -45,6 +51,15 @@ def _cuda_lib_dirs():
         if os.path.isdir(d):
             dirs.append("-L" + d)
     return dirs
+
+
+def _tensors_cmd(src: str) -> list:
+    """The host compiler's command for the binding's extension (torch is found, not imported)."""
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"],
+            "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), src, "-L" + lib, "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-o", LIB_TENSORS]
 
 
 def _newer(src: str, obj: str, deps) -> bool:
@@ -72,6 +87,10 @@ def build(verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
         if _newer(s, obj, deps):
             jobs.append([nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", obj])
     objs = [os.path.join(BUILD, os.path.basename(s) + ".o") for s in srcs]
+    link = bool(jobs)
+    tensors = os.path.join(CSRC, "tensors.cpp")
+    if not checked and _newer(tensors, LIB_TENSORS, ()):
+        jobs.insert(0, _tensors_cmd(tensors))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -82,8 +101,8 @@ def build(verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {cmd[-3]}")
-    if jobs or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
+                raise RuntimeError(f"{cmd[0]} failed on {cmd[-3] if cmd[0] == nvcc else tensors}")
+    if link or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, *_cuda_lib_dirs(), "-lcudart"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:

@@ -222,3 +222,32 @@ def test_binding_refuses_what_does_not_fit(lm, i):
     match, fn = cases[i]
     with pytest.raises(ValueError, match=match):
         fn()
+
+
+def test_lists_of_gradients_that_do_not_fit(lm):
+    from latent_mixture_experts_router_gb300._lib import _tensors
+    t = torch.zeros(4)
+    for grads, match in (([t], "g: all tensors must be on cuda:0"), ([t, 1], "g: all tensors must be on cuda:0"),
+                         ([None, t], "g: element 0 is not a tensor"), (iter(["t"]), "g: element 0 is not a tensor")):
+        with pytest.raises(ValueError, match=match):
+            _tensors.gradients(grads, "g", 0)
+    for grads in (None, 3):
+        with pytest.raises(TypeError):
+            _tensors.gradients(grads, "g", 0)
+
+    def broken():
+        yield t
+        raise KeyError("its own")
+    with pytest.raises(KeyError, match="its own"):
+        _tensors.gradients(broken(), "g", 0)
+    assert _tensors.gradients([], "g", 0) == (b"", b"", b"", 0)
+
+
+def test_addresses_of_what_does_not_fit(lm):
+    from latent_mixture_experts_router_gb300._lib import _tensors
+    t = torch.zeros(2, 8, dtype=torch.bfloat16)
+    for x in (t, None, 1, t.to_sparse(), torch.empty(2, 8, dtype=torch.bfloat16, device="meta")):
+        assert _tensors.bf16_at(x, (2, 8), 0) == -1
+    for args in ((t, [2, 8], 0), (t, (2, 8)), (t, (2, 8), "0")):
+        with pytest.raises(TypeError):
+            _tensors.bf16_at(*args)

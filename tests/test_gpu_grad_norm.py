@@ -163,6 +163,31 @@ def test_any_iterable_of_tensors(lm):
         close(o, v, tol)
 
 
+def test_lists_that_do_not_fit(lm):
+    g, norm, ws = torch.ones(64, device="cuda"), torch.ones(1, device="cuda"), workspace(lm, 3)
+    out = torch.zeros(64, device="cuda")
+
+    class Mine(torch.Tensor):
+        pass
+    for grads, match in (([g, g.cpu()], "grads: all tensors must be on cuda:0"), ([g, g[::2]], "grads: tensors must be contiguous"),
+                         ([g.half()], "grads: tensors must be float32 or bfloat16"), ([g, None], "grads: element 1 is not a tensor"),
+                         ([g.to_sparse()], "grads: tensors must be contiguous")):
+        for call in (lambda: lm.lmoe_grad_norm(grads, norm, ws), lambda: lm.lmoe_grad_clip(grads, norm, 0.5),
+                     lambda: lm.lmoe_clip_grad_norm(grads, norm, 0.5, ws)):
+            with pytest.raises(ValueError, match=match):
+                call()
+    for o, match in (([out, out], "out: as many"), ([], "out: as many"), ([out[:32]], "out: sizes"), ([out.bfloat16()], "out: sizes"),
+                     ([out.cpu()], "out: all tensors")):
+        with pytest.raises(ValueError, match=match):
+            lm.lmoe_clip_grad_norm([g], norm, 0.5, ws, out=o)
+    assert bool((g == 1).all()) and bool((norm == 1).all()) and bool((out == 0).all())
+    grads = [torch.nn.Parameter(g.clone()), g.clone().as_subclass(Mine), g.clone().reshape(8, 8).t().contiguous()]
+    lm.lmoe_clip_grad_norm(grads, norm, 1.0, ws)
+    v, tol = xu.clipped(g, norm, 1.0)
+    for t in grads:
+        close(t.detach().as_subclass(torch.Tensor).reshape(-1), v, tol)
+
+
 def test_overlapping_outputs_are_refused(lm):
     flat = torch.ones(1000, device="cuda")
     norm, ws = torch.ones(1, device="cuda"), workspace(lm, 3)
