@@ -36,9 +36,9 @@
 // through its own shared memory and leave by tensor stores; where they are not all the tile's, by stores of whole segments.
 //
 // Measured (other inputs in each call, power-limited at 1.6 to 1.7 GHz where it is tensor-bound): 32768 uneven rows over 64 experts
-// of 4096 x 4096, g and u stored, 1790 us; the gradient of 16384 over 32 475 us; dx of 16384 over 32, two pairs, 917 us;
+// of 4096 x 4096, g and u stored, 1790 to 1900 us; the gradient of 16384 over 32 480 us; dx of 16384 over 32, two pairs, 920 us;
 // 16384 x 8192 x 8192 1100 us (2.0 PFLOP/s) cold, 1270 sustained; two weight gradients of 8192 rows over 16 to fp32 525 us
-// (4.5 TB/s); one token on 8 of 64 experts, gate and up, 79 us, 1024 rows over 64 experts 320 us (6.8 TB/s).  Tensor pipe busy 88 to
+// (4.5 TB/s); one token on 8 of 64 experts, gate and up, 73 to 79 us, 1024 rows over 64 experts 320 us (6.8 TB/s).  Tensor pipe busy 88 to
 // 95 % (gradient 78, weight gradient 56 beside 62 % of HBM's nominal rate) at 512 rows per expert.
 #include <mutex>
 
