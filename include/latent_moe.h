@@ -591,7 +591,8 @@ lmoe_status lmoe_bf16_wait_selftest(long long budget_cycles, cudaStream_t stream
  * of infinity f is 0 (and infinite elements become NaN), with a NaN everything becomes NaN.
  * Host arrays of `count` (up to 2^20, copied before the call returns): grads, out (device pointers, aligned to
  * their elements; out = grads: in place), sizes (elements, 0 allowed: such a tensor is skipped), dtypes (LMOE_F32 or
- * LMOE_BF16).  An output may be its own gradient, but overlap no other tensor (LMOE_ERR_ARG).
+ * LMOE_BF16).  An output may be its own gradient, but overlap no other tensor, and the norm and the workspace that a call
+ * writes overlap nothing (LMOE_ERR_ARG).
  *  norm [1] fp32 device; max_norm >= 0
  *  workspace  lmoe_grad_norm_workspace_size() bytes, 8-byte aligned, nothing to be set or kept
  * Sums are taken in a fixed order: the same tensors give the same bits (copies that start otherwise within 16

@@ -361,6 +361,23 @@ lmoe_status check_outputs(const Grads& g) {
   return LMOE_OK;
 }
 
+// The norm and the workspace (bytes: 0, none) may share memory with each other or with a tensor no more than tensors may: CTAs write
+// them while others read or write those.  (A norm that is only read, lmoe_grad_clip's, may lie in a tensor that is.)
+lmoe_status check_own(const Grads& g, const float* norm, const void* workspace, size_t bytes) {
+  const auto meet = [](const void* a, size_t n, const void* b, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + m && y < x + n;
+  };
+  if (meet(norm, 4, workspace, bytes)) return LMOE_ERR_ARG;
+  for (int i = 0; i < g.count; ++i) {
+    const size_t n = static_cast<size_t>(g.sizes[i]) * (g.dtypes[i] == LMOE_F32 ? 4 : 2);
+    if (n == 0) continue;
+    if (bytes != 0 && (meet(g.src[i], n, norm, 4) || meet(g.src[i], n, workspace, bytes))) return LMOE_ERR_ARG;
+    if (g.dst != nullptr && (meet(g.dst[i], n, norm, 4) || meet(g.dst[i], n, workspace, bytes))) return LMOE_ERR_ARG;
+  }
+  return LMOE_OK;
+}
+
 }  // namespace
 }  // namespace lmoe
 
@@ -385,7 +402,8 @@ static lmoe_status check_norm(const Grads& g, const float* norm, const void* wor
 extern "C" lmoe_status lmoe_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes, int count,
                                       float* norm, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   const Grads g = {grads, nullptr, sizes, dtypes, count};
-  const lmoe_status st = check_norm(g, norm, workspace, workspace_bytes);
+  lmoe_status st = check_norm(g, norm, workspace, workspace_bytes);
+  if (st == LMOE_OK) st = check_own(g, norm, workspace, workspace_of(count));
   if (st != LMOE_OK) return st;
   double* partial = static_cast<double*>(workspace);
   int partials = 0;
@@ -403,6 +421,7 @@ extern "C" lmoe_status lmoe_grad_clip(const void* const* grads, void* const* out
   if (norm == nullptr || !(max_norm >= 0.f)) return LMOE_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(norm) & 3) return LMOE_ERR_ALIGN;
   st = check_outputs(g);
+  if (st == LMOE_OK) st = check_own(g, norm, nullptr, 0);
   if (st != LMOE_OK) return st;
   float* nm = const_cast<float*>(norm);
   const cudaError_t e = clip(g, nullptr, 0, nm, max_norm, stream);
@@ -417,6 +436,7 @@ extern "C" lmoe_status lmoe_clip_grad_norm(const void* const* grads, void* const
   if (st != LMOE_OK) return st;
   if (!(max_norm >= 0.f)) return LMOE_ERR_ARG;
   st = check_outputs(g);
+  if (st == LMOE_OK) st = check_own(g, norm, workspace, workspace_of(count));
   if (st != LMOE_OK) return st;
   double* partial = static_cast<double*>(workspace);
   int partials = 0;

@@ -168,6 +168,17 @@ GRADS_BAD = [
 ]
 
 
+@pytest.mark.parametrize("name,change", [
+    (n, c) for n in ALL for c in (dict(out=[Q], norm=Q + 396), dict(norm=P + 396), dict(out=[Q], ws=Q - 8), dict(ws=P + 392),
+                                  dict(norm=Q + 4096, ws=Q), dict(norm=Q, ws=Q))
+    if not (n == "lmoe_grad_clip" and "ws" in c) and not (n == "lmoe_grad_norm" and "out" in c)])
+def test_norm_and_workspace_that_share_memory_are_refused(lm, C, name, change):
+    far = dict(norm=P + (1 << 24), ws=P + (1 << 25))
+    n0 = lm.lmoe_kernel_launches()
+    assert grads(C, name, *ONE, **{**far, **change}) == ARG
+    assert lm.lmoe_kernel_launches() == n0
+
+
 @pytest.mark.parametrize("name,i", [(n, i) for i, c in enumerate(GRADS_BAD) for n in c[0]])
 def test_gradients_refused_without_launching(lm, C, name, i):
     _, status, args, change = GRADS_BAD[i]
