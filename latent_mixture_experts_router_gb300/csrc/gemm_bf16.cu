@@ -52,11 +52,12 @@ namespace {
 
 enum Bf16Mode : int { kGated = 0, kGatedGrad = 1, kProduct = 2, kProductT = 3, kWgrad = 4 };
 constexpr int kRaster = 8;       // row tiles that take turns before the next column of tiles
-// Tensor memory's fp32 sums are cut, not rounded, at each addition: 4096 products in a row leave 4.4e-6 of the result (2-norm),
-// in proportion to their number.  bf16 results do not show it; for fp32 results a sum in TMEM ends after kChunk
-// blocks of 64, and the epilogue adds those in registers (8e-7.  Sums of 8 blocks: 5e-7, but
-// experts of about 512 rows then take two: their weight gradients 246 us instead of 239).
-constexpr int kChunk = 12;
+// Tensor memory's fp32 sums are cut, not rounded, at each addition, in proportion to their number: 4096 products in a row leave
+// 4.4e-6 of the result (2-norm), and products of one sign, which are all cut in one direction, 6e-9 each.  For fp32 results a
+// sum in TMEM ends after kChunk blocks of 64, and the epilogue adds those in registers (7e-7, of one sign 1.3e-6.  Sums of 8
+// blocks: 5e-7, but experts of about 512 rows then take two: their weight gradients 246 us instead of 239).  bf16 results, whose
+// rounding is 1.7e-3 (2-norm), go the same way from kLong blocks on, where the cuts are 1e-4 (of 2^20 products they were 3.9e-3).
+constexpr int kChunk = 12, kLong = 256;
 // Budget of the waits for a CTA's own copies and MMAs at its end: they take microseconds.  (In a pair whose second CTA gave
 // up, the first one waits that long for copies that never started.)
 constexpr long long kDrain = 20000000;
@@ -88,8 +89,8 @@ __global__ void take_status_kernel() {
 }
 
 // UNIT: rows of a tile; 256: a pair of CTAs, 128 rows and half of the column operand's tile each.
-// F32: fp32 results of long reductions, see kChunk.
-template <int MODE, int UNIT, bool F32>
+// CHUNKED: sums of kChunk blocks, added in registers: fp32 results, and bf16 ones of more than kLong blocks.
+template <int MODE, int UNIT, bool CHUNKED>
 struct Bf16Cfg {
   static constexpr bool kPair = UNIT == 256;
   static constexpr bool kLanesMn = MODE == kWgrad;
@@ -97,7 +98,7 @@ struct Bf16Cfg {
   static constexpr int kLanes = kPair ? 128 : UNIT;               // that a CTA loads
   static constexpr int kBN = kPair ? 256 : 128;                   // accumulator columns
   static constexpr int kOutCols = MODE == kGated ? kBN / 2 : kBN;  // columns of a tile
-  static constexpr int kEpiWarps = kPair && F32 ? 8 : 4;
+  static constexpr int kEpiWarps = kPair && CHUNKED ? 8 : 4;
   // few rows: the one warp that has them leaves the sums in shared memory (in two buffers by turns), and all four finish them
   static constexpr bool kFlat = UNIT == 32;
   static constexpr int kLdFlat = 132;                             // floats of a row of 128 sums
@@ -107,9 +108,9 @@ struct Bf16Cfg {
   static constexpr int kRow = MODE == kGatedGrad ? 64 : 128;
   static constexpr int kWarpBytes = 32 * kRow * (MODE == kGatedGrad ? 3 : 1);
   static constexpr int kStagingBytes = kFlat ? 2 * 32 * kLdFlat * 4 : kEpiWarps * kWarpBytes;
-  // off[], and start[] (not kWgrad).  An fp32 kWgrad has room for a stage more than with all offsets: from kOffsets experts
+  // off[], and start[] (not kWgrad).  A chunked kWgrad has room for a stage more than with all offsets: from kOffsets experts
   // on they are read where they are (read there always, 16 experts' weight gradients to bf16 took 195 us, so 181).
-  static constexpr int kOffsets = F32 && MODE == kWgrad ? 320 : kMaxGroups + 4;
+  static constexpr int kOffsets = CHUNKED && MODE == kWgrad ? 320 : kMaxGroups + 4;
   static constexpr int kTableBytes = kOffsets * 4 * (MODE == kWgrad ? 1 : 2);
   static constexpr int kFixed = kStagingBytes + kTableBytes + 512 + 1024;
   static constexpr int kFit = (227 * 1024 - kFixed) / kStageBytes;
@@ -119,7 +120,7 @@ struct Bf16Cfg {
   // A pair's last tile of an expert, with no more than 128 rows: an MMA of 128 rows (64 of each CTA) takes half the time.
   // Its sums lie with their first 128 columns in lanes 0..63 and the others in lanes 64..127.
   static constexpr bool kShort = kPair && MODE != kWgrad;
-  static constexpr int kChunkBlocks = F32 ? kChunk : 1 << 30;
+  static constexpr int kChunkBlocks = CHUNKED ? kChunk : kLong;   // (kLong: all of it, no reduction is longer)
   static_assert((3 * kStages + 2 * 2 + 1 + 4) * 8 + 8 <= 512, "barriers");
   // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
   static_assert(kStageBytes >= 128 * 128, "lane operand");
@@ -279,9 +280,9 @@ struct Bf16Walk {
   int total;
 };
 
-template <int MODE, int UNIT, bool F32>
+template <int MODE, int UNIT, bool CHUNKED>
 LMOE_DEV Bf16Tile tile_at(const Bf16Walk& w, const Bf16Args& a, int id, int rank) {
-  using C = Bf16Cfg<MODE, UNIT, F32>;
+  using C = Bf16Cfg<MODE, UNIT, CHUNKED>;
   Bf16Tile t = {};
   int i, rows;   // tile i of `rows` row tiles by by_others.d
   if (MODE == kWgrad) {
@@ -564,20 +565,20 @@ struct Bf16Maps {
   const CUtensorMap *out, *out2, *out3, *gate, *up;
 };
 
-template <int MODE, int UNIT, bool F32>
+template <int MODE, int UNIT, bool CHUNKED>
 LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Ring& ring, const Bf16Maps& maps,
                        uint8_t* staging, uint64_t* landed, uint32_t tmem, int id0, int step, int rank) {
-  using C = Bf16Cfg<MODE, UNIT, F32>;
+  using C = Bf16Cfg<MODE, UNIT, CHUNKED>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = (warp - 4) >> 2;
   constexpr int kCols = C::kOutCols * 4 / C::kEpiWarps;   // of this warp
-  constexpr int kEs = F32 ? 4 : 2;
+  const int es = CHUNKED && args.out_f32 ? 4 : 2;
   const int width = MODE == kWgrad ? args.k : args.n;
   uint8_t* st = staging + (warp - 4) * C::kWarpBytes;
   uint8_t* in = st + 32 * C::kRow;   // kGatedGrad: gate's rows, and up's behind them
   uint64_t* mine = landed + (warp - 4);
   int tc = 0, loads = 0;
   for (int id = id0; id < walk.total; id += step) {
-    const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+    const Bf16Tile t = tile_at<MODE, UNIT, CHUNKED>(walk, args, id, rank);
     const int blocks = t.kb1 - t.kb0;   // (kWgrad: an expert without rows has none, and gets zeros)
     // (short tiles: 64 rows, whose other columns are two quadrants on)
     const int rows0 = C::kShort && t.brief ? (quad & 1) * 32 : quad * 32;
@@ -589,8 +590,8 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
     o.from = max(t.skip - rows0, 0);
     o.to = min(t.live - rows0, 32);
     o.row = (MODE == kWgrad ? static_cast<long long>(t.e) * args.n : 0) + t.p0 + rows0;
-    o.ld = static_cast<long long>(width) * kEs;
-    o.limit = width * kEs;
+    o.ld = static_cast<long long>(width) * es;
+    o.limit = width * es;
     o.r0 = t.p0 + rows0;
     o.e = t.e;
     // (kWgrad's tensors end with an expert's rows; elsewhere the rows behind may be another expert's)
@@ -603,20 +604,43 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = 0;
       if (any && !args.accumulate)
-        for (int c = 0; c < kCols && q0 + c < width; c += C::kRow / kEs) emit<MODE, C::kRow>(o, map, out, (q0 + c) * kEs, w);
+        for (int c = 0; c < kCols && q0 + c < width; c += C::kRow / es) emit<MODE, C::kRow>(o, map, out, (q0 + c) * es, w);
       continue;
     }
-    if constexpr (F32) {
+    if constexpr (CHUNKED) {
+      constexpr bool kTwo = MODE == kGated || MODE == kGatedGrad;   // (another product beside each sum)
+      static_assert(!kTwo || !C::kPair, "a warp has 64 columns of gate and the same of up");
       float acc[128];
       const int chunks = (blocks + C::kChunkBlocks - 1) / C::kChunkBlocks;
-      if (!gather_sums<C::kBN>(ring, tmem, half * cols, cols, chunks, tc, lane, quad, acc)) break;
+      if (!gather_sums<C::kBN>(ring, tmem, half * cols, kTwo ? 128 : cols, chunks, tc, lane, quad, acc)) break;
       if (!any) continue;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(acc);
+      if constexpr (kTwo) {   // (a row to a thread: a few us behind so long a reduction)
+        if (lane >= o.from && lane < o.to) {
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        if (c >= cols || q0 + c >= width) break;
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(acc + c);
-        if (MODE == kWgrad && args.accumulate) emit_added(o, out, width, q0 + c, true, w);
-        else emit<MODE, C::kRow>(o, map, out, (q0 + c) * 4, w);
+          for (int c = 0; c < kCols; c += 4) {
+            constexpr int kUp = MODE == kGated ? 64 : 0;
+            if (q0 + c < width)
+              finish4<MODE>(args, out, (o.row + lane) * width + q0 + c, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]),
+                            make_float4(acc[c + kUp], acc[c + kUp + 1], acc[c + kUp + 2], acc[c + kUp + 3]));
+          }
+        }
+      } else if (args.out_f32 || (MODE == kWgrad && args.accumulate)) {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          if (c >= cols || q0 + c >= width) break;
+          if (MODE == kWgrad && args.accumulate) emit_added(o, out, width, q0 + c, args.out_f32, w + c);
+          else emit<MODE, C::kRow>(o, map, out, (q0 + c) * 4, w + c);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 64) {
+          if (c >= cols || q0 + c >= width) break;
+          uint32_t h[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) h[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
+          emit<MODE, C::kRow>(o, map, out, (q0 + c) * 2, h);
+        }
       }
     } else {
       const auto load_gate = [&](int c) {   // 32 columns of gate and up
@@ -725,20 +749,20 @@ LMOE_DEV void epilogue(const Bf16Args& args, const Bf16Walk& walk, const Bf16Rin
 
 // Epilogue of tiles of few rows.  What a tile takes here is what bounds short reductions: a warp's own way (rows by tensor or
 // segment stores, gate and up of 32 columns at a time) took 5.8 us a tile for kGatedGrad.
-template <int MODE, int UNIT, bool F32>
+template <int MODE, int UNIT, bool CHUNKED>
 LMOE_DEV void epilogue_flat(const Bf16Args& args, const Bf16Walk& walk, const Bf16Ring& ring, float* sums, uint32_t tmem, int id0,
                             int step) {
-  using C = Bf16Cfg<MODE, UNIT, F32>;
+  using C = Bf16Cfg<MODE, UNIT, CHUNKED>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kShift = C::kOutCols == 128 ? 5 : 4;   // fours of columns
   int tc = 0, turn = 0;
   for (int id = id0; id < walk.total; id += step, turn ^= 1) {
-    const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, 0);
+    const Bf16Tile t = tile_at<MODE, UNIT, CHUNKED>(walk, args, id, 0);
     float* buf = sums + turn * 32 * C::kLdFlat;
     bool ok = true;
     if (warp == 4) {
       float acc[128];
-      const int chunks = F32 ? (t.blocks + kChunk - 1) / kChunk : 1;
+      const int chunks = (t.blocks + C::kChunkBlocks - 1) / C::kChunkBlocks;
       ok = gather_sums<C::kBN>(ring, tmem, 0, 128, chunks, tc, lane, 0, acc);
       if (ok && lane >= t.skip && lane < t.live) {
 #pragma unroll
@@ -753,14 +777,14 @@ LMOE_DEV void epilogue_flat(const Bf16Args& args, const Bf16Walk& walk, const Bf
   }
 }
 
-template <int MODE, int UNIT, bool F32>
-__global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
+template <int MODE, int UNIT, bool CHUNKED>
+__global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, CHUNKED>::kThreads, 1)
     gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmO2,
                      const __grid_constant__ CUtensorMap tmO3, const __grid_constant__ CUtensorMap tmGate,
                      const __grid_constant__ CUtensorMap tmUp, const Bf16Args args) {
-  using C = Bf16Cfg<MODE, UNIT, F32>;
+  using C = Bf16Cfg<MODE, UNIT, CHUNKED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -846,7 +870,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
 
   const Bf16Ring ring = {acc_full, C::kPair ? cluster_map(smem_u32(acc_empty), 0) : smem_u32(acc_empty), status, budget};
   if (warp < 4) {
-    if constexpr (C::kPair && F32) regs_dec<56>();
+    if constexpr (C::kPair && CHUNKED) regs_dec<56>();
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty), tail0 = smem_u32(tail);
     const uint32_t lead0 = C::kPair ? cluster_map(full0, 0) : full0;   // the barriers that the MMA issuer waits for
     if ((warp == 0 || warp == 3) && elect_one()) {
@@ -859,7 +883,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       uint32_t cleared = 0, phases = 0;   // stages whose last block went by its tail barrier; those barriers' parities
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
-        const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+        const Bf16Tile t = tile_at<MODE, UNIT, CHUNKED>(walk, args, id, rank);
         // the column operand's part of this CTA
         const int qb = t.q0 + (C::kPair ? rank * (C::kOutCols / 2) : 0);
         const CUtensorMap* map = lanes ? (MODE == kWgrad && t.second ? &tmA2 : &tmA) : &tmB;
@@ -949,7 +973,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       int tc = 0;
       bool ok = true;
       for (int id = id0; ok && id < walk.total; id += step) {
-        const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+        const Bf16Tile t = tile_at<MODE, UNIT, CHUNKED>(walk, args, id, rank);
         if (C::kShort) idesc = t.brief ? kBrief : kWhole;
         for (int c0 = t.kb0; ok && c0 < t.kb1; c0 += C::kChunkBlocks, ++tc) {
           const int buf = tc & 1, c1 = min(t.kb1 - c0, C::kChunkBlocks) + c0;
@@ -988,7 +1012,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       int it = 0;
       uint32_t phases = 0;
       for (int id = id0; id < walk.total; id += step) {
-        const Bf16Tile t = tile_at<MODE, UNIT, F32>(walk, args, id, rank);
+        const Bf16Tile t = tile_at<MODE, UNIT, CHUNKED>(walk, args, id, rank);
         it += t.kb1 - t.kb0;
         if (t.rows % 16 == 0 || t.kb0 == t.kb1 || t.kb1 != t.blocks) continue;
         const int s = (it - 1) % C::kStages;
@@ -1009,13 +1033,13 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (C::kPair && F32) regs_inc<224>();
+    if constexpr (C::kPair && CHUNKED) regs_inc<224>();
     if (C::kPair || S == 1) {
       if constexpr (C::kFlat) {
-        epilogue_flat<MODE, UNIT, F32>(args, walk, ring, reinterpret_cast<float*>(staging), tmem, id0, step);
+        epilogue_flat<MODE, UNIT, CHUNKED>(args, walk, ring, reinterpret_cast<float*>(staging), tmem, id0, step);
       } else {
         const Bf16Maps maps = {&tmO, &tmO2, &tmO3, &tmGate, &tmUp};
-        epilogue<MODE, UNIT, F32>(args, walk, ring, maps, staging, landed, tmem, id0, step, rank);
+        epilogue<MODE, UNIT, CHUNKED>(args, walk, ring, maps, staging, landed, tmem, id0, step, rank);
       }
     }
   }
@@ -1033,9 +1057,9 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
       Bf16Tile t = {};
       float acc[128];
       if (mine) {
-        t = tile_at<MODE, UNIT, F32>(walk, args, id0, rank);
+        t = tile_at<MODE, UNIT, CHUNKED>(walk, args, id0, rank);
         int tc = 0;
-        const int n = t.kb1 - t.kb0, chunks = F32 ? (n + kChunk - 1) / kChunk : n > 0;
+        const int n = t.kb1 - t.kb0, chunks = (n + C::kChunkBlocks - 1) / C::kChunkBlocks;
         const bool ok = C::kFlat && warp != 4 ? true : gather_sums<C::kBN>(ring, tmem, 0, 128, chunks, tc, lane, warp & 3, acc);
         if (!ok || chunks == 0) {
 #pragma unroll
@@ -1075,16 +1099,16 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, F32>::kThreads, 1)
   }
 }
 
-template <int MODE, int UNIT, bool F32>
+template <int MODE, int UNIT, bool CHUNKED>
 cudaError_t launch_one(const CUtensorMap (&m)[9], Bf16Args a, cudaStream_t s) {
-  using C = Bf16Cfg<MODE, UNIT, F32>;
+  using C = Bf16Cfg<MODE, UNIT, CHUNKED>;
   const unsigned others = ((MODE == kWgrad ? a.k : a.n) + C::kOutCols - 1) / C::kOutCols;
   const long long row_tiles = MODE == kWgrad ? (a.n + UNIT - 1) / UNIT : most_tiles(static_cast<int>(a.rows), a.E, UNIT);
   a.by_others = FastDiv::of(others);
   a.by_group = FastDiv::of(others * kRaster);
   a.by_tiles = FastDiv::of(static_cast<unsigned>(MODE == kWgrad ? row_tiles * others * a.pairs : 1));
   const long long tiles = row_tiles * others * (MODE == kWgrad ? 1LL * a.E * a.pairs : 1);
-  auto kern = gemm_bf16_kernel<MODE, UNIT, F32>;
+  auto kern = gemm_bf16_kernel<MODE, UNIT, CHUNKED>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if (a.splits > 1)
@@ -1223,7 +1247,7 @@ long long one_cycles(long long tiles, long long blocks, int s) {
 // rows of 2048 x 2048 8.5 and 10.7, of 1024 x 1024 8.4 and 8.1; 100 rows of 2048 x 4096 13.2 and 15.4, of 2048 x 2048 11.8 and 11.0;
 // kGatedGrad 16 rows of 1024 x 1024 9.4 and 13.8; weight gradients of 256 x 256 over 32768, 8000, 4000, 2000 rows 24.5, 15.4, 13.8,
 // 11.9 and (a pair's tile) 142, 22, 16.9, 11.4.
-template <int MODE, bool F32>
+template <int MODE, bool CHUNKED>
 lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a2, const void* w2, cudaStream_t stream) {
   const int R = static_cast<int>(g.rows), live = g.E < R ? g.E : R;
   const auto tiles_of = [&](int unit) {
@@ -1235,8 +1259,11 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
   const int wr = mn ? g.k : g.n, wc = mn ? g.n : g.k;   // a weight's rows and columns
   const long long blocks = g.num_kb * g.pairs;
   const int from = MODE == kGatedGrad ? 8 : few ? 24 : 48, shared = splits_for(tiles_of(few ? 32 : 128), blocks, from);
-  const bool pair = g.E == 1 ? pair_cycles(tiles_of(256), blocks, R <= 128) < one_cycles(tiles_of(128), blocks, shared)
-                             : tiles_of(256) >= kPairTiles && (wc % 64 != 0 || R / live >= kPairRows);
+  // (gate's and up's sums of more than one chunk: a warp of one CTA has the same columns of both in registers, a pair's has not)
+  constexpr bool single = CHUNKED && (MODE == kGated || MODE == kGatedGrad);
+  const bool pair = single     ? false
+                    : g.E == 1 ? pair_cycles(tiles_of(256), blocks, R <= 128) < one_cycles(tiles_of(128), blocks, shared)
+                               : tiles_of(256) >= kPairTiles && (wc % 64 != 0 || R / live >= kPairRows);
   const int unit = few ? 32 : pair ? 256 : 128;
   g.box = R < unit ? R : unit;
   if (unit < 256) g.splits = shared;
@@ -1248,7 +1275,7 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
     if (i != 2) m[i] = m[i == 3 ? 2 : 0];
   g.whole = unit > 32 && g.splits == 1;
   if (g.whole) {
-    const int es = F32 ? 2 : 1;   // (in 16-bit columns)
+    const int es = g.out_f32 ? 2 : 1;   // (in 16-bit columns)
     constexpr bool half = MODE == kGatedGrad;
     if (!map_rows(&m[4], g.out, R, g.n * es, 32, half) || (g.out2 != nullptr && !map_rows(&m[5], g.out2, R, g.n * es, 32, half)) ||
         (g.out3 != nullptr && !map_rows(&m[6], g.out3, R, g.n * es, 32)))
@@ -1258,9 +1285,14 @@ lmoe_status rows_product(Bf16Args g, const void* a, const void* w, const void* a
     return LMOE_ERR_CUDA;
   if ((a2 != nullptr && !map_rows(&m[1], a2, R, g.k, rows)) || (w2 != nullptr && !map_weights(&m[3], w2, g.E, wr, wc, high)))
     return LMOE_ERR_CUDA;
-  const cudaError_t e = unit == 32    ? launch_one<MODE, 32, F32>(m, g, stream)
-                        : unit == 128 ? launch_one<MODE, 128, F32>(m, g, stream)
-                                      : launch_one<MODE, 256, F32>(m, g, stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  if (unit == 32) {
+    e = launch_one<MODE, 32, CHUNKED>(m, g, stream);
+  } else if (unit == 128) {
+    e = launch_one<MODE, 128, CHUNKED>(m, g, stream);
+  } else if constexpr (!single) {
+    e = launch_one<MODE, 256, CHUNKED>(m, g, stream);
+  }
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
@@ -1288,7 +1320,8 @@ extern "C" lmoe_status lmoe_gated_ffn(const lmoe_bf16_matmul* c, const void* x, 
   g.out = h;
   g.out2 = gate;
   g.out3 = up;
-  return rows_product<kGated, false>(g, x, w_gate, nullptr, w_up, stream);
+  return g.num_kb > kLong ? rows_product<kGated, true>(g, x, w_gate, nullptr, w_up, stream)
+                          : rows_product<kGated, false>(g, x, w_gate, nullptr, w_up, stream);
 }
 
 extern "C" lmoe_status lmoe_gated_ffn_grad(const lmoe_bf16_matmul* c, const void* dy, const void* w_down,
@@ -1314,7 +1347,8 @@ extern "C" lmoe_status lmoe_gated_ffn_grad(const lmoe_bf16_matmul* c, const void
   g.up = static_cast<const __nv_bfloat16*>(up);
   g.out = dgate;
   g.out2 = dup;
-  return rows_product<kGatedGrad, false>(g, dy, w_down, nullptr, nullptr, stream);
+  return g.num_kb > kLong ? rows_product<kGatedGrad, true>(g, dy, w_down, nullptr, nullptr, stream)
+                          : rows_product<kGatedGrad, false>(g, dy, w_down, nullptr, nullptr, stream);
 }
 
 extern "C" lmoe_status lmoe_matmul_bf16(const lmoe_bf16_matmul* c, const void* a, const void* w, const void* a2,
@@ -1335,11 +1369,12 @@ extern "C" lmoe_status lmoe_matmul_bf16(const lmoe_bf16_matmul* c, const void* a
   Bf16Args g = args_of(c, offsets, status);
   g.pairs = a2 != nullptr ? 2 : 1;
   g.out = out;
+  const bool chunked = g.out_f32 || g.num_kb * g.pairs > kLong;
   if (c->transposed)
-    return g.out_f32 ? rows_product<kProductT, true>(g, a, w, a2, w2, stream)
-                     : rows_product<kProductT, false>(g, a, w, a2, w2, stream);
-  return g.out_f32 ? rows_product<kProduct, true>(g, a, w, a2, w2, stream)
-                   : rows_product<kProduct, false>(g, a, w, a2, w2, stream);
+    return chunked ? rows_product<kProductT, true>(g, a, w, a2, w2, stream)
+                   : rows_product<kProductT, false>(g, a, w, a2, w2, stream);
+  return chunked ? rows_product<kProduct, true>(g, a, w, a2, w2, stream)
+                 : rows_product<kProduct, false>(g, a, w, a2, w2, stream);
 }
 
 extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const void* dy, const void* x,
@@ -1387,8 +1422,9 @@ extern "C" lmoe_status lmoe_matmul_bf16_wgrad(const lmoe_bf16_matmul* c, const v
     if (i != 2 && i != 4) m[i] = m[0];
   if (dw2 != nullptr && !map_weights(&m[5], dw2, g.E, g.n, g.k * es, 32)) return LMOE_ERR_CUDA;
   if (dy2 != nullptr && !map_rows(&m[1], dy2, c->rows, c->N, kBK)) return LMOE_ERR_CUDA;
-  const cudaError_t e = g.out_f32 ? (pair ? launch_one<kWgrad, 256, true>(m, g, stream) : launch_one<kWgrad, 128, true>(m, g, stream))
-                                  : (pair ? launch_one<kWgrad, 256, false>(m, g, stream) : launch_one<kWgrad, 128, false>(m, g, stream));
+  const bool chunked = g.out_f32 || c->rows > 1LL * kLong * kBK;   // (one expert may have all rows)
+  const cudaError_t e = chunked ? (pair ? launch_one<kWgrad, 256, true>(m, g, stream) : launch_one<kWgrad, 128, true>(m, g, stream))
+                                : (pair ? launch_one<kWgrad, 256, false>(m, g, stream) : launch_one<kWgrad, 128, false>(m, g, stream));
   return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
