@@ -59,8 +59,8 @@ constexpr int kRaster = 8;       // row tiles that take turns before the next co
 // rounding is 1.7e-3 (2-norm), go the same way from kLong blocks on, where the cuts are 1e-4 (of 2^20 products they were 3.9e-3).
 constexpr int kChunk = 12, kLong = 256;
 // Budget of the waits for a CTA's own copies and MMAs at its end: they take microseconds.  (In a pair whose second CTA gave
-// up, the first one waits that long for copies that never started.)
-constexpr long long kDrain = 20000000;
+// up, the first one waits that long for copies that never started.)  A pair with a producer that gave up stays kLast more.
+constexpr long long kDrain = 20000000, kLast = 2000000;
 
 struct Bf16Args {
   FastDiv by_others, by_group;   // tiles across; kRaster rows of them
@@ -121,7 +121,7 @@ struct Bf16Cfg {
   // Its sums lie with their first 128 columns in lanes 0..63 and the others in lanes 64..127.
   static constexpr bool kShort = kPair && MODE != kWgrad;
   static constexpr int kChunkBlocks = CHUNKED ? kChunk : kLong;   // (kLong: all of it, no reduction is longer)
-  static_assert((3 * kStages + 2 * 2 + 1 + 4) * 8 + 8 <= 512, "barriers");
+  static_assert((3 * kStages + 2 * 2 + 1 + 4) * 8 + 2 * 4 <= 512, "barriers, tmem_slot, gave_up");
   // the MMA reads 128 lanes, the tile's rows and whatever lies behind them in the stage
   static_assert(kStageBytes >= 128 * 128, "lane operand");
   // sums of a tile shared by a cluster of up to 8: of each row 128, and 4 or 8 floats of padding for each CTA
@@ -236,6 +236,7 @@ struct RingAt {
 LMOE_DEV void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+LMOE_DEV void set_at(uint32_t addr) { asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(addr) : "memory"); }
 // Registers of a warpgroup: 4 x 32 x 56 + 8 x 32 x 224 = 384 x 168, what the block was launched with.
 template <int N>
 LMOE_DEV void regs_dec() {
@@ -799,6 +800,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, CHUNKED>::kThreads, 1)
   uint64_t* mma_done = acc_empty + 2;
   uint64_t* landed = mma_done + 1;           // [4] kGatedGrad: a warp's rows of gate and up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + 4);
+  uint32_t* gave_up = tmem_slot + 1;         // whether a producer of either CTA of a pair did
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -813,6 +815,7 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, CHUNKED>::kThreads, 1)
     }
     mbar_init(mma_done, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&landed[i], 1);
+    *gave_up = 0;
     fence_mbar_init();
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
@@ -938,8 +941,12 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, CHUNKED>::kThreads, 1)
           ++issued;
         }
       }
-      // Every copy lands before the CTA leaves.  A pair's are counted by the first CTA, and neither leaves before the other; a
-      // second CTA that gave up may have copies that the first one did not count, which land within this millisecond.
+      // Every copy lands before the CTA leaves.  A pair's are counted by the first CTA, and neither leaves before the other; once
+      // any of a pair's producers gave up, the others may have copies that the first CTA does not count (see the teardown).
+      if (C::kPair && !ok) {
+        set_at(cluster_map(smem_u32(gave_up), 0));
+        set_at(cluster_map(smem_u32(gave_up), 1));
+      }
       for (int j = max(0, issued - C::kStages); j < issued; ++j) {
         const int s = j % C::kStages;
         const bool tail_bar = MODE == kWgrad && (cleared >> s & 1);
@@ -951,7 +958,6 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, CHUNKED>::kThreads, 1)
           break;
         }
       }
-      if (C::kPair && rank != 0 && !ok) wait_at(full0, 0, kDrain / 10);   // (a barrier that nothing arrives on)
     } else if (warp == 1 && (!C::kPair || rank == 0) && elect_one()) {
       // ---- MMA issuer
       constexpr uint32_t kMajor = (C::kLanesMn ? 1u << 15 : 0u) | (C::kColsMn ? 1u << 16 : 0u);
@@ -1089,6 +1095,10 @@ __global__ void __launch_bounds__(Bf16Cfg<MODE, UNIT, CHUNKED>::kThreads, 1)
   tc_fence_before();
   if (C::kPair) cluster_sync();
   else __syncthreads();
+  // (no producer of either CTA issues any more: what was not counted lands within this millisecond, in both CTAs' memory and on
+  // the first one's barriers)
+  if (C::kPair && warp == 3 && lane == 0 && *gave_up != 0)
+    for (const long long t0 = clock64(); clock64() - t0 < kLast;) __nanosleep(1000);
   if (!issuer && warp == 1) {
     if (!warp_wait(mma_done, 0, kDrain) && lane == 0) atomicOr(status, kErrDrain);
   }
