@@ -379,6 +379,7 @@ def lmoe_permute_noalloc(topk_idx, E: int, offsets, row_of, tok_of, stream=None)
     fn.argtypes = [_P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P]
     fn.restype = ctypes.c_int
     T, k = topk_idx.shape
+    _need(max(T, k, E) <= _INT_MAX, _TOO_LARGE)
     # the library looks its scratch up for the current device: make the ids' device current
     # and take the stream from it
     with torch.cuda.device(topk_idx.device):
@@ -394,6 +395,7 @@ def lmoe_quantize_nvfp4(src, codes, scales, s_row=None, row_scale=True, stream=N
     fn.argtypes = [_P, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P]
     fn.restype = ctypes.c_int
     rows, K = src.shape
+    _need(K <= _INT_MAX, _TOO_LARGE)
     _check(fn(_ptr(src), rows, K, 1 if row_scale else 0, _ptr(codes), _ptr(scales), _ptr(s_row),
               _stream(stream)), "lmoe_quantize_nvfp4")
 
@@ -406,6 +408,7 @@ def lmoe_nvfp4_block_scales(src, K: int, block_rows: int = 128, dst=None, stream
     fn = L.lmoe_nvfp4_block_scales
     fn.argtypes = [_P, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, _P, _P]
     fn.restype = ctypes.c_int
+    _need(K <= _INT_MAX, _TOO_LARGE)
     rows = src.numel() // (K // 16)
     if dst is None:
         dst = torch.zeros(rows // block_rows * (K // 64) * 512, dtype=torch.uint8, device=src.device)
@@ -427,6 +430,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
+
+
+# The library takes sizes in 32 bits, and ctypes cuts what is longer: 2**32 + 8 would arrive as 8.
+_INT_MAX = 0x7fffffff
+_TOO_LARGE = "a size is beyond 32 bits"
 
 
 def _want(t, name, dtypes, shape, device, strided=False):
@@ -459,6 +467,7 @@ def _call(fn, where, device, stream, *args):
 
 
 def lmoe_router_losses_workspace_size(T: int, E: int) -> int:
+    _need(max(T, E) <= _INT_MAX, _TOO_LARGE)
     n = ctypes.c_size_t()
     _check(_lib().lmoe_router_losses_workspace_size(int(T), int(E), ctypes.byref(n)),
            "lmoe_router_losses_workspace_size")
@@ -468,6 +477,7 @@ def lmoe_router_losses_workspace_size(T: int, E: int) -> int:
 def _router_args(logits, topk_idx, router_bias, row_mask):
     _need(logits.dim() == 2 and topk_idx.dim() == 2, "logits [T, E] and topk_idx [T, k]")
     dev, (T, E), k = logits.get_device(), logits.shape, topk_idx.shape[1]
+    _need(max(T, E, k) <= _INT_MAX, _TOO_LARGE)
     _want(logits, "logits", _DENSE, (T, E), dev, strided=True)
     _want(topk_idx, "topk_idx", torch.int32, (T, k), dev)
     if router_bias is not None:
@@ -516,12 +526,14 @@ def lmoe_router_grad(logits, topk_idx, counts, dlogits, topk_w_grad=None, loss_g
 
 def lmoe_fp8_padded_rows(rows: int, n_experts: int) -> int:
     """Columns that any split of ``rows`` among ``n_experts`` fits in, each padded to blocks of 128."""
+    _need(n_experts <= _INT_MAX, _TOO_LARGE)
     return int(_lib().lmoe_fp8_padded_rows(int(rows), int(n_experts)))
 
 
 def _routed_src(src, row_index):
     _need(src.dim() == 2, "src [rows, K]")
     dev, (n, K) = src.get_device(), src.shape
+    _need(K <= _INT_MAX, _TOO_LARGE)
     _want(src, "src", _DENSE, (n, K), dev, strided=True)
     if row_index is None:
         return dev, n, K, n
@@ -548,6 +560,7 @@ def lmoe_quantize_fp8_weight(src, codes, scales, codes_t=None, scales_t=None, po
     also the transposed pair."""
     _need(src.dim() in (2, 3), "src [N, K] or [E, N, K]")
     dev, (N, K), lead = src.get_device(), src.shape[-2:], src.shape[:-2]
+    _need(max(src.shape) <= _INT_MAX, _TOO_LARGE)
     nb, kb = -(-N // 128), -(-K // 128)
     _want(src, "src", _DENSE, src.shape, dev)
     _want(codes, "codes", _FP8, src.shape, dev)
@@ -582,6 +595,7 @@ def lmoe_quantize_fp8_cols(src, codes_t, scales_t, offsets=None, row_index=None,
 
 def _fp8_product(fn, where, dev, stream, rows, N, K, E, a, a_scales, b, b_scales, offsets, out, accumulate, status,
                  unpadded=0):
+    _need(max(N, K, E) <= _INT_MAX, _TOO_LARGE)
     if offsets is not None:
         _want(offsets, "offsets", torch.int32, (E + 1,), dev)
     if status is not None:
@@ -666,6 +680,7 @@ def _bf16(t, name, shape, device):
 
 @functools.lru_cache(maxsize=1024)
 def _bf16_shape(rows, N, K, E, out_dtype, transposed, accumulate):
+    _need(max(N, K, E) <= _INT_MAX, _TOO_LARGE)
     return ctypes.byref(lmoe_bf16_matmul(rows, N, K, E, out_dtype, transposed, accumulate, 0))
 
 
@@ -787,6 +802,7 @@ def lmoe_bf16_wait_selftest(budget_cycles: int, device=None, stream=None):
 
 # ------------------------------------------------------------------ the norm over all gradients, clipping
 def lmoe_grad_norm_workspace_size(count: int) -> int:
+    _need(count <= _INT_MAX, _TOO_LARGE)
     n = ctypes.c_size_t()
     _check(_lib().lmoe_grad_norm_workspace_size(int(count), ctypes.byref(n)), "lmoe_grad_norm_workspace_size")
     return n.value
