@@ -3,21 +3,38 @@
 Every function here turns torch tensors into device pointers, calls the C entry
 point of the same name, and raises ``LmoeError`` on a non-zero status.  No part
 of the block is computed in Python; if the shared library is missing, importing
-it fails loudly (there is no fallback path).
+it fails loudly (there is no fallback path).  The extension _tensors looks tensors over for
+the bf16 experts' calls and the gradients' norm: without it those raise, the others do not need it.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
 from dataclasses import dataclass
 
 import torch
 
+_HOW = "python -c 'import __graft_entry__ as g; g.build()' builds it"   # (from the repository's root)
+
+
+class _NoTensors:
+    """The extension's functions where it cannot be loaded."""
+
+    def __init__(self, why):
+        self.why = f"{why}; {_HOW}"
+
+    def bf16_at(self, *args):
+        raise ImportError(self.why)
+
+    gradients = bf16_at
+
+
 try:
-    from . import _tensors   # csrc/tensors.cpp
+    _tensors = importlib.import_module("._tensors", __package__)   # csrc/tensors.cpp
 except ImportError as e:
-    raise ImportError(f"{e}; run latent_mixture_experts_router_gb300.build.build()") from None
+    _tensors = _NoTensors(e)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblatent_moe.so")
@@ -101,7 +118,7 @@ def _lib():
     global _lib_handle
     if _lib_handle is None:
         if not os.path.exists(LIB_PATH):
-            raise ImportError(f"{LIB_PATH} is not built; run latent_mixture_experts_router_gb300.build.build()")
+            raise ImportError(f"{LIB_PATH} is not built; {_HOW}")
         L = ctypes.CDLL(LIB_PATH)
         L.lmoe_status_string.restype = ctypes.c_char_p
         L.lmoe_status_string.argtypes = [ctypes.c_int]

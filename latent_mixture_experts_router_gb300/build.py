@@ -5,7 +5,8 @@ to ``_build/`` next to this file.  A unit is recompiled when it or any header
 under csrc/ or include/ is newer than its object.
 
 The binding's extension _tensors.so (csrc/tensors.cpp, torch's and Python's headers, no CUDA) is compiled beside them by
-the host compiler.
+the host compiler.  Where that fails the library is made all the same, before build() raises: only the calls that need
+the extension are missing then.
 
 ``build(checked=True)`` makes the checked variant liblatent_moe_checked.so (objects
 in ``_build_checked/``): the same sources with -DLMOE_BOUNDS_CHECKS=1, whose forward
@@ -69,6 +70,22 @@ def _newer(src: str, obj: str, deps) -> bool:
     return os.path.getmtime(src) > t or any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_tensors(verbose: bool):
+    """The binding's extension, if it is older than its source."""
+    src = os.path.join(CSRC, "tensors.cpp")
+    if not _newer(src, LIB_TENSORS, ()):
+        return
+    try:
+        cmd = _tensors_cmd(src)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except (OSError, AttributeError) as e:   # no compiler, no torch
+        raise RuntimeError(f"{src}: {e}") from None
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {src}")
+
+
 def build(verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
     """Build (or reuse) the shared library and return its path (checked: the bounds-checked
     variant)."""
@@ -88,20 +105,18 @@ def build(verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
             jobs.append([nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", obj])
     objs = [os.path.join(BUILD, os.path.basename(s) + ".o") for s in srcs]
     link = bool(jobs)
-    tensors = os.path.join(CSRC, "tensors.cpp")
-    if not checked and _newer(tensors, LIB_TENSORS, ()):
-        jobs.insert(0, _tensors_cmd(tensors))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        extension = None if checked else ex.submit(_build_tensors, verbose)
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"{cmd[0]} failed on {cmd[-3] if cmd[0] == nvcc else tensors}")
+                raise RuntimeError(f"nvcc failed on {cmd[-3]}")
     if link or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, *_cuda_lib_dirs(), "-lcudart"]
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -109,6 +124,8 @@ def build(verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError("link failed")
+    if extension is not None:
+        extension.result()
     return LIB
 
 
