@@ -33,6 +33,8 @@ class _NoTensors:
 
 try:
     _tensors = importlib.import_module("._tensors", __package__)   # csrc/tensors.cpp
+    if getattr(_tensors, "torch_version", None) != str(torch.__version__):
+        raise ImportError(f"{_tensors.__name__} was built for another torch than {torch.__version__}")
 except ImportError as e:
     _tensors = _NoTensors(e)
 

@@ -4,8 +4,9 @@ Each translation unit compiles in its own nvcc process, in parallel; objects go
 to ``_build/`` next to this file.  A unit is recompiled when it or any header
 under csrc/ or include/ is newer than its object.
 
-The binding's extension _tensors.so (csrc/tensors.cpp, torch's and Python's headers, no CUDA) is compiled beside them by
-the host compiler.  Where that fails the library is made all the same, before build() raises: only the calls that need
+The binding's extension _tensors.*.so (csrc/tensors.cpp, torch's and Python's headers, no CUDA) is compiled beside them by
+the host compiler, and again where torch, Python or the command are others: it reads torch's objects as those headers lay
+them out.  Where that fails the library is made all the same, before build() raises: only the calls that need
 the extension are missing then.
 
 ``build(checked=True)`` makes the checked variant liblatent_moe_checked.so (objects
@@ -19,6 +20,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -28,7 +30,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblatent_moe.so")
-LIB_TENSORS = os.path.join(PKG, "_tensors.so")
+LIB_TENSORS = os.path.join(PKG, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))   # (with Python's ABI)
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "liblatent_moe_checked.so")
 
@@ -54,13 +56,23 @@ def _cuda_lib_dirs():
     return dirs
 
 
+def _torch() -> tuple:
+    """torch's directory and version (torch is found, not imported)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    root = list(spec.submodule_search_locations)[0]
+    with open(os.path.join(root, "version.py")) as f:
+        return root, re.search(r"__version__ = ['\"]([^'\"]+)", f.read()).group(1)
+
+
 def _tensors_cmd(src: str) -> list:
-    """The host compiler's command for the binding's extension (torch is found, not imported)."""
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
-    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"],
-            "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), src, "-L" + lib, "-ltorch_python",
-            "-ltorch_cpu", "-lc10", "-o", LIB_TENSORS]
+    """The host compiler's command for the binding's extension."""
+    root, version = _torch()
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f'-DLMOE_TORCH_VERSION="{version}"',
+            "-I" + sysconfig.get_paths()["include"], "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+            src, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def _newer(src: str, obj: str, deps) -> bool:
@@ -71,19 +83,26 @@ def _newer(src: str, obj: str, deps) -> bool:
 
 
 def _build_tensors(verbose: bool):
-    """The binding's extension, if it is older than its source."""
+    """The binding's extension, if its source is newer or it was made by another command (for another torch)."""
     src = os.path.join(CSRC, "tensors.cpp")
-    if not _newer(src, LIB_TENSORS, ()):
-        return
+    cmd = _tensors_cmd(src)
+    key, path = "\n".join(cmd), LIB_TENSORS + ".key"
+    if os.path.exists(path) and not _newer(src, LIB_TENSORS, ()):
+        with open(path) as f:
+            if f.read() == key:
+                return
+    made = LIB_TENSORS + ".new"
     try:
-        cmd = _tensors_cmd(src)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-    except (OSError, AttributeError) as e:   # no compiler, no torch
+        r = subprocess.run([*cmd, "-o", made], capture_output=True, text=True)
+    except OSError as e:   # no compiler
         raise RuntimeError(f"{src}: {e}") from None
     if verbose or r.returncode != 0:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {src}")
+    os.replace(made, LIB_TENSORS)
+    with open(path, "w") as f:
+        f.write(key)
 
 
 def build(verbose: bool = False, extra_flags=(), checked: bool = False) -> str:

@@ -105,4 +105,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensors(void) { return PyModule_Create(&module); }
+// torch_version: of the headers, whose layout of torch's objects is compiled in
+PyMODINIT_FUNC PyInit__tensors(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", LMOE_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -57,3 +57,42 @@ def test_the_library_is_made_where_the_extension_is_not(build, tmp_path, monkeyp
             build.build()
         assert os.path.exists(lib)
         os.remove(lib)
+
+
+def test_the_extension_is_made_again_for_another_torch(build, tmp_path, monkeypatch):
+    """As after an upgrade: the source is as old as it was, torch is not."""
+    made = []
+
+    def fake(cmd, **kw):
+        made.append(cmd)
+        if "-o" in cmd:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    root, version = build._torch()
+    monkeypatch.setattr(build, "LIB_TENSORS", str(tmp_path / "_tensors.so"))
+    monkeypatch.setattr(build.subprocess, "run", fake)
+    for v, commands in ((version, 1), (version, 1), ("1.0+other", 2), ("1.0+other", 2), (version, 3)):
+        monkeypatch.setattr(build, "_torch", lambda: (root, v))
+        build.build()
+        assert len(made) == commands and all(any("tensors.cpp" in a for a in c) for c in made)
+    monkeypatch.setenv("CXX", "another-compiler")
+    build.build()
+    assert len(made) == 4 and made[-1][0] == "another-compiler"
+
+
+def test_an_extension_of_another_torch_is_not_used(build, tmp_path):
+    r = run(f"""
+import sys, types
+old = types.ModuleType("{PKG}._tensors")
+old.torch_version, old.bf16_at, old.gradients = "1.0+other", None, None
+sys.modules[old.__name__] = old
+import torch, {PKG} as lm
+x = torch.zeros(8, 64, dtype=torch.bfloat16)
+try:
+    lm.lmoe_gated_ffn(x, x, x, x)
+except ImportError as e:
+    assert "another torch" in str(e) and "__graft_entry__" in str(e), e
+else:
+    raise AssertionError("called")
+""", ROOT)
+    assert r.returncode == 0, r.stderr
