@@ -249,12 +249,13 @@ LMOE_DEV void regs_inc() {
 
 LMOE_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 1 / (1 + exp(-g)); exp may reach infinity, its reciprocal is 0 then (an approximation with subnormal
-// results: __fdividef would give 0 from 2^126 on).
+// 1 / (1 + exp(-g)), for g below 0 exp(g) / (1 + exp(g)): exp(-g) is infinity from g = -88.7 on, where the result is still
+// 3e-39, and beside an up of 1e38 or so far from nothing.
 LMOE_DEV float sigmoid(float g) {
+  const float t = __expf(-fabsf(g));
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
-  return r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + t));
+  return g < 0.f ? t * r : r;
 }
 
 // A tile as one CTA sees it.
@@ -361,7 +362,7 @@ LMOE_DEV void store4(void* out, long long at, float4 v, bool f32) {
 }
 LMOE_DEV void gated_grad(float dh, float g, float u, float& dg, float& du) {
   const float s = sigmoid(g);
-  dg = dh * u * (s * (1.f + g * (1.f - s)));
+  dg = dh * (u * (s * (1.f + g * (1.f - s))));   // (dh u may leave fp32's range before the rest takes it back)
   du = dh * (g * s);
 }
 LMOE_DEV float silu_mul(float g, float u) { return g * sigmoid(g) * u; }
