@@ -540,8 +540,8 @@ lmoe_status lmoe_matmul_fp8_wgrad(const lmoe_fp8_matmul* shape, const uint8_t* d
  *  accumulate wgrad: nonzero adds to what dw holds, rounded once after the addition (else 0)
  *  wait_budget_cycles  SM clock cycles a device wait may spin before it gives up (0: default)
  * offsets [n_experts + 1] int32 device, non-decreasing, clamped into [0, rows]; NULL with n_experts = 1: all rows.
- * Rows of no expert are neither read nor written.  What a masked (padded) row holds does not reach other
- * rows; in a weight gradient, rows of no expert or of another one do not count, whatever they hold.
+ * Rows of no expert are not written, and what they hold does not count.  What a masked (padded) row holds does not reach
+ * other rows; in a weight gradient, rows of no expert or of another one do not count, whatever they hold.
  * Matrices are contiguous and 16-byte aligned, offsets and status 4-byte.  A result that shares memory with another one or
  * with an operand is refused (LMOE_ERR_ARG), but for dgate = gate and dup = up.  status (device): error word, a bit is set if a device wait
  * gives up and leaves the result unfinished; the caller zeroes it.  NULL: the device's own word

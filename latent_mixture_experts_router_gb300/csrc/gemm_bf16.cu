@@ -22,9 +22,10 @@
 // Tiles (UNIT rows, see rows_product for which where and what was measured):
 //   256   a pair of CTAs (cta_group::2), 256 x 256 sums: each CTA loads 128 rows of the lane operand and half of the
 //         column operand's tile, 32 KB for 128 x 256 x 64 products, which shared memory can take in in the time of the MMAs
-//         (a single CTA's 128 x 128 tiles take in twice as much: 32768 rows over 64 experts of 4096 x 4096, gate and up 2568
-//         us, so 1360).  kGated: columns are 64 of gate, the same 64 of up, and so on.  An expert's last tile, if it has
-//         no more than 128 rows, goes by MMAs of half the height (612 and 412 rows in turn: 1600 us without, so 1480).
+//         (a single CTA's 128 x 128 tiles take in twice as much: 32768 uneven rows over 64 experts of 4096 x 4096, gate and
+//         up 2568 us, by pairs 2010 with all else as it was).  kGated: columns are 64 of gate, the same 64 of up, and so on.  An
+//         expert's last tile, if it has no more than 128 rows, goes by MMAs of half the height (612 and 412 rows in turn: 1600 us
+//         without, so 1440 to 1480).
 //   128   one CTA, 128 x 128 sums: fewer rows per expert, or too few tiles of 256.
 //   32    the same with loads of up to 32 rows: a few tokens.  Bound by the stream of weights.
 // Few tiles with a long reduction are shared by a cluster of up to 8 CTAs.
@@ -36,10 +37,11 @@
 // through its own shared memory and leave by tensor stores; where they are not all the tile's, by stores of whole segments.
 //
 // Measured (other inputs in each call, power-limited at 1.6 to 1.7 GHz where it is tensor-bound): 32768 uneven rows over 64 experts
-// of 4096 x 4096, g and u stored, 1790 to 1900 us; the gradient of 16384 over 32 480 us; dx of 16384 over 32, two pairs, 920 us;
-// 16384 x 8192 x 8192 1100 us (2.0 PFLOP/s) cold, 1270 sustained; two weight gradients of 8192 rows over 16 to fp32 525 us
-// (4.5 TB/s); one token on 8 of 64 experts, gate and up, 73 to 79 us, 1024 rows over 64 experts 320 us (6.8 TB/s).  Tensor pipe busy 88 to
-// 95 % (gradient 78, weight gradient 56 beside 62 % of HBM's nominal rate) at 512 rows per expert.
+// of 4096 x 4096, g and u stored, 1790 to 1900 us (even experts, the same inputs: 1270); the gradient of 16384 over 32 475 us (even, the
+// same 384); dx of 16384 over 32, two pairs, 925 us (650); 16384 x 8192 x 8192 1120 to 1220 us a call (1.8 to 1.96 PFLOP/s), 1315 back
+// to back (1.67); two weight gradients of 8192 rows over 16 to fp32 520 us (4.5 TB/s); one token on 8 of 64 experts, gate and up, 73
+// to 81 us, 1024 rows over 64 experts 323 us (6.8 TB/s).  Tensor pipe busy 88 to 95 % (gradient 80, weight gradient 56
+// beside 62 % of HBM's nominal rate) at 512 rows per expert.
 #include <mutex>
 
 #include "../../include/latent_moe.h"

@@ -10,7 +10,7 @@
 //
 // A thread sums its 8 x 16 bytes of a chunk in fp32 and adds that to an fp64 sum.  Squares leave fp32's range for
 // elements beyond 2^+-63: a sum that is not between 2^-80 and 2^100 (and not of zeros alone) is taken again
-// in fp64, from registers; terms that an accepted sum loses below 2^-126 are 2^-40 of it.
+// in fp64, from memory once more; terms that an accepted sum loses below 2^-126 are 2^-40 of it.
 #include "../../include/latent_moe.h"
 #include "internal.h"
 #include "ptx.cuh"
